@@ -409,6 +409,173 @@ ns_status ns_orthogonalize_waves(int32_t n, const ns_shape *shapes, const void *
                                  void *stream);
 
 /* ------------------------------------------------------------------------ *
+ * Operators of a training step around the update: the ones between the
+ * library matrix products of a transformer whose matrices
+ * ns_orthogonalize_* updates. Each takes bf16 or f32 tensors, computes in
+ * fp32 and rounds every output once, to nearest even.
+ *
+ * Every tensor may be a strided view as its arguments say; data needs the
+ * alignment of its element type only. A workspace belongs to one call in
+ * flight at a time, need not be cleared, and must be 256-byte aligned. No
+ * call allocates, synchronises or copies to the host, so all can be captured
+ * into a HIP graph. Results do not depend on launch order: the same inputs
+ * give the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* A (batch, seq, heads, head_dim) tensor: value d of head h of token s of
+ * sequence b is at data[b * batch_stride + s * token_stride + h * head_stride
+ * + d] (strides in elements, >= 0). Covers both (batch, seq, heads, head_dim)
+ * and (batch, heads, seq, head_dim) order and the query or key part of a fused
+ * projection's output. data may be NULL if heads, batch or seq is 0. */
+typedef struct ns_heads {
+    void *data;
+    int64_t batch_stride, token_stride, head_stride;
+    int32_t heads;
+} ns_heads;
+
+/* RMS norm of each query and key head over its head_dim values, times its
+ * weight, then the position rotation, in one pass:
+ *   u = x / sqrt(mean(x^2) + eps) * weight
+ *   out = u with its first rope_dim values turned in pairs: with angle i of the
+ *         token's position, (u_i, u_j) -> (u_i cos - u_j sin, u_j cos + u_i sin)
+ *         where j = i + rope_dim / 2, or with `interleaved` the pair is
+ *         (u_2i, u_2i+1). The other values of a head pass through.
+ * head_dim 1 .. 1024; rope_dim even, 0 .. head_dim (0: no rotation, cos, sin
+ * and pos unused).
+ * q, k         inputs (either may have 0 heads); q_out, k_out: outputs with as
+ *              many heads. An output may be its input with the same strides
+ *              (in place); otherwise tensors must not overlap.
+ * q_weight,    [head_dim] of weight_dtype, or NULL for ones.
+ * k_weight
+ * cos, sin     [table_rows, rope_dim / 2] f32: the angles of position p in row
+ *              p (computed by the caller in as many bits as far positions need).
+ * pos          positions, int32 or int64 (pos_bytes 4 or 8): token s of
+ *              sequence b is at pos[b * pos_batch_stride + s]; NULL: s itself.
+ *              A position outside [0, table_rows) turns its rotated values
+ *              into NaN.
+ * batch * seq * (q heads + k heads) < 2^31. One launch.
+ * Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
+ns_status ns_qk_norm_rope(int64_t batch, int64_t seq, int32_t head_dim, ns_dtype dtype, const ns_heads *q,
+                          const ns_heads *k, const void *q_weight, const void *k_weight,
+                          ns_dtype weight_dtype, float eps, const float *cos, const float *sin,
+                          int64_t table_rows, int32_t rope_dim, int32_t interleaved, const void *pos,
+                          int32_t pos_bytes, int64_t pos_batch_stride, const ns_heads *q_out,
+                          const ns_heads *k_out, void *stream);
+
+/* Workspace of ns_qk_norm_rope_backward (needed only for weight gradients).
+ * Errors: INVALID_ARG, OVERFLOW. */
+ns_status ns_qk_norm_rope_workspace_bytes(int64_t batch, int64_t seq, int32_t head_dim, size_t *bytes);
+
+/* The gradient of ns_qk_norm_rope: from the forward's inputs q, k and the
+ * gradients dq_out, dk_out of its outputs, writes dq, dk and, where not NULL,
+ * the weights' gradients dq_weight, dk_weight ([head_dim] f32 whatever
+ * weight_dtype; summed over batch, seq and heads, not added to what is there).
+ * dq may be dq_out or q with the same strides (in place), dk likewise.
+ * workspace may be NULL if both weight gradients are. One launch, or two with
+ * weight gradients. Other arguments as for ns_qk_norm_rope.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
+ns_status ns_qk_norm_rope_backward(int64_t batch, int64_t seq, int32_t head_dim, ns_dtype dtype, const ns_heads *q,
+                                   const ns_heads *k, const ns_heads *dq_out, const ns_heads *dk_out,
+                                   const void *q_weight, const void *k_weight, ns_dtype weight_dtype,
+                                   float eps, const float *cos, const float *sin, int64_t table_rows,
+                                   int32_t rope_dim, int32_t interleaved, const void *pos, int32_t pos_bytes,
+                                   int64_t pos_batch_stride, const ns_heads *dq, const ns_heads *dk,
+                                   float *dq_weight, float *dk_weight, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* Tokens sorted by expert. The tokens' top_k choices are tokens * top_k slots
+ * (slot = token * top_k + choice, < 2^31), and every slot gets one of as many
+ * rows: kept slots by expert, then by slot (stable). Slots whose expert id is
+ * outside [0, experts) (a dropped choice, e.g. -1) take the rows behind them
+ * in slot order and appear complemented (~row, ~slot: negative).
+ * experts      1 .. 1024.
+ * expert_ids   int32 or int64 (id_bytes 4 or 8): choice k of token t is at
+ *              expert_ids[t * ids_ld + k], ids_ld >= top_k.
+ * offsets      [experts + 1]: expert e's rows are offsets[e] .. offsets[e + 1].
+ * slot_of_row  [tokens * top_k]: the slot in each row.
+ * row_of_slot  [tokens * top_k]: the row of each slot, which the calls below
+ *              take (they leave alone an entry that names no row).
+ * One launch up to 8192 slots, two above.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
+ns_status ns_moe_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts, size_t *bytes);
+ns_status ns_moe_sort(int64_t tokens, int32_t top_k, int32_t experts, const void *expert_ids, int32_t id_bytes,
+                      int64_t ids_ld, int32_t *offsets, int32_t *slot_of_row, int32_t *row_of_slot,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* xs[row_of_slot[s]] = x[s / top_k] for every slot s; dropped slots' rows are
+ * zeros, so all of xs is written. x: (tokens, hidden), xs: (tokens * top_k,
+ * hidden), rows x_ld and xs_ld elements apart (>= hidden <= 2^28). Tensors
+ * must not overlap. One launch. Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
+ns_status ns_moe_dispatch(int64_t tokens, int32_t top_k, int32_t hidden, ns_dtype dtype, const void *x,
+                          int64_t x_ld, const int32_t *row_of_slot, void *xs, int64_t xs_ld, void *stream);
+
+/* Gradient of ns_moe_dispatch: dx[t] = the sum of its kept slots' rows of dxs
+ * (zeros if none was kept). */
+ns_status ns_moe_dispatch_backward(int64_t tokens, int32_t top_k, int32_t hidden, ns_dtype dtype, const void *dxs,
+                                   int64_t dxs_ld, const int32_t *row_of_slot, void *dx, int64_t dx_ld,
+                                   void *stream);
+
+/* out[t] = the sum over token t's kept slots s of weights[s] * y[row_of_slot[s]]
+ * (zeros if none was kept). weights: [tokens, top_k] f32, or NULL for ones.
+ * Rows and weights of dropped slots are not used. Other arguments as above. */
+ns_status ns_moe_combine(int64_t tokens, int32_t top_k, int32_t hidden, ns_dtype dtype, const void *y,
+                         int64_t y_ld, const int32_t *row_of_slot, const float *weights, void *out,
+                         int64_t out_ld, void *stream);
+
+/* Gradient of ns_moe_combine: for every kept slot s of token t
+ * dy[row_of_slot[s]] = weights[s] * dout[t] and dweights[s] =
+ * <dout[t], y[row_of_slot[s]]> (f32); zeros for dropped slots. dy may be y with
+ * the same row stride (in place). weights and dweights are required. */
+ns_status ns_moe_combine_backward(int64_t tokens, int32_t top_k, int32_t hidden, ns_dtype dtype, const void *dout,
+                                  int64_t dout_ld, const void *y, int64_t y_ld, const int32_t *row_of_slot,
+                                  const float *weights, void *dy, int64_t dy_ld, float *dweights, void *stream);
+
+/* Loss of a student's logits against a teacher's top logits, for each row:
+ * with q = softmax(logits / temperature) over the vocabulary and p the
+ * softmax of teacher / temperature over the row's top_k pairs (ids, teacher),
+ *   loss = sum_k p_k (log p_k - log q[ids_k]).
+ * With teacher_lse (the teacher's logsumexp of its own logits / temperature
+ * over its whole vocabulary) p_k = exp(teacher_k / temperature - teacher_lse),
+ * and all tokens outside the pairs form one more class with p_r = max(0, 1 -
+ * sum p_k) and q_r the sum of their q: loss += p_r (log p_r - log q_r).
+ * Terms with p = 0 count as 0. Pairs whose id is outside [0, vocab) are
+ * absent; several pairs may hold one token (their p add up). A row without
+ * pairs, or without teacher_lse one whose teacher logits are all -inf, has
+ * loss, lse, rest_lse and gradient 0 whatever its logits hold.
+ *
+ * rows 0 .. 2^24, vocab 1 .. 2^24, top_k 1 .. 1024, temperature > 0.
+ * logits       (rows, vocab), rows logits_ld >= vocab elements apart.
+ * ids          [rows, top_k] int32 or int64 (id_bytes 4 or 8).
+ * teacher      [rows, top_k] of teacher_dtype.
+ * teacher_lse  [rows] or NULL.
+ * loss, lse    [rows] f32 outputs; lse = logsumexp(logits / temperature).
+ * rest_lse     [rows] f32 output, required with teacher_lse (else unused): the
+ *              logsumexp over the tokens outside the pairs.
+ * dlogits,     both or neither: the gradient of sum(grad_loss * loss), written
+ * grad_loss    in the same pass over the logits (rows dlogits_ld apart; may be
+ *              logits with the same stride, in place).
+ * workspace    from ns_distill_workspace_bytes (0 bytes when rows fill the
+ *              GPU on their own: then it may be NULL).
+ * One launch, or two for few or very long rows.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
+ns_status ns_distill_workspace_bytes(int64_t rows, int32_t vocab, int32_t top_k, size_t *bytes);
+ns_status ns_distill_topk(int64_t rows, int32_t vocab, int32_t top_k, ns_dtype dtype, const void *logits,
+                          int64_t logits_ld, const void *ids, int32_t id_bytes, const void *teacher,
+                          ns_dtype teacher_dtype, const float *teacher_lse, float temperature,
+                          const float *grad_loss, float *loss, float *lse, float *rest_lse, void *dlogits,
+                          int64_t dlogits_ld, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The gradient by itself, from the lse (and rest_lse) of an earlier
+ * ns_distill_topk on the same inputs: dlogits of sum(grad_loss * loss). In
+ * place allowed as above. One launch.
+ * Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
+ns_status ns_distill_topk_backward(int64_t rows, int32_t vocab, int32_t top_k, ns_dtype dtype, const void *logits,
+                                   int64_t logits_ld, const void *ids, int32_t id_bytes, const void *teacher,
+                                   ns_dtype teacher_dtype, const float *teacher_lse, float temperature,
+                                   const float *lse, const float *rest_lse, const float *grad_loss,
+                                   void *dlogits, int64_t dlogits_ld, void *stream);
+
+/* ------------------------------------------------------------------------ *
  * Measurement support
  * ------------------------------------------------------------------------ */
 

@@ -30,6 +30,10 @@ EXPORTS = [
     "ns_orthogonalize_strided", "ns_routed_workspace_bytes",
     "ns_orthogonalize_routed", "ns_gram_workspace_bytes", "ns_orthogonalize_gram", "ns_wave_plan", "ns_orthogonalize_waves", "ns_timing_enable",
     "ns_timing_read",
+    "ns_qk_norm_rope", "ns_qk_norm_rope_workspace_bytes", "ns_qk_norm_rope_backward",
+    "ns_moe_sort_workspace_bytes", "ns_moe_sort", "ns_moe_dispatch", "ns_moe_dispatch_backward", "ns_moe_combine",
+    "ns_moe_combine_backward",
+    "ns_distill_workspace_bytes", "ns_distill_topk", "ns_distill_topk_backward",
 ]
 
 
@@ -78,6 +82,22 @@ _SIGS = {
                                       _P, _SZ, _P]),
     "ns_timing_enable": (_I32, [_I32]),
     "ns_timing_read": (_I32, [_I32, _P, _P, _P]),
+    "ns_qk_norm_rope": (_I32, [_I64, _I64, _I32, _I32, _P, _P, _P, _P, _I32, _F32, _P, _P, _I64, _I32, _I32, _P, _I32,
+                               _I64, _P, _P, _P]),
+    "ns_qk_norm_rope_workspace_bytes": (_I32, [_I64, _I64, _I32, _P]),
+    "ns_qk_norm_rope_backward": (_I32, [_I64, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _I32, _F32, _P, _P, _I64, _I32,
+                                        _I32, _P, _I32, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ns_moe_sort_workspace_bytes": (_I32, [_I64, _I32, _I32, _P]),
+    "ns_moe_sort": (_I32, [_I64, _I32, _I32, _P, _I32, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "ns_moe_dispatch": (_I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _I64, _P]),
+    "ns_moe_dispatch_backward": (_I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _I64, _P]),
+    "ns_moe_combine": (_I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _I64, _P]),
+    "ns_moe_combine_backward": (_I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P]),
+    "ns_distill_workspace_bytes": (_I32, [_I64, _I32, _I32, _P]),
+    "ns_distill_topk": (_I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _P, _F32, _P, _P, _P, _P, _P, _I64,
+                               _P, _SZ, _P]),
+    "ns_distill_topk_backward": (_I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _P, _F32, _P, _P, _P, _P,
+                                        _I64, _P]),
 }
 
 _lock = threading.Lock()

@@ -1,0 +1,707 @@
+// Loss of a student's logits against a teacher's top logits, and its gradient.
+//
+// A row has V student logits z and K pairs (token, teacher logit t); pairs
+// whose token is outside [0, V) are absent. At temperature tau:
+//   q = softmax(z / tau),  p_k = softmax over the row's pairs of t / tau,
+//   loss = sum_k p_k (log p_k - log q[token_k]),
+//   dz_j = g / tau (q_j - sum of p_k over the pairs of token j).
+// With the teacher's logsumexp over its whole vocabulary (at tau), p_k =
+// exp(t_k / tau - lse_T) and all other tokens form one more class with
+// p_r = max(0, 1 - sum p_k) and q_r = the sum of their q:
+//   loss += p_r (log p_r - log q_r),  their dz_j = g / tau q_j (1 - p_r / q_r).
+// Terms with p = 0 count as 0. A row without pairs (or, without lse_T, with
+// every teacher logit -inf) has loss and gradient 0 and its logits are not used.
+//
+// q_r comes from a logsumexp of its own over the other tokens, found while the
+// row is read (a bit per token in LDS marks the pairs' tokens): 1 - sum of the
+// pairs' q would lose all its digits where q_r is small.
+//
+// Bound by memory: loss and gradient in one call read the row once and write
+// its gradient once, the row staying in registers in between.
+
+#include <algorithm>
+#include <type_traits>
+
+#include "op_util.h"
+
+namespace nsq {
+namespace {
+
+constexpr int kMaxTop = 1024;
+constexpr int kMaxVocab = 1 << 24;
+constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxChunks = 64;            // parts of a row that is split over workgroups
+constexpr int kBitVocab = 1 << 18;        // tokens one workgroup marks in LDS (32 KiB)
+constexpr int kSplitThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct DistillArgs {
+    const void *logits;
+    const void *ids;
+    const void *teacher;
+    const float *teacher_lse;
+    const float *grad_loss;
+    float *loss, *lse, *rest_lse;
+    void *dlogits;
+    int64_t ld, dld;
+    float2 *partial;        // split rows: [rows][chunks] largest value and sum of each part
+    float *top_z;           // split rows: [rows][top_k] student logits of the pairs
+    int32_t rows, vocab, top_k;
+    int32_t id_bytes, teacher_f32;
+    int32_t chunks, chunk;  // parts of a row, tokens of one
+    float inv_tau;
+};
+
+// ---------------------------------------------------------------------------
+// sums of exponentials
+// ---------------------------------------------------------------------------
+
+// s = the sum of exp((x - m) / tau) over some x, m the largest of them.
+struct Lse {
+    float m, s;
+};
+constexpr float kNegInf = -__builtin_inff();
+
+// exp((x - m) / tau) with c = log2(e) / tau; 0 where both are -inf.
+__device__ inline float shifted(float x, float m, float c) {
+    return __builtin_amdgcn_exp2f((x - (m == kNegInf ? 0.f : m)) * c);
+}
+__device__ inline Lse join(Lse a, Lse b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    return {m, a.s * shifted(a.m, m, c) + b.s * shifted(b.m, m, c)};
+}
+__device__ inline Lse wave_join(Lse a, float c) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) a = join(a, {__shfl_xor(a.m, d), __shfl_xor(a.s, d)}, c);
+    return a;
+}
+__device__ inline float wave_max(float v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// q of a logit z is exp((z - m) / tau) scale.
+struct Norm {
+    float m, scale, log_scale;
+};
+__device__ inline Norm norm_of(Lse l, float inv_tau) { return {l.m == kNegInf ? 0.f : l.m, 1.f / l.s, -logf(l.s)}; }
+// From a logsumexp rounded to fp32: m is lse tau rounded, and the scale takes
+// up the rest of it, so q is off by no more than lse's own rounding.
+__device__ inline Norm norm_of_lse(float lse, float inv_tau) {
+    const float m = lse / inv_tau, rest = fmaf(m, inv_tau, -lse);
+    return {m, expf(rest), rest};
+}
+__device__ inline float q_of(float z, const Norm &n, float c) { return __builtin_amdgcn_exp2f((z - n.m) * c) * n.scale; }
+
+// ---------------------------------------------------------------------------
+// a row's pairs
+// ---------------------------------------------------------------------------
+
+struct PairLds {
+    int32_t id[kMaxTop + 4];   // token, -1 if absent
+    float p[kMaxTop + 4];      // first t / tau, then p
+    float t[kMaxTop];          // log p
+    float z[kMaxTop];          // student logit
+    float p_token[kMaxTop];    // p summed over the token's pairs
+    int32_t owner[kMaxTop];    // the token, in the lowest of its pairs; -1 in the others
+    Lse wave[16];
+};
+
+struct Pairs {
+    bool some;      // the row has a loss
+    float t_max, t_sub, p_rest;
+};
+
+__device__ inline float teacher_at(const DistillArgs &A, int64_t at) {
+    return A.teacher_f32 ? reinterpret_cast<const float *>(A.teacher)[at]
+                         : (float)reinterpret_cast<const __bf16 *>(A.teacher)[at];
+}
+
+// Brings the row's pairs into LDS; says whether the row has a loss. Ends with
+// every thread past the barrier.
+template <bool REST>
+__device__ inline Pairs read_pairs(const DistillArgs &A, int64_t row, PairLds &L, uint32_t *bits, int words) {
+    const int lane = threadIdx.x & 63, threads = blockDim.x;
+    for (int k = threadIdx.x; k < A.top_k; k += threads) {
+        const int64_t at = row * A.top_k + k;
+        const int64_t id = A.id_bytes == 8 ? reinterpret_cast<const int64_t *>(A.ids)[at]
+                                           : (int64_t) reinterpret_cast<const int32_t *>(A.ids)[at];
+        L.id[k] = id < 0 || id >= A.vocab ? -1 : (int32_t)id;
+        L.t[k] = teacher_at(A, at);
+    }
+    if (threadIdx.x < 4) L.id[A.top_k + threadIdx.x] = -1, L.p[A.top_k + threadIdx.x] = 0.f;
+    if constexpr (REST)
+        for (int i = threadIdx.x; i < words; i += threads) bits[i] = 0;
+    __syncthreads();
+    float mx = kNegInf;
+    bool any = false, nan = false;
+    for (int k = lane; k < A.top_k; k += 64)   // every wave for itself
+        if (L.id[k] >= 0) {
+            any = true;
+            nan |= L.t[k] != L.t[k];
+            mx = fmaxf(mx, L.t[k]);
+        }
+    Pairs r;
+    r.t_max = wave_max(mx);
+    if (__any(nan)) r.t_max = __builtin_nanf("");
+    r.some = __any(any) && (REST || r.t_max != kNegInf);
+    r.t_sub = r.p_rest = 0.f;
+    return r;
+}
+
+// p of every pair, the tokens' lowest pairs, and with REST the tokens' bits
+// among [e0, e1). Ends with every thread past a barrier.
+template <bool REST>
+__device__ inline void weigh_pairs(const DistillArgs &A, int64_t row, PairLds &L, Pairs &r, uint32_t *bits, int e0,
+                                   int e1) {
+    const int lane = threadIdx.x & 63, threads = blockDim.x;
+    if constexpr (REST) {
+        const float lse = A.teacher_lse[row];
+        if (r.t_max == kNegInf) r.t_max = 0.f;
+        r.t_sub = fmaf(-r.t_max, A.inv_tau, lse);
+    } else {
+        float s = 0.f;
+        for (int k = lane; k < A.top_k; k += 64)
+            if (L.id[k] >= 0) s += __builtin_amdgcn_exp2f((L.t[k] - r.t_max) * (A.inv_tau * kLog2e));
+        r.t_sub = logf(wave_sum(s));
+    }
+    __syncthreads();   // L.t has been read by every wave
+    for (int k = threadIdx.x; k < A.top_k; k += threads) {
+        const float log_p = (L.t[k] - r.t_max) * A.inv_tau - r.t_sub;
+        L.t[k] = log_p;
+        L.p[k] = L.id[k] >= 0 ? __builtin_amdgcn_exp2f(log_p * kLog2e) : 0.f;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < A.top_k; k += threads) {
+        const int id = L.id[k];
+        bool lowest = id >= 0;
+        float sum = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < A.top_k; j += 4) {
+            const int4 other = *reinterpret_cast<const int4 *>(&L.id[j]);
+            const float4 p = *reinterpret_cast<const float4 *>(&L.p[j]);
+            lowest = lowest && !(other.x == id && j < k) && !(other.y == id && j + 1 < k) &&
+                     !(other.z == id && j + 2 < k) && !(other.w == id && j + 3 < k);
+            sum += (other.x == id ? p.x : 0.f) + (other.y == id ? p.y : 0.f) + (other.z == id ? p.z : 0.f) +
+                   (other.w == id ? p.w : 0.f);
+        }
+        L.owner[k] = lowest ? id : -1;
+        L.p_token[k] = sum;
+        if constexpr (REST)
+            if (lowest && id >= e0 && id < e1) atomicOr(&bits[(id - e0) >> 5], 1u << ((id - e0) & 31));
+    }
+    __syncthreads();
+    if constexpr (REST) {
+        float sum = 0.f;
+        int tokens = 0;
+        for (int k = lane; k < A.top_k; k += 64) {
+            sum += L.p[k];
+            tokens += L.owner[k] >= 0;
+        }
+        r.p_rest = 1.f - wave_sum(sum);
+        // nothing outside the pairs: no class to hold what rounding leaves
+        if (r.p_rest < 0.f || (int)wave_sum((float)tokens) == A.vocab) r.p_rest = 0.f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// a part of a row
+// ---------------------------------------------------------------------------
+
+// Tokens [e0, e1): whole vectors dealt to the threads in turn, the few tokens
+// behind them one each to the first threads.
+template <typename T> struct Span {
+    static constexpr int N = Vec16<T>::N;
+    int e0, e1, vecs, tail;
+    __device__ Span(int from, int to) : e0(from), e1(to), vecs((to - from) / N), tail((to - from) % N) {}
+    // The thread that holds a token of the span.
+    __device__ int thread_of(int token, int threads) const {
+        const int j = token - e0;
+        return j < vecs * N ? j / N % threads : j - vecs * N;
+    }
+};
+
+__device__ inline uint32_t vec_bits(const uint32_t *bits, int v, int n) {
+    return reinterpret_cast<const uint8_t *>(bits)[v * n >> 3] >> (v * n & 7) & ((1u << n) - 1);
+}
+
+// Adds a vector's values to a thread's running sum; with REST only those whose bit is clear.
+template <typename T, bool REST>
+__device__ inline void add_vec(Lse &a, typename Vec16<T>::raw v, uint32_t skip, float c) {
+    constexpr int N = Vec16<T>::N;
+    float x[N], mx = a.m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = REST && (skip >> i & 1) ? kNegInf : elem<T>(v, i);
+        mx = fmaxf(mx, x[i]);
+    }
+    float s = 0.f;
+    const float m = mx == kNegInf ? 0.f : mx;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += __builtin_amdgcn_exp2f((x[i] - m) * c);
+    a.s = a.s * __builtin_amdgcn_exp2f((a.m - m) * c) + s;
+    a.m = mx;
+}
+
+template <typename T, bool REST>
+__device__ inline void add_tail(Lse &a, const T *z, const Span<T> &S, const uint32_t *bits, float c) {
+    if ((int)threadIdx.x >= S.tail) return;
+    const int j = S.vecs * S.N + threadIdx.x;
+    if (REST && (bits[j >> 5] >> (j & 31) & 1)) return;
+    const float x = (float)z[S.e0 + j];
+    a = join(a, {x, x == x && x != __builtin_inff() && x != kNegInf ? 1.f : x == kNegInf ? 0.f : __builtin_nanf("")}, c);
+}
+
+// The sum over a span of a row in memory, joined over the workgroup.
+template <typename T, bool REST>
+__device__ inline Lse sum_span(const T *z, const Span<T> &S, const uint32_t *bits, float c) {
+    constexpr int B = 4;
+    const int threads = blockDim.x;
+    Lse a = {kNegInf, 0.f};
+    int v = threadIdx.x;
+    for (; v + (B - 1) * threads < S.vecs; v += B * threads) {
+        typename Vec16<T>::raw r[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) r[i] = load_vec<T>(z + S.e0 + (int64_t)(v + i * threads) * S.N);
+#pragma unroll
+        for (int i = 0; i < B; ++i) add_vec<T, REST>(a, r[i], REST ? vec_bits(bits, v + i * threads, S.N) : 0, c);
+    }
+    for (; v < S.vecs; v += threads)
+        add_vec<T, REST>(a, load_vec<T>(z + S.e0 + (int64_t)v * S.N), REST ? vec_bits(bits, v, S.N) : 0, c);
+    add_tail<T, REST>(a, z, S, bits, c);
+    return a;
+}
+
+// Joins the threads' sums; every thread gets the result. One barrier inside.
+__device__ inline Lse block_join(Lse a, PairLds &L, float c) {
+    a = wave_join(a, c);
+    if ((threadIdx.x & 63) == 0) L.wave[threadIdx.x >> 6] = a;
+    __syncthreads();
+    a = {kNegInf, 0.f};
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) a = join(a, L.wave[w], c);
+    return a;
+}
+
+// The sum over the pairs' tokens (each once); every wave for itself.
+__device__ inline Lse sum_tokens(const DistillArgs &A, const PairLds &L, float c) {
+    Lse a = {kNegInf, 0.f};
+    for (int k = threadIdx.x & 63; k < A.top_k; k += 64)
+        if (L.owner[k] >= 0) {
+            const float x = L.z[k];
+            a = join(a, {x, x == kNegInf ? 0.f : shifted(x, x, c)}, c);
+        }
+    return wave_join(a, c);
+}
+
+template <typename T>
+__device__ inline typename Vec16<T>::raw grad_vec(typename Vec16<T>::raw v, const Norm &n, float c, float g) {
+    typename Vec16<T>::raw o;
+#pragma unroll
+    for (int i = 0; i < Vec16<T>::N; ++i) set_elem<T>(o, i, g * q_of(elem<T>(v, i), n, c));
+    return o;
+}
+
+// The tail's gradient, then that of the pairs' tokens, each written over the
+// other tokens' formula by the thread that wrote it.
+template <typename T>
+__device__ inline void finish_span(const DistillArgs &A, const PairLds &L, const T *z, T *dz, const Span<T> &S, float zt,
+                                   const Norm &n, float c, float g, float g_rest) {
+    if ((int)threadIdx.x < S.tail) dz[S.e0 + S.vecs * S.N + threadIdx.x] = (T)(g_rest * q_of(zt, n, c));
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int k0 = 0; k0 < A.top_k; k0 += 64) {
+        const int k = k0 + lane;
+        const int id = k < A.top_k ? L.owner[k] : -1;
+        int thread = -1;
+        float val = 0.f;
+        if (id >= S.e0 && id < S.e1) {
+            thread = S.thread_of(id, blockDim.x);
+            val = g * (q_of(L.z[k], n, c) - L.p_token[k]);
+        }
+        uint64_t mine = __ballot(thread >= 0 && thread >> 6 == wave);
+        while (mine) {
+            const int b = __builtin_ctzll(mine);
+            mine &= mine - 1;
+            const int to = __shfl(thread, b) & 63, token = __shfl(id, b);
+            const float x = __shfl(val, b);
+            if (lane == to) dz[token] = (T)x;
+        }
+    }
+}
+
+// The row's loss and logsumexps, by the first wave.
+template <bool REST>
+__device__ inline void write_loss(const DistillArgs &A, const PairLds &L, const Pairs &r, int64_t row, const Norm &n,
+                                  Lse all, Lse rest) {
+    if (threadIdx.x >= 64) return;
+    float sum = 0.f;
+    for (int k = threadIdx.x; k < A.top_k; k += 64) {
+        const float p = L.p[k];
+        if (p != 0.f) sum += p * (L.t[k] - ((L.z[k] - n.m) * A.inv_tau + n.log_scale));
+    }
+    sum = wave_sum(sum);
+    if (threadIdx.x) return;
+    if constexpr (REST) {
+        const float log_rest = logf(rest.s);
+        if (r.p_rest != 0.f) {
+            const float log_q = (rest.m - n.m) * A.inv_tau + log_rest + n.log_scale;
+            sum += r.p_rest * (logf(r.p_rest) - log_q);
+        }
+        A.rest_lse[row] = rest.m * A.inv_tau + log_rest;
+    }
+    A.loss[row] = sum;
+    A.lse[row] = all.m * A.inv_tau + logf(all.s);
+}
+
+// A row without a loss: zeros. `first`: also its loss and logsumexps.
+template <typename T, bool REST>
+__device__ inline void write_empty(const DistillArgs &A, int64_t row, const Span<T> &S, bool first) {
+    if (A.dlogits) {
+        T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
+        for (int v = threadIdx.x; v < S.vecs; v += blockDim.x) {
+            const typename Vec16<T>::raw o = {};
+            store_vec<T>(dz + S.e0 + (int64_t)v * S.N, o);
+        }
+        if ((int)threadIdx.x < S.tail) dz[S.e0 + S.vecs * S.N + threadIdx.x] = (T)0.f;
+    }
+    if (first && threadIdx.x == 0) {
+        A.loss[row] = A.lse[row] = 0.f;
+        if constexpr (REST) A.rest_lse[row] = 0.f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// kernels
+// ---------------------------------------------------------------------------
+
+// One workgroup a row: loss, and with dlogits the gradient. NV > 0: the row
+// stays in registers, NV vectors a thread; NV = 0: it is read from memory
+// again for the gradient.
+template <typename T, int THREADS, int NV, bool REST>
+__global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
+    extern __shared__ uint32_t bits[];
+    __shared__ __attribute__((aligned(16))) PairLds L;
+    const Span<T> S(0, A.vocab);
+    const float c = A.inv_tau * kLog2e;
+    for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+        const T *z = reinterpret_cast<const T *>(A.logits) + row * A.ld;
+        Pairs r = read_pairs<REST>(A, row, L, bits, (A.vocab + 31) >> 5);
+        if (!r.some) {
+            write_empty<T, REST>(A, row, S, true);
+            __syncthreads();
+            continue;
+        }
+        typename Vec16<T>::raw held[NV > 0 ? NV : 1];
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = threadIdx.x + i * THREADS;
+                if (v < S.vecs) held[i] = load_vec<T>(z + (int64_t)v * S.N);
+            }
+        }
+        for (int k = threadIdx.x; k < A.top_k; k += THREADS) L.z[k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
+        const float zt = (int)threadIdx.x < S.tail ? (float)z[S.vecs * S.N + threadIdx.x] : 0.f;
+        weigh_pairs<REST>(A, row, L, r, bits, 0, A.vocab);
+        Lse rest;
+        if constexpr (NV > 0) {
+            rest = {kNegInf, 0.f};
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = threadIdx.x + i * THREADS;
+                if (v < S.vecs) add_vec<T, REST>(rest, held[i], REST ? vec_bits(bits, v, S.N) : 0, c);
+            }
+            add_tail<T, REST>(rest, z, S, bits, c);
+        } else {
+            rest = sum_span<T, REST>(z, S, bits, c);
+        }
+        rest = block_join(rest, L, c);
+        const Lse all = REST ? join(rest, sum_tokens(A, L, c), c) : rest;
+        const Norm n = norm_of(all, A.inv_tau);
+        if (A.dlogits) {
+            T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
+            const float g = A.grad_loss[row] * A.inv_tau;
+            float g_rest = g;
+            if (REST && r.p_rest != 0.f)
+                g_rest = g * (1.f - r.p_rest * all.s / rest.s * shifted(all.m, rest.m, c));
+            if constexpr (NV > 0) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int v = threadIdx.x + i * THREADS;
+                    if (v < S.vecs) store_vec<T>(dz + (int64_t)v * S.N, grad_vec<T>(held[i], n, c, g_rest));
+                }
+            } else {
+                for (int v = threadIdx.x; v < S.vecs; v += THREADS)
+                    store_vec<T>(dz + (int64_t)v * S.N, grad_vec<T>(load_vec<T>(z + (int64_t)v * S.N), n, c, g_rest));
+            }
+            finish_span<T>(A, L, z, dz, S, zt, n, c, g, g_rest);
+        }
+        write_loss<REST>(A, L, r, row, n, all, rest);
+        __syncthreads();   // the next row's pairs go into the same LDS
+    }
+}
+
+// Few or very long rows: workgroup (chunk, row) sums its part of the row.
+template <typename T, bool REST>
+__global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillArgs A) {
+    extern __shared__ uint32_t bits[];
+    __shared__ __attribute__((aligned(16))) PairLds L;
+    const float c = A.inv_tau * kLog2e;
+    for (uint32_t b = blockIdx.x; b < (uint32_t)A.rows * A.chunks; b += gridDim.x) {
+        const int64_t row = b / (uint32_t)A.chunks;
+        const int chunk = b % (uint32_t)A.chunks;
+        const int e0 = chunk * A.chunk, e1 = min(e0 + A.chunk, A.vocab);
+        const Span<T> S(e0, e1);
+        const T *z = reinterpret_cast<const T *>(A.logits) + row * A.ld;
+        if (REST || chunk == 0) {
+            Pairs r = read_pairs<REST>(A, row, L, bits, (A.chunk + 31) >> 5);
+            if (chunk == 0)
+                for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads)
+                    A.top_z[row * A.top_k + k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
+            if constexpr (REST) weigh_pairs<REST>(A, row, L, r, bits, e0, e1);
+        }
+        const Lse a = block_join(sum_span<T, REST>(z, S, bits, c), L, c);
+        if (threadIdx.x == 0) A.partial[row * A.chunks + chunk] = make_float2(a.m, a.s);
+        __syncthreads();   // the next part uses the same LDS
+    }
+}
+
+// Workgroup (chunk, row) writes its part of the gradient, from the parts' sums
+// (LOSS: the first one also the loss) or from the logsumexps of a forward call.
+template <typename T, bool REST, bool LOSS>
+__global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArgs A, int32_t parts) {
+    extern __shared__ uint32_t bits[];
+    __shared__ __attribute__((aligned(16))) PairLds L;
+    const float c = A.inv_tau * kLog2e;
+    for (uint32_t b = blockIdx.x; b < (uint32_t)A.rows * A.chunks; b += gridDim.x) {
+        const int64_t row = b / (uint32_t)A.chunks;
+        const int chunk = b % (uint32_t)A.chunks;
+        const int e0 = chunk * A.chunk, e1 = min(e0 + A.chunk, A.vocab);
+        const Span<T> S(e0, e1);
+        const T *z = reinterpret_cast<const T *>(A.logits) + row * A.ld;
+        Pairs r = read_pairs<REST>(A, row, L, bits, 0);
+        if (!r.some) {
+            write_empty<T, REST>(A, row, S, LOSS && chunk == 0);
+            __syncthreads();
+            continue;
+        }
+        for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) {
+            const int id = L.id[k];
+            if (LOSS) L.z[k] = A.top_z[row * A.top_k + k];
+            else L.z[k] = id >= e0 && id < e1 ? (float)z[id] : 0.f;
+        }
+        const float zt = (int)threadIdx.x < S.tail ? (float)z[e0 + S.vecs * S.N + threadIdx.x] : 0.f;
+        weigh_pairs<REST>(A, row, L, r, bits, 0, 0);
+        Lse all = {kNegInf, 0.f}, rest = {kNegInf, 0.f};
+        Norm n;
+        float others = 1.f;   // the factor of the tokens outside the pairs
+        if constexpr (LOSS) {
+            for (int i = threadIdx.x & 63; i < parts; i += 64) {
+                const float2 p = A.partial[row * parts + i];
+                rest = join(rest, {p.x, p.y}, c);
+            }
+            rest = wave_join(rest, c);
+            all = REST ? join(rest, sum_tokens(A, L, c), c) : rest;
+            n = norm_of(all, A.inv_tau);
+            if (REST && r.p_rest != 0.f) others = 1.f - r.p_rest * all.s / rest.s * shifted(all.m, rest.m, c);
+        } else {
+            const float lse = A.lse[row];
+            n = norm_of_lse(lse, A.inv_tau);
+            if (REST && r.p_rest != 0.f) others = 1.f - r.p_rest * expf(lse - A.rest_lse[row]);
+        }
+        if (A.dlogits) {
+            T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
+            const float g = A.grad_loss[row] * A.inv_tau;
+            constexpr int B = 4;
+            int v = threadIdx.x;
+            for (; v + (B - 1) * kSplitThreads < S.vecs; v += B * kSplitThreads) {
+                typename Vec16<T>::raw w[B];
+    #pragma unroll
+                for (int i = 0; i < B; ++i) w[i] = load_vec<T>(z + e0 + (int64_t)(v + i * kSplitThreads) * S.N);
+    #pragma unroll
+                for (int i = 0; i < B; ++i)
+                    store_vec<T>(dz + e0 + (int64_t)(v + i * kSplitThreads) * S.N, grad_vec<T>(w[i], n, c, g * others));
+            }
+            for (; v < S.vecs; v += kSplitThreads)
+                store_vec<T>(dz + e0 + (int64_t)v * S.N, grad_vec<T>(load_vec<T>(z + e0 + (int64_t)v * S.N), n, c, g * others));
+            finish_span<T>(A, L, z, dz, S, zt, n, c, g, g * others);
+        }
+        if (LOSS && chunk == 0) write_loss<REST>(A, L, r, row, n, all, rest);
+        __syncthreads();   // the next part uses the same LDS
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// Parts of a row for the split kernels: enough workgroups to fill the GPU, of
+// at least 8192 tokens (and no more than one workgroup marks in LDS).
+void set_chunks(DistillArgs &a) {
+    int64_t parts = (1024 + a.rows - 1) / a.rows;
+    parts = std::min<int64_t>(parts, (a.vocab + 8191) / 8192);
+    parts = std::max<int64_t>(parts, (a.vocab + kBitVocab - 1) / kBitVocab);
+    parts = std::max<int64_t>(1, std::min<int64_t>(parts, kMaxChunks));
+    a.chunk = (int32_t)(((a.vocab + parts - 1) / parts + 31) / 32 * 32);
+    a.chunks = (a.vocab + a.chunk - 1) / a.chunk;
+}
+
+// Rows that fill the GPU one workgroup each; fewer are split.
+bool split_rows(int64_t rows, int32_t vocab, bool rest) { return rows < 256 || (rest && vocab > kBitVocab); }
+
+size_t distill_workspace(int64_t rows, int32_t top_k, bool split) {
+    return split ? (size_t)rows * ((size_t)kMaxChunks * sizeof(float2) + (size_t)top_k * sizeof(float)) : 0;
+}
+
+ns_status check_sizes(int64_t rows, int32_t vocab, int32_t top_k) {
+    if (rows < 0 || rows > kMaxRows) return fail(NS_ERR_INVALID_ARG, "rows = %lld outside [0, %d]", (long long)rows, kMaxRows);
+    if (vocab < 1 || vocab > kMaxVocab) return fail(NS_ERR_INVALID_ARG, "vocab = %d outside [1, %d]", vocab, kMaxVocab);
+    if (top_k < 1 || top_k > kMaxTop) return fail(NS_ERR_INVALID_ARG, "top_k = %d outside [1, %d]", top_k, kMaxTop);
+    return NS_OK;
+}
+
+ns_status check_distill(int64_t rows, int32_t vocab, int32_t top_k, int32_t dtype, const void *logits, int64_t ld,
+                        const void *ids, int32_t id_bytes, const void *teacher, int32_t teacher_dtype,
+                        const float *teacher_lse, float temperature, const float *grad_loss, void *dlogits,
+                        int64_t dld, bool grad, DistillArgs *a) {
+    const int es = dtype_bytes(dtype);
+    if (!es) return fail(NS_ERR_DTYPE, "dtype %d is not NS_BF16 or NS_F32", dtype);
+    if (!dtype_bytes(teacher_dtype)) return fail(NS_ERR_DTYPE, "teacher_dtype %d is not NS_BF16 or NS_F32", teacher_dtype);
+    if (ns_status s = check_sizes(rows, vocab, top_k)) return s;
+    if (id_bytes != 4 && id_bytes != 8) return fail(NS_ERR_DTYPE, "id_bytes = %d (must be 4 or 8)", id_bytes);
+    const float inv_tau = 1.f / temperature;
+    if (!(temperature > 0.f) || !(inv_tau > 0.f) || inv_tau > 1e30f || temperature > 1e30f)
+        return fail(NS_ERR_INVALID_ARG, "temperature must be within [1e-30, 1e30]");
+    if (ld < vocab || (dlogits && dld < vocab)) return fail(NS_ERR_INVALID_ARG, "row stride < vocab");
+    if (too_far(rows, ld) || too_far(rows * ld, es) || (dlogits && (too_far(rows, dld) || too_far(rows * dld, es))))
+        return fail(NS_ERR_OVERFLOW, "logits: offsets overflow");
+    if (rows > 0 && (!logits || !ids || !teacher)) return fail(NS_ERR_INVALID_ARG, "logits, ids and teacher are required");
+    if (rows > 0 && grad && (!dlogits || !grad_loss))
+        return fail(NS_ERR_INVALID_ARG, "dlogits and grad_loss are required together");
+    if (misaligned(logits, es) || misaligned(dlogits, es) || misaligned(ids, id_bytes) ||
+        misaligned(teacher, dtype_bytes(teacher_dtype)) || misaligned(teacher_lse, 4) || misaligned(grad_loss, 4))
+        return fail(NS_ERR_INVALID_ARG, "a buffer is not aligned to its type");
+    if (dlogits == logits && dlogits && dld != ld)
+        return fail(NS_ERR_INVALID_ARG, "dlogits in place of logits needs the same row stride");
+    *a = DistillArgs{};
+    a->logits = logits;
+    a->ld = ld;
+    a->ids = ids;
+    a->id_bytes = id_bytes;
+    a->teacher = teacher;
+    a->teacher_f32 = teacher_dtype == NS_F32;
+    a->teacher_lse = teacher_lse;
+    a->grad_loss = grad_loss;
+    a->dlogits = dlogits;
+    a->dld = dld;
+    a->rows = (int32_t)rows;
+    a->vocab = vocab;
+    a->top_k = top_k;
+    a->inv_tau = inv_tau;
+    return NS_OK;
+}
+
+// Workgroups of a split launch: at most 2^20, which then take several parts each.
+unsigned split_grid(const DistillArgs &a) { return (unsigned)std::min<int64_t>((int64_t)a.rows * a.chunks, 1 << 20); }
+
+template <typename T, bool REST>
+ns_status launch_rows(const DistillArgs &a, hipStream_t st) {
+    const size_t lds = REST ? (size_t)((a.vocab + 31) / 32) * 4 : 0;
+    const int64_t vecs = a.vocab / Vec16<T>::N;
+    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 1 << 20);
+    auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), lds, st, a); };
+    if (!a.dlogits) vecs <= 4096 ? go(distill_row_kernel<T, 256, 0, REST>, 256) : go(distill_row_kernel<T, 1024, 0, REST>, 1024);
+    else if (vecs <= 2048) go(distill_row_kernel<T, 256, 8, REST>, 256);
+    else if (vecs <= 4096) go(distill_row_kernel<T, 512, 8, REST>, 512);
+    else if (vecs <= 8192) go(distill_row_kernel<T, 1024, 8, REST>, 1024);
+    else if (vecs <= 16384) go(distill_row_kernel<T, 1024, 16, REST>, 1024);
+    else go(distill_row_kernel<T, 1024, 0, REST>, 1024);
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
+template <typename T, bool REST>
+ns_status launch_split(DistillArgs a, hipStream_t st) {
+    set_chunks(a);
+    const size_t lds = REST ? (size_t)((a.chunk + 31) / 32) * 4 : 0;
+    hipLaunchKernelGGL((distill_partial_kernel<T, REST>), dim3(split_grid(a)), dim3(kSplitThreads), lds, st, a);
+    NSQ_HIP(hipGetLastError());
+    const int32_t parts = a.chunks;
+    if (!a.dlogits) a.chunks = 1, a.chunk = a.vocab;
+    hipLaunchKernelGGL((distill_apply_kernel<T, REST, true>), dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, parts);
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
+template <typename T, bool REST>
+ns_status launch_backward(DistillArgs a, hipStream_t st) {
+    set_chunks(a);
+    hipLaunchKernelGGL((distill_apply_kernel<T, REST, false>), dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, 0);
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
+}  // namespace
+}  // namespace nsq
+
+using namespace nsq;
+
+extern "C" ns_status ns_distill_workspace_bytes(int64_t rows, int32_t vocab, int32_t top_k, size_t *bytes) {
+    if (!bytes) return fail(NS_ERR_INVALID_ARG, "bytes is NULL");
+    if (ns_status s = check_sizes(rows, vocab, top_k)) return s;
+    *bytes = distill_workspace(rows, top_k, split_rows(rows, vocab, true));
+    return NS_OK;
+}
+
+extern "C" ns_status ns_distill_topk(int64_t rows, int32_t vocab, int32_t top_k, ns_dtype dtype, const void *logits,
+                                     int64_t logits_ld, const void *ids, int32_t id_bytes, const void *teacher,
+                                     ns_dtype teacher_dtype, const float *teacher_lse, float temperature,
+                                     const float *grad_loss, float *loss, float *lse, float *rest_lse, void *dlogits,
+                                     int64_t dlogits_ld, void *workspace, size_t workspace_bytes, void *stream) {
+    DistillArgs a;
+    if (ns_status s = check_distill(rows, vocab, top_k, dtype, logits, logits_ld, ids, id_bytes, teacher, teacher_dtype,
+                                    teacher_lse, temperature, grad_loss, dlogits, dlogits_ld, dlogits || grad_loss, &a))
+        return s;
+    if (rows > 0 && (!loss || !lse)) return fail(NS_ERR_INVALID_ARG, "loss and lse are required");
+    if (rows > 0 && teacher_lse && !rest_lse) return fail(NS_ERR_INVALID_ARG, "teacher_lse needs rest_lse");
+    if (misaligned(loss, 4) || misaligned(lse, 4) || misaligned(rest_lse, 4))
+        return fail(NS_ERR_INVALID_ARG, "loss, lse or rest_lse not 4-byte aligned");
+    const bool rest = teacher_lse != nullptr, split = split_rows(rows, vocab, rest);
+    const size_t need = distill_workspace(rows, top_k, split);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(NS_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    if (misaligned(workspace, 256)) return fail(NS_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    if (rows == 0) return NS_OK;
+    a.loss = loss;
+    a.lse = lse;
+    a.rest_lse = rest_lse;
+    const hipStream_t st = as_stream(stream);
+    if (split) {
+        a.partial = reinterpret_cast<float2 *>(workspace);
+        a.top_z = reinterpret_cast<float *>(a.partial + rows * kMaxChunks);
+        if (dtype == NS_BF16) return rest ? launch_split<__bf16, true>(a, st) : launch_split<__bf16, false>(a, st);
+        return rest ? launch_split<float, true>(a, st) : launch_split<float, false>(a, st);
+    }
+    if (dtype == NS_BF16) return rest ? launch_rows<__bf16, true>(a, st) : launch_rows<__bf16, false>(a, st);
+    return rest ? launch_rows<float, true>(a, st) : launch_rows<float, false>(a, st);
+}
+
+extern "C" ns_status ns_distill_topk_backward(int64_t rows, int32_t vocab, int32_t top_k, ns_dtype dtype,
+                                              const void *logits, int64_t logits_ld, const void *ids, int32_t id_bytes,
+                                              const void *teacher, ns_dtype teacher_dtype, const float *teacher_lse,
+                                              float temperature, const float *lse, const float *rest_lse,
+                                              const float *grad_loss, void *dlogits, int64_t dlogits_ld,
+                                              void *stream) {
+    DistillArgs a;
+    if (ns_status s = check_distill(rows, vocab, top_k, dtype, logits, logits_ld, ids, id_bytes, teacher, teacher_dtype,
+                                    teacher_lse, temperature, grad_loss, dlogits, dlogits_ld, true, &a))
+        return s;
+    if (rows > 0 && !lse) return fail(NS_ERR_INVALID_ARG, "lse is required");
+    if (rows > 0 && teacher_lse && !rest_lse) return fail(NS_ERR_INVALID_ARG, "teacher_lse needs rest_lse");
+    if (misaligned(lse, 4) || misaligned(rest_lse, 4)) return fail(NS_ERR_INVALID_ARG, "lse or rest_lse not 4-byte aligned");
+    if (rows == 0) return NS_OK;
+    a.lse = const_cast<float *>(lse);
+    a.rest_lse = const_cast<float *>(rest_lse);
+    const hipStream_t st = as_stream(stream);
+    if (dtype == NS_BF16) return teacher_lse ? launch_backward<__bf16, true>(a, st) : launch_backward<__bf16, false>(a, st);
+    return teacher_lse ? launch_backward<float, true>(a, st) : launch_backward<float, false>(a, st);
+}

@@ -1,0 +1,555 @@
+// Tokens sorted by expert and back, with the router's weights, and gradients.
+//
+// The T tokens' K choices are T K slots (slot = token K + choice). ns_moe_sort
+// gives every slot a row: kept slots by expert and, within one, by slot (a
+// stable counting sort); slots whose id is outside [0, E) are dropped and take
+// the rows behind, in slot order, marked by the complement of their row.
+//   dispatch            xs[row] = x[token]          (dropped rows: zeros)
+//   its gradient        dx[t] = sum_k dxs[row(t, k)]
+//   combine             out[t] = sum_k w[t, k] y[row(t, k)]
+//   its gradient        dy[row] = w dout[t],  dw[t, k] = <dout[t], y[row]>
+// Sums run in fp32 over the choices in order and are rounded once; dropped
+// slots' rows and weights take no part, whatever they hold. Every row is
+// written once, by its own token, so there are no atomics and each result has
+// one order.
+//
+// Bound by memory: a pass reads or writes K rows a token and one more.
+
+#include <type_traits>
+
+#include "op_util.h"
+
+namespace nsq {
+namespace {
+
+// ---------------------------------------------------------------------------
+// sort
+// ---------------------------------------------------------------------------
+
+constexpr int kMaxExperts = 1024;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kMaxSortBlocks = 128;
+
+struct SortArgs {
+    const void *ids;
+    int64_t ids_ld;          // elements from a token's ids to the next one's
+    int32_t id_bytes;
+    int32_t slots, top_k, experts;
+    int32_t per;             // slots per workgroup: a multiple of 1024
+    int32_t blocks;
+    int32_t *offsets, *slot_of_row, *row_of_slot;
+    int32_t *hist;           // [blocks][experts + 1]
+};
+
+// The sort key of a slot: its expert, or `experts` if dropped.
+__device__ inline int key_of(const SortArgs &A, uint32_t slot) {
+    const uint32_t t = slot / (uint32_t)A.top_k, k = slot - t * A.top_k;
+    const int64_t at = (int64_t)t * A.ids_ld + k;
+    const int64_t id = A.id_bytes == 8 ? reinterpret_cast<const int64_t *>(A.ids)[at]
+                                       : (int64_t) reinterpret_cast<const int32_t *>(A.ids)[at];
+    return id < 0 || id >= A.experts ? A.experts : (int)id;
+}
+
+// The lanes of the wave that hold the same key (`bits` bits of it) as this one.
+__device__ inline uint64_t same_key(int key, bool active, int bits) {
+    uint64_t m = __ballot(active);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((key >> b) & 1);
+        m &= (key >> b) & 1 ? set : ~set;
+    }
+    return m;
+}
+
+// Counts of each key in one workgroup's slots.
+__global__ __launch_bounds__(kSortThreads) void moe_count_kernel(SortArgs A) {
+    __shared__ int32_t cnt[kMaxExperts + 1];
+    for (int e = threadIdx.x; e <= A.experts; e += kSortThreads) cnt[e] = 0;
+    __syncthreads();
+    const int64_t s0 = (int64_t)blockIdx.x * A.per;
+    const int64_t s1 = s0 + A.per < A.slots ? s0 + A.per : A.slots;
+    for (int64_t s = s0 + threadIdx.x; s < s1; s += kSortThreads) atomicAdd(&cnt[key_of(A, (uint32_t)s)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= A.experts; e += kSortThreads)
+        A.hist[(int64_t)blockIdx.x * (A.experts + 1) + e] = cnt[e];
+}
+
+// Rows of one workgroup's slots. Wave w holds the w-th run of per / 16 of
+// them; a slot's row is its key's first row, plus the same key's slots in
+// earlier workgroups, earlier waves, earlier rounds of this wave and lower
+// lanes. ONE: the only workgroup, which counts for itself.
+template <bool ONE>
+__global__ __launch_bounds__(kSortThreads) void moe_rank_kernel(SortArgs A) {
+    __shared__ int32_t cnt[kSortWaves][kMaxExperts + 1];
+    __shared__ int32_t before[kMaxExperts + 1], total[kMaxExperts + 1];
+    __shared__ int32_t wave_total[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int E = A.experts, K1 = E + 1;
+    const int bits = 32 - __builtin_clz(E);   // keys 0 .. E
+    for (int i = tid; i < K1; i += kSortThreads) before[i] = total[i] = 0;
+    for (int w = 0; w < kSortWaves; ++w)
+        for (int i = tid; i < K1; i += kSortThreads) cnt[w][i] = 0;
+    __syncthreads();
+    const int run = A.per / kSortWaves;
+    const int64_t w0 = (int64_t)blockIdx.x * A.per + (int64_t)wave * run;
+    for (int i = lane; i < run; i += 64)
+        if (w0 + i < A.slots) atomicAdd(&cnt[wave][key_of(A, (uint32_t)(w0 + i))], 1);
+    if constexpr (!ONE) {
+        int lg = 32 - __builtin_clz(E);       // 2^lg > E: lanes for one workgroup's counts
+        if (lg > 10) lg = 10;
+        const int step = 1 << lg, group = tid >> lg, groups = kSortThreads >> lg;
+        for (int e = tid & (step - 1); e < K1; e += step) {
+            int32_t b = 0, t = 0;
+            for (int c = group; c < A.blocks; c += groups) {
+                const int32_t v = A.hist[(int64_t)c * K1 + e];
+                t += v;
+                if (c < (int)blockIdx.x) b += v;
+            }
+            atomicAdd(&before[e], b);   // integers: any order gives the same sum
+            atomicAdd(&total[e], t);
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < K1; e += kSortThreads) {   // counts to first ranks, wave by wave
+        int32_t sum = 0;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int32_t v = cnt[w][e];
+            cnt[w][e] = sum;
+            sum += v;
+        }
+        if constexpr (ONE) total[e] = sum;
+    }
+    __syncthreads();
+    // first row of each expert: an exclusive sum over the (at most 1024) experts
+    const int32_t mine = tid < E ? total[tid] : 0;
+    int32_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t up = __shfl_up(incl, d);
+        if (lane >= d) incl += up;
+    }
+    if (lane == 63) wave_total[wave] = incl;
+    __syncthreads();
+    int32_t first = incl - mine, kept = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        if (w < wave) first += wave_total[w];
+        kept += wave_total[w];
+    }
+    if (tid < E) before[tid] += first;
+    if (tid == 0) before[E] += kept;
+    if (blockIdx.x == 0) {
+        if (tid < E) A.offsets[tid] = first;
+        if (tid == 0) A.offsets[E] = kept;
+    }
+    __syncthreads();
+    volatile int32_t *mycnt = cnt[wave];
+    for (int i = 0; i < run; i += 64) {
+        const int64_t s = w0 + i + lane;
+        const bool active = s < A.slots;
+        if (!__ballot(active)) break;
+        const int key = active ? key_of(A, (uint32_t)s) : E;
+        const uint64_t m = same_key(key, active, bits);
+        const int rank = __popcll(m & ((1ull << lane) - 1));
+        int32_t prior = 0;
+        if (active) prior = mycnt[key];
+        __builtin_amdgcn_wave_barrier();      // every lane has read before the first of each key writes
+        if (active && rank == 0) mycnt[key] = prior + __popcll(m);
+        __builtin_amdgcn_wave_barrier();
+        if (active) {
+            const int32_t row = before[key] + prior + rank, slot = (int32_t)s;
+            A.row_of_slot[slot] = key == E ? ~row : row;
+            A.slot_of_row[row] = key == E ? ~slot : slot;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+
+struct RowArgs {
+    const void *x, *y;       // token rows, sorted rows (inputs of the pass)
+    void *tok, *rows;        // token rows, sorted rows (outputs)
+    int64_t x_ld, y_ld, tok_ld, rows_ld;
+    const int32_t *row_of_slot;
+    const float *w;
+    float *dw;
+    int64_t tokens;
+    int32_t top_k, hidden;
+    int32_t units;           // 16-byte units of a row, the last one perhaps partial
+    int32_t pieces;          // workgroups per token
+    uint32_t blocks;         // tokens x pieces, < 2^31
+    uint32_t slots;          // tokens x top_k: rows of the sorted side
+};
+
+// A slot's entry in the map: its row, and whether it was kept. An entry that
+// names no row of the buffer (no map of ns_moe_sort's holds one) is left alone.
+struct RowRef {
+    int64_t row;
+    bool kept, in;
+};
+__device__ inline RowRef row_ref(const RowArgs &A, int64_t slot) {
+    const int32_t r = A.row_of_slot[slot];
+    const uint32_t row = r < 0 ? ~r : r;
+    return {(int64_t)row, r >= 0 && row < A.slots, row < A.slots};
+}
+
+// Unit u of a row of `hidden` elements; elements past its end read as zero and are not written.
+template <typename T>
+__device__ inline typename Vec16<T>::raw load_unit(const T *row, int u, int hidden) {
+    constexpr int N = Vec16<T>::N;
+    if ((u + 1) * N <= hidden) return load_vec<T>(row + u * N);
+    typename Vec16<T>::raw v = {};
+    for (int i = 0; i < N - 1; ++i)
+        if (u * N + i < hidden) v[i] = reinterpret_cast<const std::remove_reference_t<decltype(v[0])> *>(row)[u * N + i];
+    return v;
+}
+template <typename T>
+__device__ inline void store_unit(T *row, int u, int hidden, typename Vec16<T>::raw v) {
+    constexpr int N = Vec16<T>::N;
+    if ((u + 1) * N <= hidden) {
+        store_vec<T>(row + u * N, v);
+        return;
+    }
+    for (int i = 0; i < N - 1; ++i)
+        if (u * N + i < hidden) reinterpret_cast<std::remove_reference_t<decltype(v[0])> *>(row)[u * N + i] = v[i];
+}
+
+// xs[row] = x[token]: a thread reads one unit and writes it K times.
+template <typename T>
+__global__ __launch_bounds__(512) void moe_dispatch_kernel(RowArgs A) {
+    for (uint32_t b = blockIdx.x; b < A.blocks; b += gridDim.x) {
+        const uint32_t t32 = b / (uint32_t)A.pieces;
+        const int64_t t = t32;
+        const int u = (int)(b - t32 * A.pieces) * blockDim.x + threadIdx.x;
+        if (u >= A.units) continue;
+        const auto v = load_unit<T>(reinterpret_cast<const T *>(A.x) + t * A.x_ld, u, A.hidden);
+        for (int k = 0; k < A.top_k; ++k) {
+            const RowRef r = row_ref(A, t * A.top_k + k);
+            typename Vec16<T>::raw z = {};
+            if (r.in) store_unit<T>(reinterpret_cast<T *>(A.rows) + r.row * A.rows_ld, u, A.hidden, r.kept ? v : z);
+        }
+    }
+}
+
+// tok[t] = sum_k w[t, k] y[row(t, k)] (W = false: w = 1), up to KC rows in flight.
+template <typename T, bool W, int KC>
+__global__ __launch_bounds__(512) void moe_combine_kernel(RowArgs A) {
+    constexpr int N = Vec16<T>::N;
+    for (uint32_t b = blockIdx.x; b < A.blocks; b += gridDim.x) {
+        const uint32_t t32 = b / (uint32_t)A.pieces;
+        const int64_t t = t32;
+        const int u = (int)(b - t32 * A.pieces) * blockDim.x + threadIdx.x;
+        if (u >= A.units) continue;
+        float acc[N] = {};
+        for (int k0 = 0; k0 < A.top_k; k0 += KC) {
+            typename Vec16<T>::raw v[KC];
+            float w[KC];
+            bool kept[KC];
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+                kept[j] = false;
+                if (k0 + j < A.top_k) {
+                    const int64_t s = t * A.top_k + k0 + j;
+                    const RowRef r = row_ref(A, s);
+                    kept[j] = r.kept;
+                    w[j] = W ? A.w[s] : 1.f;
+                    if (kept[j]) v[j] = load_unit<T>(reinterpret_cast<const T *>(A.y) + r.row * A.y_ld, u, A.hidden);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KC; ++j)
+                if (kept[j])
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] += w[j] * elem<T>(v[j], i);
+        }
+        typename Vec16<T>::raw o;
+#pragma unroll
+        for (int i = 0; i < N; ++i) set_elem<T>(o, i, acc[i]);
+        store_unit<T>(reinterpret_cast<T *>(A.tok) + t * A.tok_ld, u, A.hidden, o);
+    }
+}
+
+// dy[row] = w dout[t] and dw[t, k] = <dout[t], y[row]>: one workgroup per
+// token, KC choices at a time, their partial dot products in registers.
+template <typename T, int KC>
+__global__ __launch_bounds__(512) void moe_combine_backward_kernel(RowArgs A) {
+    constexpr int N = Vec16<T>::N;
+    __shared__ float part[8][KC];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    for (int64_t t = blockIdx.x; t < A.tokens; t += gridDim.x) {
+        const T *g = reinterpret_cast<const T *>(A.x) + t * A.x_ld;
+        for (int k0 = 0; k0 < A.top_k; k0 += KC) {
+            RowRef r[KC];
+            float w[KC], dot[KC];
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+                r[j] = {0, false, false};
+                w[j] = dot[j] = 0.f;
+                if (k0 + j < A.top_k) {
+                    r[j] = row_ref(A, t * A.top_k + k0 + j);
+                    if (r[j].kept) w[j] = A.w[t * A.top_k + k0 + j];
+                }
+            }
+            for (int u = threadIdx.x; u < A.units; u += blockDim.x) {
+                const auto gv = load_unit<T>(g, u, A.hidden);
+                typename Vec16<T>::raw v[KC];
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+                    if (r[j].kept)
+                        v[j] = load_unit<T>(reinterpret_cast<const T *>(A.y) + r[j].row * A.y_ld, u, A.hidden);
+#pragma unroll
+                for (int j = 0; j < KC; ++j) {
+                    if (!r[j].in) continue;
+                    typename Vec16<T>::raw o = {};
+                    if (r[j].kept) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            dot[j] += elem<T>(gv, i) * elem<T>(v[j], i);
+                            set_elem<T>(o, i, w[j] * elem<T>(gv, i));
+                        }
+                    }
+                    store_unit<T>(reinterpret_cast<T *>(A.rows) + r[j].row * A.rows_ld, u, A.hidden, o);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+                dot[j] = wave_sum(dot[j]);
+                if (lane == 0) part[wave][j] = dot[j];
+            }
+            __syncthreads();
+            if (threadIdx.x < KC && k0 + threadIdx.x < (unsigned)A.top_k) {
+                float s = 0.f;
+                for (int i = 0; i < waves; ++i) s += part[i][threadIdx.x];
+                A.dw[t * A.top_k + k0 + threadIdx.x] = s;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+ns_status check_slots(int64_t tokens, int32_t top_k) {
+    if (tokens < 0) return fail(NS_ERR_INVALID_ARG, "tokens < 0");
+    if (top_k < 1) return fail(NS_ERR_INVALID_ARG, "top_k = %d < 1", top_k);
+    if (tokens >= (int64_t(1) << 31) / top_k) return fail(NS_ERR_OVERFLOW, "tokens x top_k does not fit in 31 bits");
+    return NS_OK;
+}
+
+// A (rows, hidden) operand with its row stride.
+ns_status check_rows(const char *name, const void *p, int64_t rows, int32_t hidden, int64_t ld, int es) {
+    if (ld < hidden) return fail(NS_ERR_INVALID_ARG, "%s: row stride %lld < hidden %d", name, (long long)ld, hidden);
+    if (too_far(rows, ld) || too_far(rows * ld, es)) return fail(NS_ERR_OVERFLOW, "%s: offsets overflow", name);
+    if (rows == 0 || hidden == 0) return NS_OK;
+    if (!p) return fail(NS_ERR_INVALID_ARG, "%s is NULL", name);
+    if (misaligned(p, es)) return fail(NS_ERR_INVALID_ARG, "%s not %d-byte aligned", name, es);
+    return NS_OK;
+}
+
+ns_status check_map(int64_t slots, const int32_t *row_of_slot) {
+    if (slots > 0 && !row_of_slot) return fail(NS_ERR_INVALID_ARG, "row_of_slot is NULL");
+    if (misaligned(row_of_slot, 4)) return fail(NS_ERR_INVALID_ARG, "row_of_slot not 4-byte aligned");
+    return NS_OK;
+}
+
+// Workgroups of at most 512 threads over a row's units: the fewest, evenly filled.
+unsigned row_threads(int32_t units, int32_t *pieces) {
+    *pieces = units > 512 ? (units + 511) / 512 : 1;
+    const int32_t each = (units + *pieces - 1) / *pieces;
+    return (unsigned)(each + 63) / 64 * 64;
+}
+
+unsigned row_grid(uint32_t blocks) { return blocks < (1u << 22) ? blocks : 1u << 22; }
+
+ns_status check_call(int64_t tokens, int32_t top_k, int32_t hidden, int32_t dtype, int *es) {
+    *es = dtype_bytes(dtype);
+    if (!*es) return fail(NS_ERR_DTYPE, "dtype %d is not NS_BF16 or NS_F32", dtype);
+    if (ns_status s = check_slots(tokens, top_k)) return s;
+    if (hidden < 0) return fail(NS_ERR_INVALID_ARG, "hidden < 0");
+    const int64_t pieces = (((int64_t)hidden * *es + 15) / 16 + 511) / 512;
+    if (hidden > 1 << 28 || tokens * (double)pieces >= 2147483648.0)
+        return fail(NS_ERR_OVERFLOW, "%lld tokens of %d values are more than one call counts", (long long)tokens, hidden);
+    return NS_OK;
+}
+
+// Sizes, map and workgroups; returns the threads of a workgroup.
+unsigned fill(RowArgs &a, int64_t tokens, int32_t top_k, int32_t hidden, int es, const int32_t *row_of_slot) {
+    a.row_of_slot = row_of_slot;
+    a.tokens = tokens;
+    a.top_k = top_k;
+    a.hidden = hidden;
+    a.slots = (uint32_t)(tokens * top_k);
+    a.units = (hidden + 16 / es - 1) / (16 / es);
+    const unsigned threads = row_threads(a.units, &a.pieces);
+    a.blocks = (uint32_t)(tokens * a.pieces);
+    return threads;
+}
+
+ns_status combine(int64_t tokens, int32_t top_k, int32_t hidden, int32_t dtype, const void *y, int64_t y_ld,
+                  const int32_t *row_of_slot, const float *w, void *out, int64_t out_ld, const char *y_name,
+                  const char *out_name, void *stream) {
+    int es;
+    if (ns_status s = check_call(tokens, top_k, hidden, dtype, &es)) return s;
+    if (ns_status s = check_rows(y_name, y, tokens * top_k, hidden, y_ld, es)) return s;
+    if (ns_status s = check_rows(out_name, out, tokens, hidden, out_ld, es)) return s;
+    if (ns_status s = check_map(tokens * top_k, row_of_slot)) return s;
+    if (tokens == 0 || hidden == 0) return NS_OK;
+    RowArgs a{};
+    a.y = y;
+    a.y_ld = y_ld;
+    a.tok = out;
+    a.tok_ld = out_ld;
+    a.w = w;
+    const unsigned threads = fill(a, tokens, top_k, hidden, es, row_of_slot);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(row_grid(a.blocks)), dim3(threads), 0, as_stream(stream), a);
+    };
+    auto pick = [&](auto t) {
+        typedef decltype(t) T;
+        if (w) top_k <= 4 ? go(moe_combine_kernel<T, true, 4>) : go(moe_combine_kernel<T, true, 8>);
+        else top_k <= 4 ? go(moe_combine_kernel<T, false, 4>) : go(moe_combine_kernel<T, false, 8>);
+    };
+    if (dtype == NS_BF16) pick((__bf16)0.f);
+    else pick(0.f);
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
+}  // namespace
+}  // namespace nsq
+
+using namespace nsq;
+
+extern "C" ns_status ns_moe_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts, size_t *bytes) {
+    if (!bytes) return fail(NS_ERR_INVALID_ARG, "bytes is NULL");
+    if (ns_status s = check_slots(tokens, top_k)) return s;
+    if (experts < 1 || experts > kMaxExperts)
+        return fail(NS_ERR_INVALID_ARG, "experts = %d outside [1, %d]", experts, kMaxExperts);
+    *bytes = (size_t)kMaxSortBlocks * (experts + 1) * sizeof(int32_t);
+    return NS_OK;
+}
+
+extern "C" ns_status ns_moe_sort(int64_t tokens, int32_t top_k, int32_t experts, const void *expert_ids,
+                                 int32_t id_bytes, int64_t ids_ld, int32_t *offsets, int32_t *slot_of_row,
+                                 int32_t *row_of_slot, void *workspace, size_t workspace_bytes, void *stream) {
+    size_t need;
+    if (ns_status s = ns_moe_sort_workspace_bytes(tokens, top_k, experts, &need)) return s;
+    if (id_bytes != 4 && id_bytes != 8) return fail(NS_ERR_DTYPE, "id_bytes = %d (must be 4 or 8)", id_bytes);
+    if (ids_ld < top_k) return fail(NS_ERR_INVALID_ARG, "ids_ld = %lld < top_k", (long long)ids_ld);
+    if (too_far(tokens, ids_ld) || too_far(tokens * ids_ld, id_bytes))
+        return fail(NS_ERR_OVERFLOW, "expert_ids: offsets overflow");
+    if (!offsets || misaligned(offsets, 4)) return fail(NS_ERR_INVALID_ARG, "offsets is NULL or not 4-byte aligned");
+    if (tokens > 0 && (!expert_ids || !slot_of_row || !row_of_slot))
+        return fail(NS_ERR_INVALID_ARG, "expert_ids, slot_of_row and row_of_slot are required");
+    if (misaligned(expert_ids, id_bytes) || misaligned(slot_of_row, 4) || misaligned(row_of_slot, 4))
+        return fail(NS_ERR_INVALID_ARG, "expert_ids, slot_of_row or row_of_slot not aligned to its type");
+    if (!workspace || workspace_bytes < need)
+        return fail(NS_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    if (misaligned(workspace, 256)) return fail(NS_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    SortArgs a{};
+    a.ids = expert_ids;
+    a.ids_ld = ids_ld;
+    a.id_bytes = id_bytes;
+    a.slots = (int32_t)(tokens * top_k);
+    a.top_k = top_k;
+    a.experts = experts;
+    a.offsets = offsets;
+    a.slot_of_row = slot_of_row;
+    a.row_of_slot = row_of_slot;
+    a.hist = reinterpret_cast<int32_t *>(workspace);
+    // One workgroup up to 8 rounds of 1024 slots; past that two launches over up to 128 workgroups.
+    const int64_t rounds = (a.slots + kSortThreads - 1) / kSortThreads;
+    const bool one = rounds <= 8;
+    const int64_t per = one ? (rounds > 0 ? rounds : 1) : (rounds + kMaxSortBlocks - 1) / kMaxSortBlocks;
+    a.per = (int32_t)(per * kSortThreads);
+    a.blocks = one ? 1 : (int32_t)((rounds + per - 1) / per);
+    const hipStream_t st = as_stream(stream);
+    if (one) {
+        hipLaunchKernelGGL(moe_rank_kernel<true>, dim3(1), dim3(kSortThreads), 0, st, a);
+    } else {
+        hipLaunchKernelGGL(moe_count_kernel, dim3(a.blocks), dim3(kSortThreads), 0, st, a);
+        hipLaunchKernelGGL(moe_rank_kernel<false>, dim3(a.blocks), dim3(kSortThreads), 0, st, a);
+    }
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
+extern "C" ns_status ns_moe_dispatch(int64_t tokens, int32_t top_k, int32_t hidden, ns_dtype dtype, const void *x,
+                                     int64_t x_ld, const int32_t *row_of_slot, void *xs, int64_t xs_ld,
+                                     void *stream) {
+    int es;
+    if (ns_status s = check_call(tokens, top_k, hidden, dtype, &es)) return s;
+    if (ns_status s = check_rows("x", x, tokens, hidden, x_ld, es)) return s;
+    if (ns_status s = check_rows("xs", xs, tokens * top_k, hidden, xs_ld, es)) return s;
+    if (ns_status s = check_map(tokens * top_k, row_of_slot)) return s;
+    if (tokens == 0 || hidden == 0) return NS_OK;
+    RowArgs a{};
+    a.x = x;
+    a.x_ld = x_ld;
+    a.rows = xs;
+    a.rows_ld = xs_ld;
+    const unsigned threads = fill(a, tokens, top_k, hidden, es, row_of_slot);
+    const dim3 grid(row_grid(a.blocks));
+    if (dtype == NS_BF16)
+        hipLaunchKernelGGL(moe_dispatch_kernel<__bf16>, grid, dim3(threads), 0, as_stream(stream), a);
+    else
+        hipLaunchKernelGGL(moe_dispatch_kernel<float>, grid, dim3(threads), 0, as_stream(stream), a);
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
+extern "C" ns_status ns_moe_dispatch_backward(int64_t tokens, int32_t top_k, int32_t hidden, ns_dtype dtype,
+                                              const void *dxs, int64_t dxs_ld, const int32_t *row_of_slot, void *dx,
+                                              int64_t dx_ld, void *stream) {
+    return combine(tokens, top_k, hidden, dtype, dxs, dxs_ld, row_of_slot, nullptr, dx, dx_ld, "dxs", "dx", stream);
+}
+
+extern "C" ns_status ns_moe_combine(int64_t tokens, int32_t top_k, int32_t hidden, ns_dtype dtype, const void *y,
+                                    int64_t y_ld, const int32_t *row_of_slot, const float *weights, void *out,
+                                    int64_t out_ld, void *stream) {
+    if (misaligned(weights, 4)) return fail(NS_ERR_INVALID_ARG, "weights not 4-byte aligned");
+    return combine(tokens, top_k, hidden, dtype, y, y_ld, row_of_slot, weights, out, out_ld, "y", "out", stream);
+}
+
+extern "C" ns_status ns_moe_combine_backward(int64_t tokens, int32_t top_k, int32_t hidden, ns_dtype dtype,
+                                             const void *dout, int64_t dout_ld, const void *y, int64_t y_ld,
+                                             const int32_t *row_of_slot, const float *weights, void *dy,
+                                             int64_t dy_ld, float *dweights, void *stream) {
+    int es;
+    if (ns_status s = check_call(tokens, top_k, hidden, dtype, &es)) return s;
+    if (ns_status s = check_rows("dout", dout, tokens, hidden, dout_ld, es)) return s;
+    if (ns_status s = check_rows("y", y, tokens * top_k, hidden, y_ld, es)) return s;
+    if (ns_status s = check_rows("dy", dy, tokens * top_k, hidden, dy_ld, es)) return s;
+    if (ns_status s = check_map(tokens * top_k, row_of_slot)) return s;
+    if (tokens > 0 && (!weights || !dweights)) return fail(NS_ERR_INVALID_ARG, "weights and dweights are required");
+    if (misaligned(weights, 4) || misaligned(dweights, 4))
+        return fail(NS_ERR_INVALID_ARG, "weights or dweights not 4-byte aligned");
+    if (tokens == 0) return NS_OK;
+    RowArgs a{};
+    a.x = dout;
+    a.x_ld = dout_ld;
+    a.y = y;
+    a.y_ld = y_ld;
+    a.rows = dy;
+    a.rows_ld = dy_ld;
+    a.w = weights;
+    a.dw = dweights;
+    fill(a, tokens, top_k, hidden, es, row_of_slot);
+    // As many threads as spread the row's units evenly over their rounds.
+    const int32_t rounds = (a.units + 511) / 512 > 0 ? (a.units + 511) / 512 : 1;
+    const int32_t each = (a.units + rounds - 1) / rounds;
+    const unsigned threads = each > 0 ? (unsigned)(each + 63) / 64 * 64 : 64;
+    const dim3 grid(row_grid((uint32_t)tokens));
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, as_stream(stream), a); };
+    auto pick = [&](auto t) {
+        typedef decltype(t) T;
+        top_k <= 4 ? go(moe_combine_backward_kernel<T, 4>) : go(moe_combine_backward_kernel<T, 8>);
+    };
+    if (dtype == NS_BF16) pick((__bf16)0.f);
+    else pick(0.f);
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
