@@ -113,30 +113,40 @@ struct Pairs {
     float t_max, t_sub, p_rest;
 };
 
-__device__ inline float teacher_at(const DistillArgs &A, int64_t at) {
-    return A.teacher_f32 ? reinterpret_cast<const float *>(A.teacher)[at]
-                         : (float)reinterpret_cast<const __bf16 *>(A.teacher)[at];
+// One pair as it lies in memory (so that a load can be under way while other
+// work is done), and its token (-1 if absent) and teacher logit.
+struct RawPair {
+    uint32_t id, id_high, t;
+};
+__device__ inline RawPair pair_at(const DistillArgs &A, int64_t row, int k) {
+    const int64_t at = row * A.top_k + k;
+    RawPair p = {0, 0, 0};
+    if (A.id_bytes == 8) {
+        const uint2 w = reinterpret_cast<const uint2 *>(A.ids)[at];
+        p.id = w.x;
+        p.id_high = w.y;
+    } else {
+        p.id = reinterpret_cast<const uint32_t *>(A.ids)[at];
+    }
+    if (A.teacher_f32) p.t = reinterpret_cast<const uint32_t *>(A.teacher)[at];
+    else p.t = reinterpret_cast<const uint16_t *>(A.teacher)[at];
+    return p;
+}
+__device__ inline int32_t token_of(const DistillArgs &A, const RawPair &p) {
+    const bool here = p.id < (uint32_t)A.vocab && p.id_high == 0;   // negative ones have their top bit set
+    return here ? (int32_t)p.id : -1;
+}
+__device__ inline float teacher_of(const DistillArgs &A, const RawPair &p) {
+    return __builtin_bit_cast(float, A.teacher_f32 ? p.t : p.t << 16);
 }
 
-// Brings the row's pairs into LDS; says whether the row has a loss. Ends with
-// every thread past the barrier.
+// Whether the row, whose tokens and teacher logits are in LDS, has a loss; its
+// largest teacher logit. Every wave for itself.
 template <bool REST>
-__device__ inline Pairs read_pairs(const DistillArgs &A, int64_t row, PairLds &L, uint32_t *bits, int words) {
-    const int lane = threadIdx.x & 63, threads = blockDim.x;
-    for (int k = threadIdx.x; k < A.top_k; k += threads) {
-        const int64_t at = row * A.top_k + k;
-        const int64_t id = A.id_bytes == 8 ? reinterpret_cast<const int64_t *>(A.ids)[at]
-                                           : (int64_t) reinterpret_cast<const int32_t *>(A.ids)[at];
-        L.id[k] = id < 0 || id >= A.vocab ? -1 : (int32_t)id;
-        L.t[k] = teacher_at(A, at);
-    }
-    if (threadIdx.x < 4) L.id[A.top_k + threadIdx.x] = -1, L.p[A.top_k + threadIdx.x] = 0.f;
-    if constexpr (REST)
-        for (int i = threadIdx.x; i < words; i += threads) bits[i] = 0;
-    __syncthreads();
+__device__ inline Pairs look_at_pairs(const DistillArgs &A, const PairLds &L) {
     float mx = kNegInf;
     bool any = false, nan = false;
-    for (int k = lane; k < A.top_k; k += 64)   // every wave for itself
+    for (int k = threadIdx.x & 63; k < A.top_k; k += 64)
         if (L.id[k] >= 0) {
             any = true;
             nan |= L.t[k] != L.t[k];
@@ -150,14 +160,40 @@ __device__ inline Pairs read_pairs(const DistillArgs &A, int64_t row, PairLds &L
     return r;
 }
 
+// Clears what a row's pairs are added to.
+template <bool REST>
+__device__ inline void clear_pairs(const DistillArgs &A, PairLds &L, uint32_t *bits, int words) {
+    if (threadIdx.x < 4) L.id[A.top_k + threadIdx.x] = -1, L.p[A.top_k + threadIdx.x] = 0.f;
+    if constexpr (REST)
+        for (int i = threadIdx.x; i < words; i += blockDim.x) bits[i] = 0;
+}
+
+// Brings the row's pairs into LDS; says whether the row has a loss. Ends with
+// every thread past the barrier.
+template <bool REST>
+__device__ inline Pairs read_pairs(const DistillArgs &A, int64_t row, PairLds &L, uint32_t *bits, int words) {
+    for (int k = threadIdx.x; k < A.top_k; k += blockDim.x) {
+        const RawPair p = pair_at(A, row, k);
+        L.id[k] = token_of(A, p);
+        L.t[k] = teacher_of(A, p);
+    }
+    clear_pairs<REST>(A, L, bits, words);
+    __syncthreads();
+    return look_at_pairs<REST>(A, L);
+}
+
+template <bool REST>
+__device__ inline float teacher_lse(const DistillArgs &A, int64_t row) {
+    return REST ? A.teacher_lse[row] : 0.f;
+}
+
 // p of every pair, the tokens' lowest pairs, and with REST the tokens' bits
 // among [e0, e1). Ends with every thread past a barrier.
 template <bool REST>
-__device__ inline void weigh_pairs(const DistillArgs &A, int64_t row, PairLds &L, Pairs &r, uint32_t *bits, int e0,
+__device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds &L, Pairs &r, uint32_t *bits, int e0,
                                    int e1) {
     const int lane = threadIdx.x & 63, threads = blockDim.x;
     if constexpr (REST) {
-        const float lse = A.teacher_lse[row];
         if (r.t_max == kNegInf) r.t_max = 0.f;
         r.t_sub = fmaf(-r.t_max, A.inv_tau, lse);
     } else {
@@ -177,7 +213,7 @@ __device__ inline void weigh_pairs(const DistillArgs &A, int64_t row, PairLds &L
         const int id = L.id[k];
         bool lowest = id >= 0;
         float sum = 0.f;
-#pragma unroll 4
+#pragma unroll 2
         for (int j = 0; j < A.top_k; j += 4) {
             const int4 other = *reinterpret_cast<const int4 *>(&L.id[j]);
             const float4 p = *reinterpret_cast<const float4 *>(&L.p[j]);
@@ -226,6 +262,12 @@ __device__ inline uint32_t vec_bits(const uint32_t *bits, int v, int n) {
     return reinterpret_cast<const uint8_t *>(bits)[v * n >> 3] >> (v * n & 7) & ((1u << n) - 1);
 }
 
+// The thread's value behind the span's vectors.
+template <typename T>
+__device__ inline float tail_of(const T *z, const Span<T> &S) {
+    return (int)threadIdx.x < S.tail ? (float)z[S.e0 + S.vecs * S.N + threadIdx.x] : 0.f;
+}
+
 // Adds a vector's values to a thread's running sum; with REST only those whose bit is clear.
 template <typename T, bool REST>
 __device__ inline void add_vec(Lse &a, typename Vec16<T>::raw v, uint32_t skip, float c) {
@@ -244,18 +286,18 @@ __device__ inline void add_vec(Lse &a, typename Vec16<T>::raw v, uint32_t skip, 
     a.m = mx;
 }
 
+// The thread's value of the span's tail, x, likewise.
 template <typename T, bool REST>
-__device__ inline void add_tail(Lse &a, const T *z, const Span<T> &S, const uint32_t *bits, float c) {
+__device__ inline void add_tail(Lse &a, float x, const Span<T> &S, const uint32_t *bits, float c) {
     if ((int)threadIdx.x >= S.tail) return;
     const int j = S.vecs * S.N + threadIdx.x;
     if (REST && (bits[j >> 5] >> (j & 31) & 1)) return;
-    const float x = (float)z[S.e0 + j];
     a = join(a, {x, x == x && x != __builtin_inff() && x != kNegInf ? 1.f : x == kNegInf ? 0.f : __builtin_nanf("")}, c);
 }
 
 // The sum over a span of a row in memory, joined over the workgroup.
 template <typename T, bool REST>
-__device__ inline Lse sum_span(const T *z, const Span<T> &S, const uint32_t *bits, float c) {
+__device__ inline Lse sum_span(const T *z, float zt, const Span<T> &S, const uint32_t *bits, float c) {
     constexpr int B = 4;
     const int threads = blockDim.x;
     Lse a = {kNegInf, 0.f};
@@ -269,7 +311,7 @@ __device__ inline Lse sum_span(const T *z, const Span<T> &S, const uint32_t *bit
     }
     for (; v < S.vecs; v += threads)
         add_vec<T, REST>(a, load_vec<T>(z + S.e0 + (int64_t)v * S.N), REST ? vec_bits(bits, v, S.N) : 0, c);
-    add_tail<T, REST>(a, z, S, bits, c);
+    add_tail<T, REST>(a, zt, S, bits, c);
     return a;
 }
 
@@ -294,20 +336,41 @@ __device__ inline Lse sum_tokens(const DistillArgs &A, const PairLds &L, float c
     return wave_join(a, c);
 }
 
+// g q of a vector's logits.
 template <typename T>
 __device__ inline typename Vec16<T>::raw grad_vec(typename Vec16<T>::raw v, const Norm &n, float c, float g) {
     typename Vec16<T>::raw o;
+    const float factor = g * n.scale;
 #pragma unroll
-    for (int i = 0; i < Vec16<T>::N; ++i) set_elem<T>(o, i, g * q_of(elem<T>(v, i), n, c));
+    for (int i = 0; i < Vec16<T>::N; ++i)
+        set_elem<T>(o, i, factor * __builtin_amdgcn_exp2f((elem<T>(v, i) - n.m) * c));
     return o;
+}
+
+// A span's vectors' gradient, read from memory.
+template <typename T>
+__device__ inline void grad_span(const T *z, T *dz, const Span<T> &S, const Norm &n, float c, float g) {
+    constexpr int B = 4;
+    const int threads = blockDim.x;
+    int v = threadIdx.x;
+    for (; v + (B - 1) * threads < S.vecs; v += B * threads) {
+        typename Vec16<T>::raw w[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) w[i] = load_vec<T>(z + S.e0 + (int64_t)(v + i * threads) * S.N);
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            store_vec<T>(dz + S.e0 + (int64_t)(v + i * threads) * S.N, grad_vec<T>(w[i], n, c, g));
+    }
+    for (; v < S.vecs; v += threads)
+        store_vec<T>(dz + S.e0 + (int64_t)v * S.N, grad_vec<T>(load_vec<T>(z + S.e0 + (int64_t)v * S.N), n, c, g));
 }
 
 // The tail's gradient, then that of the pairs' tokens, each written over the
 // other tokens' formula by the thread that wrote it.
-template <typename T>
-__device__ inline void finish_span(const DistillArgs &A, const PairLds &L, const T *z, T *dz, const Span<T> &S, float zt,
+template <typename T, typename Put>
+__device__ inline void finish_span(const DistillArgs &A, const PairLds &L, const Put &put, const Span<T> &S, float zt,
                                    const Norm &n, float c, float g, float g_rest) {
-    if ((int)threadIdx.x < S.tail) dz[S.e0 + S.vecs * S.N + threadIdx.x] = (T)(g_rest * q_of(zt, n, c));
+    if ((int)threadIdx.x < S.tail) put(S.e0 + S.vecs * S.N + threadIdx.x, (T)(g_rest * q_of(zt, n, c)));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int k0 = 0; k0 < A.top_k; k0 += 64) {
         const int k = k0 + lane;
@@ -324,7 +387,7 @@ __device__ inline void finish_span(const DistillArgs &A, const PairLds &L, const
             mine &= mine - 1;
             const int to = __shfl(thread, b) & 63, token = __shfl(id, b);
             const float x = __shfl(val, b);
-            if (lane == to) dz[token] = (T)x;
+            if (lane == to) put(token, (T)x);
         }
     }
 }
@@ -353,6 +416,12 @@ __device__ inline void write_loss(const DistillArgs &A, const PairLds &L, const 
     A.lse[row] = all.m * A.inv_tau + logf(all.s);
 }
 
+template <bool REST>
+__device__ inline void write_no_loss(const DistillArgs &A, int64_t row) {
+    A.loss[row] = A.lse[row] = 0.f;
+    if constexpr (REST) A.rest_lse[row] = 0.f;
+}
+
 // A row without a loss: zeros. `first`: also its loss and logsumexps.
 template <typename T, bool REST>
 __device__ inline void write_empty(const DistillArgs &A, int64_t row, const Span<T> &S, bool first) {
@@ -364,20 +433,162 @@ __device__ inline void write_empty(const DistillArgs &A, int64_t row, const Span
         }
         if ((int)threadIdx.x < S.tail) dz[S.e0 + S.vecs * S.N + threadIdx.x] = (T)0.f;
     }
-    if (first && threadIdx.x == 0) {
-        A.loss[row] = A.lse[row] = 0.f;
-        if constexpr (REST) A.rest_lse[row] = 0.f;
-    }
+    if (first && threadIdx.x == 0) write_no_loss<REST>(A, row);
 }
 
 // ---------------------------------------------------------------------------
 // kernels
 // ---------------------------------------------------------------------------
 
-// One workgroup a row: loss, and with dlogits the gradient. NV > 0: the row
-// stays in registers, NV vectors a thread; NV = 0: it is read from memory
-// again for the gradient.
+// What the loss and the gradient of a row take from its sums.
+struct RowSums {
+    Lse all, rest;
+    Norm n;
+    float g, g_rest;   // factors of the pairs' tokens and of the others
+};
+template <bool REST>
+__device__ inline RowSums row_sums(const DistillArgs &A, const PairLds &L, const Pairs &r, float grad_loss, Lse rest,
+                                   float c) {
+    RowSums s;
+    s.rest = rest;
+    s.all = REST ? join(rest, sum_tokens(A, L, c), c) : rest;
+    s.n = norm_of(s.all, A.inv_tau);
+    s.g = grad_loss * A.inv_tau;
+    s.g_rest = s.g;
+    if (REST && r.p_rest != 0.f)
+        s.g_rest = s.g * (1.f - r.p_rest * s.all.s / rest.s * shifted(s.all.m, rest.m, c));
+    return s;
+}
+
+// Loss and gradient, the row in registers in between: NV vectors a thread, at
+// most one pair a thread. A workgroup takes rows in turn and loads each vector
+// of its next row as soon as it has written the one before. Loads return in
+// order, so what the next row needs besides (its tokens' logits, and the pairs
+// of the row after it, whose tokens those logits' addresses come from) is asked
+// for ahead of its vectors: its pairs are then weighed while its vectors come in.
+// Vectors go through buffer descriptors: lanes past the row's last whole vector
+// read zeros (not used) and write nothing.
 template <typename T, int THREADS, int NV, bool REST>
+__global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
+    extern __shared__ uint32_t bits[];
+    __shared__ __attribute__((aligned(16))) PairLds L;
+    typedef uint32_t dwords __attribute__((ext_vector_type(4)));
+    typedef typename Vec16<T>::raw raw;
+    const Span<T> S(0, A.vocab);
+    const float c = A.inv_tau * kLog2e;
+    const int tid = threadIdx.x;
+    const auto row_of = [&](const void *base, int64_t row, int64_t ld) {
+        return reinterpret_cast<T *>(const_cast<void *>(base)) + row * ld;
+    };
+    const auto vecs_of = [&](const void *base, int64_t row, int64_t ld, bool there) {
+        return __builtin_amdgcn_make_buffer_rsrc(row_of(base, there ? row : 0, ld), (short)0, there ? S.vecs * 16 : 0,
+                                                 0x00020000);
+    };
+    const auto all_of = [&](const void *base, int64_t row, int64_t ld) {   // element by element, to the row's end
+        return __builtin_amdgcn_make_buffer_rsrc(row_of(base, row, ld), (short)0, A.vocab * (int)sizeof(T), 0x00020000);
+    };
+    const auto get = [](__amdgpu_buffer_rsrc_t r, int j) {
+        if constexpr (sizeof(T) == 2) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, j * 2, 0, 0));
+        else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, j * 4, 0, 0));
+    };
+    // What a row needs besides its vectors; nothing of it is looked at before the row's turn.
+    const auto pair_of = [&](int64_t row) { return tid < A.top_k && row < A.rows ? pair_at(A, row, tid) : RawPair{~0u, 0, 0}; };
+    struct Beside {
+        T pz, zt;             // logits of the thread's pair and of its place behind the vectors
+        float g, teacher_lse;
+    };
+    const auto beside_of = [&](int64_t row, const RawPair &p) {
+        Beside b = {(T)0.f, (T)0.f, 0.f, 0.f};
+        if (row < A.rows) {
+            const auto z = all_of(A.logits, row, A.ld);
+            const int32_t id = token_of(A, p);
+            if (id >= 0) b.pz = get(z, id);
+            if (tid < S.tail) b.zt = get(z, S.vecs * S.N + tid);
+            b.g = A.grad_loss[row];
+            if constexpr (REST) b.teacher_lse = A.teacher_lse[row];
+        }
+        return b;
+    };
+
+    // The waits for what is under way count the loads and stores issued since, over every path to them. So that the
+    // counts are exact there is no branch around a vector's load or store (past the row, or for no next row, their
+    // descriptors end before them), and the first row's loads go out like the others': in order, each behind a store
+    // (to a descriptor of length zero).
+    dwords held[NV];
+    int64_t row = blockIdx.x;
+    RawPair p = pair_of(row), ahead = pair_of(row + gridDim.x);
+    Beside now = beside_of(row, p);
+    {
+        const auto z = vecs_of(A.logits, row, A.ld, true), nowhere = vecs_of(A.logits, row, A.ld, false);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            __builtin_amdgcn_raw_buffer_store_b128(dwords{0, 0, 0, 0}, nowhere, tid * 16 + i * THREADS * 16, 0, 0);
+            held[i] = __builtin_amdgcn_raw_buffer_load_b128(z, tid * 16 + i * THREADS * 16, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    for (; row < A.rows; row += gridDim.x) {
+        const int64_t next = row + gridDim.x;
+        if (tid < A.top_k) {
+            L.id[tid] = token_of(A, p);
+            L.t[tid] = teacher_of(A, p);
+            L.z[tid] = (float)now.pz;
+        }
+        clear_pairs<REST>(A, L, bits, (A.vocab + 31) >> 5);
+        __syncthreads();
+        Pairs r = look_at_pairs<REST>(A, L);
+        weigh_pairs<REST>(A, now.teacher_lse, L, r, bits, 0, A.vocab);
+        Lse a = {kNegInf, 0.f};
+        int at = tid;
+        asm volatile("" : "+v"(at));   // what follows from it is found anew for each row, not held in 2 NV registers
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int left = S.vecs - i * THREADS;
+            raw v = __builtin_bit_cast(raw, held[i]);
+            if (left < THREADS)
+#pragma unroll
+                for (int j = 0; j < S.N; ++j)
+                    if (at >= left) set_elem<T>(v, j, kNegInf);
+            if (left > 0) add_vec<T, REST>(a, v, REST ? vec_bits(bits, min(at + i * THREADS, S.vecs), S.N) : 0, c);
+        }
+        const float zt = (float)now.zt;
+        add_tail<T, REST>(a, zt, S, bits, c);
+        const RowSums s = row_sums<REST>(A, L, r, now.g, block_join(a, L, c), c);
+        // The next row: first what lies besides its vectors, and the pairs of the row after it.
+        p = ahead;
+        now = beside_of(next, p);
+        ahead = pair_of(next + gridDim.x);
+        const auto dz = vecs_of(A.dlogits, row, A.dld, true), z = vecs_of(A.logits, next, A.ld, next < A.rows);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            raw o = {};
+            if (r.some && S.vecs > i * THREADS) o = grad_vec<T>(__builtin_bit_cast(raw, held[i]), s.n, c, s.g_rest);
+            // soffset stays 0: with an SGPR there the compiler takes it that the store has read its data at
+            // once, but a VALU write to the last two dwords right behind it was seen to reach memory.
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(dwords, o), dz, at * 16 + i * THREADS * 16, 0, 0);
+            held[i] = __builtin_amdgcn_raw_buffer_load_b128(z, at * 16 + i * THREADS * 16, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        asm volatile("" ::: "memory");   // the pairs' tokens are written over what these stores left
+        const auto out = all_of(A.dlogits, row, A.dld);
+        const auto put = [&](int j, T x) {
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, x), out, j * 2, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), out, j * 4, 0, 0);
+        };
+        if (r.some) {
+            finish_span<T>(A, L, put, S, zt, s.n, c, s.g, s.g_rest);
+            write_loss<REST>(A, L, r, row, s.n, s.all, s.rest);
+        } else {
+            if (tid < S.tail) put(S.vecs * S.N + tid, (T)0.f);
+            if (tid == 0) write_no_loss<REST>(A, row);
+        }
+        __syncthreads();   // the next row's pairs go into the same LDS
+    }
+}
+
+// Loss, and with dlogits the gradient, of rows too long to hold: the row is
+// read a second time for the gradient.
+template <typename T, int THREADS, bool REST>
 __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
     __shared__ __attribute__((aligned(16))) PairLds L;
@@ -391,51 +602,17 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
             __syncthreads();
             continue;
         }
-        typename Vec16<T>::raw held[NV > 0 ? NV : 1];
-        if constexpr (NV > 0) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = threadIdx.x + i * THREADS;
-                if (v < S.vecs) held[i] = load_vec<T>(z + (int64_t)v * S.N);
-            }
-        }
         for (int k = threadIdx.x; k < A.top_k; k += THREADS) L.z[k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
-        const float zt = (int)threadIdx.x < S.tail ? (float)z[S.vecs * S.N + threadIdx.x] : 0.f;
-        weigh_pairs<REST>(A, row, L, r, bits, 0, A.vocab);
-        Lse rest;
-        if constexpr (NV > 0) {
-            rest = {kNegInf, 0.f};
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = threadIdx.x + i * THREADS;
-                if (v < S.vecs) add_vec<T, REST>(rest, held[i], REST ? vec_bits(bits, v, S.N) : 0, c);
-            }
-            add_tail<T, REST>(rest, z, S, bits, c);
-        } else {
-            rest = sum_span<T, REST>(z, S, bits, c);
-        }
-        rest = block_join(rest, L, c);
-        const Lse all = REST ? join(rest, sum_tokens(A, L, c), c) : rest;
-        const Norm n = norm_of(all, A.inv_tau);
+        const float zt = tail_of<T>(z, S);
+        weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, 0, A.vocab);
+        const Lse rest = block_join(sum_span<T, REST>(z, zt, S, bits, c), L, c);
+        const RowSums s = row_sums<REST>(A, L, r, A.dlogits ? A.grad_loss[row] : 0.f, rest, c);
         if (A.dlogits) {
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
-            const float g = A.grad_loss[row] * A.inv_tau;
-            float g_rest = g;
-            if (REST && r.p_rest != 0.f)
-                g_rest = g * (1.f - r.p_rest * all.s / rest.s * shifted(all.m, rest.m, c));
-            if constexpr (NV > 0) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int v = threadIdx.x + i * THREADS;
-                    if (v < S.vecs) store_vec<T>(dz + (int64_t)v * S.N, grad_vec<T>(held[i], n, c, g_rest));
-                }
-            } else {
-                for (int v = threadIdx.x; v < S.vecs; v += THREADS)
-                    store_vec<T>(dz + (int64_t)v * S.N, grad_vec<T>(load_vec<T>(z + (int64_t)v * S.N), n, c, g_rest));
-            }
-            finish_span<T>(A, L, z, dz, S, zt, n, c, g, g_rest);
+            grad_span<T>(z, dz, S, s.n, c, s.g_rest);
+            finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, s.n, c, s.g, s.g_rest);
         }
-        write_loss<REST>(A, L, r, row, n, all, rest);
+        write_loss<REST>(A, L, r, row, s.n, s.all, s.rest);
         __syncthreads();   // the next row's pairs go into the same LDS
     }
 }
@@ -457,9 +634,9 @@ __global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillA
             if (chunk == 0)
                 for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads)
                     A.top_z[row * A.top_k + k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
-            if constexpr (REST) weigh_pairs<REST>(A, row, L, r, bits, e0, e1);
+            if constexpr (REST) weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, e0, e1);
         }
-        const Lse a = block_join(sum_span<T, REST>(z, S, bits, c), L, c);
+        const Lse a = block_join(sum_span<T, REST>(z, tail_of<T>(z, S), S, bits, c), L, c);
         if (threadIdx.x == 0) A.partial[row * A.chunks + chunk] = make_float2(a.m, a.s);
         __syncthreads();   // the next part uses the same LDS
     }
@@ -489,8 +666,8 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
             if (LOSS) L.z[k] = A.top_z[row * A.top_k + k];
             else L.z[k] = id >= e0 && id < e1 ? (float)z[id] : 0.f;
         }
-        const float zt = (int)threadIdx.x < S.tail ? (float)z[e0 + S.vecs * S.N + threadIdx.x] : 0.f;
-        weigh_pairs<REST>(A, row, L, r, bits, 0, 0);
+        const float zt = tail_of<T>(z, S);
+        weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, 0, 0);
         Lse all = {kNegInf, 0.f}, rest = {kNegInf, 0.f};
         Norm n;
         float others = 1.f;   // the factor of the tokens outside the pairs
@@ -511,19 +688,8 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
         if (A.dlogits) {
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
             const float g = A.grad_loss[row] * A.inv_tau;
-            constexpr int B = 4;
-            int v = threadIdx.x;
-            for (; v + (B - 1) * kSplitThreads < S.vecs; v += B * kSplitThreads) {
-                typename Vec16<T>::raw w[B];
-    #pragma unroll
-                for (int i = 0; i < B; ++i) w[i] = load_vec<T>(z + e0 + (int64_t)(v + i * kSplitThreads) * S.N);
-    #pragma unroll
-                for (int i = 0; i < B; ++i)
-                    store_vec<T>(dz + e0 + (int64_t)(v + i * kSplitThreads) * S.N, grad_vec<T>(w[i], n, c, g * others));
-            }
-            for (; v < S.vecs; v += kSplitThreads)
-                store_vec<T>(dz + e0 + (int64_t)v * S.N, grad_vec<T>(load_vec<T>(z + e0 + (int64_t)v * S.N), n, c, g * others));
-            finish_span<T>(A, L, z, dz, S, zt, n, c, g, g * others);
+            grad_span<T>(z, dz, S, n, c, g * others);
+            finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, n, c, g, g * others);
         }
         if (LOSS && chunk == 0) write_loss<REST>(A, L, r, row, n, all, rest);
         __syncthreads();   // the next part uses the same LDS
@@ -605,16 +771,19 @@ unsigned split_grid(const DistillArgs &a) { return (unsigned)std::min<int64_t>((
 
 template <typename T, bool REST>
 ns_status launch_rows(const DistillArgs &a, hipStream_t st) {
-    const size_t lds = REST ? (size_t)((a.vocab + 31) / 32) * 4 : 0;
+    const size_t lds = REST ? (size_t)((a.vocab + 31) / 32 + 1) * 4 : 0;   // lanes past the row read one byte behind it
     const int64_t vecs = a.vocab / Vec16<T>::N;
-    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 1 << 20);
-    auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), lds, st, a); };
-    if (!a.dlogits) vecs <= 4096 ? go(distill_row_kernel<T, 256, 0, REST>, 256) : go(distill_row_kernel<T, 1024, 0, REST>, 1024);
-    else if (vecs <= 2048) go(distill_row_kernel<T, 256, 8, REST>, 256);
-    else if (vecs <= 4096) go(distill_row_kernel<T, 512, 8, REST>, 512);
-    else if (vecs <= 8192) go(distill_row_kernel<T, 1024, 8, REST>, 1024);
-    else if (vecs <= 16384) go(distill_row_kernel<T, 1024, 16, REST>, 1024);
-    else go(distill_row_kernel<T, 1024, 0, REST>, 1024);
+    auto go = [&](auto kernel, int threads, int64_t most) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows, most)), dim3(threads), lds, st, a);
+    };
+    // Held rows: as many workgroups as are resident at once (16 waves a CU), a thread for each pair.
+    const int64_t need = a.dlogits ? std::max<int64_t>(vecs, 8 * a.top_k) : INT64_MAX;
+    if (need <= 2048) go(distill_held_kernel<T, 256, 8, REST>, 256, 1024);
+    else if (need <= 4096) go(distill_held_kernel<T, 512, 8, REST>, 512, 512);
+    else if (need <= 8192) go(distill_held_kernel<T, 1024, 8, REST>, 1024, 256);
+    else if (need <= 16384) go(distill_held_kernel<T, 1024, 16, REST>, 1024, 256);
+    else if (a.rows >= 1024) go(distill_row_kernel<T, 256, REST>, 256, 1 << 20);
+    else go(distill_row_kernel<T, 1024, REST>, 1024, 1 << 20);
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }
