@@ -8,7 +8,8 @@
 // With the teacher's logsumexp over its whole vocabulary (at tau), p_k =
 // exp(t_k / tau - lse_T) and all other tokens form one more class with
 // p_r = max(0, 1 - sum p_k) and q_r = the sum of their q:
-//   loss += p_r (log p_r - log q_r),  their dz_j = g / tau q_j (1 - p_r / q_r).
+//   loss += p_r (log p_r - log q_r),  their dz_j = g / tau (q_r - p_r) q_j / q_r,
+// q_j / q_r being the softmax over them alone, finite however small q_r is.
 // Terms with p = 0 count as 0. A row without pairs (or, without lse_T, with
 // every teacher logit -inf) has loss and gradient 0 and its logits are not used.
 //
@@ -34,6 +35,7 @@ constexpr int kMaxChunks = 64;            // parts of a row that is split over w
 constexpr int kBitVocab = 1 << 18;        // tokens one workgroup marks in LDS (32 KiB)
 constexpr int kSplitThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kNonTemporal = 2;           // a buffer store's cache policy
 
 struct DistillArgs {
     const void *logits;
@@ -85,7 +87,7 @@ __device__ inline float wave_max(float v) {
 struct Norm {
     float m, scale, log_scale;
 };
-__device__ inline Norm norm_of(Lse l, float inv_tau) { return {l.m == kNegInf ? 0.f : l.m, 1.f / l.s, -logf(l.s)}; }
+__device__ inline Norm norm_of(Lse l) { return {l.m == kNegInf ? 0.f : l.m, 1.f / l.s, -logf(l.s)}; }
 // From a logsumexp rounded to fp32: m is lse tau rounded, and the scale takes
 // up the rest of it, so q is off by no more than lse's own rounding.
 __device__ inline Norm norm_of_lse(float lse, float inv_tau) {
@@ -325,6 +327,16 @@ __device__ inline Lse block_join(Lse a, PairLds &L, float c) {
     return a;
 }
 
+// The threads' sum, in every thread. One barrier inside.
+__device__ inline float block_sum(float v, PairLds &L) {
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) L.wave[threadIdx.x >> 6].s = v;
+    __syncthreads();
+    v = 0.f;
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) v += L.wave[w].s;
+    return v;
+}
+
 // The sum over the pairs' tokens (each once); every wave for itself.
 __device__ inline Lse sum_tokens(const DistillArgs &A, const PairLds &L, float c) {
     Lse a = {kNegInf, 0.f};
@@ -344,6 +356,46 @@ __device__ inline typename Vec16<T>::raw grad_vec(typename Vec16<T>::raw v, cons
 #pragma unroll
     for (int i = 0; i < Vec16<T>::N; ++i)
         set_elem<T>(o, i, factor * __builtin_amdgcn_exp2f((elem<T>(v, i) - n.m) * c));
+    return o;
+}
+
+// The same two with exp((z - m) / tau) as 2^(z c + hi), see distill_held_kernel.
+template <typename T, bool REST>
+__device__ inline float fast_sum(typename Vec16<T>::raw v, uint32_t skip, float c, float hi) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < Vec16<T>::N; ++i) s[i & 1] += __builtin_amdgcn_exp2f(fmaf(elem<T>(v, i), c, hi));
+    if (REST && skip) {   // few vectors: without the pairs' tokens, in the same order
+        s[0] = s[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < Vec16<T>::N; ++i)
+            s[i & 1] += skip >> i & 1 ? 0.f : __builtin_amdgcn_exp2f(fmaf(elem<T>(v, i), c, hi));
+    }
+    return s[0] + s[1];
+}
+// factor 2^(z c + hi). For bf16 results log2 |factor| goes into the exponent
+// (its rounding, 2^-24 of a number below 100, is far under theirs) and the
+// sign is set afterwards.
+struct FastFactor {
+    float hi, factor;
+    uint32_t sign;
+};
+template <typename T> __device__ inline FastFactor fast_factor(float factor, float hi) {
+    const bool fold = sizeof(T) == 2;
+    return {fold ? hi + __builtin_amdgcn_logf(fabsf(factor)) : hi, factor, fold && factor < 0.f ? 0x80008000u : 0u};
+}
+template <typename T>
+__device__ inline typename Vec16<T>::raw fast_grad(typename Vec16<T>::raw v, float c, const FastFactor &f) {
+    typename Vec16<T>::raw o;
+#pragma unroll
+    for (int i = 0; i < Vec16<T>::N; ++i) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(elem<T>(v, i), c, f.hi));
+        set_elem<T>(o, i, sizeof(T) == 2 ? e : e * f.factor);
+    }
+    if constexpr (sizeof(T) == 2) {
+        typedef uint32_t dwords __attribute__((ext_vector_type(4)));
+        o = __builtin_bit_cast(typename Vec16<T>::raw, __builtin_bit_cast(dwords, o) ^ f.sign);
+    }
     return o;
 }
 
@@ -369,8 +421,8 @@ __device__ inline void grad_span(const T *z, T *dz, const Span<T> &S, const Norm
 // other tokens' formula by the thread that wrote it.
 template <typename T, typename Put>
 __device__ inline void finish_span(const DistillArgs &A, const PairLds &L, const Put &put, const Span<T> &S, float zt,
-                                   const Norm &n, float c, float g, float g_rest) {
-    if ((int)threadIdx.x < S.tail) put(S.e0 + S.vecs * S.N + threadIdx.x, (T)(g_rest * q_of(zt, n, c)));
+                                   const Norm &n, const Norm &others, float c, float g, float g_others) {
+    if ((int)threadIdx.x < S.tail) put(S.e0 + S.vecs * S.N + threadIdx.x, (T)(g_others * q_of(zt, others, c)));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int k0 = 0; k0 < A.top_k; k0 += 64) {
         const int k = k0 + lane;
@@ -443,20 +495,25 @@ __device__ inline void write_empty(const DistillArgs &A, int64_t row, const Span
 // What the loss and the gradient of a row take from its sums.
 struct RowSums {
     Lse all, rest;
-    Norm n;
-    float g, g_rest;   // factors of the pairs' tokens and of the others
+    Norm n, others;    // q of any token, and what the others' gradient is g_others times
+    float g, g_others;
 };
+// The others' factor, from their share of the student's mass.
+template <bool REST>
+__device__ inline float others_factor(const Pairs &r, float g, float q_rest) {
+    return REST ? g * (q_rest - r.p_rest) : g;
+}
 template <bool REST>
 __device__ inline RowSums row_sums(const DistillArgs &A, const PairLds &L, const Pairs &r, float grad_loss, Lse rest,
                                    float c) {
     RowSums s;
     s.rest = rest;
     s.all = REST ? join(rest, sum_tokens(A, L, c), c) : rest;
-    s.n = norm_of(s.all, A.inv_tau);
+    s.n = norm_of(s.all);
+    s.others = norm_of(s.rest);
+    if (REST && rest.s == 0.f && r.p_rest == 0.f) s.others.scale = 0.f;   // no others, or all masked: q is 0
     s.g = grad_loss * A.inv_tau;
-    s.g_rest = s.g;
-    if (REST && r.p_rest != 0.f)
-        s.g_rest = s.g * (1.f - r.p_rest * s.all.s / rest.s * shifted(s.all.m, rest.m, c));
+    s.g_others = others_factor<REST>(r, s.g, rest.s / s.all.s * shifted(rest.m, s.all.m, c));
     return s;
 }
 
@@ -538,37 +595,61 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
         __syncthreads();
         Pairs r = look_at_pairs<REST>(A, L);
         weigh_pairs<REST>(A, now.teacher_lse, L, r, bits, 0, A.vocab);
-        Lse a = {kNegInf, 0.f};
         int at = tid;
         asm volatile("" : "+v"(at));   // what follows from it is found anew for each row, not held in 2 NV registers
+        const float zt = (float)now.zt;
+        // exp((z - m) / tau) = 2^(z c + hi) 2^-lo with m the pairs' largest logit: one fma a value, and no maximum to
+        // find. It serves unless some logit lies so far above m that the sum overflows, or (REST) all lie so far below
+        // that it is lost, or one is NaN or infinite; then the row is summed again relative to its own largest.
+        float m = kNegInf;
+        for (int k = tid & 63; k < A.top_k; k += 64)
+            if (L.id[k] >= 0) m = fmaxf(m, L.z[k]);
+        m = wave_max(m);
+        const float hi = -m * c, lo = fmaf(m, c, hi);
+        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int left = S.vecs - i * THREADS;
-            raw v = __builtin_bit_cast(raw, held[i]);
-            if (left < THREADS)
-#pragma unroll
-                for (int j = 0; j < S.N; ++j)
-                    if (at >= left) set_elem<T>(v, j, kNegInf);
-            if (left > 0) add_vec<T, REST>(a, v, REST ? vec_bits(bits, min(at + i * THREADS, S.vecs), S.N) : 0, c);
+            if (left > 0 && (left >= THREADS || at < left)) {
+                const uint32_t skip = REST ? vec_bits(bits, at + i * THREADS, S.N) : 0;
+                sum += fast_sum<T, REST>(__builtin_bit_cast(raw, held[i]), skip, c, hi);
+            }
         }
-        const float zt = (float)now.zt;
-        add_tail<T, REST>(a, zt, S, bits, c);
-        const RowSums s = row_sums<REST>(A, L, r, now.g, block_join(a, L, c), c);
+        if (tid < S.tail && !(REST && vec_bits(bits, S.vecs * S.N + tid, 1))) sum += __builtin_amdgcn_exp2f(fmaf(zt, c, hi));
+        Lse rest = {m, block_sum(sum, L) * __builtin_amdgcn_exp2f(-lo)};
+        const bool fast = !r.some || (rest.s > 1e-10f && rest.s < 1e30f);
+        if (!fast) {
+            Lse a = {kNegInf, 0.f};
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = at + i * THREADS;
+                if (v < S.vecs) add_vec<T, REST>(a, __builtin_bit_cast(raw, held[i]), REST ? vec_bits(bits, v, S.N) : 0, c);
+            }
+            add_tail<T, REST>(a, zt, S, bits, c);
+            __syncthreads();
+            rest = block_join(a, L, c);
+        }
+        const RowSums s = row_sums<REST>(A, L, r, now.g, rest, c);
         // The next row: first what lies besides its vectors, and the pairs of the row after it.
         p = ahead;
         now = beside_of(next, p);
         ahead = pair_of(next + gridDim.x);
         const auto dz = vecs_of(A.dlogits, row, A.dld, true), z = vecs_of(A.logits, next, A.ld, next < A.rows);
+        const FastFactor f = fast_factor<T>(s.g_others * s.others.scale * __builtin_amdgcn_exp2f(-lo), hi);
+        const auto turn = [&](auto value) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            raw o = {};
-            if (r.some && S.vecs > i * THREADS) o = grad_vec<T>(__builtin_bit_cast(raw, held[i]), s.n, c, s.g_rest);
-            // soffset stays 0: with an SGPR there the compiler takes it that the store has read its data at
-            // once, but a VALU write to the last two dwords right behind it was seen to reach memory.
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(dwords, o), dz, at * 16 + i * THREADS * 16, 0, 0);
-            held[i] = __builtin_amdgcn_raw_buffer_load_b128(z, at * 16 + i * THREADS * 16, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+            for (int i = 0; i < NV; ++i) {
+                raw o = {};
+                if (r.some && S.vecs > i * THREADS) o = value(__builtin_bit_cast(raw, held[i]));
+                // soffset stays 0: with an SGPR there the compiler takes it that the store has read its data at
+                // once, but a VALU write to the last two dwords right behind it was seen to reach memory.
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(dwords, o), dz, at * 16 + i * THREADS * 16, 0, kNonTemporal);
+                held[i] = __builtin_amdgcn_raw_buffer_load_b128(z, at * 16 + i * THREADS * 16, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (fast) turn([&](raw v) { return fast_grad<T>(v, c, f); });
+        else turn([&](raw v) { return grad_vec<T>(v, s.others, c, s.g_others); });
         asm volatile("" ::: "memory");   // the pairs' tokens are written over what these stores left
         const auto out = all_of(A.dlogits, row, A.dld);
         const auto put = [&](int j, T x) {
@@ -576,7 +657,7 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
             else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), out, j * 4, 0, 0);
         };
         if (r.some) {
-            finish_span<T>(A, L, put, S, zt, s.n, c, s.g, s.g_rest);
+            finish_span<T>(A, L, put, S, zt, s.n, s.others, c, s.g, s.g_others);
             write_loss<REST>(A, L, r, row, s.n, s.all, s.rest);
         } else {
             if (tid < S.tail) put(S.vecs * S.N + tid, (T)0.f);
@@ -609,8 +690,8 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
         const RowSums s = row_sums<REST>(A, L, r, A.dlogits ? A.grad_loss[row] : 0.f, rest, c);
         if (A.dlogits) {
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
-            grad_span<T>(z, dz, S, s.n, c, s.g_rest);
-            finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, s.n, c, s.g, s.g_rest);
+            grad_span<T>(z, dz, S, s.others, c, s.g_others);
+            finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, s.n, s.others, c, s.g, s.g_others);
         }
         write_loss<REST>(A, L, r, row, s.n, s.all, s.rest);
         __syncthreads();   // the next row's pairs go into the same LDS
@@ -668,30 +749,32 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
         }
         const float zt = tail_of<T>(z, S);
         weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, 0, 0);
-        Lse all = {kNegInf, 0.f}, rest = {kNegInf, 0.f};
-        Norm n;
-        float others = 1.f;   // the factor of the tokens outside the pairs
+        RowSums s{};
+        const float g = A.dlogits ? A.grad_loss[row] : 0.f;
         if constexpr (LOSS) {
+            Lse rest = {kNegInf, 0.f};
             for (int i = threadIdx.x & 63; i < parts; i += 64) {
                 const float2 p = A.partial[row * parts + i];
                 rest = join(rest, {p.x, p.y}, c);
             }
-            rest = wave_join(rest, c);
-            all = REST ? join(rest, sum_tokens(A, L, c), c) : rest;
-            n = norm_of(all, A.inv_tau);
-            if (REST && r.p_rest != 0.f) others = 1.f - r.p_rest * all.s / rest.s * shifted(all.m, rest.m, c);
+            s = row_sums<REST>(A, L, r, g, wave_join(rest, c), c);
         } else {
             const float lse = A.lse[row];
-            n = norm_of_lse(lse, A.inv_tau);
-            if (REST && r.p_rest != 0.f) others = 1.f - r.p_rest * expf(lse - A.rest_lse[row]);
+            s.n = s.others = norm_of_lse(lse, A.inv_tau);
+            s.g = s.g_others = g * A.inv_tau;
+            if constexpr (REST) {
+                const float rest_lse = A.rest_lse[row];
+                if (rest_lse == kNegInf) s.others = {0.f, r.p_rest == 0.f ? 0.f : __builtin_inff(), 0.f};
+                else s.others = norm_of_lse(rest_lse, A.inv_tau);
+                s.g_others = others_factor<REST>(r, s.g, expf(rest_lse - lse));
+            }
         }
         if (A.dlogits) {
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
-            const float g = A.grad_loss[row] * A.inv_tau;
-            grad_span<T>(z, dz, S, n, c, g * others);
-            finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, n, c, g, g * others);
+            grad_span<T>(z, dz, S, s.others, c, s.g_others);
+            finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, s.n, s.others, c, s.g, s.g_others);
         }
-        if (LOSS && chunk == 0) write_loss<REST>(A, L, r, row, n, all, rest);
+        if (LOSS && chunk == 0) write_loss<REST>(A, L, r, row, s.n, s.all, s.rest);
         __syncthreads();   // the next part uses the same LDS
     }
 }

@@ -116,18 +116,20 @@ def distill_row(z, ids, t, tau, teacher_lse=None, grad_loss=None):
         log_p = tk - (_lse(tk) if teacher_lse is None else teacher_lse)
         p = np.exp(log_p)
         lse = _lse(z)
-        loss = sum(p[i] * (log_p[i] - (z[j] - lse)) for i, (j, _) in enumerate(here) if p[i] != 0)
-        q = np.exp(z - lse)
+        z0 = z - np.max(z)            # log q keeps its digits where z is as large as a type's lowest value
+        log_q = z0 - _lse(z0)
+        loss = sum(p[i] * (log_p[i] - log_q[j]) for i, (j, _) in enumerate(here) if p[i] != 0)
+        q = np.exp(log_q)
         dz = q.copy()
         rest_lse, p_rest = 0.0, 0.0
         if teacher_lse is not None:
             outside = np.ones(v, bool)
             outside[[j for j, _ in here]] = False
-            rest_lse = _lse(z[outside])
+            rest_lse, log_q_rest = _lse(z[outside]), _lse(log_q[outside])
             p_rest = max(0.0, 1.0 - p.sum()) if outside.any() else 0.0
             if p_rest > 0:
-                loss += p_rest * (np.log(p_rest) - (rest_lse - lse))
-                dz[outside] *= 1.0 - p_rest * np.exp(lse - rest_lse)
+                loss += p_rest * (np.log(p_rest) - log_q_rest)
+                dz[outside] = (np.exp(log_q_rest) - p_rest) * np.exp(log_q[outside] - log_q_rest)
         for i, (j, _) in enumerate(here):
             dz[j] -= p[i]
         g = 1.0 if grad_loss is None else grad_loss

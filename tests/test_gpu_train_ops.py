@@ -490,6 +490,7 @@ def _check_distill(c, got, rows=None):
         w = ops.distill_row(c["z64"][i], c["ids"][i], c["t64"][i], tau, tl, c["g64"][i])
         g = c["g64"][i]
         got_z = _f64(dz[i])
+        w["dlogits"][np.abs(w["dlogits"]) < 2.0 ** -126] = 0.0   # neither type holds it as a normal number
         if not w["some"]:
             assert loss[i] == 0 and lse[i] == 0 and not got_z.any()
             continue
@@ -570,6 +571,46 @@ def test_distill_many_rows(dtype, n, v, k, kind, rest, form):
     rng = np.random.default_rng([n, v, k])
     c = _distill_case(rng, n, v, k, dtype, "f32", rest, 2.0, kind)
     _check_distill(c, _distill_run(c, form), rows=sorted(set(rng.integers(0, n, 5)) | {0, 1, 3, n - 1}))
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype,v", [("bf16", 3001), ("f32", 20002)])
+def test_distill_rows_far_from_their_pairs(dtype, v, rest):
+    """Rows whose sum does not fit relative to their pairs' largest logit: others far above it, all others far below
+    it, masked by infinity or by the lowest value; next to ordinary rows."""
+    log(f"distill far rows {dtype} {v} {rest}")
+    rng = np.random.default_rng([v, rest])
+    c = _distill_case(rng, 270, v, 6, dtype, rest=rest, tau=1.0)
+    z = c["z64"].copy()
+    top = np.zeros(z.shape, bool)
+    np.put_along_axis(top, c["ids"], True, 1)
+    z[0] += np.where(top[0], 0.0, 200.0)
+    z[1] -= np.where(top[1], 0.0, 300.0)
+    z[2] = np.where(top[2], z[2], -np.inf)
+    z[2, np.flatnonzero(~top[2])[0]] = 1.0
+    z[3] = np.where(top[3], -500.0, z[3])
+    low = -3.3895313892515355e38
+    z[4] = np.where(top[4], z[4], low)
+    z[4, np.flatnonzero(~top[4])[5]] = -1.0
+    z[5] += 1000.0
+    z[6] -= 3.0e4
+    z[7] = low
+    bits = f32_to_bf16_bits(z.astype(np.float32)) if dtype == "bf16" else z.astype(np.float32)
+    c["z64"], c["z"] = host_to_f64(bits, dtype), to_device(bits, dtype)
+    c["g"][8] *= -1
+    c["g64"][8] *= -1
+    c["g"][9], c["g64"][9] = 0, 0
+    for form in ("train", "step"):
+        got = _distill_run(c, form)
+        g = c["g64"]
+        _check_distill(dict(c, g64=np.abs(g)), got[:3] + (_signed(got[3], g),),
+                       rows=[r for r in range(12) if r != 9])
+        assert not got[3][9].float().abs().any()
+
+
+def _signed(dz, g):
+    import torch
+    return dz * torch.from_numpy(np.where(g < 0, -1.0, 1.0)).to(dz)[:, None]
 
 
 def test_distill_same_bits():
