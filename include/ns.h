@@ -453,7 +453,7 @@ typedef struct ns_heads {
  *              sequence b is at pos[b * pos_batch_stride + s]; NULL: s itself.
  *              A position outside [0, table_rows) turns its rotated values
  *              into NaN.
- * batch * seq * (q heads + k heads) < 2^31. One launch.
+ * batch * seq < 2^31, at most 1024 heads each. One launch.
  * Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
 ns_status ns_qk_norm_rope(int64_t batch, int64_t seq, int32_t head_dim, ns_dtype dtype, const ns_heads *q,
                           const ns_heads *k, const void *q_weight, const void *k_weight,

@@ -20,6 +20,7 @@
 //
 // Bound by memory: each input is read once and each output written once.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "op_util.h"
@@ -30,9 +31,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxHeadDim = 1024;
-constexpr int64_t kMaxGrid = 1 << 20;
-// Backward: partial sums of the weights' gradients, one row of 2 D values per workgroup.
-constexpr int kMaxPartials = 1024;
+constexpr int kMaxHeads = 1024;
+// Workgroups of a launch, for pieces of 8, 4 and 1 elements: as many as are
+// resident at once by the kernels' registers, so that a wave keeps its weights
+// and its place in a head over all its tokens. 16384 tokens of 32 + 8 bf16 heads
+// of 128, forward: 1024 workgroups 66 us, 1280 (a second, partial round) 77, a
+// wave for each token 81. Backward: 512 104 us, 768 106, 1024 118.
+constexpr int blocks_for(int vec, bool backward) {
+    return backward ? (vec == 4 ? 1024 : 512) : (vec == 8 ? 1024 : vec == 4 ? 2048 : 768);
+}
+constexpr int kMostPartials = 1024;
+// Outputs of calls that move more than the last-level cache holds are stored
+// past it: 66 us become 63 in the case above, 104 become 102. Smaller ones stay in
+// it for the kernel that reads them next (35 us against 43 for 45 MB each way).
+constexpr int64_t kMallBytes = 256ll << 20;
 
 struct HeadSet {
     char *x, *g, *y;                 // input, gradient of the output (backward), output
@@ -40,14 +52,15 @@ struct HeadSet {
     int64_t gb, gt, gh;
     int64_t yb, yt, yh;
     const void *w;
-    int32_t heads, chunks;           // chunks of (64 / G) U heads
+    int32_t heads, chunks;           // chunks of 64 / G heads
+    int32_t blocks, stride;          // workgroups of the set, tokens taken at once
     float *dw;
 };
 
 struct HeadArgs {
-    HeadSet s[2];                    // queries, keys
-    int64_t batch, seq, tokens;
-    int32_t D, R, P, RP;             // head size, rotated part, pieces pairs per head, rotated ones
+    HeadSet s[2];                    // queries, keys: the first s[0].blocks workgroups, the others
+    uint32_t seq, tokens;            // tokens = batch x seq
+    int32_t D, R, P, RP;             // head size, rotated part, pairs of pieces per head, rotated ones
     int32_t lg;                      // log2 G
     int32_t interleaved, w_f32;
     float eps;
@@ -56,7 +69,7 @@ struct HeadArgs {
     const void *pos;
     int32_t pos_bytes;
     int64_t pos_bs;
-    float *partial;                  // backward: [gridDim.x][2][D]
+    float *partial;                  // backward: [workgroups][D]
 };
 
 // VEC elements at any element alignment, as one or two loads or stores.
@@ -64,34 +77,31 @@ template <typename T, int VEC> struct Piece {
     typedef typename std::conditional<sizeof(T) == 2, uint16_t, float>::type E;
     typedef E raw __attribute__((ext_vector_type(VEC)));
     typedef raw __attribute__((aligned(sizeof(T)))) raw_u;
-    static __device__ inline void load(const T *p, float (&v)[VEC]) {
-        if constexpr (VEC == 1) {
-            v[0] = (float)p[0];
-        } else {
-            const raw r = *reinterpret_cast<const raw_u *>(p);
+    static __device__ inline raw load(const T *p) {
+        if constexpr (VEC == 1) return raw{*reinterpret_cast<const E *>(p)};
+        else return *reinterpret_cast<const raw_u *>(p);
+    }
+    static __device__ inline void widen(raw r, float (&v)[VEC]) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                if constexpr (sizeof(T) == 2) v[i] = __builtin_bit_cast(float, (uint32_t)r[i] << 16);
-                else v[i] = r[i];
-            }
+        for (int i = 0; i < VEC; ++i) {
+            if constexpr (sizeof(T) == 2) v[i] = __builtin_bit_cast(float, (uint32_t)r[i] << 16);
+            else v[i] = r[i];
         }
     }
-    static __device__ inline void store(T *p, const float (&v)[VEC]) {
-        if constexpr (VEC == 1) {
-            p[0] = (T)v[0];
-        } else {
-            raw r;
+    template <bool NT> static __device__ inline void store(T *p, const float (&v)[VEC]) {
+        raw r;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                if constexpr (sizeof(T) == 2) r[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
-                else r[i] = v[i];
-            }
-            *reinterpret_cast<raw_u *>(p) = r;
+        for (int i = 0; i < VEC; ++i) {
+            if constexpr (sizeof(T) == 2) r[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+            else r[i] = v[i];
         }
+        if constexpr (VEC == 1) *reinterpret_cast<E *>(p) = r[0];
+        else if constexpr (NT) __builtin_nontemporal_store(r, reinterpret_cast<raw_u *>(p));
+        else *reinterpret_cast<raw_u *>(p) = r;
     }
 };
 
-// A lane's two pieces of a head: element offsets a and b, and their angles' table offset.
+// A lane's two pieces of a head: element offsets a and b, and their angles' place in a table row.
 struct Place {
     int a, b, angle;
     bool in, has_b, turned;
@@ -111,42 +121,70 @@ __device__ inline Place place_of(const HeadArgs &A, int i) {
         p.b = p.a + VEC;
     }
     p.has_b = p.in && p.b < A.D;   // VEC = 1: an odd unrotated tail has no partner
+    // lanes without a piece read the head's first one, so that loads need no branch
+    if (!p.in) p.a = 0;
+    if (!p.has_b) p.b = p.a;
     return p;
 }
 
 template <int VEC>
-__device__ inline void load_weight(const HeadArgs &A, const HeadSet &S, const Place &p, float (&wa)[VEC],
-                                   float (&wb)[VEC]) {
+__device__ inline void load_weight(const HeadArgs &A, const void *w, const Place &p, float (&wa)[VEC], float (&wb)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) wa[i] = wb[i] = 1.f;
-    if (!S.w || !p.in) return;
+    if (!w) return;
     if (A.w_f32) {
-        Piece<float, VEC>::load(reinterpret_cast<const float *>(S.w) + p.a, wa);
-        if (p.has_b) Piece<float, VEC>::load(reinterpret_cast<const float *>(S.w) + p.b, wb);
+        Piece<float, VEC>::widen(Piece<float, VEC>::load(reinterpret_cast<const float *>(w) + p.a), wa);
+        Piece<float, VEC>::widen(Piece<float, VEC>::load(reinterpret_cast<const float *>(w) + p.b), wb);
     } else {
-        Piece<__bf16, VEC>::load(reinterpret_cast<const __bf16 *>(S.w) + p.a, wa);
-        if (p.has_b) Piece<__bf16, VEC>::load(reinterpret_cast<const __bf16 *>(S.w) + p.b, wb);
+        Piece<__bf16, VEC>::widen(Piece<__bf16, VEC>::load(reinterpret_cast<const __bf16 *>(w) + p.a), wa);
+        Piece<__bf16, VEC>::widen(Piece<__bf16, VEC>::load(reinterpret_cast<const __bf16 *>(w) + p.b), wb);
     }
 }
 
-// cos and sin of the token's angles; NaN for a position outside the table.
-template <int VEC>
-__device__ inline void load_angles(const HeadArgs &A, int64_t b, int64_t s, const Place &p, float (&c)[VEC],
-                                   float (&sn)[VEC]) {
-    if (!p.turned) return;
-    int64_t at = s;
-    if (A.pos)
-        at = A.pos_bytes == 8 ? reinterpret_cast<const int64_t *>(A.pos)[b * A.pos_bs + s]
-                              : (int64_t) reinterpret_cast<const int32_t *>(A.pos)[b * A.pos_bs + s];
-    if (at < 0 || at >= A.table_rows) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) c[i] = sn[i] = __builtin_nanf("");
-        return;
-    }
-    const int64_t o = at * (A.R / 2) + p.angle;
-    Piece<float, VEC>::load(A.cos + o, c);
-    Piece<float, VEC>::load(A.sin + o, sn);
+// The token's position (read through the scalar cache: no kernel writes it).
+#define NSQ_CONST __attribute__((address_space(4)))
+__device__ inline int64_t position(const HeadArgs &A, uint32_t token) {
+    const uint32_t b = token / A.seq, s = token - b * A.seq;
+    if (!A.pos) return s;
+    const int64_t at = b * A.pos_bs + s;
+    if (A.pos_bytes == 8) return *(const int64_t NSQ_CONST *)(reinterpret_cast<const int64_t *>(A.pos) + at);
+    return *(const int32_t NSQ_CONST *)(reinterpret_cast<const int32_t *>(A.pos) + at);
 }
+
+// cos and sin of a position's angles: from a descriptor of one table row, of length
+// zero for a position outside the table; such a row's values are then set to NaN.
+template <int VEC, int NP> struct Angles {
+    float c[NP][VEC], s[NP][VEC];
+    __device__ inline void load(const HeadArgs &A, int64_t at, const Place (&pl)[NP]) {
+        const bool in = at >= 0 && at < A.table_rows;
+        const int64_t row = in ? at * (A.R / 2) : 0;
+        const auto rc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(A.cos + row), (short)0, in ? A.R * 2 : 0, 0x00020000);
+        const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(A.sin + row), (short)0, in ? A.R * 2 : 0, 0x00020000);
+        typedef float f4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            if constexpr (VEC == 1) {
+                c[n][0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rc, pl[n].angle * 4, 0, 0));
+                s[n][0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, pl[n].angle * 4, 0, 0));
+            } else {
+#pragma unroll
+                for (int q = 0; q < VEC / 4; ++q) {
+                    const f4 x = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rc, pl[n].angle * 4 + 16 * q, 0, 0));
+                    const f4 y = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rs, pl[n].angle * 4 + 16 * q, 0, 0));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[n][4 * q + i] = x[i], s[n][4 * q + i] = y[i];
+                }
+            }
+        }
+    }
+    __device__ inline void check(const HeadArgs &A, int64_t at) {
+        if (at >= 0 && at < A.table_rows) return;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) c[n][i] = s[n][i] = __builtin_nanf("");
+    }
+};
 
 // Turns the pieces a, b by the angles (dir = 1) or back (dir = -1).
 template <int VEC>
@@ -177,177 +215,201 @@ __device__ inline float group_sum(float v, int lg) {
     return v;
 }
 
-// One item: the heads [h0, h0 + (64 / G) U) of one set at one token. BWD: the
-// gradient; dwa / dwb collect the lane's pieces of dw.
-template <typename T, int VEC, int NP, int U, bool BWD>
-__device__ inline void head_item(const HeadArgs &A, const HeadSet &S, uint32_t token, int h0, const Place (&pl)[NP],
-                                 const float (&wa)[NP][VEC], const float (&wb)[NP][VEC], float (&dwa)[NP][VEC],
-                                 float (&dwb)[NP][VEC]) {
-    const int lane = threadIdx.x & 63;
-    const int per = 64 >> A.lg, sub = lane >> A.lg;
-    const uint32_t bi = token / (uint32_t)A.seq, si = token - bi * (uint32_t)A.seq;
-    const T *x = reinterpret_cast<const T *>(S.x) + bi * S.xb + si * S.xt;
-    const T *g = BWD ? reinterpret_cast<const T *>(S.g) + bi * S.gb + si * S.gt : nullptr;
-    T *y = reinterpret_cast<T *>(S.y) + bi * S.yb + si * S.yt;
-    float c[NP][VEC], sn[NP][VEC];
+// One (batch, seq, heads, head_dim) operand as a lane sees it: its head's offset is the same at every token.
+struct Walk {
+    char *p;
+    int64_t b, t;
+    template <typename T> __device__ inline T *at(const HeadArgs &A, uint32_t token) const {
+        const uint32_t i = token / A.seq, s = token - i * A.seq;
+        return reinterpret_cast<T *>(p) + (i * b + s * t);
+    }
+};
+
+// Forward, or with BWD the gradient. A wave holds chunk w % chunks of its set's
+// heads and takes the tokens w / chunks, + stride, ...; the next token's values
+// and angles are on their way while it computes. Lanes without a head or a piece
+// load another's and store nothing.
+template <typename T, int VEC, int NP, bool BWD, bool NT>
+__global__ __launch_bounds__(kThreads) void qk_kernel(HeadArgs A) {
+    typedef Piece<T, VEC> PT;
+    typedef typename PT::raw raw;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool key = (int)blockIdx.x >= A.s[0].blocks;
+    const HeadSet S = key ? A.s[1] : A.s[0];
+    const uint32_t w = (blockIdx.x - (key ? A.s[0].blocks : 0)) * kWaves + wave;
+    const uint32_t first = w / (uint32_t)S.chunks, chunk = w - first * S.chunks;
+    const int head = (int)chunk * (64 >> A.lg) + (lane >> A.lg);
+    const bool here = head < S.heads;
+    const int64_t h = here ? head : 0;
+    Place pl[NP];
+    float wa[NP][VEC], wb[NP][VEC], dwa[NP][VEC], dwb[NP][VEC];
 #pragma unroll
-    for (int n = 0; n < NP; ++n) load_angles<VEC>(A, bi, si, pl[n], c[n], sn[n]);
-    float va[U][NP][VEC], vb[U][NP][VEC], ga[U][NP][VEC], gb[U][NP][VEC];
+    for (int n = 0; n < NP; ++n) {
+        pl[n] = place_of<VEC>(A, (lane & ((1 << A.lg) - 1)) + (n << A.lg));
+        load_weight<VEC>(A, S.w, pl[n], wa[n], wb[n]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * per + sub;
+        for (int i = 0; i < VEC; ++i) dwa[n][i] = dwb[n][i] = 0.f;
+    }
+    const Walk X = {S.x, S.xb, S.xt}, G = {S.g, S.gb, S.gt}, Y = {S.y, S.yb, S.yt};
+    const float inv_d = 1.f / (float)A.D;
+    raw xa[NP], xb[NP], ga[NP], gb[NP];
+    Angles<VEC, NP> ang;
+    const auto load = [&](uint32_t token) {
+        const T *x = X.at<T>(A, token) + h * S.xh;
+        const T *g = BWD ? G.at<T>(A, token) + h * S.gh : nullptr;
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) va[u][n][i] = vb[u][n][i] = ga[u][n][i] = gb[u][n][i] = 0.f;
-            if (h < S.heads && pl[n].in) {
-                Piece<T, VEC>::load(x + h * S.xh + pl[n].a, va[u][n]);
-                if (pl[n].has_b) Piece<T, VEC>::load(x + h * S.xh + pl[n].b, vb[u][n]);
-                if constexpr (BWD) {
-                    Piece<T, VEC>::load(g + h * S.gh + pl[n].a, ga[u][n]);
-                    if (pl[n].has_b) Piece<T, VEC>::load(g + h * S.gh + pl[n].b, gb[u][n]);
-                }
+            xa[n] = PT::load(x + pl[n].a);
+            xb[n] = PT::load(x + pl[n].b);
+            if constexpr (BWD) {
+                ga[n] = PT::load(g + pl[n].a);
+                gb[n] = PT::load(g + pl[n].b);
             }
         }
+    };
+    // waves past the last whole round of chunks have no tokens
+    const uint32_t stride = S.stride, begin = first < stride ? first : A.tokens;
+    int64_t pos = 0, pos_next = 0;
+    if (begin < A.tokens) {
+        pos = position(A, begin);
+        load(begin);
+        ang.load(A, pos, pl);
+        pos_next = position(A, begin + stride < A.tokens ? begin + stride : begin);
     }
-    const float inv_d = 1.f / (float)A.D;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * per + sub;
+    for (uint32_t t = begin; t < A.tokens; t += stride) {
+        float va[NP][VEC], vb[NP][VEC], da[NP][VEC], db[NP][VEC];
+        Angles<VEC, NP> now = ang;
+        now.check(A, pos);
         float ss = 0.f, sd = 0.f;
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            if constexpr (BWD)
-                if (pl[n].turned) turn<VEC>(A.interleaved, -1.f, ga[u][n], gb[u][n], c[n], sn[n]);
+            PT::widen(xa[n], va[n]);
+            PT::widen(xb[n], vb[n]);
+            if constexpr (BWD) {
+                PT::widen(ga[n], da[n]);
+                PT::widen(gb[n], db[n]);
+            }
+        }
+        // tokens < 2^31 and stride < 2^31: no wrap
+        const uint32_t next = t + stride < A.tokens ? t + stride : t;
+        const uint32_t after = next + stride < A.tokens ? next + stride : next;
+        load(next);
+        ang.load(A, pos_next, pl);
+        pos = pos_next;
+        pos_next = position(A, after);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                ss += va[u][n][i] * va[u][n][i] + vb[u][n][i] * vb[u][n][i];
-                if constexpr (BWD)
-                    sd += ga[u][n][i] * wa[n][i] * va[u][n][i] + gb[u][n][i] * wb[n][i] * vb[u][n][i];
+                if (!pl[n].in) va[n][i] = 0.f;
+                if (!pl[n].has_b) vb[n][i] = 0.f;
+            }
+            if constexpr (BWD) {
+                if (pl[n].turned) turn<VEC>(A.interleaved, -1.f, da[n], db[n], now.c[n], now.s[n]);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    if (!pl[n].in) da[n][i] = 0.f;
+                    if (!pl[n].has_b) db[n][i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                ss += va[n][i] * va[n][i] + vb[n][i] * vb[n][i];
+                if constexpr (BWD) sd += da[n][i] * wa[n][i] * va[n][i] + db[n][i] * wb[n][i] * vb[n][i];
             }
         }
         ss = group_sum(ss, A.lg);
         const float r = 1.f / sqrtf(ss * inv_d + A.eps);
         float m = 0.f;
         if constexpr (BWD) m = group_sum(sd, A.lg) * r * inv_d;   // mean(dn n)
+        T *y = Y.at<T>(A, t) + h * S.yh;
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            if constexpr (BWD) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float na = va[u][n][i] * r, nb = vb[u][n][i] * r;
-                    if (h < S.heads) {
-                        dwa[n][i] += ga[u][n][i] * na;
-                        dwb[n][i] += gb[u][n][i] * nb;
-                    }
-                    va[u][n][i] = r * (ga[u][n][i] * wa[n][i] - na * m);
-                    vb[u][n][i] = r * (gb[u][n][i] * wb[n][i] - nb * m);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    va[u][n][i] = va[u][n][i] * r * wa[n][i];
-                    vb[u][n][i] = vb[u][n][i] * r * wb[n][i];
-                }
-                if (pl[n].turned) turn<VEC>(A.interleaved, 1.f, va[u][n], vb[u][n], c[n], sn[n]);
-            }
-            if (h < S.heads && pl[n].in) {
-                Piece<T, VEC>::store(y + h * S.yh + pl[n].a, va[u][n]);
-                if (pl[n].has_b) Piece<T, VEC>::store(y + h * S.yh + pl[n].b, vb[u][n]);
-            }
-        }
-    }
-}
-
-// Items are (token, chunk of heads), a wave each: the query chunks of a token,
-// then its key chunks, then the next token's.
-template <typename T, int VEC, int NP, int U>
-__global__ __launch_bounds__(kThreads) void qk_forward_kernel(HeadArgs A) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t chunks = A.s[0].chunks + A.s[1].chunks;
-    const uint32_t items = (uint32_t)A.tokens * chunks;   // < 2^31
-    Place pl[NP];
-#pragma unroll
-    for (int n = 0; n < NP; ++n) pl[n] = place_of<VEC>(A, (lane & ((1 << A.lg) - 1)) + (n << A.lg));
-    float none[NP][VEC];
-    for (uint32_t it = blockIdx.x * kWaves + wave; it < items; it += gridDim.x * kWaves) {
-        const uint32_t token = it / chunks;
-        const int ch = (int)(it - token * chunks);
-        const bool key = ch >= A.s[0].chunks;
-        const HeadSet S = key ? A.s[1] : A.s[0];
-        float wa[NP][VEC], wb[NP][VEC];
-#pragma unroll
-        for (int n = 0; n < NP; ++n) load_weight<VEC>(A, S, pl[n], wa[n], wb[n]);
-        head_item<T, VEC, NP, U, false>(A, S, token, (key ? ch - A.s[0].chunks : ch) * ((64 >> A.lg) * U), pl, wa, wb,
-                                        none, none);
-    }
-}
-
-// blockIdx.y: 0 queries, 1 keys. Each workgroup sums its part of dw in
-// registers, joins its waves in a fixed order and writes one row of partials.
-template <typename T, int VEC, int NP, int U>
-__global__ __launch_bounds__(kThreads) void qk_backward_kernel(HeadArgs A) {
-    __shared__ float lds[kWaves][2 * VEC * NP * 64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const HeadSet S = blockIdx.y ? A.s[1] : A.s[0];
-    const uint32_t items = (uint32_t)A.tokens * S.chunks;   // < 2^31
-    Place pl[NP];
-    float wa[NP][VEC], wb[NP][VEC], dwa[NP][VEC], dwb[NP][VEC];
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        pl[n] = place_of<VEC>(A, (lane & ((1 << A.lg) - 1)) + (n << A.lg));
-        load_weight<VEC>(A, S, pl[n], wa[n], wb[n]);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dwa[n][i] = dwb[n][i] = 0.f;
-    }
-    for (uint32_t it = blockIdx.x * kWaves + wave; it < items; it += gridDim.x * kWaves) {
-        const uint32_t token = it / S.chunks;
-        head_item<T, VEC, NP, U, true>(A, S, token, (int)(it - token * S.chunks) * ((64 >> A.lg) * U), pl, wa, wb, dwa,
-                                       dwb);
-    }
-    if (!S.dw) return;
-    // join the wave's head groups, then the waves
-#pragma unroll
-    for (int n = 0; n < NP; ++n)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            for (int m = 1 << A.lg; m < 64; m <<= 1) {
-                dwa[n][i] += __shfl_xor(dwa[n][i], m);
-                dwb[n][i] += __shfl_xor(dwb[n][i], m);
-            }
-            lds[wave][((n * VEC + i) * 2) * 64 + lane] = dwa[n][i];
-            lds[wave][((n * VEC + i) * 2 + 1) * 64 + lane] = dwb[n][i];
-        }
-    __syncthreads();
-    if (wave == 0 && lane < 1 << A.lg) {
-        float *row = A.partial + ((int64_t)blockIdx.x * 2 + blockIdx.y) * A.D;
-#pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            if (!pl[n].in) continue;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                float a = 0.f, b = 0.f;
-                for (int w = 0; w < kWaves; ++w) {
-                    a += lds[w][((n * VEC + i) * 2) * 64 + lane];
-                    b += lds[w][((n * VEC + i) * 2 + 1) * 64 + lane];
+                const float na = va[n][i] * r, nb = vb[n][i] * r;
+                if constexpr (BWD) {
+                    if (here) {
+                        dwa[n][i] += da[n][i] * na;
+                        dwb[n][i] += db[n][i] * nb;
+                    }
+                    va[n][i] = r * (da[n][i] * wa[n][i] - na * m);
+                    vb[n][i] = r * (db[n][i] * wb[n][i] - nb * m);
+                } else {
+                    va[n][i] = na * wa[n][i];
+                    vb[n][i] = nb * wb[n][i];
                 }
-                row[pl[n].a + i] = a;
-                if (pl[n].has_b) row[pl[n].b + i] = b;
+            }
+            if constexpr (!BWD)
+                if (pl[n].turned) turn<VEC>(A.interleaved, 1.f, va[n], vb[n], now.c[n], now.s[n]);
+            if (here && pl[n].in) {
+                PT::template store<NT>(y + pl[n].a, va[n]);
+                if (pl[n].has_b) PT::template store<NT>(y + pl[n].b, vb[n]);
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if (!S.dw) return;
+        // the workgroup's part of dw: its waves' head groups, then its waves, in a fixed order
+        __shared__ float lds[kWaves][2 * VEC * NP * 64];
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                for (int m = 1 << A.lg; m < 64; m <<= 1) {
+                    dwa[n][i] += __shfl_xor(dwa[n][i], m);
+                    dwb[n][i] += __shfl_xor(dwb[n][i], m);
+                }
+                lds[wave][((n * VEC + i) * 2) * 64 + lane] = dwa[n][i];
+                lds[wave][((n * VEC + i) * 2 + 1) * 64 + lane] = dwb[n][i];
+            }
+        __syncthreads();
+        if (wave == 0 && lane < 1 << A.lg) {
+            float *row = A.partial + (int64_t)blockIdx.x * A.D;
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                if (!pl[n].in) continue;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    float a = 0.f, b = 0.f;
+                    for (int v = 0; v < kWaves; ++v) {
+                        a += lds[v][((n * VEC + i) * 2) * 64 + lane];
+                        b += lds[v][((n * VEC + i) * 2 + 1) * 64 + lane];
+                    }
+                    row[pl[n].a + i] = a;
+                    if (pl[n].has_b) row[pl[n].b + i] = b;
+                }
             }
         }
     }
 }
 
-// dw[j] = sum of the workgroups' partials: one wave per 4 values (16 bytes a
-// row at most), 16 lanes down the rows each, joined in a fixed order.
-__global__ __launch_bounds__(64) void qk_join_kernel(HeadArgs A, int32_t rows) {
-    const int j = blockIdx.x * 4 + (threadIdx.x & 3), k = blockIdx.y;
-    if (!A.s[k].dw) return;
+// dw[j] = sum of the workgroups' partials: 16 values a workgroup, 64 threads
+// down the rows of each, joined in a fixed order.
+constexpr int kJoinCols = 16, kJoinRows = 64;
+__global__ __launch_bounds__(kJoinCols * kJoinRows) void qk_join_kernel(HeadArgs A) {
+    __shared__ float part[kJoinRows / 4][kJoinCols];
+    const int col = threadIdx.x % kJoinCols, down = threadIdx.x / kJoinCols;
+    const int j = blockIdx.x * kJoinCols + col;
+    const bool key = blockIdx.y;
+    float *dw = key ? A.s[1].dw : A.s[0].dw;
+    if (!dw) return;
+    const float *partial = A.partial + (key ? (int64_t)A.s[0].blocks * A.D : 0);
+    const int rows = key ? A.s[1].blocks : A.s[0].blocks;
     float sum = 0.f;
-    if (j < A.D)
-        for (int r = threadIdx.x >> 2; r < rows; r += 16) sum += A.partial[((int64_t)r * 2 + k) * A.D + j];
-    for (int m = 4; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-    if (threadIdx.x < 4 && j < A.D) A.s[k].dw[j] = sum;
+    if (j < A.D) {
+#pragma unroll 8
+        for (int r = down; r < rows; r += kJoinRows) sum += partial[(int64_t)r * A.D + j];
+    }
+    sum += __shfl_xor(sum, 16);   // a wave holds four rows of the 16 values
+    sum += __shfl_xor(sum, 32);
+    if ((threadIdx.x & 63) < kJoinCols) part[threadIdx.x >> 6][col] = sum;
+    __syncthreads();
+    if (threadIdx.x < kJoinCols && j < A.D) {
+        sum = 0.f;
+        for (int i = 0; i < kJoinRows / 4; ++i) sum += part[i][col];
+        dw[j] = sum;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -359,6 +421,7 @@ ns_status check_heads(const char *name, const ns_heads *h, int64_t batch, int64_
                       int32_t want_heads) {
     if (!h) return fail(NS_ERR_INVALID_ARG, "%s is NULL", name);
     if (h->heads < 0) return fail(NS_ERR_INVALID_ARG, "%s: heads = %d < 0", name, h->heads);
+    if (h->heads > kMaxHeads) return fail(NS_ERR_OVERFLOW, "%s: more than %d heads", name, kMaxHeads);
     if (want_heads >= 0 && h->heads != want_heads)
         return fail(NS_ERR_INVALID_ARG, "%s has %d heads, not %d", name, h->heads, want_heads);
     if (h->heads == 0 || batch == 0 || seq == 0) return NS_OK;
@@ -377,6 +440,7 @@ ns_status check_heads(const char *name, const ns_heads *h, int64_t batch, int64_
 struct HeadCall {
     HeadArgs a;
     int vec;       // elements of a piece: 8, 4 or 1
+    bool past_cache;
     int es;
 };
 
@@ -398,9 +462,6 @@ ns_status plan_heads(int64_t batch, int64_t seq, int32_t head_dim, int32_t dtype
     if (interleaved != 0 && interleaved != 1) return fail(NS_ERR_INVALID_ARG, "interleaved must be 0 or 1");
     if (ns_status s = check_heads("q", q, batch, seq, head_dim, c->es, -1)) return s;
     if (ns_status s = check_heads("k", k, batch, seq, head_dim, c->es, -1)) return s;
-    // Work items are (token, chunk of heads), at most one a head, counted in 31 bits.
-    if (batch * seq * ((double)q->heads + k->heads) >= 2147483648.0)
-        return fail(NS_ERR_OVERFLOW, "batch x seq x heads does not fit in 31 bits");
     if (misaligned(q_weight, dtype_bytes(weight_dtype)) || misaligned(k_weight, dtype_bytes(weight_dtype)))
         return fail(NS_ERR_INVALID_ARG, "weights not aligned to their type");
     if (rope_dim > 0) {
@@ -417,9 +478,8 @@ ns_status plan_heads(int64_t batch, int64_t seq, int32_t head_dim, int32_t dtype
     }
     HeadArgs &a = c->a;
     a = HeadArgs{};
-    a.batch = batch;
-    a.seq = seq;
-    a.tokens = batch * seq;
+    a.seq = (uint32_t)seq;
+    a.tokens = (uint32_t)(batch * seq);
     a.D = head_dim;
     a.R = rope_dim;
     a.interleaved = interleaved;
@@ -460,9 +520,43 @@ void set_out(HeadSet &s, const ns_heads *o) {
     s.yh = o->head_stride;
 }
 
-void set_chunks(HeadArgs &a, int U) {
-    const int per = (64 >> a.lg) * U;
-    for (HeadSet &s : a.s) s.chunks = (s.heads + per - 1) / per;
+// Deals the workgroups to the two sets by their work: a wave for each (token,
+// chunk of heads), or several of one chunk's tokens a wave.
+void deal(HeadCall &c, bool backward) {
+    HeadArgs &a = c.a;
+    const int64_t most = blocks_for(c.vec, backward);
+    const int64_t moved = (int64_t)a.tokens * (a.s[0].heads + a.s[1].heads) * a.D * c.es * (backward ? 3 : 2);
+    c.past_cache = moved > kMallBytes;
+    int64_t items[2], all = 0;
+    for (int i = 0; i < 2; ++i) {
+        a.s[i].chunks = (a.s[i].heads + (64 >> a.lg) - 1) >> (6 - a.lg);
+        items[i] = (int64_t)a.tokens * a.s[i].chunks;
+        all += items[i];
+    }
+    for (int i = 0; i < 2; ++i) {
+        HeadSet &s = a.s[i];
+        const int64_t full = (items[i] + kWaves - 1) / kWaves, least = (s.chunks + kWaves - 1) / kWaves;
+        int64_t blocks = full;
+        if ((all + kWaves - 1) / kWaves > most) blocks = std::max(least, (int64_t)((double)most * items[i] / all));
+        s.blocks = (int32_t)(items[i] ? std::max<int64_t>(1, std::min(blocks, full)) : 0);
+        s.stride = s.chunks ? (int32_t)std::max<int64_t>(1, (int64_t)s.blocks * kWaves / s.chunks) : 1;
+    }
+}
+
+template <bool BWD> ns_status launch(const HeadCall &c, int32_t dtype, void *stream) {
+    const int32_t blocks = c.a.s[0].blocks + c.a.s[1].blocks;
+    if (!blocks) return NS_OK;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kThreads), 0, as_stream(stream), c.a); };
+    auto pick = [&](auto t) {
+        typedef decltype(t) T;
+        if (c.vec == 8) c.past_cache ? go(qk_kernel<T, 8, 1, BWD, true>) : go(qk_kernel<T, 8, 1, BWD, false>);
+        else if (c.vec == 4) go(qk_kernel<T, 4, 1, BWD, false>);
+        else go(qk_kernel<T, 1, 8, BWD, false>);
+    };
+    if (dtype == NS_BF16) pick((__bf16)0.f);
+    else pick(0.f);
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
 }
 
 }  // namespace
@@ -484,23 +578,8 @@ extern "C" ns_status ns_qk_norm_rope(int64_t batch, int64_t seq, int32_t head_di
     if (ns_status s = check_heads("k_out", k_out, batch, seq, head_dim, c.es, k->heads)) return s;
     set_out(c.a.s[0], q_out);
     set_out(c.a.s[1], k_out);
-    if (c.a.tokens == 0 || q->heads + k->heads == 0) return NS_OK;
-    constexpr int U = 1;
-    set_chunks(c.a, U);
-    const int64_t items = c.a.tokens * (c.a.s[0].chunks + c.a.s[1].chunks);
-    const int64_t blocks = (items + kWaves - 1) / kWaves;
-    const dim3 grid((unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid));
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, as_stream(stream), c.a); };
-    auto pick = [&](auto t) {
-        typedef decltype(t) T;
-        if (c.vec == 8) go(qk_forward_kernel<T, 8, 1, U>);
-        else if (c.vec == 4) go(qk_forward_kernel<T, 4, 1, U>);
-        else go(qk_forward_kernel<T, 1, 8, U>);
-    };
-    if (dtype == NS_BF16) pick((__bf16)0.f);
-    else pick(0.f);
-    NSQ_HIP(hipGetLastError());
-    return NS_OK;
+    deal(c, false);
+    return launch<false>(c, dtype, stream);
 }
 
 extern "C" ns_status ns_qk_norm_rope_workspace_bytes(int64_t batch, int64_t seq, int32_t head_dim, size_t *bytes) {
@@ -510,7 +589,8 @@ extern "C" ns_status ns_qk_norm_rope_workspace_bytes(int64_t batch, int64_t seq,
         return fail(NS_ERR_OVERFLOW, "batch x seq does not fit in 31 bits");
     if (head_dim < 1 || head_dim > kMaxHeadDim)
         return fail(NS_ERR_INVALID_ARG, "head_dim = %d outside [1, %d]", head_dim, kMaxHeadDim);
-    *bytes = (size_t)kMaxPartials * 2 * head_dim * sizeof(float);
+    // One row of partial sums a workgroup. A set takes its share of them, or more if its chunks need it (deal()).
+    *bytes = (size_t)(kMostPartials + 2 * kMaxHeads / kWaves) * head_dim * sizeof(float);
     return NS_OK;
 }
 
@@ -553,29 +633,11 @@ extern "C" ns_status ns_qk_norm_rope_backward(int64_t batch, int64_t seq, int32_
         s.dw = dws[i];
     }
     c.a.partial = reinterpret_cast<float *>(workspace);
-    constexpr int U = 1;
-    set_chunks(c.a, U);
-    // Every workgroup writes its row of both sets' partials, so with no tokens
-    // or heads at all the join sums no rows and writes zeros.
-    const int32_t most = c.a.s[0].chunks > c.a.s[1].chunks ? c.a.s[0].chunks : c.a.s[1].chunks;
-    const int64_t items = c.a.tokens * most;
-    const int64_t blocks = (items + kWaves - 1) / kWaves, cap = weights ? kMaxPartials : kMaxGrid;
-    const int32_t rows = (int32_t)(blocks < cap ? blocks : cap);
-    if (rows > 0) {
-        const dim3 grid(rows, 2);
-        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, as_stream(stream), c.a); };
-        auto pick = [&](auto t) {
-            typedef decltype(t) T;
-            if (c.vec == 8) go(qk_backward_kernel<T, 8, 1, U>);
-            else if (c.vec == 4) go(qk_backward_kernel<T, 4, 1, U>);
-            else go(qk_backward_kernel<T, 1, 8, U>);
-        };
-        if (dtype == NS_BF16) pick((__bf16)0.f);
-        else pick(0.f);
-        NSQ_HIP(hipGetLastError());
-    }
+    deal(c, true);
+    if (ns_status s = launch<true>(c, dtype, stream)) return s;
     if (weights) {
-        hipLaunchKernelGGL(qk_join_kernel, dim3((head_dim + 3) / 4, 2), dim3(64), 0, as_stream(stream), c.a, rows);
+        hipLaunchKernelGGL(qk_join_kernel, dim3((head_dim + kJoinCols - 1) / kJoinCols, 2), dim3(kJoinCols * kJoinRows), 0,
+                           as_stream(stream), c.a);
         NSQ_HIP(hipGetLastError());
     }
     return NS_OK;
