@@ -495,7 +495,7 @@ ns_status ns_qk_norm_rope_backward(int64_t batch, int64_t seq, int32_t head_dim,
  * slot_of_row  [tokens * top_k]: the slot in each row.
  * row_of_slot  [tokens * top_k]: the row of each slot, which the calls below
  *              take (they leave alone an entry that names no row).
- * One launch up to 8192 slots, two above.
+ * One launch up to 2048 slots, two above.
  * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
 ns_status ns_moe_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts, size_t *bytes);
 ns_status ns_moe_sort(int64_t tokens, int32_t top_k, int32_t experts, const void *expert_ids, int32_t id_bytes,

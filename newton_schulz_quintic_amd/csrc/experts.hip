@@ -44,8 +44,11 @@ struct SortArgs {
 
 // The sort key of a slot: its expert, or `experts` if dropped.
 __device__ inline int key_of(const SortArgs &A, uint32_t slot) {
-    const uint32_t t = slot / (uint32_t)A.top_k, k = slot - t * A.top_k;
-    const int64_t at = (int64_t)t * A.ids_ld + k;
+    int64_t at = slot;
+    if (A.ids_ld != A.top_k) {
+        const uint32_t t = slot / (uint32_t)A.top_k;
+        at += (int64_t)t * (A.ids_ld - A.top_k);
+    }
     const int64_t id = A.id_bytes == 8 ? reinterpret_cast<const int64_t *>(A.ids)[at]
                                        : (int64_t) reinterpret_cast<const int32_t *>(A.ids)[at];
     return id < 0 || id >= A.experts ? A.experts : (int)id;
@@ -68,6 +71,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(SortArgs A) {
     __syncthreads();
     const int64_t s0 = (int64_t)blockIdx.x * A.per;
     const int64_t s1 = s0 + A.per < A.slots ? s0 + A.per : A.slots;
+#pragma unroll 4
     for (int64_t s = s0 + threadIdx.x; s < s1; s += kSortThreads) atomicAdd(&cnt[key_of(A, (uint32_t)s)], 1);
     __syncthreads();
     for (int e = threadIdx.x; e <= A.experts; e += kSortThreads)
@@ -92,18 +96,19 @@ __global__ __launch_bounds__(kSortThreads) void moe_rank_kernel(SortArgs A) {
     __syncthreads();
     const int run = A.per / kSortWaves;
     const int64_t w0 = (int64_t)blockIdx.x * A.per + (int64_t)wave * run;
-    for (int i = lane; i < run; i += 64)
-        if (w0 + i < A.slots) atomicAdd(&cnt[wave][key_of(A, (uint32_t)(w0 + i))], 1);
+    const int64_t w1 = w0 + run < A.slots ? w0 + run : A.slots;
+#pragma unroll 4
+    for (int64_t s = w0 + lane; s < w1; s += 64) atomicAdd(&cnt[wave][key_of(A, (uint32_t)s)], 1);
     if constexpr (!ONE) {
-        int lg = 32 - __builtin_clz(E);       // 2^lg > E: lanes for one workgroup's counts
-        if (lg > 10) lg = 10;
-        const int step = 1 << lg, group = tid >> lg, groups = kSortThreads >> lg;
-        for (int e = tid & (step - 1); e < K1; e += step) {
+        const int step = min(kSortThreads, (K1 + 63) & ~63);   // threads for one workgroup's counts
+        const int group = tid / step, groups = kSortThreads / step;
+        for (int e = tid % step; group < groups && e < K1; e += step) {
             int32_t b = 0, t = 0;
+#pragma unroll 8
             for (int c = group; c < A.blocks; c += groups) {
                 const int32_t v = A.hist[(int64_t)c * K1 + e];
                 t += v;
-                if (c < (int)blockIdx.x) b += v;
+                b += c < (int)blockIdx.x ? v : 0;
             }
             atomicAdd(&before[e], b);   // integers: any order gives the same sum
             atomicAdd(&total[e], t);
@@ -143,11 +148,12 @@ __global__ __launch_bounds__(kSortThreads) void moe_rank_kernel(SortArgs A) {
     }
     __syncthreads();
     volatile int32_t *mycnt = cnt[wave];
-    for (int i = 0; i < run; i += 64) {
-        const int64_t s = w0 + i + lane;
-        const bool active = s < A.slots;
-        if (!__ballot(active)) break;
-        const int key = active ? key_of(A, (uint32_t)s) : E;
+    int key_next = w0 + lane < w1 ? key_of(A, (uint32_t)(w0 + lane)) : E;
+    for (int64_t s0 = w0; s0 < w1; s0 += 64) {
+        const int64_t s = s0 + lane;
+        const bool active = s < w1;
+        const int key = key_next;
+        if (s + 64 < w1) key_next = key_of(A, (uint32_t)(s + 64));
         const uint64_t m = same_key(key, active, bits);
         const int rank = __popcll(m & ((1ull << lane) - 1));
         int32_t prior = 0;
@@ -195,20 +201,21 @@ __device__ inline RowRef row_ref(const RowArgs &A, int64_t slot) {
 }
 
 // Unit u of a row of `hidden` elements; elements past its end read as zero and are not written.
-template <typename T>
+// NT: read or written past the cache.
+template <typename T, bool NT>
 __device__ inline typename Vec16<T>::raw load_unit(const T *row, int u, int hidden) {
     constexpr int N = Vec16<T>::N;
-    if ((u + 1) * N <= hidden) return load_vec<T>(row + u * N);
+    if ((u + 1) * N <= hidden) return load_vec<T, NT>(row + u * N);
     typename Vec16<T>::raw v = {};
     for (int i = 0; i < N - 1; ++i)
         if (u * N + i < hidden) v[i] = reinterpret_cast<const std::remove_reference_t<decltype(v[0])> *>(row)[u * N + i];
     return v;
 }
-template <typename T>
+template <typename T, bool NT>
 __device__ inline void store_unit(T *row, int u, int hidden, typename Vec16<T>::raw v) {
     constexpr int N = Vec16<T>::N;
     if ((u + 1) * N <= hidden) {
-        store_vec<T>(row + u * N, v);
+        store_vec<T, NT>(row + u * N, v);
         return;
     }
     for (int i = 0; i < N - 1; ++i)
@@ -216,24 +223,24 @@ __device__ inline void store_unit(T *row, int u, int hidden, typename Vec16<T>::
 }
 
 // xs[row] = x[token]: a thread reads one unit and writes it K times.
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(512) void moe_dispatch_kernel(RowArgs A) {
     for (uint32_t b = blockIdx.x; b < A.blocks; b += gridDim.x) {
         const uint32_t t32 = b / (uint32_t)A.pieces;
         const int64_t t = t32;
         const int u = (int)(b - t32 * A.pieces) * blockDim.x + threadIdx.x;
         if (u >= A.units) continue;
-        const auto v = load_unit<T>(reinterpret_cast<const T *>(A.x) + t * A.x_ld, u, A.hidden);
+        const auto v = load_unit<T, false>(reinterpret_cast<const T *>(A.x) + t * A.x_ld, u, A.hidden);
         for (int k = 0; k < A.top_k; ++k) {
             const RowRef r = row_ref(A, t * A.top_k + k);
             typename Vec16<T>::raw z = {};
-            if (r.in) store_unit<T>(reinterpret_cast<T *>(A.rows) + r.row * A.rows_ld, u, A.hidden, r.kept ? v : z);
+            if (r.in) store_unit<T, NT>(reinterpret_cast<T *>(A.rows) + r.row * A.rows_ld, u, A.hidden, r.kept ? v : z);
         }
     }
 }
 
 // tok[t] = sum_k w[t, k] y[row(t, k)] (W = false: w = 1), up to KC rows in flight.
-template <typename T, bool W, int KC>
+template <typename T, bool W, int KC, bool NT>
 __global__ __launch_bounds__(512) void moe_combine_kernel(RowArgs A) {
     constexpr int N = Vec16<T>::N;
     for (uint32_t b = blockIdx.x; b < A.blocks; b += gridDim.x) {
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(512) void moe_combine_kernel(RowArgs A) {
                     const RowRef r = row_ref(A, s);
                     kept[j] = r.kept;
                     w[j] = W ? A.w[s] : 1.f;
-                    if (kept[j]) v[j] = load_unit<T>(reinterpret_cast<const T *>(A.y) + r.row * A.y_ld, u, A.hidden);
+                    if (kept[j]) v[j] = load_unit<T, NT>(reinterpret_cast<const T *>(A.y) + r.row * A.y_ld, u, A.hidden);
                 }
             }
 #pragma unroll
@@ -266,13 +273,13 @@ __global__ __launch_bounds__(512) void moe_combine_kernel(RowArgs A) {
         typename Vec16<T>::raw o;
 #pragma unroll
         for (int i = 0; i < N; ++i) set_elem<T>(o, i, acc[i]);
-        store_unit<T>(reinterpret_cast<T *>(A.tok) + t * A.tok_ld, u, A.hidden, o);
+        store_unit<T, NT>(reinterpret_cast<T *>(A.tok) + t * A.tok_ld, u, A.hidden, o);
     }
 }
 
 // dy[row] = w dout[t] and dw[t, k] = <dout[t], y[row]>: one workgroup per
 // token, KC choices at a time, their partial dot products in registers.
-template <typename T, int KC>
+template <typename T, int KC, bool NT>
 __global__ __launch_bounds__(512) void moe_combine_backward_kernel(RowArgs A) {
     constexpr int N = Vec16<T>::N;
     __shared__ float part[8][KC];
@@ -292,12 +299,12 @@ __global__ __launch_bounds__(512) void moe_combine_backward_kernel(RowArgs A) {
                 }
             }
             for (int u = threadIdx.x; u < A.units; u += blockDim.x) {
-                const auto gv = load_unit<T>(g, u, A.hidden);
+                const auto gv = load_unit<T, NT>(g, u, A.hidden);
                 typename Vec16<T>::raw v[KC];
 #pragma unroll
                 for (int j = 0; j < KC; ++j)
                     if (r[j].kept)
-                        v[j] = load_unit<T>(reinterpret_cast<const T *>(A.y) + r[j].row * A.y_ld, u, A.hidden);
+                        v[j] = load_unit<T, NT>(reinterpret_cast<const T *>(A.y) + r[j].row * A.y_ld, u, A.hidden);
 #pragma unroll
                 for (int j = 0; j < KC; ++j) {
                     if (!r[j].in) continue;
@@ -309,7 +316,7 @@ __global__ __launch_bounds__(512) void moe_combine_backward_kernel(RowArgs A) {
                             set_elem<T>(o, i, w[j] * elem<T>(gv, i));
                         }
                     }
-                    store_unit<T>(reinterpret_cast<T *>(A.rows) + r[j].row * A.rows_ld, u, A.hidden, o);
+                    store_unit<T, NT>(reinterpret_cast<T *>(A.rows) + r[j].row * A.rows_ld, u, A.hidden, o);
                 }
             }
 #pragma unroll
@@ -388,6 +395,14 @@ unsigned fill(RowArgs &a, int64_t tokens, int32_t top_k, int32_t hidden, int es,
     return threads;
 }
 
+// Whether a call that moves `rows` rows a token moves more than the last-level
+// cache holds. Its rows are then read and written past it: 8192 tokens x 8 rows
+// of 14 KiB, dispatch 208 -> 176 us (its reads stay as they are: with them 219),
+// combine 221 -> 207, its gradient 395 -> 384.
+bool past_cache(const RowArgs &a, int es, int64_t rows) {
+    return (double)a.tokens * rows * a.hidden * es > (double)kMallBytes;
+}
+
 ns_status combine(int64_t tokens, int32_t top_k, int32_t hidden, int32_t dtype, const void *y, int64_t y_ld,
                   const int32_t *row_of_slot, const float *w, void *out, int64_t out_ld, const char *y_name,
                   const char *out_name, void *stream) {
@@ -409,8 +424,12 @@ ns_status combine(int64_t tokens, int32_t top_k, int32_t hidden, int32_t dtype, 
     };
     auto pick = [&](auto t) {
         typedef decltype(t) T;
-        if (w) top_k <= 4 ? go(moe_combine_kernel<T, true, 4>) : go(moe_combine_kernel<T, true, 8>);
-        else top_k <= 4 ? go(moe_combine_kernel<T, false, 4>) : go(moe_combine_kernel<T, false, 8>);
+        const auto weighted = [&](auto nt) {
+            constexpr bool NT = decltype(nt)::value;
+            if (w) top_k <= 4 ? go(moe_combine_kernel<T, true, 4, NT>) : go(moe_combine_kernel<T, true, 8, NT>);
+            else top_k <= 4 ? go(moe_combine_kernel<T, false, 4, NT>) : go(moe_combine_kernel<T, false, 8, NT>);
+        };
+        past_cache(a, es, top_k + 1) ? weighted(std::true_type{}) : weighted(std::false_type{});
     };
     if (dtype == NS_BF16) pick((__bf16)0.f);
     else pick(0.f);
@@ -460,9 +479,10 @@ extern "C" ns_status ns_moe_sort(int64_t tokens, int32_t top_k, int32_t experts,
     a.slot_of_row = slot_of_row;
     a.row_of_slot = row_of_slot;
     a.hist = reinterpret_cast<int32_t *>(workspace);
-    // One workgroup up to 8 rounds of 1024 slots; past that two launches over up to 128 workgroups.
+    // One workgroup up to 2 rounds of 1024 slots (2048 slots: 5.8 us, two launches 7.2; 4096: 8.6 and 7.4), past
+    // that two launches over up to 128 workgroups.
     const int64_t rounds = (a.slots + kSortThreads - 1) / kSortThreads;
-    const bool one = rounds <= 8;
+    const bool one = rounds <= 2;
     const int64_t per = one ? (rounds > 0 ? rounds : 1) : (rounds + kMaxSortBlocks - 1) / kMaxSortBlocks;
     a.per = (int32_t)(per * kSortThreads);
     a.blocks = one ? 1 : (int32_t)((rounds + per - 1) / per);
@@ -493,10 +513,10 @@ extern "C" ns_status ns_moe_dispatch(int64_t tokens, int32_t top_k, int32_t hidd
     a.rows_ld = xs_ld;
     const unsigned threads = fill(a, tokens, top_k, hidden, es, row_of_slot);
     const dim3 grid(row_grid(a.blocks));
-    if (dtype == NS_BF16)
-        hipLaunchKernelGGL(moe_dispatch_kernel<__bf16>, grid, dim3(threads), 0, as_stream(stream), a);
-    else
-        hipLaunchKernelGGL(moe_dispatch_kernel<float>, grid, dim3(threads), 0, as_stream(stream), a);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, as_stream(stream), a); };
+    const bool nt = past_cache(a, es, top_k + 1);
+    if (dtype == NS_BF16) nt ? go(moe_dispatch_kernel<__bf16, true>) : go(moe_dispatch_kernel<__bf16, false>);
+    else nt ? go(moe_dispatch_kernel<float, true>) : go(moe_dispatch_kernel<float, false>);
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }
@@ -546,7 +566,10 @@ extern "C" ns_status ns_moe_combine_backward(int64_t tokens, int32_t top_k, int3
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, as_stream(stream), a); };
     auto pick = [&](auto t) {
         typedef decltype(t) T;
-        top_k <= 4 ? go(moe_combine_backward_kernel<T, 4>) : go(moe_combine_backward_kernel<T, 8>);
+        if (past_cache(a, es, 2 * top_k + 1))
+            top_k <= 4 ? go(moe_combine_backward_kernel<T, 4, true>) : go(moe_combine_backward_kernel<T, 8, true>);
+        else
+            top_k <= 4 ? go(moe_combine_backward_kernel<T, 4, false>) : go(moe_combine_backward_kernel<T, 8, false>);
     };
     if (dtype == NS_BF16) pick((__bf16)0.f);
     else pick(0.f);

@@ -43,8 +43,8 @@ constexpr int blocks_for(int vec, bool backward) {
 constexpr int kMostPartials = 1024;
 // Outputs of calls that move more than the last-level cache holds are stored
 // past it: 66 us become 63 in the case above, 104 become 102. Smaller ones stay in
-// it for the kernel that reads them next (35 us against 43 for 45 MB each way).
-constexpr int64_t kMallBytes = 256ll << 20;
+// it for the kernel that reads them next (35 us against 43 for 45 MB each way):
+// see deal().
 
 struct HeadSet {
     char *x, *g, *y;                 // input, gradient of the output (backward), output

@@ -22,13 +22,18 @@ template <> struct Vec16<float> {
     typedef raw __attribute__((aligned(4))) raw_u;
 };
 
-template <typename T>
+// NT: with the non-temporal hint, for data past what the caches can keep.
+template <typename T, bool NT = false>
 __device__ inline typename Vec16<T>::raw load_vec(const T *p) {
-    return *reinterpret_cast<const typename Vec16<T>::raw_u *>(p);
+    const auto *q = reinterpret_cast<const typename Vec16<T>::raw_u *>(p);
+    if constexpr (NT) return __builtin_nontemporal_load(q);
+    else return *q;
 }
-template <typename T>
+template <typename T, bool NT = false>
 __device__ inline void store_vec(T *p, typename Vec16<T>::raw v) {
-    *reinterpret_cast<typename Vec16<T>::raw_u *>(p) = v;
+    auto *q = reinterpret_cast<typename Vec16<T>::raw_u *>(p);
+    if constexpr (NT) __builtin_nontemporal_store(v, q);
+    else *q = v;
 }
 
 template <typename T> __device__ inline float elem(typename Vec16<T>::raw v, int i);
@@ -49,6 +54,9 @@ __device__ inline float wave_sum(float v) {
     for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
     return v;
 }
+
+// The last-level cache (MALL).
+constexpr int64_t kMallBytes = 256ll << 20;
 
 // Host side -----------------------------------------------------------------
 
