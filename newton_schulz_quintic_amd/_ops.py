@@ -27,7 +27,17 @@ _pack_heads = struct.Struct("@Pqqqi4x").pack
 _NO_HEADS = _pack_heads(0, 0, 0, 0, 0)
 assert len(_NO_HEADS) == ctypes.sizeof(ns_heads)
 
+_torch = None      # imported with the first call
 _codes, _int_sizes = {}, {}
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _codes.update({torch.bfloat16: NS_BF16, torch.float32: NS_F32})
+    _int_sizes.update({torch.int32: 4, torch.int64: 8})
+    _torch = torch
+    return torch
 
 
 def _c():
@@ -37,28 +47,22 @@ def _c():
 
 def _code(t, name: str) -> int:
     """The ns_dtype of a float tensor."""
-    if not _codes:
-        import torch
-        _codes.update({torch.bfloat16: NS_BF16, torch.float32: NS_F32})
-    try:
-        return _codes[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}") from None
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return code
 
 
 def _int_bytes(t, name: str) -> int:
-    if not _int_sizes:
-        import torch
-        _int_sizes.update({torch.int32: 4, torch.int64: 8})
-    try:
-        return _int_sizes[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name} must be int32 or int64, not {t.dtype}") from None
+    size = _int_sizes.get(t.dtype)
+    if size is None:
+        raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
+    return size
 
 
 def _on_gpu(names: str, tensors) -> int:
-    """Checks that all tensors (or None) are on the current GPU; returns its index."""
-    import torch
+    """Checks that all tensors (or None) are on the current GPU; returns its index. Every call's first step."""
+    torch = _torch or _load_torch()
     here = None
     for t in tensors:
         if t is None:
@@ -76,26 +80,32 @@ def _on_gpu(names: str, tensors) -> int:
 def _stream(stream, device: int) -> int:
     """The stream's handle; torch's current one on the device by default."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _torch._C._cuda_getCurrentRawStream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _array(t, name: str, shape, dtype: str):
-    """Checks a contiguous tensor of one shape and of a dtype named as in torch; returns its address."""
+def _array(t, name: str, shape, dtype):
+    """Checks a contiguous tensor of one shape and dtype; returns its address."""
     if t is None:
         return None
-    import torch
-    if t.dtype != getattr(torch, dtype):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and of shape {tuple(shape)}, not {tuple(t.shape)}")
     return t.data_ptr()
 
 
+def _floats(t, name: str, shape):
+    return _array(t, name, shape, _torch.float32)
+
+
+def _ints(t, name: str, shape):
+    return _array(t, name, shape, _torch.int32)
+
+
 def _rows(t, name: str, rows: int, cols: int, dtype) -> int:
     """Checks a (rows, cols) tensor whose rows are contiguous; returns its row stride."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape ({rows}, {cols}), not {tuple(t.shape)}")
@@ -109,8 +119,7 @@ def _workspace(workspace, nbytes, device, stream):
     """The caller's workspace, or a new one of ``nbytes()`` (the library checks the size of a given one)."""
     if workspace is None:
         return _new_workspace(nbytes(), device, stream)
-    import torch
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+    if workspace.dtype is not _torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     return workspace
 
@@ -121,7 +130,7 @@ def _workspace(workspace, nbytes, device, stream):
 
 def _heads(t, name: str, shape, dtype) -> bytes:
     """The ns_heads of a tensor with contiguous heads, checked against the shape and dtype it must have."""
-    if t.shape != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must have shape {tuple(shape)} and dtype {dtype}, not {tuple(t.shape)}, {t.dtype}")
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1 and t.numel():
@@ -175,7 +184,7 @@ def _head_args(q, k, like, q_weight, k_weight, cos, sin, pos, eps, interleaved):
         table = cos.shape
         if len(table) != 2:
             raise ValueError("cos and sin must be (positions, rope_dim / 2)")
-        cos_ptr, sin_ptr = _array(cos, "cos", table, "float32"), _array(sin, "sin", table, "float32")
+        cos_ptr, sin_ptr = _floats(cos, "cos", table), _floats(sin, "sin", table)
         rows, rope = table[0], 2 * table[1]
     if pos is not None:
         pos_bytes = _int_bytes(pos, "pos")
@@ -223,7 +232,7 @@ def ns_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight=None, dk_we
     sizes, (hq, hk, gq, gk, oq, ok), rest = _head_args(q, k, ((dq_out, dk_out, "d%s_out"), (dq, dk, "d%s")), q_weight,
                                                        k_weight, cos, sin, pos, eps, interleaved)
     dim = (sizes[2],)
-    wq, wk = _array(dq_weight, "dq_weight", dim, "float32"), _array(dk_weight, "dk_weight", dim, "float32")
+    wq, wk = _floats(dq_weight, "dq_weight", dim), _floats(dk_weight, "dk_weight", dim)
     if wq or wk:
         workspace = _workspace(workspace, lambda: ns_qk_norm_rope_workspace_bytes(*sizes[:3]),
                                (k if q is None else q).device, stream)
@@ -262,9 +271,9 @@ def ns_moe_sort(expert_ids, num_experts: int, offsets, slot_of_row, row_of_slot,
                            expert_ids.device, stream)
     _check(_c().ns_moe_sort(
         tokens, top_k, num_experts, expert_ids.data_ptr(), id_bytes, ld,
-        _array(offsets, "offsets", (num_experts + 1,), "int32"),
-        _array(slot_of_row, "slot_of_row", (tokens * top_k,), "int32"),
-        _array(row_of_slot, "row_of_slot", (tokens, top_k), "int32"), workspace.data_ptr(), workspace.numel(),
+        _ints(offsets, "offsets", (num_experts + 1,)),
+        _ints(slot_of_row, "slot_of_row", (tokens * top_k,)),
+        _ints(row_of_slot, "row_of_slot", (tokens, top_k)), workspace.data_ptr(), workspace.numel(),
         _stream(stream, device)))
     return workspace
 
@@ -276,7 +285,7 @@ def _moe_sizes(tok, name: str, row_of_slot):
     if tok.dim() != 2:
         raise ValueError(f"{name} must be (tokens, hidden)")
     tokens, top_k = row_of_slot.shape
-    return tokens, top_k, tok.shape[1], _code(tok, name), _array(row_of_slot, "row_of_slot", row_of_slot.shape, "int32")
+    return tokens, top_k, tok.shape[1], _code(tok, name), _ints(row_of_slot, "row_of_slot", row_of_slot.shape)
 
 
 def ns_moe_dispatch(x, row_of_slot, xs, stream=None) -> None:
@@ -300,7 +309,7 @@ def ns_moe_combine(y, row_of_slot, weights, out, stream=None) -> None:
     device = _on_gpu("y row_of_slot weights out", (y, row_of_slot, weights, out))
     t, k, h, code, rows = _moe_sizes(out, "out", row_of_slot)
     _check(_c().ns_moe_combine(t, k, h, code, y.data_ptr(), _rows(y, "y", t * k, h, out.dtype), rows,
-                                _array(weights, "weights", (t, k), "float32"), out.data_ptr(),
+                                _floats(weights, "weights", (t, k)), out.data_ptr(),
                                 _rows(out, "out", t, h, out.dtype), _stream(stream, device)))
 
 
@@ -310,8 +319,8 @@ def ns_moe_combine_backward(dout, y, row_of_slot, weights, dy, dweights, stream=
     t, k, h, code, rows = _moe_sizes(dout, "dout", row_of_slot)
     _check(_c().ns_moe_combine_backward(
         t, k, h, code, dout.data_ptr(), _rows(dout, "dout", t, h, dout.dtype), y.data_ptr(),
-        _rows(y, "y", t * k, h, dout.dtype), rows, _array(weights, "weights", (t, k), "float32"), dy.data_ptr(),
-        _rows(dy, "dy", t * k, h, dout.dtype), _array(dweights, "dweights", (t, k), "float32"),
+        _rows(y, "y", t * k, h, dout.dtype), rows, _floats(weights, "weights", (t, k)), dy.data_ptr(),
+        _rows(dy, "dy", t * k, h, dout.dtype), _floats(dweights, "dweights", (t, k)),
         _stream(stream, device)))
 
 
@@ -331,7 +340,7 @@ def _distill_args(logits, ids, teacher, teacher_lse, temperature):
         raise ValueError("teacher must be contiguous and shaped like ids")
     return (rows, vocab, top_k, _code(logits, "logits"), logits.data_ptr(), ld, ids.data_ptr(),
             _int_bytes(ids, "ids"), teacher.data_ptr(), _code(teacher, "teacher"),
-            _array(teacher_lse, "teacher_lse", (rows,), "float32"), float(temperature))
+            _floats(teacher_lse, "teacher_lse", (rows,)), float(temperature))
 
 
 def ns_distill_workspace_bytes(rows: int, vocab: int, top_k: int) -> int:
@@ -360,8 +369,8 @@ def ns_distill_topk(logits, ids, teacher, loss, lse, teacher_lse=None, rest_lse=
     workspace = _workspace(workspace, lambda: ns_distill_workspace_bytes(rows, vocab, top_k), logits.device, stream)
     one = (rows,)
     _check(_c().ns_distill_topk(
-        *args, _array(grad_loss, "grad_loss", one, "float32"), _array(loss, "loss", one, "float32"),
-        _array(lse, "lse", one, "float32"), _array(rest_lse, "rest_lse", one, "float32"),
+        *args, _floats(grad_loss, "grad_loss", one), _floats(loss, "loss", one),
+        _floats(lse, "lse", one), _floats(rest_lse, "rest_lse", one),
         None if dlogits is None else dlogits.data_ptr(),
         0 if dlogits is None else _rows(dlogits, "dlogits", rows, vocab, logits.dtype), workspace.data_ptr(),
         workspace.numel(), _stream(stream, device)))
@@ -379,6 +388,6 @@ def ns_distill_topk_backward(logits, ids, teacher, lse, grad_loss, dlogits, teac
         raise ValueError("rest_lse and teacher_lse go together")
     one = (rows,)
     _check(_c().ns_distill_topk_backward(
-        *args, _array(lse, "lse", one, "float32"), _array(rest_lse, "rest_lse", one, "float32"),
-        _array(grad_loss, "grad_loss", one, "float32"), dlogits.data_ptr(),
+        *args, _floats(lse, "lse", one), _floats(rest_lse, "rest_lse", one),
+        _floats(grad_loss, "grad_loss", one), dlogits.data_ptr(),
         _rows(dlogits, "dlogits", rows, vocab, logits.dtype), _stream(stream, device)))

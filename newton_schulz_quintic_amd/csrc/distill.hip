@@ -34,6 +34,7 @@ constexpr int kMaxRows = 1 << 24;
 constexpr int kMaxChunks = 64;            // parts of a row that is split over workgroups
 constexpr int kBitVocab = 1 << 18;        // tokens one workgroup marks in LDS (32 KiB)
 constexpr int kSplitThreads = 256;
+constexpr int kAhead = 4;                 // vectors a thread of a split row loads ahead of everything else
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kNonTemporal = 2;           // a buffer store's cache policy
 
@@ -85,14 +86,14 @@ __device__ inline float wave_max(float v) {
 
 // q of a logit z is exp((z - m) / tau) scale.
 struct Norm {
-    float m, scale, log_scale;
+    float m, scale;
 };
-__device__ inline Norm norm_of(Lse l) { return {l.m == kNegInf ? 0.f : l.m, 1.f / l.s, -logf(l.s)}; }
+__device__ inline Norm norm_of(Lse l) { return {l.m == kNegInf ? 0.f : l.m, 1.f / l.s}; }
 // From a logsumexp rounded to fp32: m is lse tau rounded, and the scale takes
 // up the rest of it, so q is off by no more than lse's own rounding.
 __device__ inline Norm norm_of_lse(float lse, float inv_tau) {
     const float m = lse / inv_tau, rest = fmaf(m, inv_tau, -lse);
-    return {m, expf(rest), rest};
+    return {m, expf(rest)};
 }
 __device__ inline float q_of(float z, const Norm &n, float c) { return __builtin_amdgcn_exp2f((z - n.m) * c) * n.scale; }
 
@@ -108,6 +109,7 @@ struct PairLds {
     float p_token[kMaxTop];    // p summed over the token's pairs
     int32_t owner[kMaxTop];    // the token, in the lowest of its pairs; -1 in the others
     Lse wave[16];
+    float wave_sum[16];
 };
 
 struct Pairs {
@@ -215,7 +217,7 @@ __device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds &L, 
         const int id = L.id[k];
         bool lowest = id >= 0;
         float sum = 0.f;
-#pragma unroll 2
+#pragma unroll 1
         for (int j = 0; j < A.top_k; j += 4) {
             const int4 other = *reinterpret_cast<const int4 *>(&L.id[j]);
             const float4 p = *reinterpret_cast<const float4 *>(&L.p[j]);
@@ -327,13 +329,18 @@ __device__ inline Lse block_join(Lse a, PairLds &L, float c) {
     return a;
 }
 
-// The threads' sum, in every thread. One barrier inside.
+// The threads' sum, in every thread; the workgroup has THREADS of them. One barrier inside.
+template <int THREADS>
 __device__ inline float block_sum(float v, PairLds &L) {
     v = wave_sum(v);
-    if ((threadIdx.x & 63) == 0) L.wave[threadIdx.x >> 6].s = v;
+    if ((threadIdx.x & 63) == 0) L.wave_sum[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) v += L.wave[w].s;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; w += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(&L.wave_sum[w]);
+        v += (q.x + q.y) + (q.z + q.w);
+    }
     return v;
 }
 
@@ -359,7 +366,11 @@ __device__ inline typename Vec16<T>::raw grad_vec(typename Vec16<T>::raw v, cons
     return o;
 }
 
-// The same two with exp((z - m) / tau) as 2^(z c + hi), see distill_held_kernel.
+// The same two with exp((z - m) / tau) = 2^(z c + hi) 2^-lo, where m is the
+// pairs' largest logit: one fma a value, and no maximum to find. They serve
+// unless some logit lies so far above m that the sum overflows, or (REST) all
+// lie so far below that it is lost, or one is NaN or infinite; such a row is
+// summed again relative to its own largest.
 template <typename T, bool REST>
 __device__ inline float fast_sum(typename Vec16<T>::raw v, uint32_t skip, float c, float hi) {
     float s[2] = {0.f, 0.f};
@@ -373,6 +384,26 @@ __device__ inline float fast_sum(typename Vec16<T>::raw v, uint32_t skip, float 
     }
     return s[0] + s[1];
 }
+template <typename T, bool REST>
+__device__ inline float fast_tail(float zt, const Span<T> &S, const uint32_t *bits, float c, float hi) {
+    if ((int)threadIdx.x >= S.tail || (REST && vec_bits(bits, S.vecs * S.N + threadIdx.x, 1))) return 0.f;
+    return __builtin_amdgcn_exp2f(fmaf(zt, c, hi));
+}
+// The exponent's offset for sums relative to the pairs' largest logit m, and
+// whether such a sum can be used.
+struct FastBase {
+    float m, hi, lo;
+};
+__device__ inline FastBase fast_base(const DistillArgs &A, const PairLds &L, float c) {
+    float m = kNegInf;
+    for (int k = threadIdx.x & 63; k < A.top_k; k += 64)
+        if (L.id[k] >= 0) m = fmaxf(m, L.z[k]);
+    m = wave_max(m);
+    const float hi = -m * c;
+    return {m, hi, fmaf(m, c, hi)};
+}
+__device__ inline bool fast_holds(const Lse &s) { return s.s > 1e-10f && s.s < 1e30f; }
+
 // factor 2^(z c + hi). For bf16 results log2 |factor| goes into the exponent
 // (its rounding, 2^-24 of a number below 100, is far under theirs) and the
 // sign is set afterwards.
@@ -399,22 +430,42 @@ __device__ inline typename Vec16<T>::raw fast_grad(typename Vec16<T>::raw v, flo
     return o;
 }
 
-// A span's vectors' gradient, read from memory.
-template <typename T>
-__device__ inline void grad_span(const T *z, T *dz, const Span<T> &S, const Norm &n, float c, float g) {
+// The thread's part of a span's sum, read from memory, likewise.
+template <typename T, bool REST>
+__device__ inline float fast_span(const T *z, float zt, const Span<T> &S, const uint32_t *bits, float c, float hi) {
+    constexpr int B = 8;
+    const int threads = blockDim.x;
+    float sum = 0.f;
+    int v = threadIdx.x;
+    for (; v + (B - 1) * threads < S.vecs; v += B * threads) {
+        typename Vec16<T>::raw r[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) r[i] = load_vec<T>(z + S.e0 + (int64_t)(v + i * threads) * S.N);
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            sum += fast_sum<T, REST>(r[i], REST ? vec_bits(bits, v + i * threads, S.N) : 0, c, hi);
+    }
+    for (; v < S.vecs; v += threads)
+        sum += fast_sum<T, REST>(load_vec<T>(z + S.e0 + (int64_t)v * S.N), REST ? vec_bits(bits, v, S.N) : 0, c, hi);
+    return sum + fast_tail<T, REST>(zt, S, bits, c, hi);
+}
+
+// The gradient of a span's vectors from the given one on, read from memory.
+template <typename T, bool NT>
+__device__ inline void grad_span(const T *z, T *dz, const Span<T> &S, const Norm &n, float c, float g, int from = 0) {
     constexpr int B = 4;
     const int threads = blockDim.x;
-    int v = threadIdx.x;
+    int v = from + threadIdx.x;
     for (; v + (B - 1) * threads < S.vecs; v += B * threads) {
         typename Vec16<T>::raw w[B];
 #pragma unroll
         for (int i = 0; i < B; ++i) w[i] = load_vec<T>(z + S.e0 + (int64_t)(v + i * threads) * S.N);
 #pragma unroll
         for (int i = 0; i < B; ++i)
-            store_vec<T>(dz + S.e0 + (int64_t)(v + i * threads) * S.N, grad_vec<T>(w[i], n, c, g));
+            store_vec<T, NT>(dz + S.e0 + (int64_t)(v + i * threads) * S.N, grad_vec<T>(w[i], n, c, g));
     }
     for (; v < S.vecs; v += threads)
-        store_vec<T>(dz + S.e0 + (int64_t)v * S.N, grad_vec<T>(load_vec<T>(z + S.e0 + (int64_t)v * S.N), n, c, g));
+        store_vec<T, NT>(dz + S.e0 + (int64_t)v * S.N, grad_vec<T>(load_vec<T>(z + S.e0 + (int64_t)v * S.N), n, c, g));
 }
 
 // The tail's gradient, then that of the pairs' tokens, each written over the
@@ -449,23 +500,24 @@ template <bool REST>
 __device__ inline void write_loss(const DistillArgs &A, const PairLds &L, const Pairs &r, int64_t row, const Norm &n,
                                   Lse all, Lse rest) {
     if (threadIdx.x >= 64) return;
+    const float log_all = logf(all.s);
     float sum = 0.f;
     for (int k = threadIdx.x; k < A.top_k; k += 64) {
         const float p = L.p[k];
-        if (p != 0.f) sum += p * (L.t[k] - ((L.z[k] - n.m) * A.inv_tau + n.log_scale));
+        if (p != 0.f) sum += p * (L.t[k] - ((L.z[k] - n.m) * A.inv_tau - log_all));
     }
     sum = wave_sum(sum);
     if (threadIdx.x) return;
     if constexpr (REST) {
         const float log_rest = logf(rest.s);
         if (r.p_rest != 0.f) {
-            const float log_q = (rest.m - n.m) * A.inv_tau + log_rest + n.log_scale;
+            const float log_q = (rest.m - n.m) * A.inv_tau + log_rest - log_all;
             sum += r.p_rest * (logf(r.p_rest) - log_q);
         }
         A.rest_lse[row] = rest.m * A.inv_tau + log_rest;
     }
     A.loss[row] = sum;
-    A.lse[row] = all.m * A.inv_tau + logf(all.s);
+    A.lse[row] = all.m * A.inv_tau + log_all;
 }
 
 template <bool REST>
@@ -598,26 +650,19 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
         int at = tid;
         asm volatile("" : "+v"(at));   // what follows from it is found anew for each row, not held in 2 NV registers
         const float zt = (float)now.zt;
-        // exp((z - m) / tau) = 2^(z c + hi) 2^-lo with m the pairs' largest logit: one fma a value, and no maximum to
-        // find. It serves unless some logit lies so far above m that the sum overflows, or (REST) all lie so far below
-        // that it is lost, or one is NaN or infinite; then the row is summed again relative to its own largest.
-        float m = kNegInf;
-        for (int k = tid & 63; k < A.top_k; k += 64)
-            if (L.id[k] >= 0) m = fmaxf(m, L.z[k]);
-        m = wave_max(m);
-        const float hi = -m * c, lo = fmaf(m, c, hi);
+        const FastBase f0 = fast_base(A, L, c);
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int left = S.vecs - i * THREADS;
             if (left > 0 && (left >= THREADS || at < left)) {
                 const uint32_t skip = REST ? vec_bits(bits, at + i * THREADS, S.N) : 0;
-                sum += fast_sum<T, REST>(__builtin_bit_cast(raw, held[i]), skip, c, hi);
+                sum += fast_sum<T, REST>(__builtin_bit_cast(raw, held[i]), skip, c, f0.hi);
             }
         }
-        if (tid < S.tail && !(REST && vec_bits(bits, S.vecs * S.N + tid, 1))) sum += __builtin_amdgcn_exp2f(fmaf(zt, c, hi));
-        Lse rest = {m, block_sum(sum, L) * __builtin_amdgcn_exp2f(-lo)};
-        const bool fast = !r.some || (rest.s > 1e-10f && rest.s < 1e30f);
+        sum += fast_tail<T, REST>(zt, S, bits, c, f0.hi);
+        Lse rest = {f0.m, block_sum<THREADS>(sum, L) * __builtin_amdgcn_exp2f(-f0.lo)};
+        const bool fast = !r.some || fast_holds(rest);
         if (!fast) {
             Lse a = {kNegInf, 0.f};
 #pragma unroll
@@ -635,7 +680,7 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
         now = beside_of(next, p);
         ahead = pair_of(next + gridDim.x);
         const auto dz = vecs_of(A.dlogits, row, A.dld, true), z = vecs_of(A.logits, next, A.ld, next < A.rows);
-        const FastFactor f = fast_factor<T>(s.g_others * s.others.scale * __builtin_amdgcn_exp2f(-lo), hi);
+        const FastFactor f = fast_factor<T>(s.g_others * s.others.scale * __builtin_amdgcn_exp2f(-f0.lo), f0.hi);
         const auto turn = [&](auto value) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -669,8 +714,8 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
 
 // Loss, and with dlogits the gradient, of rows too long to hold: the row is
 // read a second time for the gradient.
-template <typename T, int THREADS, bool REST>
-__global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
+template <typename T, bool REST, bool NT>
+__global__ __launch_bounds__(kSplitThreads) void distill_row_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
     __shared__ __attribute__((aligned(16))) PairLds L;
     const Span<T> S(0, A.vocab);
@@ -683,14 +728,19 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
             __syncthreads();
             continue;
         }
-        for (int k = threadIdx.x; k < A.top_k; k += THREADS) L.z[k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
+        for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) L.z[k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
         const float zt = tail_of<T>(z, S);
         weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, 0, A.vocab);
-        const Lse rest = block_join(sum_span<T, REST>(z, zt, S, bits, c), L, c);
+        const FastBase f = fast_base(A, L, c);
+        Lse rest = {f.m, block_sum<kSplitThreads>(fast_span<T, REST>(z, zt, S, bits, c, f.hi), L) * __builtin_amdgcn_exp2f(-f.lo)};
+        if (!fast_holds(rest)) {
+            __syncthreads();
+            rest = block_join(sum_span<T, REST>(z, zt, S, bits, c), L, c);
+        }
         const RowSums s = row_sums<REST>(A, L, r, A.dlogits ? A.grad_loss[row] : 0.f, rest, c);
         if (A.dlogits) {
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
-            grad_span<T>(z, dz, S, s.others, c, s.g_others);
+            grad_span<T, NT>(z, dz, S, s.others, c, s.g_others);
             finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, s.n, s.others, c, s.g, s.g_others);
         }
         write_loss<REST>(A, L, r, row, s.n, s.all, s.rest);
@@ -725,7 +775,7 @@ __global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillA
 
 // Workgroup (chunk, row) writes its part of the gradient, from the parts' sums
 // (LOSS: the first one also the loss) or from the logsumexps of a forward call.
-template <typename T, bool REST, bool LOSS>
+template <typename T, bool REST, bool LOSS, bool NT>
 __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArgs A, int32_t parts) {
     extern __shared__ uint32_t bits[];
     __shared__ __attribute__((aligned(16))) PairLds L;
@@ -736,6 +786,16 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
         const int e0 = chunk * A.chunk, e1 = min(e0 + A.chunk, A.vocab);
         const Span<T> S(e0, e1);
         const T *z = reinterpret_cast<const T *>(A.logits) + row * A.ld;
+        // what the part needs last is asked for first
+        typename Vec16<T>::raw ahead[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int v = threadIdx.x + i * kSplitThreads;
+            if (A.dlogits && v < S.vecs) ahead[i] = load_vec<T>(z + e0 + (int64_t)v * S.N);
+        }
+        const float zt = tail_of<T>(z, S);
+        float2 part = make_float2(kNegInf, 0.f);   // at most kMaxChunks = 64: one a lane
+        if (LOSS && (int)(threadIdx.x & 63) < parts) part = A.partial[row * parts + (threadIdx.x & 63)];
         Pairs r = read_pairs<REST>(A, row, L, bits, 0);
         if (!r.some) {
             write_empty<T, REST>(A, row, S, LOSS && chunk == 0);
@@ -747,31 +807,30 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
             if (LOSS) L.z[k] = A.top_z[row * A.top_k + k];
             else L.z[k] = id >= e0 && id < e1 ? (float)z[id] : 0.f;
         }
-        const float zt = tail_of<T>(z, S);
         weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, 0, 0);
         RowSums s{};
         const float g = A.dlogits ? A.grad_loss[row] : 0.f;
         if constexpr (LOSS) {
-            Lse rest = {kNegInf, 0.f};
-            for (int i = threadIdx.x & 63; i < parts; i += 64) {
-                const float2 p = A.partial[row * parts + i];
-                rest = join(rest, {p.x, p.y}, c);
-            }
-            s = row_sums<REST>(A, L, r, g, wave_join(rest, c), c);
+            s = row_sums<REST>(A, L, r, g, wave_join({part.x, part.y}, c), c);
         } else {
             const float lse = A.lse[row];
             s.n = s.others = norm_of_lse(lse, A.inv_tau);
             s.g = s.g_others = g * A.inv_tau;
             if constexpr (REST) {
                 const float rest_lse = A.rest_lse[row];
-                if (rest_lse == kNegInf) s.others = {0.f, r.p_rest == 0.f ? 0.f : __builtin_inff(), 0.f};
+                if (rest_lse == kNegInf) s.others = {0.f, r.p_rest == 0.f ? 0.f : __builtin_inff()};
                 else s.others = norm_of_lse(rest_lse, A.inv_tau);
                 s.g_others = others_factor<REST>(r, s.g, expf(rest_lse - lse));
             }
         }
         if (A.dlogits) {
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
-            grad_span<T>(z, dz, S, s.others, c, s.g_others);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int v = threadIdx.x + i * kSplitThreads;
+                if (v < S.vecs) store_vec<T, NT>(dz + e0 + (int64_t)v * S.N, grad_vec<T>(ahead[i], s.others, c, s.g_others));
+            }
+            grad_span<T, NT>(z, dz, S, s.others, c, s.g_others, kAhead * kSplitThreads);
             finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, s.n, s.others, c, s.g, s.g_others);
         }
         if (LOSS && chunk == 0) write_loss<REST>(A, L, r, row, s.n, s.all, s.rest);
@@ -786,16 +845,26 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
 // Parts of a row for the split kernels: enough workgroups to fill the GPU, of
 // at least 8192 tokens (and no more than one workgroup marks in LDS).
 void set_chunks(DistillArgs &a) {
-    int64_t parts = (1024 + a.rows - 1) / a.rows;
-    parts = std::min<int64_t>(parts, (a.vocab + 8191) / 8192);
+    const auto deal = [&](int64_t workgroups, int64_t tokens) {
+        return std::min((workgroups + a.rows - 1) / a.rows, (a.vocab + tokens - 1) / tokens);
+    };
+    int64_t parts = std::max(deal(512, 2048), deal(4096, 16384));
     parts = std::max<int64_t>(parts, (a.vocab + kBitVocab - 1) / kBitVocab);
     parts = std::max<int64_t>(1, std::min<int64_t>(parts, kMaxChunks));
     a.chunk = (int32_t)(((a.vocab + parts - 1) / parts + 31) / 32 * 32);
     a.chunks = (a.vocab + a.chunk - 1) / a.chunk;
 }
 
-// Rows that fill the GPU one workgroup each; fewer are split.
-bool split_rows(int64_t rows, int32_t vocab, bool rest) { return rows < 256 || (rest && vocab > kBitVocab); }
+// Which rows are held in registers (a thread for each pair, at most 16 vectors a thread).
+int64_t held_vecs(const DistillArgs &a, int es) { return std::max<int64_t>((int64_t)a.vocab * es / 16, 8 * a.top_k); }
+// Which calls split their rows over workgroups and run two kernels. Training
+// holds rows that it can from 256 on (one a CU; 600 x 131072 bf16: 81 us, split
+// 91); otherwise rows are read one to a workgroup of 256 threads once these fill
+// the GPU (600 x 131072 bf16 forward: split 38 us, a workgroup a row 44).
+bool split_rows(const DistillArgs &a, int es) {
+    if (a.teacher_lse && a.vocab > kBitVocab) return true;
+    return a.rows < (a.dlogits && held_vecs(a, es) <= 16384 ? 256 : 1024);
+}
 
 size_t distill_workspace(int64_t rows, int32_t top_k, bool split) {
     return split ? (size_t)rows * ((size_t)kMaxChunks * sizeof(float2) + (size_t)top_k * sizeof(float)) : 0;
@@ -852,21 +921,25 @@ ns_status check_distill(int64_t rows, int32_t vocab, int32_t top_k, int32_t dtyp
 // Workgroups of a split launch: at most 2^20, which then take several parts each.
 unsigned split_grid(const DistillArgs &a) { return (unsigned)std::min<int64_t>((int64_t)a.rows * a.chunks, 1 << 20); }
 
+// Whether reading the logits and writing their gradient passes more than the
+// last-level cache holds; the gradient is then stored past it (1025 x 50021 f32
+// backward: 83 -> 67 us; 300 x 131072 bf16, 157 MB: no difference).
+bool past_cache(const DistillArgs &a, int es) { return 2.0 * a.rows * a.vocab * es > (double)kMallBytes; }
+
 template <typename T, bool REST>
 ns_status launch_rows(const DistillArgs &a, hipStream_t st) {
     const size_t lds = REST ? (size_t)((a.vocab + 31) / 32 + 1) * 4 : 0;   // lanes past the row read one byte behind it
-    const int64_t vecs = a.vocab / Vec16<T>::N;
     auto go = [&](auto kernel, int threads, int64_t most) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows, most)), dim3(threads), lds, st, a);
     };
-    // Held rows: as many workgroups as are resident at once (16 waves a CU), a thread for each pair.
-    const int64_t need = a.dlogits ? std::max<int64_t>(vecs, 8 * a.top_k) : INT64_MAX;
-    if (need <= 2048) go(distill_held_kernel<T, 256, 8, REST>, 256, 1024);
-    else if (need <= 4096) go(distill_held_kernel<T, 512, 8, REST>, 512, 512);
-    else if (need <= 8192) go(distill_held_kernel<T, 1024, 8, REST>, 1024, 256);
-    else if (need <= 16384) go(distill_held_kernel<T, 1024, 16, REST>, 1024, 256);
-    else if (a.rows >= 1024) go(distill_row_kernel<T, 256, REST>, 256, 1 << 20);
-    else go(distill_row_kernel<T, 1024, REST>, 1024, 1 << 20);
+    // Held rows: as many workgroups as are resident at once (16 waves a CU).
+    const int64_t vecs = held_vecs(a, sizeof(T));
+    if (!a.dlogits) go(distill_row_kernel<T, REST, false>, 256, 1 << 20);
+    else if (vecs <= 2048) go(distill_held_kernel<T, 256, 8, REST>, 256, 1024);
+    else if (vecs <= 4096) go(distill_held_kernel<T, 512, 8, REST>, 512, 512);
+    else if (vecs <= 8192) go(distill_held_kernel<T, 1024, 8, REST>, 1024, 256);
+    else if (vecs <= 16384) go(distill_held_kernel<T, 1024, 16, REST>, 1024, 256);
+    else past_cache(a, sizeof(T)) ? go(distill_row_kernel<T, REST, true>, 256, 1 << 20) : go(distill_row_kernel<T, REST, false>, 256, 1 << 20);
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }
@@ -879,7 +952,7 @@ ns_status launch_split(DistillArgs a, hipStream_t st) {
     NSQ_HIP(hipGetLastError());
     const int32_t parts = a.chunks;
     if (!a.dlogits) a.chunks = 1, a.chunk = a.vocab;
-    hipLaunchKernelGGL((distill_apply_kernel<T, REST, true>), dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, parts);
+    hipLaunchKernelGGL((distill_apply_kernel<T, REST, true, false>), dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, parts);
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }
@@ -887,7 +960,8 @@ ns_status launch_split(DistillArgs a, hipStream_t st) {
 template <typename T, bool REST>
 ns_status launch_backward(DistillArgs a, hipStream_t st) {
     set_chunks(a);
-    hipLaunchKernelGGL((distill_apply_kernel<T, REST, false>), dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, 0);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, 0); };
+    past_cache(a, sizeof(T)) ? go(distill_apply_kernel<T, REST, false, true>) : go(distill_apply_kernel<T, REST, false, false>);
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }
@@ -900,7 +974,7 @@ using namespace nsq;
 extern "C" ns_status ns_distill_workspace_bytes(int64_t rows, int32_t vocab, int32_t top_k, size_t *bytes) {
     if (!bytes) return fail(NS_ERR_INVALID_ARG, "bytes is NULL");
     if (ns_status s = check_sizes(rows, vocab, top_k)) return s;
-    *bytes = distill_workspace(rows, top_k, split_rows(rows, vocab, true));
+    *bytes = distill_workspace(rows, top_k, rows < 1024 || vocab > kBitVocab);
     return NS_OK;
 }
 
@@ -917,7 +991,7 @@ extern "C" ns_status ns_distill_topk(int64_t rows, int32_t vocab, int32_t top_k,
     if (rows > 0 && teacher_lse && !rest_lse) return fail(NS_ERR_INVALID_ARG, "teacher_lse needs rest_lse");
     if (misaligned(loss, 4) || misaligned(lse, 4) || misaligned(rest_lse, 4))
         return fail(NS_ERR_INVALID_ARG, "loss, lse or rest_lse not 4-byte aligned");
-    const bool rest = teacher_lse != nullptr, split = split_rows(rows, vocab, rest);
+    const bool rest = teacher_lse != nullptr, split = split_rows(a, dtype_bytes(dtype));
     const size_t need = distill_workspace(rows, top_k, split);
     if (need && (!workspace || workspace_bytes < need))
         return fail(NS_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);

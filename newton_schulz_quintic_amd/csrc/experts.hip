@@ -15,6 +15,7 @@
 //
 // Bound by memory: a pass reads or writes K rows a token and one more.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "op_util.h"
@@ -558,10 +559,11 @@ extern "C" ns_status ns_moe_combine_backward(int64_t tokens, int32_t top_k, int3
     a.w = weights;
     a.dw = dweights;
     fill(a, tokens, top_k, hidden, es, row_of_slot);
-    // As many threads as spread the row's units evenly over their rounds.
-    const int32_t rounds = (a.units + 511) / 512 > 0 ? (a.units + 511) / 512 : 1;
-    const int32_t each = (a.units + rounds - 1) / rounds;
-    const unsigned threads = each > 0 ? (unsigned)(each + 63) / 64 * 64 : 64;
+    // At least two rounds of units a thread, spread evenly over at most 512 threads: a workgroup's sums and barriers
+    // then cost less beside its rows (385 units, 3 choices: 192 threads 25 us, 448 32; 896 units, 8 choices: 448
+    // threads 385 us, 256 393, 64 401).
+    const int32_t rounds = a.units <= 64 ? 1 : std::max(2, (a.units + 511) / 512);
+    const unsigned threads = (unsigned)std::max(1, ((a.units + rounds - 1) / rounds + 63) / 64) * 64;
     const dim3 grid(row_grid((uint32_t)tokens));
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, as_stream(stream), a); };
     auto pick = [&](auto t) {
