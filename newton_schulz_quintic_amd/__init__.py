@@ -1,8 +1,8 @@
 """MI355X (gfx950) Newton-Schulz orthogonalisation with shard routing.
 
 The work happens in the HIP library ``libnsq.so`` behind the C ABI of
-``include/ns.h``; this package is its ctypes binding (``_lib``, and ``_ops`` for
-the training-step operators) plus the in-tree build (``build``). Importing the package does not load the library;
+``include/ns.h``; this package is its ctypes binding (``_lib``), the compiled
+binding of the training-step operators (``_ops``) and the in-tree build (``build``). Importing the package does not load the library;
 the first call does, and fails loudly if it was never built.
 """
 
@@ -41,16 +41,20 @@ from ._lib import (  # noqa: F401
     ns_workspace_bytes,
 )
 from ._ops import (  # noqa: F401
-    ns_distill_topk,
-    ns_distill_topk_backward,
+    OPERATORS as _OPERATORS,
     ns_distill_workspace_bytes,
-    ns_moe_combine,
-    ns_moe_combine_backward,
-    ns_moe_dispatch,
-    ns_moe_dispatch_backward,
-    ns_moe_sort,
     ns_moe_sort_workspace_bytes,
-    ns_qk_norm_rope,
-    ns_qk_norm_rope_backward,
     ns_qk_norm_rope_workspace_bytes,
 )
+
+
+def __getattr__(name):
+    if name in _OPERATORS:
+        from ._ops import operator
+        globals()[name] = operator(name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted([*globals(), *_OPERATORS])
