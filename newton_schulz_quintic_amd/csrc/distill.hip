@@ -34,6 +34,7 @@ constexpr int kMaxRows = 1 << 24;
 constexpr int kMaxChunks = 64;            // parts of a row that is split over workgroups
 constexpr int kBitVocab = 1 << 18;        // tokens one workgroup marks in LDS (32 KiB)
 constexpr int kSplitThreads = 256;
+constexpr int kHeldVecs = 16;             // vectors of a row that a thread holds
 constexpr int kAhead = 4;                 // vectors a thread of a split row loads ahead of everything else
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kNonTemporal = 2;           // a buffer store's cache policy
@@ -101,13 +102,14 @@ __device__ inline float q_of(float z, const Norm &n, float c) { return __builtin
 // a row's pairs
 // ---------------------------------------------------------------------------
 
+template <int TOP>             // room for so many pairs
 struct PairLds {
-    int32_t id[kMaxTop + 4];   // token, -1 if absent
-    float p[kMaxTop + 4];      // first t / tau, then p
-    float t[kMaxTop];          // log p
-    float z[kMaxTop];          // student logit
-    float p_token[kMaxTop];    // p summed over the token's pairs
-    int32_t owner[kMaxTop];    // the token, in the lowest of its pairs; -1 in the others
+    int32_t id[TOP + 4];       // token, -1 if absent
+    float p[TOP + 4];
+    float t[TOP];              // teacher logit, then log p
+    float z[TOP];              // student logit
+    float p_token[TOP];        // p summed over the token's pairs
+    int32_t owner[TOP];        // the token, in the lowest of its pairs; -1 in the others
     Lse wave[16];
     float wave_sum[16];
 };
@@ -146,8 +148,8 @@ __device__ inline float teacher_of(const DistillArgs &A, const RawPair &p) {
 
 // Whether the row, whose tokens and teacher logits are in LDS, has a loss; its
 // largest teacher logit. Every wave for itself.
-template <bool REST>
-__device__ inline Pairs look_at_pairs(const DistillArgs &A, const PairLds &L) {
+template <bool REST, int TOP>
+__device__ inline Pairs look_at_pairs(const DistillArgs &A, const PairLds<TOP> &L) {
     float mx = kNegInf;
     bool any = false, nan = false;
     for (int k = threadIdx.x & 63; k < A.top_k; k += 64)
@@ -165,8 +167,8 @@ __device__ inline Pairs look_at_pairs(const DistillArgs &A, const PairLds &L) {
 }
 
 // Clears what a row's pairs are added to.
-template <bool REST>
-__device__ inline void clear_pairs(const DistillArgs &A, PairLds &L, uint32_t *bits, int words) {
+template <bool REST, int TOP>
+__device__ inline void clear_pairs(const DistillArgs &A, PairLds<TOP> &L, uint32_t *bits, int words) {
     if (threadIdx.x < 4) L.id[A.top_k + threadIdx.x] = -1, L.p[A.top_k + threadIdx.x] = 0.f;
     if constexpr (REST)
         for (int i = threadIdx.x; i < words; i += blockDim.x) bits[i] = 0;
@@ -174,8 +176,8 @@ __device__ inline void clear_pairs(const DistillArgs &A, PairLds &L, uint32_t *b
 
 // Brings the row's pairs into LDS; says whether the row has a loss. Ends with
 // every thread past the barrier.
-template <bool REST>
-__device__ inline Pairs read_pairs(const DistillArgs &A, int64_t row, PairLds &L, uint32_t *bits, int words) {
+template <bool REST, int TOP>
+__device__ inline Pairs read_pairs(const DistillArgs &A, int64_t row, PairLds<TOP> &L, uint32_t *bits, int words) {
     for (int k = threadIdx.x; k < A.top_k; k += blockDim.x) {
         const RawPair p = pair_at(A, row, k);
         L.id[k] = token_of(A, p);
@@ -193,8 +195,8 @@ __device__ inline float teacher_lse(const DistillArgs &A, int64_t row) {
 
 // p of every pair, the tokens' lowest pairs, and with REST the tokens' bits
 // among [e0, e1). Ends with every thread past a barrier.
-template <bool REST>
-__device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds &L, Pairs &r, uint32_t *bits, int e0,
+template <bool REST, int TOP>
+__device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds<TOP> &L, Pairs &r, uint32_t *bits, int e0,
                                    int e1) {
     const int lane = threadIdx.x & 63, threads = blockDim.x;
     if constexpr (REST) {
@@ -320,7 +322,8 @@ __device__ inline Lse sum_span(const T *z, float zt, const Span<T> &S, const uin
 }
 
 // Joins the threads' sums; every thread gets the result. One barrier inside.
-__device__ inline Lse block_join(Lse a, PairLds &L, float c) {
+template <int TOP>
+__device__ inline Lse block_join(Lse a, PairLds<TOP> &L, float c) {
     a = wave_join(a, c);
     if ((threadIdx.x & 63) == 0) L.wave[threadIdx.x >> 6] = a;
     __syncthreads();
@@ -330,22 +333,27 @@ __device__ inline Lse block_join(Lse a, PairLds &L, float c) {
 }
 
 // The threads' sum, in every thread; the workgroup has THREADS of them. One barrier inside.
-template <int THREADS>
-__device__ inline float block_sum(float v, PairLds &L) {
+template <int THREADS, int TOP>
+__device__ inline float block_sum(float v, PairLds<TOP> &L) {
     v = wave_sum(v);
     if ((threadIdx.x & 63) == 0) L.wave_sum[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.f;
+    if constexpr (THREADS >= 256) {
 #pragma unroll
-    for (int w = 0; w < THREADS / 64; w += 4) {
-        const float4 q = *reinterpret_cast<const float4 *>(&L.wave_sum[w]);
-        v += (q.x + q.y) + (q.z + q.w);
+        for (int w = 0; w < THREADS / 64; w += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(&L.wave_sum[w]);
+            v += (q.x + q.y) + (q.z + q.w);
+        }
+    } else {
+        for (int w = 0; w < THREADS / 64; ++w) v += L.wave_sum[w];
     }
     return v;
 }
 
 // The sum over the pairs' tokens (each once); every wave for itself.
-__device__ inline Lse sum_tokens(const DistillArgs &A, const PairLds &L, float c) {
+template <int TOP>
+__device__ inline Lse sum_tokens(const DistillArgs &A, const PairLds<TOP> &L, float c) {
     Lse a = {kNegInf, 0.f};
     for (int k = threadIdx.x & 63; k < A.top_k; k += 64)
         if (L.owner[k] >= 0) {
@@ -394,7 +402,8 @@ __device__ inline float fast_tail(float zt, const Span<T> &S, const uint32_t *bi
 struct FastBase {
     float m, hi, lo;
 };
-__device__ inline FastBase fast_base(const DistillArgs &A, const PairLds &L, float c) {
+template <int TOP>
+__device__ inline FastBase fast_base(const DistillArgs &A, const PairLds<TOP> &L, float c) {
     float m = kNegInf;
     for (int k = threadIdx.x & 63; k < A.top_k; k += 64)
         if (L.id[k] >= 0) m = fmaxf(m, L.z[k]);
@@ -470,8 +479,8 @@ __device__ inline void grad_span(const T *z, T *dz, const Span<T> &S, const Norm
 
 // The tail's gradient, then that of the pairs' tokens, each written over the
 // other tokens' formula by the thread that wrote it.
-template <typename T, typename Put>
-__device__ inline void finish_span(const DistillArgs &A, const PairLds &L, const Put &put, const Span<T> &S, float zt,
+template <typename T, typename Put, int TOP>
+__device__ inline void finish_span(const DistillArgs &A, const PairLds<TOP> &L, const Put &put, const Span<T> &S, float zt,
                                    const Norm &n, const Norm &others, float c, float g, float g_others) {
     if ((int)threadIdx.x < S.tail) put(S.e0 + S.vecs * S.N + threadIdx.x, (T)(g_others * q_of(zt, others, c)));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -496,8 +505,8 @@ __device__ inline void finish_span(const DistillArgs &A, const PairLds &L, const
 }
 
 // The row's loss and logsumexps, by the first wave.
-template <bool REST>
-__device__ inline void write_loss(const DistillArgs &A, const PairLds &L, const Pairs &r, int64_t row, const Norm &n,
+template <bool REST, int TOP>
+__device__ inline void write_loss(const DistillArgs &A, const PairLds<TOP> &L, const Pairs &r, int64_t row, const Norm &n,
                                   Lse all, Lse rest) {
     if (threadIdx.x >= 64) return;
     const float log_all = logf(all.s);
@@ -555,8 +564,8 @@ template <bool REST>
 __device__ inline float others_factor(const Pairs &r, float g, float q_rest) {
     return REST ? g * (q_rest - r.p_rest) : g;
 }
-template <bool REST>
-__device__ inline RowSums row_sums(const DistillArgs &A, const PairLds &L, const Pairs &r, float grad_loss, Lse rest,
+template <bool REST, int TOP>
+__device__ inline RowSums row_sums(const DistillArgs &A, const PairLds<TOP> &L, const Pairs &r, float grad_loss, Lse rest,
                                    float c) {
     RowSums s;
     s.rest = rest;
@@ -569,18 +578,19 @@ __device__ inline RowSums row_sums(const DistillArgs &A, const PairLds &L, const
     return s;
 }
 
-// Loss and gradient, the row in registers in between: NV vectors a thread, at
-// most one pair a thread. A workgroup takes rows in turn and loads each vector
+// Loss and gradient, the row in registers in between: kHeldVecs vectors and at
+// most one pair a thread, in the fewest threads that this takes (64 to 1024), so
+// that a CU's registers hold as many rows at once as they can. A workgroup takes rows in turn and loads each vector
 // of its next row as soon as it has written the one before. Loads return in
 // order, so what the next row needs besides (its tokens' logits, and the pairs
 // of the row after it, whose tokens those logits' addresses come from) is asked
 // for ahead of its vectors: its pairs are then weighed while its vectors come in.
 // Vectors go through buffer descriptors: lanes past the row's last whole vector
 // read zeros (not used) and write nothing.
-template <typename T, int THREADS, int NV, bool REST>
-__global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
+template <typename T, int THREADS, bool REST>
+__global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
-    __shared__ __attribute__((aligned(16))) PairLds L;
+    __shared__ __attribute__((aligned(16))) PairLds<THREADS> L;
     typedef uint32_t dwords __attribute__((ext_vector_type(4)));
     typedef typename Vec16<T>::raw raw;
     const Span<T> S(0, A.vocab);
@@ -623,14 +633,19 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
     // counts are exact there is no branch around a vector's load or store (past the row, or for no next row, their
     // descriptors end before them), and the first row's loads go out like the others': in order, each behind a store
     // (to a descriptor of length zero).
-    dwords held[NV];
+    // With one workgroup a CU and equal rows the CUs stay in step: all load, then all compute while memory rests.
+    // Over many bf16 rows those of four neighbouring XCDs start a quarter of a row apart (4096 x 131072: 480 us
+    // become 459, 1024 rows 132 become 138 if they do; f32 rows, with half the work a byte, 224 become 227).
+    if (THREADS == 1024 && sizeof(T) == 2 && A.rows >= 8 * (int)gridDim.x)
+        for (uint32_t i = 0; i < (blockIdx.x & 3) * 2; ++i) __builtin_amdgcn_s_sleep(127);
+    dwords held[kHeldVecs];
     int64_t row = blockIdx.x;
     RawPair p = pair_of(row), ahead = pair_of(row + gridDim.x);
     Beside now = beside_of(row, p);
     {
         const auto z = vecs_of(A.logits, row, A.ld, true), nowhere = vecs_of(A.logits, row, A.ld, false);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
+        for (int i = 0; i < kHeldVecs; ++i) {
             __builtin_amdgcn_raw_buffer_store_b128(dwords{0, 0, 0, 0}, nowhere, tid * 16 + i * THREADS * 16, 0, 0);
             held[i] = __builtin_amdgcn_raw_buffer_load_b128(z, tid * 16 + i * THREADS * 16, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
@@ -648,12 +663,12 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
         Pairs r = look_at_pairs<REST>(A, L);
         weigh_pairs<REST>(A, now.teacher_lse, L, r, bits, 0, A.vocab);
         int at = tid;
-        asm volatile("" : "+v"(at));   // what follows from it is found anew for each row, not held in 2 NV registers
+        asm volatile("" : "+v"(at));   // what follows from it is found anew for each row, not held in 2 kHeldVecs registers
         const float zt = (float)now.zt;
         const FastBase f0 = fast_base(A, L, c);
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
+        for (int i = 0; i < kHeldVecs; ++i) {
             const int left = S.vecs - i * THREADS;
             if (left > 0 && (left >= THREADS || at < left)) {
                 const uint32_t skip = REST ? vec_bits(bits, at + i * THREADS, S.N) : 0;
@@ -666,7 +681,7 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
         if (!fast) {
             Lse a = {kNegInf, 0.f};
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
+            for (int i = 0; i < kHeldVecs; ++i) {
                 const int v = at + i * THREADS;
                 if (v < S.vecs) add_vec<T, REST>(a, __builtin_bit_cast(raw, held[i]), REST ? vec_bits(bits, v, S.N) : 0, c);
             }
@@ -683,7 +698,7 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
         const FastFactor f = fast_factor<T>(s.g_others * s.others.scale * __builtin_amdgcn_exp2f(-f0.lo), f0.hi);
         const auto turn = [&](auto value) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
+            for (int i = 0; i < kHeldVecs; ++i) {
                 raw o = {};
                 if (r.some && S.vecs > i * THREADS) o = value(__builtin_bit_cast(raw, held[i]));
                 // soffset stays 0: with an SGPR there the compiler takes it that the store has read its data at
@@ -717,7 +732,7 @@ __global__ __launch_bounds__(THREADS) void distill_held_kernel(DistillArgs A) {
 template <typename T, bool REST, bool NT>
 __global__ __launch_bounds__(kSplitThreads) void distill_row_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
-    __shared__ __attribute__((aligned(16))) PairLds L;
+    __shared__ __attribute__((aligned(16))) PairLds<kMaxTop> L;
     const Span<T> S(0, A.vocab);
     const float c = A.inv_tau * kLog2e;
     for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
@@ -752,7 +767,7 @@ __global__ __launch_bounds__(kSplitThreads) void distill_row_kernel(DistillArgs 
 template <typename T, bool REST>
 __global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
-    __shared__ __attribute__((aligned(16))) PairLds L;
+    __shared__ __attribute__((aligned(16))) PairLds<kMaxTop> L;
     const float c = A.inv_tau * kLog2e;
     for (uint32_t b = blockIdx.x; b < (uint32_t)A.rows * A.chunks; b += gridDim.x) {
         const int64_t row = b / (uint32_t)A.chunks;
@@ -778,7 +793,7 @@ __global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillA
 template <typename T, bool REST, bool LOSS, bool NT>
 __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArgs A, int32_t parts) {
     extern __shared__ uint32_t bits[];
-    __shared__ __attribute__((aligned(16))) PairLds L;
+    __shared__ __attribute__((aligned(16))) PairLds<kMaxTop> L;
     const float c = A.inv_tau * kLog2e;
     for (uint32_t b = blockIdx.x; b < (uint32_t)A.rows * A.chunks; b += gridDim.x) {
         const int64_t row = b / (uint32_t)A.chunks;
@@ -855,15 +870,22 @@ void set_chunks(DistillArgs &a) {
     a.chunks = (a.vocab + a.chunk - 1) / a.chunk;
 }
 
-// Which rows are held in registers (a thread for each pair, at most 16 vectors a thread).
-int64_t held_vecs(const DistillArgs &a, int es) { return std::max<int64_t>((int64_t)a.vocab * es / 16, 8 * a.top_k); }
+// Threads that hold a row in registers and have a pair each; over 1024 for a row
+// that cannot be held. (More of them where few rows leave some idle gained
+// nothing: 300 x 8192 bf16 13.7 us, with 512 threads in place of 64 15.8.)
+int64_t held_threads(const DistillArgs &a, int es) {
+    const int64_t vecs = (int64_t)a.vocab * es / 16;
+    int64_t threads = 64;
+    while (threads <= 1024 && (vecs > kHeldVecs * threads || a.top_k > threads)) threads *= 2;
+    return threads;
+}
 // Which calls split their rows over workgroups and run two kernels. Training
 // holds rows that it can from 256 on (one a CU; 600 x 131072 bf16: 81 us, split
 // 91); otherwise rows are read one to a workgroup of 256 threads once these fill
 // the GPU (600 x 131072 bf16 forward: split 38 us, a workgroup a row 44).
 bool split_rows(const DistillArgs &a, int es) {
     if (a.teacher_lse && a.vocab > kBitVocab) return true;
-    return a.rows < (a.dlogits && held_vecs(a, es) <= 16384 ? 256 : 1024);
+    return a.rows < (a.dlogits && held_threads(a, es) <= 1024 ? 256 : 1024);
 }
 
 size_t distill_workspace(int64_t rows, int32_t top_k, bool split) {
@@ -932,14 +954,18 @@ ns_status launch_rows(const DistillArgs &a, hipStream_t st) {
     auto go = [&](auto kernel, int threads, int64_t most) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(a.rows, most)), dim3(threads), lds, st, a);
     };
-    // Held rows: as many workgroups as are resident at once (16 waves a CU).
-    const int64_t vecs = held_vecs(a, sizeof(T));
-    if (!a.dlogits) go(distill_row_kernel<T, REST, false>, 256, 1 << 20);
-    else if (vecs <= 2048) go(distill_held_kernel<T, 256, 8, REST>, 256, 1024);
-    else if (vecs <= 4096) go(distill_held_kernel<T, 512, 8, REST>, 512, 512);
-    else if (vecs <= 8192) go(distill_held_kernel<T, 1024, 8, REST>, 1024, 256);
-    else if (vecs <= 16384) go(distill_held_kernel<T, 1024, 16, REST>, 1024, 256);
-    else past_cache(a, sizeof(T)) ? go(distill_row_kernel<T, REST, true>, 256, 1 << 20) : go(distill_row_kernel<T, REST, false>, 256, 1 << 20);
+    // Held rows: as many workgroups as are resident at once, 16 waves a CU.
+    const auto held = [&](auto kernel, int threads) { go(kernel, threads, 256 * (1024 / threads)); };
+    switch (a.dlogits ? held_threads(a, sizeof(T)) : 2048) {
+    case 64: held(distill_held_kernel<T, 64, REST>, 64); break;
+    case 128: held(distill_held_kernel<T, 128, REST>, 128); break;
+    case 256: held(distill_held_kernel<T, 256, REST>, 256); break;
+    case 512: held(distill_held_kernel<T, 512, REST>, 512); break;
+    case 1024: held(distill_held_kernel<T, 1024, REST>, 1024); break;
+    default:
+        if (a.dlogits && past_cache(a, sizeof(T))) go(distill_row_kernel<T, REST, true>, kSplitThreads, 1 << 20);
+        else go(distill_row_kernel<T, REST, false>, kSplitThreads, 1 << 20);
+    }
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }

@@ -243,6 +243,25 @@ def test_qk_many_tokens():
     _check_backward(c, dk, dwk, c["k64"], c["gk64"], c["wk64"], False, 1e-6, "k")
 
 
+def test_qk_large_call_gives_the_bits_of_its_parts():
+    """A call that moves more than the last-level cache holds (its stores take another path), sequence by sequence."""
+    import torch
+    log("qk large")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    q, g = (torch.randn(9, 2048, 32, 128, device="cuda", generator=gen, dtype=torch.bfloat16) for _ in "qg")
+    cos, sin = torch.rand(2048, 64, device="cuda"), torch.rand(2048, 64, device="cuda")
+    out, dq = torch.empty_like(q), torch.empty_like(q)
+    nsq.ns_qk_norm_rope(q, None, out, None, cos=cos, sin=sin)
+    nsq.ns_qk_norm_rope_backward(q, None, g, None, dq, None, cos=cos, sin=sin)
+    part, dpart = torch.empty_like(q[:1]), torch.empty_like(q[:1])
+    for b in range(9):
+        nsq.ns_qk_norm_rope(q[b:b + 1], None, part, None, cos=cos, sin=sin)
+        nsq.ns_qk_norm_rope_backward(q[b:b + 1], None, g[b:b + 1], None, dpart, None, cos=cos, sin=sin)
+        torch.cuda.synchronize()
+        assert torch.equal(part[0], out[b]) and torch.equal(dpart[0], dq[b])
+
+
 def test_qk_offsets_past_32_bits():
     import torch
     log("qk far")
@@ -389,6 +408,44 @@ def test_moe_map_entries_outside_the_rows_are_left_alone():
     torch.cuda.synchronize()
     assert torch.equal(xs[[0, 3]], x) and (xs[1:3] == 5).all() and torch.equal(out, x)
     assert torch.equal(dy[[0, 3]], x) and (dy[1:3] == 5).all() and dw[0, 1] == 0 and dw[1, 0] == 0
+
+
+@pytest.mark.parametrize("dtype,hidden", [("bf16", 4096), ("f32", 2049)])
+def test_moe_large_calls_give_the_bits_of_their_parts(dtype, hidden):
+    """Calls that move more than the last-level cache holds (their rows take another path), token range by token range."""
+    import torch
+    log(f"moe large {dtype} {hidden}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    t, k = 9000, 4
+    x, g = (torch.randn(t, hidden, device="cuda", generator=gen).to(_torch_dtype(dtype)) for _ in "xg")
+    y = torch.randn(t * k, hidden, device="cuda", generator=gen).to(_torch_dtype(dtype))
+    w = torch.rand(t, k, device="cuda", generator=gen)
+    row = torch.randperm(t * k, device="cuda", generator=gen).to(torch.int32).view(t, k)
+    row[5] = ~row[5]
+    xs, dy, out, dx = (torch.empty_like(v) for v in (y, y, x, x))
+    dw = torch.empty_like(w)
+    nsq.ns_moe_dispatch(x, row, xs)
+    nsq.ns_moe_combine(y, row, w, out)
+    nsq.ns_moe_dispatch_backward(y, row, dx)
+    nsq.ns_moe_combine_backward(g, y, row, w, dy, dw)
+    torch.cuda.synchronize()
+    kept = (row >= 0)[:, :, None]
+    at = torch.where(row >= 0, row, ~row).long()
+    assert torch.equal(xs[at], torch.where(kept, x[:, None], torch.zeros_like(x[:1])))
+    for a in range(0, t, 1500):
+        # the same tokens with their rows brought together
+        s, n = slice(a, a + 1500), 1500 * k
+        some = torch.arange(n, device="cuda", dtype=torch.int32).view(1500, k)
+        some = torch.where(row[s] >= 0, some, ~some)
+        ys = y[at[s].reshape(-1)].contiguous()
+        o, d, e, f = torch.empty_like(x[s]), torch.empty_like(x[s]), torch.empty_like(ys), torch.empty_like(w[s])
+        nsq.ns_moe_combine(ys, some, w[s], o)
+        nsq.ns_moe_dispatch_backward(ys, some, d)
+        nsq.ns_moe_combine_backward(g[s], ys, some, w[s], e, f)
+        torch.cuda.synchronize()
+        assert torch.equal(o, out[s]) and torch.equal(d, dx[s]) and torch.equal(f, dw[s])
+        assert torch.equal(e, dy[at[s].reshape(-1)])
 
 
 def test_moe_offsets_past_32_bits():
@@ -557,13 +614,40 @@ def test_distill_few_rows(n, v, k, kind, dtype, rest, form):
     _check_distill(c, _distill_run(c, form))
 
 
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype,n,v,k", [("bf16", 2600, 33000, 8), ("f32", 1100, 40001, 8), ("bf16", 2100, 70002, 5),
+                                         ("f32", 1030, 70001, 5), ("bf16", 2200, 131072, 5), ("bf16", 9000, 1001, 5)])
+def test_distill_rows_over_rounds_and_past_the_cache(dtype, n, v, k, rest):
+    """Several rows a workgroup one after the other, and gradients stored past the cache, each row as by itself."""
+    import torch
+    log(f"distill rounds {dtype} {n} {v} {rest}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(v)
+    z = (torch.randn(n, v, device="cuda", generator=gen) * 2).to(_torch_dtype(dtype))
+    ids = torch.randint(0, v, (n, 1), device="cuda", generator=gen) + torch.arange(k, device="cuda") * (v // k // 2)
+    ids = (ids % v).to(torch.int32)
+    ids[::13] = -1
+    t, g = torch.randn(n, k, device="cuda", generator=gen) + 4, torch.rand(n, device="cuda", generator=gen)
+    tl = torch.logsumexp(t, 1) + 0.3 if rest else None
+    rng = np.random.default_rng(v)
+    rows = np.unique(np.concatenate([rng.integers(0, n, 4), [0, 1, n - 1]]))
+    c = {"tau": 1.0, "dtype": dtype, "z": z, "ids_d": ids, "t": t, "g": g, "lse_d": tl}
+    pick = torch.from_numpy(rows).cuda()
+    c64 = dict(c, z64=_f64(z[pick]), ids=ids[pick].cpu().numpy(), t64=_f64(t[pick]), g64=_f64(g[pick]),
+               lse64=None if tl is None else _f64(tl[pick]))
+    for form in ("train", "step"):
+        got = _distill_run(c, form)
+        _check_distill(c64, tuple(None if x is None else x[pick] for x in got))
+
+
 @pytest.mark.parametrize("form", ["train", "step"])
 @pytest.mark.parametrize("rest", [False, True])
 @pytest.mark.parametrize("dtype,n,v,k,kind", [
     ("bf16", 257, 500, 5, "masked"), ("f32", 300, 77, 9, "masked"), ("bf16", 260, 20001, 16, "plain"),
     ("f32", 258, 12345, 16, "plain"), ("f32", 256, 20001, 8, "plain"), ("bf16", 256, 66001, 70, "plain"),
     ("bf16", 256, 131072, 64, "plain"), ("f32", 256, 50021, 20, "plain"), ("bf16", 257, 140003, 12, "plain"),
-    ("f32", 256, 70001, 12, "plain"), ("bf16", 256, 300, 300, "plain"),
+    ("f32", 256, 70001, 12, "plain"), ("bf16", 256, 300, 300, "plain"), ("bf16", 300, 5000, 200, "masked"),
+    ("f32", 300, 2000, 700, "plain"), ("bf16", 300, 16385, 100, "masked"), ("f32", 1100, 900, 9, "masked"),
 ])
 def test_distill_many_rows(dtype, n, v, k, kind, rest, form):
     """One workgroup a row, in every form of it: rows held in registers of 256 to 1024 threads, and read twice."""
