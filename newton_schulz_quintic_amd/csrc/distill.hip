@@ -74,14 +74,9 @@ __device__ inline Lse join(Lse a, Lse b, float c) {
     const float m = fmaxf(a.m, b.m);
     return {m, a.s * shifted(a.m, m, c) + b.s * shifted(b.m, m, c)};
 }
-__device__ inline Lse wave_join(Lse a, float c) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) a = join(a, {__shfl_xor(a.m, d), __shfl_xor(a.s, d)}, c);
-    return a;
-}
-__device__ inline float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+template <int STEP = 0>
+__device__ inline Lse wave_join(Lse v, float c) {
+    if constexpr (STEP < 6) return wave_join<STEP + 1>(join(v, {partner<STEP>(v.m), partner<STEP>(v.s)}, c), c);
     return v;
 }
 
@@ -775,14 +770,18 @@ __global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillA
         const int e0 = chunk * A.chunk, e1 = min(e0 + A.chunk, A.vocab);
         const Span<T> S(e0, e1);
         const T *z = reinterpret_cast<const T *>(A.logits) + row * A.ld;
-        if (REST || chunk == 0) {
+        const float zt = tail_of<T>(z, S);
+        if (chunk == 0)
+            for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) {
+                const int id = token_of(A, pair_at(A, row, k));
+                A.top_z[row * A.top_k + k] = id >= 0 ? (float)z[id] : 0.f;
+            }
+        if constexpr (REST) {
+            const float lse = teacher_lse<REST>(A, row);
             Pairs r = read_pairs<REST>(A, row, L, bits, (A.chunk + 31) >> 5);
-            if (chunk == 0)
-                for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads)
-                    A.top_z[row * A.top_k + k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
-            if constexpr (REST) weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, e0, e1);
+            weigh_pairs<REST>(A, lse, L, r, bits, e0, e1);
         }
-        const Lse a = block_join(sum_span<T, REST>(z, tail_of<T>(z, S), S, bits, c), L, c);
+        const Lse a = block_join(sum_span<T, REST>(z, zt, S, bits, c), L, c);
         if (threadIdx.x == 0) A.partial[row * A.chunks + chunk] = make_float2(a.m, a.s);
         __syncthreads();   // the next part uses the same LDS
     }
@@ -811,20 +810,22 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
         const float zt = tail_of<T>(z, S);
         float2 part = make_float2(kNegInf, 0.f);   // at most kMaxChunks = 64: one a lane
         if (LOSS && (int)(threadIdx.x & 63) < parts) part = A.partial[row * parts + (threadIdx.x & 63)];
+        const float g = A.dlogits ? A.grad_loss[row] : 0.f, t_lse = teacher_lse<REST>(A, row);
+        if (LOSS)
+            for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) L.z[k] = A.top_z[row * A.top_k + k];
         Pairs r = read_pairs<REST>(A, row, L, bits, 0);
         if (!r.some) {
             write_empty<T, REST>(A, row, S, LOSS && chunk == 0);
             __syncthreads();
             continue;
         }
-        for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) {
-            const int id = L.id[k];
-            if (LOSS) L.z[k] = A.top_z[row * A.top_k + k];
-            else L.z[k] = id >= e0 && id < e1 ? (float)z[id] : 0.f;
-        }
-        weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, 0, 0);
+        if (!LOSS)
+            for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) {
+                const int id = L.id[k];
+                L.z[k] = id >= e0 && id < e1 ? (float)z[id] : 0.f;
+            }
+        weigh_pairs<REST>(A, t_lse, L, r, bits, 0, 0);
         RowSums s{};
-        const float g = A.dlogits ? A.grad_loss[row] : 0.f;
         if constexpr (LOSS) {
             s = row_sums<REST>(A, L, r, g, wave_join({part.x, part.y}, c), c);
         } else {

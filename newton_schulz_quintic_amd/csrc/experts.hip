@@ -189,17 +189,33 @@ struct RowArgs {
     uint32_t slots;          // tokens x top_k: rows of the sorted side
 };
 
-// A slot's entry in the map: its row, and whether it was kept. An entry that
-// names no row of the buffer (no map of ns_moe_sort's holds one) is left alone.
-struct RowRef {
-    int64_t row;
-    bool kept, in;
+// A token's map entries and weights, KC choices from k0 on, all asked for at once
+// and through the scalar cache (no kernel that reads them writes them). An entry
+// that names no row of the buffer (no map of ns_moe_sort's holds one) is left
+// alone.
+template <int KC, bool W> struct Choices {
+    int64_t row[KC];
+    bool kept[KC], in[KC];
+    float w[KC];
+    __device__ Choices(const RowArgs &A, int64_t token, int k0) {
+        const int32_t NSQ_CONST *map = (const int32_t NSQ_CONST *)(A.row_of_slot + token * A.top_k);
+        const float NSQ_CONST *weights = (const float NSQ_CONST *)(A.w + token * A.top_k);
+        int32_t r[KC];
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+            const int k = min(k0 + j, A.top_k - 1);
+            r[j] = map[k];
+            w[j] = W ? weights[k] : 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+            const uint32_t at = r[j] < 0 ? ~r[j] : r[j];
+            row[j] = at;
+            in[j] = k0 + j < A.top_k && at < A.slots;
+            kept[j] = in[j] && r[j] >= 0;
+        }
+    }
 };
-__device__ inline RowRef row_ref(const RowArgs &A, int64_t slot) {
-    const int32_t r = A.row_of_slot[slot];
-    const uint32_t row = r < 0 ? ~r : r;
-    return {(int64_t)row, r >= 0 && row < A.slots, row < A.slots};
-}
 
 // Unit u of a row of `hidden` elements; elements past its end read as zero and are not written.
 // NT: read or written past the cache.
@@ -226,16 +242,20 @@ __device__ inline void store_unit(T *row, int u, int hidden, typename Vec16<T>::
 // xs[row] = x[token]: a thread reads one unit and writes it K times.
 template <typename T, bool NT>
 __global__ __launch_bounds__(128) void moe_dispatch_kernel(RowArgs A) {
+    constexpr int KC = 8;
     for (uint32_t b = blockIdx.x; b < A.blocks; b += gridDim.x) {
         const uint32_t t32 = b / (uint32_t)A.pieces;
         const int64_t t = t32;
         const int u = (int)(b - t32 * A.pieces) * blockDim.x + threadIdx.x;
         if (u >= A.units) continue;
         const auto v = load_unit<T, false>(reinterpret_cast<const T *>(A.x) + t * A.x_ld, u, A.hidden);
-        for (int k = 0; k < A.top_k; ++k) {
-            const RowRef r = row_ref(A, t * A.top_k + k);
-            typename Vec16<T>::raw z = {};
-            if (r.in) store_unit<T, NT>(reinterpret_cast<T *>(A.rows) + r.row * A.rows_ld, u, A.hidden, r.kept ? v : z);
+        for (int k0 = 0; k0 < A.top_k; k0 += KC) {
+            const Choices<KC, false> c(A, t, k0);
+            const typename Vec16<T>::raw z = {};
+#pragma unroll
+            for (int j = 0; j < KC; ++j)
+                if (c.in[j])
+                    store_unit<T, NT>(reinterpret_cast<T *>(A.rows) + c.row[j] * A.rows_ld, u, A.hidden, c.kept[j] ? v : z);
         }
     }
 }
@@ -251,25 +271,16 @@ __global__ __launch_bounds__(128) void moe_combine_kernel(RowArgs A) {
         if (u >= A.units) continue;
         float acc[N] = {};
         for (int k0 = 0; k0 < A.top_k; k0 += KC) {
+            const Choices<KC, W> c(A, t, k0);
             typename Vec16<T>::raw v[KC];
-            float w[KC];
-            bool kept[KC];
-#pragma unroll
-            for (int j = 0; j < KC; ++j) {
-                kept[j] = false;
-                if (k0 + j < A.top_k) {
-                    const int64_t s = t * A.top_k + k0 + j;
-                    const RowRef r = row_ref(A, s);
-                    kept[j] = r.kept;
-                    w[j] = W ? A.w[s] : 1.f;
-                    if (kept[j]) v[j] = load_unit<T, NT>(reinterpret_cast<const T *>(A.y) + r.row * A.y_ld, u, A.hidden);
-                }
-            }
 #pragma unroll
             for (int j = 0; j < KC; ++j)
-                if (kept[j])
+                if (c.kept[j]) v[j] = load_unit<T, NT>(reinterpret_cast<const T *>(A.y) + c.row[j] * A.y_ld, u, A.hidden);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) acc[i] += w[j] * elem<T>(v[j], i);
+            for (int j = 0; j < KC; ++j)
+                if (c.kept[j])
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] += c.w[j] * elem<T>(v[j], i);
         }
         typename Vec16<T>::raw o;
 #pragma unroll
@@ -288,36 +299,27 @@ __global__ __launch_bounds__(512) void moe_combine_backward_kernel(RowArgs A) {
     for (int64_t t = blockIdx.x; t < A.tokens; t += gridDim.x) {
         const T *g = reinterpret_cast<const T *>(A.x) + t * A.x_ld;
         for (int k0 = 0; k0 < A.top_k; k0 += KC) {
-            RowRef r[KC];
-            float w[KC], dot[KC];
-#pragma unroll
-            for (int j = 0; j < KC; ++j) {
-                r[j] = {0, false, false};
-                w[j] = dot[j] = 0.f;
-                if (k0 + j < A.top_k) {
-                    r[j] = row_ref(A, t * A.top_k + k0 + j);
-                    if (r[j].kept) w[j] = A.w[t * A.top_k + k0 + j];
-                }
-            }
+            const Choices<KC, true> c(A, t, k0);
+            float dot[KC] = {};
             for (int u = threadIdx.x; u < A.units; u += blockDim.x) {
                 const auto gv = load_unit<T, NT>(g, u, A.hidden);
                 typename Vec16<T>::raw v[KC];
 #pragma unroll
                 for (int j = 0; j < KC; ++j)
-                    if (r[j].kept)
-                        v[j] = load_unit<T, NT>(reinterpret_cast<const T *>(A.y) + r[j].row * A.y_ld, u, A.hidden);
+                    if (c.kept[j])
+                        v[j] = load_unit<T, NT>(reinterpret_cast<const T *>(A.y) + c.row[j] * A.y_ld, u, A.hidden);
 #pragma unroll
                 for (int j = 0; j < KC; ++j) {
-                    if (!r[j].in) continue;
+                    if (!c.in[j]) continue;
                     typename Vec16<T>::raw o = {};
-                    if (r[j].kept) {
+                    if (c.kept[j]) {
 #pragma unroll
                         for (int i = 0; i < N; ++i) {
                             dot[j] += elem<T>(gv, i) * elem<T>(v[j], i);
-                            set_elem<T>(o, i, w[j] * elem<T>(gv, i));
+                            set_elem<T>(o, i, c.w[j] * elem<T>(gv, i));
                         }
                     }
-                    store_unit<T, NT>(reinterpret_cast<T *>(A.rows) + r[j].row * A.rows_ld, u, A.hidden, o);
+                    store_unit<T, NT>(reinterpret_cast<T *>(A.rows) + c.row[j] * A.rows_ld, u, A.hidden, o);
                 }
             }
 #pragma unroll

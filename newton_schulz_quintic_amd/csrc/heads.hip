@@ -142,7 +142,6 @@ __device__ inline void load_weight(const HeadArgs &A, const void *w, const Place
 }
 
 // The token's position (read through the scalar cache: no kernel writes it).
-#define NSQ_CONST __attribute__((address_space(4)))
 __device__ inline int64_t position(const HeadArgs &A, uint32_t token) {
     const uint32_t b = token / A.seq, s = token - b * A.seq;
     if (!A.pos) return s;
@@ -208,11 +207,6 @@ __device__ inline void turn(bool interleaved, float dir, float (&a)[VEC], float 
             b[2 * i + 1] = v * c[VEC / 2 + i] + u * r;
         }
     }
-}
-
-__device__ inline float group_sum(float v, int lg) {
-    for (int m = 1 << lg >> 1; m; m >>= 1) v += __shfl_xor(v, m);
-    return v;
 }
 
 // One (batch, seq, heads, head_dim) operand as a lane sees it: its head's offset is the same at every token.

@@ -49,9 +49,39 @@ template <> __device__ inline void set_elem<__bf16>(Vec16<__bf16>::raw &v, int i
 }
 template <> __device__ inline void set_elem<float>(Vec16<float>::raw &v, int i, float x) { v[i] = x; }
 
+// Memory that no running kernel writes: loads from uniform addresses go through the scalar cache.
+#define NSQ_CONST __attribute__((address_space(4)))
+
+// Butterfly over a wave's lanes: after steps 0 .. n-1 every lane of a group of
+// 2^n holds the group's result. partner() is the value of a lane of the
+// neighbouring group: within rows of 16 lanes a VALU operand modifier (a shuffle
+// through LDS takes some 60 cycles), across them a shuffle.
+template <int STEP>
+__device__ inline float partner(float v) {
+    if constexpr (STEP >= 4) return __shfl_xor(v, 1 << STEP);
+    constexpr int ctrl = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140;   // quad_perm, mirrors
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), ctrl, 0xf, 0xf, true));
+}
+template <int STEP, int STEPS, typename Op>
+__device__ inline float lanes_join(float v, const Op &op) {
+    if constexpr (STEP < STEPS) return lanes_join<STEP + 1, STEPS>(op(v, partner<STEP>(v)), op);
+    return v;
+}
 __device__ inline float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+    return lanes_join<0, 6>(v, [](float a, float b) { return a + b; });
+}
+__device__ inline float wave_max(float v) {
+    return lanes_join<0, 6>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+// Sum over groups of 2^lg lanes.
+__device__ inline float group_sum(float v, int lg) {
+    const auto add = [](float a, float b) { return a + b; };
+    if (lg > 0) v = lanes_join<0, 1>(v, add);
+    if (lg > 1) v = lanes_join<1, 2>(v, add);
+    if (lg > 2) v = lanes_join<2, 3>(v, add);
+    if (lg > 3) v = lanes_join<3, 4>(v, add);
+    if (lg > 4) v = lanes_join<4, 5>(v, add);
+    if (lg > 5) v = lanes_join<5, 6>(v, add);
     return v;
 }
 
