@@ -35,31 +35,32 @@ constexpr int kMaxHeads = 1024;
 // Workgroups of a launch, for pieces of 8, 4 and 1 elements: as many as are
 // resident at once by the kernels' registers, so that a wave keeps its weights
 // and its place in a head over all its tokens. 16384 tokens of 32 + 8 bf16 heads
-// of 128, forward: 1024 workgroups 66 us, 1280 (a second, partial round) 77, a
-// wave for each token 81. Backward: 512 104 us, 768 106, 1024 118.
+// of 128, forward: 1024 workgroups 63.6 us, 2048 64.2, 1536 (a second, partial
+// round) 67.4. Backward: 512 94 us, 768 100, 1024 110, 384 110.
 constexpr int blocks_for(int vec, bool backward) {
     return backward ? (vec == 4 ? 1024 : 512) : (vec == 8 ? 1024 : vec == 4 ? 2048 : 768);
 }
 constexpr int kMostPartials = 1024;
 // Outputs of calls that move more than the last-level cache holds are stored
-// past it: 66 us become 63 in the case above, 104 become 102. Smaller ones stay in
+// past it: 66 us became 63 in the case above, 104 102. Smaller ones stay in
 // it for the kernel that reads them next (35 us against 43 for 45 MB each way):
 // see deal().
 
-struct HeadSet {
-    char *x, *g, *y;                 // input, gradient of the output (backward), output
-    int64_t xb, xt, xh;              // element strides: batch, token, head
-    int64_t gb, gt, gh;
-    int64_t yb, yt, yh;
-    const void *w;
-    int32_t heads, chunks;           // chunks of 64 / G heads
-    int32_t blocks, stride;          // workgroups of the set, tokens taken at once
-    float *dw;
+// One (batch, seq, heads, head_dim) tensor: address, and element strides of batch, token and head.
+struct Operand {
+    char *p;
+    int64_t b, t, h;
 };
 
 struct HeadArgs {
-    HeadSet s[2];                    // queries, keys: the first s[0].blocks workgroups, the others
+    Operand x[2], g[2], y[2];        // of the queries and of the keys: input, gradient of the output (backward), output
+    const void *w[2];
+    float *dw[2];
+    int32_t heads[2];
     uint32_t seq, tokens;            // tokens = batch x seq
+    uint32_t chunks, stride;         // chunks of 64 / G heads, queries before keys; tokens taken at once
+    uint32_t step_i, step_s;         // stride = step_i seq + step_s
+    int32_t blocks;
     int32_t D, R, P, RP;             // head size, rotated part, pairs of pieces per head, rotated ones
     int32_t lg;                      // log2 G
     int32_t interleaved, w_f32;
@@ -69,7 +70,7 @@ struct HeadArgs {
     const void *pos;
     int32_t pos_bytes;
     int64_t pos_bs;
-    float *partial;                  // backward: [workgroups][D]
+    float *partial;                  // backward: [workgroups][queries, keys][D]
 };
 
 // VEC elements at any element alignment, as one or two loads or stores.
@@ -141,15 +142,6 @@ __device__ inline void load_weight(const HeadArgs &A, const void *w, const Place
     }
 }
 
-// The token's position (read through the scalar cache: no kernel writes it).
-__device__ inline int64_t position(const HeadArgs &A, uint32_t token) {
-    const uint32_t b = token / A.seq, s = token - b * A.seq;
-    if (!A.pos) return s;
-    const int64_t at = b * A.pos_bs + s;
-    if (A.pos_bytes == 8) return *(const int64_t NSQ_CONST *)(reinterpret_cast<const int64_t *>(A.pos) + at);
-    return *(const int32_t NSQ_CONST *)(reinterpret_cast<const int32_t *>(A.pos) + at);
-}
-
 // cos and sin of a position's angles: from a descriptor of one table row, of length
 // zero for a position outside the table; such a row's values are then set to NaN.
 template <int VEC, int NP> struct Angles {
@@ -209,66 +201,96 @@ __device__ inline void turn(bool interleaved, float dir, float (&a)[VEC], float 
     }
 }
 
-// One (batch, seq, heads, head_dim) operand as a lane sees it: its head's offset is the same at every token.
-struct Walk {
-    char *p;
-    int64_t b, t;
-    template <typename T> __device__ inline T *at(const HeadArgs &A, uint32_t token) const {
-        const uint32_t i = token / A.seq, s = token - i * A.seq;
-        return reinterpret_cast<T *>(p) + (i * b + s * t);
+// A wave's place in (batch, seq), moved on by `stride` tokens at a time, and an
+// operand's address there as a lane sees it (its set's strides, its head), which
+// follows by additions: the way of one step, and of the turn into the next batch.
+struct Cursor {
+    uint32_t i, s;
+    __device__ inline bool step(const HeadArgs &A) {
+        i += A.step_i;
+        s += A.step_s;
+        const bool turned = s >= A.seq;
+        if (turned) i += 1, s -= A.seq;
+        return turned;
     }
 };
 
-// Forward, or with BWD the gradient. A wave holds chunk w % chunks of its set's
-// heads and takes the tokens w / chunks, + stride, ...; the next token's values
-// and angles are on their way while it computes. Lanes without a head or a piece
-// load another's and store nothing.
+// The token's position (read through the scalar cache: no kernel writes it).
+__device__ inline int64_t position(const HeadArgs &A, Cursor c) {
+    if (!A.pos) return c.s;
+    const int64_t at = c.i * A.pos_bs + c.s;
+    if (A.pos_bytes == 8) return *(const int64_t NSQ_CONST *)(reinterpret_cast<const int64_t *>(A.pos) + at);
+    return *(const int32_t NSQ_CONST *)(reinterpret_cast<const int32_t *>(A.pos) + at);
+}
+
+template <typename T> struct Walk {
+    T *p;
+    int64_t step, turn;
+    __device__ Walk(const HeadArgs &A, const Operand (&of)[2], bool key, int64_t head, Cursor at) {
+        const int64_t b = key ? of[1].b : of[0].b, t = key ? of[1].t : of[0].t;
+        p = reinterpret_cast<T *>(key ? of[1].p : of[0].p) + head * (key ? of[1].h : of[0].h) + at.i * b + at.s * t;
+        step = A.step_i * b + A.step_s * t;
+        turn = b - (int64_t)A.seq * t;
+    }
+    __device__ inline void move(bool turned) {
+        p += step;
+        if (turned) p += turn;
+    }
+};
+
+// Forward, or with BWD the gradient. A wave holds chunk w % chunks of the heads
+// (queries, then keys) and takes the tokens w / chunks, + stride, ...; the next
+// token's values and angles are on their way while it computes. Lanes without a
+// head or a piece load another's and store nothing.
 template <typename T, int VEC, int NP, bool BWD, bool NT>
 __global__ __launch_bounds__(kThreads) void qk_kernel(HeadArgs A) {
     typedef Piece<T, VEC> PT;
     typedef typename PT::raw raw;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const bool key = (int)blockIdx.x >= A.s[0].blocks;
-    const HeadSet S = key ? A.s[1] : A.s[0];
-    const uint32_t w = (blockIdx.x - (key ? A.s[0].blocks : 0)) * kWaves + wave;
-    const uint32_t first = w / (uint32_t)S.chunks, chunk = w - first * S.chunks;
+    const uint32_t w = blockIdx.x * kWaves + wave;
+    const uint32_t first = w / A.chunks, chunk = w - first * A.chunks;
     const int head = (int)chunk * (64 >> A.lg) + (lane >> A.lg);
-    const bool here = head < S.heads;
-    const int64_t h = here ? head : 0;
+    const bool here = head < A.heads[0] + A.heads[1];
+    const bool key = A.heads[0] == 0 || (here && head >= A.heads[0]);
+    const int64_t h = !here ? 0 : key ? head - A.heads[0] : head;
     Place pl[NP];
     float wa[NP][VEC], wb[NP][VEC], dwa[NP][VEC], dwb[NP][VEC];
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
         pl[n] = place_of<VEC>(A, (lane & ((1 << A.lg) - 1)) + (n << A.lg));
-        load_weight<VEC>(A, S.w, pl[n], wa[n], wb[n]);
+        load_weight<VEC>(A, key ? A.w[1] : A.w[0], pl[n], wa[n], wb[n]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dwa[n][i] = dwb[n][i] = 0.f;
     }
-    const Walk X = {S.x, S.xb, S.xt}, G = {S.g, S.gb, S.gt}, Y = {S.y, S.yb, S.yt};
+    // waves past the last whole round of chunks have no tokens
+    const uint32_t stride = A.stride, begin = first < stride ? first : A.tokens;
+    Cursor ahead;
+    ahead.i = begin < A.tokens ? begin / A.seq : 0;
+    ahead.s = begin < A.tokens ? begin - ahead.i * A.seq : 0;
+    Walk<T> X(A, A.x, key, h, ahead), G(A, A.g, key, h, ahead), Y(A, A.y, key, h, ahead);
     const float inv_d = 1.f / (float)A.D;
     raw xa[NP], xb[NP], ga[NP], gb[NP];
     Angles<VEC, NP> ang;
-    const auto load = [&](uint32_t token) {
-        const T *x = X.at<T>(A, token) + h * S.xh;
-        const T *g = BWD ? G.at<T>(A, token) + h * S.gh : nullptr;
+    const auto load = [&] {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            xa[n] = PT::load(x + pl[n].a);
-            xb[n] = PT::load(x + pl[n].b);
+            xa[n] = PT::load(X.p + pl[n].a);
+            xb[n] = PT::load(X.p + pl[n].b);
             if constexpr (BWD) {
-                ga[n] = PT::load(g + pl[n].a);
-                gb[n] = PT::load(g + pl[n].b);
+                ga[n] = PT::load(G.p + pl[n].a);
+                gb[n] = PT::load(G.p + pl[n].b);
             }
         }
     };
-    // waves past the last whole round of chunks have no tokens
-    const uint32_t stride = S.stride, begin = first < stride ? first : A.tokens;
+    // tokens and stride are below 2^31: no wrap
     int64_t pos = 0, pos_next = 0;
+    bool turned = false;   // the step to the next token enters another batch
     if (begin < A.tokens) {
-        pos = position(A, begin);
-        load(begin);
+        pos = position(A, ahead);
+        load();
         ang.load(A, pos, pl);
-        pos_next = position(A, begin + stride < A.tokens ? begin + stride : begin);
+        if (begin + stride < A.tokens) turned = ahead.step(A);
+        pos_next = position(A, ahead);
     }
     for (uint32_t t = begin; t < A.tokens; t += stride) {
         float va[NP][VEC], vb[NP][VEC], da[NP][VEC], db[NP][VEC];
@@ -284,13 +306,17 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(HeadArgs A) {
                 PT::widen(gb[n], db[n]);
             }
         }
-        // tokens < 2^31 and stride < 2^31: no wrap
-        const uint32_t next = t + stride < A.tokens ? t + stride : t;
-        const uint32_t after = next + stride < A.tokens ? next + stride : next;
-        load(next);
+        const bool more = t + stride < A.tokens;
+        if (more) {
+            X.move(turned);
+            if constexpr (BWD) G.move(turned);
+        }
+        load();
         ang.load(A, pos_next, pl);
         pos = pos_next;
-        pos_next = position(A, after);
+        bool turned_next = false;
+        if (more && t + stride + stride < A.tokens) turned_next = ahead.step(A);
+        pos_next = position(A, ahead);
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
 #pragma unroll
@@ -316,7 +342,6 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(HeadArgs A) {
         const float r = 1.f / sqrtf(ss * inv_d + A.eps);
         float m = 0.f;
         if constexpr (BWD) m = group_sum(sd, A.lg) * r * inv_d;   // mean(dn n)
-        T *y = Y.at<T>(A, t) + h * S.yh;
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
 #pragma unroll
@@ -337,43 +362,44 @@ __global__ __launch_bounds__(kThreads) void qk_kernel(HeadArgs A) {
             if constexpr (!BWD)
                 if (pl[n].turned) turn<VEC>(A.interleaved, 1.f, va[n], vb[n], now.c[n], now.s[n]);
             if (here && pl[n].in) {
-                PT::template store<NT>(y + pl[n].a, va[n]);
-                if (pl[n].has_b) PT::template store<NT>(y + pl[n].b, vb[n]);
+                PT::template store<NT>(Y.p + pl[n].a, va[n]);
+                if (pl[n].has_b) PT::template store<NT>(Y.p + pl[n].b, vb[n]);
             }
         }
+        if (more) Y.move(turned);
+        turned = turned_next;
     }
     if constexpr (BWD) {
-        if (!S.dw) return;
-        // the workgroup's part of dw: its waves' head groups, then its waves, in a fixed order
-        __shared__ float lds[kWaves][2 * VEC * NP * 64];
+        // The workgroup's parts of dw, queries' and keys': each thread sums an element over
+        // the waves and their heads, in a fixed order that starts where its banks are free.
+        __shared__ float lds[kWaves][2 * VEC * NP][64];
+        __shared__ uint64_t keys[kWaves];
 #pragma unroll
         for (int n = 0; n < NP; ++n)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                for (int m = 1 << A.lg; m < 64; m <<= 1) {
-                    dwa[n][i] += __shfl_xor(dwa[n][i], m);
-                    dwb[n][i] += __shfl_xor(dwb[n][i], m);
-                }
-                lds[wave][((n * VEC + i) * 2) * 64 + lane] = dwa[n][i];
-                lds[wave][((n * VEC + i) * 2 + 1) * 64 + lane] = dwb[n][i];
+                lds[wave][(n * 2) * VEC + i][lane] = dwa[n][i];
+                lds[wave][(n * 2 + 1) * VEC + i][lane] = dwb[n][i];
             }
+        const uint64_t mine = __ballot(key);
+        if (lane == 0) keys[wave] = mine;
         __syncthreads();
-        if (wave == 0 && lane < 1 << A.lg) {
-            float *row = A.partial + (int64_t)blockIdx.x * A.D;
-#pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                if (!pl[n].in) continue;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    float a = 0.f, b = 0.f;
-                    for (int v = 0; v < kWaves; ++v) {
-                        a += lds[v][((n * VEC + i) * 2) * 64 + lane];
-                        b += lds[v][((n * VEC + i) * 2 + 1) * 64 + lane];
-                    }
-                    row[pl[n].a + i] = a;
-                    if (pl[n].has_b) row[pl[n].b + i] = b;
+        const int groups = 64 >> A.lg, per_set = 2 * VEC * NP << A.lg;
+        for (int j = threadIdx.x; j < 2 * per_set; j += kThreads) {
+            const int set = j >= per_set, r = j - (set ? per_set : 0), e = r >> A.lg, l = r & ((1 << A.lg) - 1);
+            if (!(set ? A.dw[1] : A.dw[0])) continue;
+            const Place at = place_of<VEC>(A, l + ((e / (2 * VEC)) << A.lg));
+            const bool second = (e / VEC) & 1;
+            if (!at.in || (second && !at.has_b)) continue;
+            float sum = 0.f;
+            for (int v = 0; v < kWaves; ++v) {
+                const uint64_t k = set ? keys[v] : ~keys[v];
+                for (int i = 0; i < groups; ++i) {
+                    const int from = (((i + e) & (groups - 1)) << A.lg) + l;
+                    sum += k >> from & 1 ? lds[v][e][from] : 0.f;
                 }
             }
+            A.partial[((int64_t)blockIdx.x * 2 + set) * A.D + (second ? at.b : at.a) + e % VEC] = sum;
         }
     }
 }
@@ -386,14 +412,13 @@ __global__ __launch_bounds__(kJoinCols * kJoinRows) void qk_join_kernel(HeadArgs
     const int col = threadIdx.x % kJoinCols, down = threadIdx.x / kJoinCols;
     const int j = blockIdx.x * kJoinCols + col;
     const bool key = blockIdx.y;
-    float *dw = key ? A.s[1].dw : A.s[0].dw;
+    float *dw = key ? A.dw[1] : A.dw[0];
     if (!dw) return;
-    const float *partial = A.partial + (key ? (int64_t)A.s[0].blocks * A.D : 0);
-    const int rows = key ? A.s[1].blocks : A.s[0].blocks;
+    const float *partial = A.partial + (key ? A.D : 0);
     float sum = 0.f;
     if (j < A.D) {
 #pragma unroll 8
-        for (int r = down; r < rows; r += kJoinRows) sum += partial[(int64_t)r * A.D + j];
+        for (int r = down; r < A.blocks; r += kJoinRows) sum += partial[(int64_t)r * 2 * A.D + j];
     }
     sum += __shfl_xor(sum, 16);   // a wave holds four rows of the 16 values
     sum += __shfl_xor(sum, 32);
@@ -430,6 +455,8 @@ ns_status check_heads(const char *name, const ns_heads *h, int64_t batch, int64_
         return fail(NS_ERR_OVERFLOW, "%s: offsets overflow", name);
     return NS_OK;
 }
+
+Operand operand(const ns_heads *h) { return {(char *)h->data, h->batch_stride, h->token_stride, h->head_stride}; }
 
 struct HeadCall {
     HeadArgs a;
@@ -488,13 +515,9 @@ ns_status plan_heads(int64_t batch, int64_t seq, int32_t head_dim, int32_t dtype
     const ns_heads *hs[2] = {q, k};
     const void *ws[2] = {q_weight, k_weight};
     for (int i = 0; i < 2; ++i) {
-        HeadSet &s = a.s[i];
-        s.x = (char *)hs[i]->data;
-        s.xb = hs[i]->batch_stride;
-        s.xt = hs[i]->token_stride;
-        s.xh = hs[i]->head_stride;
-        s.heads = hs[i]->heads;
-        s.w = ws[i];
+        a.x[i] = operand(hs[i]);
+        a.heads[i] = hs[i]->heads;
+        a.w[i] = ws[i];
     }
     // The rotated half and the rest have to split into whole pieces.
     c->vec = (rope_dim | head_dim) % 16 == 0 ? 8 : (rope_dim | head_dim) % 8 == 0 && head_dim <= 512 ? 4 : 1;
@@ -507,40 +530,24 @@ ns_status plan_heads(int64_t batch, int64_t seq, int32_t head_dim, int32_t dtype
     return NS_OK;
 }
 
-void set_out(HeadSet &s, const ns_heads *o) {
-    s.y = (char *)o->data;
-    s.yb = o->batch_stride;
-    s.yt = o->token_stride;
-    s.yh = o->head_stride;
-}
-
-// Deals the workgroups to the two sets by their work: a wave for each (token,
-// chunk of heads), or several of one chunk's tokens a wave.
+// Deals the work: a wave for each (token, chunk of heads), or several tokens of
+// one chunk a wave.
 void deal(HeadCall &c, bool backward) {
     HeadArgs &a = c.a;
-    const int64_t most = blocks_for(c.vec, backward);
-    const int64_t moved = (int64_t)a.tokens * (a.s[0].heads + a.s[1].heads) * a.D * c.es * (backward ? 3 : 2);
-    c.past_cache = moved > kMallBytes;
-    int64_t items[2], all = 0;
-    for (int i = 0; i < 2; ++i) {
-        a.s[i].chunks = (a.s[i].heads + (64 >> a.lg) - 1) >> (6 - a.lg);
-        items[i] = (int64_t)a.tokens * a.s[i].chunks;
-        all += items[i];
-    }
-    for (int i = 0; i < 2; ++i) {
-        HeadSet &s = a.s[i];
-        const int64_t full = (items[i] + kWaves - 1) / kWaves, least = (s.chunks + kWaves - 1) / kWaves;
-        int64_t blocks = full;
-        if ((all + kWaves - 1) / kWaves > most) blocks = std::max(least, (int64_t)((double)most * items[i] / all));
-        s.blocks = (int32_t)(items[i] ? std::max<int64_t>(1, std::min(blocks, full)) : 0);
-        s.stride = s.chunks ? (int32_t)std::max<int64_t>(1, (int64_t)s.blocks * kWaves / s.chunks) : 1;
-    }
+    const int64_t heads = (int64_t)a.heads[0] + a.heads[1], per = 64 >> a.lg;
+    c.past_cache = (double)a.tokens * heads * a.D * c.es * (backward ? 3 : 2) > (double)kMallBytes;
+    a.chunks = (uint32_t)((heads + per - 1) / per);
+    const int64_t full = ((int64_t)a.tokens * a.chunks + kWaves - 1) / kWaves, least = (a.chunks + kWaves - 1) / kWaves;
+    a.blocks = (int32_t)std::min(full, std::max<int64_t>(blocks_for(c.vec, backward), least));
+    if (!a.blocks) return;
+    a.stride = (uint32_t)((int64_t)a.blocks * kWaves / a.chunks);
+    a.step_i = a.stride / a.seq;
+    a.step_s = a.stride % a.seq;
 }
 
 template <bool BWD> ns_status launch(const HeadCall &c, int32_t dtype, void *stream) {
-    const int32_t blocks = c.a.s[0].blocks + c.a.s[1].blocks;
-    if (!blocks) return NS_OK;
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kThreads), 0, as_stream(stream), c.a); };
+    if (!c.a.blocks) return NS_OK;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(c.a.blocks), dim3(kThreads), 0, as_stream(stream), c.a); };
     auto pick = [&](auto t) {
         typedef decltype(t) T;
         if (c.vec == 8) c.past_cache ? go(qk_kernel<T, 8, 1, BWD, true>) : go(qk_kernel<T, 8, 1, BWD, false>);
@@ -570,8 +577,8 @@ extern "C" ns_status ns_qk_norm_rope(int64_t batch, int64_t seq, int32_t head_di
         return s;
     if (ns_status s = check_heads("q_out", q_out, batch, seq, head_dim, c.es, q->heads)) return s;
     if (ns_status s = check_heads("k_out", k_out, batch, seq, head_dim, c.es, k->heads)) return s;
-    set_out(c.a.s[0], q_out);
-    set_out(c.a.s[1], k_out);
+    c.a.y[0] = operand(q_out);
+    c.a.y[1] = operand(k_out);
     deal(c, false);
     return launch<false>(c, dtype, stream);
 }
@@ -583,8 +590,8 @@ extern "C" ns_status ns_qk_norm_rope_workspace_bytes(int64_t batch, int64_t seq,
         return fail(NS_ERR_OVERFLOW, "batch x seq does not fit in 31 bits");
     if (head_dim < 1 || head_dim > kMaxHeadDim)
         return fail(NS_ERR_INVALID_ARG, "head_dim = %d outside [1, %d]", head_dim, kMaxHeadDim);
-    // One row of partial sums a workgroup. A set takes its share of them, or more if its chunks need it (deal()).
-    *bytes = (size_t)(kMostPartials + 2 * kMaxHeads / kWaves) * head_dim * sizeof(float);
+    static_assert(2 * kMaxHeads / kWaves <= kMostPartials, "a wave for every chunk of heads");
+    *bytes = (size_t)kMostPartials * 2 * head_dim * sizeof(float);
     return NS_OK;
 }
 
@@ -615,17 +622,12 @@ extern "C" ns_status ns_qk_norm_rope_backward(int64_t batch, int64_t seq, int32_
             return fail(NS_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
         if (misaligned(workspace, 256)) return fail(NS_ERR_INVALID_ARG, "workspace not 256-byte aligned");
     }
-    const ns_heads *gs[2] = {dq_out, dk_out}, *os[2] = {dq, dk};
-    float *dws[2] = {dq_weight, dk_weight};
-    for (int i = 0; i < 2; ++i) {
-        HeadSet &s = c.a.s[i];
-        s.g = (char *)gs[i]->data;
-        s.gb = gs[i]->batch_stride;
-        s.gt = gs[i]->token_stride;
-        s.gh = gs[i]->head_stride;
-        set_out(s, os[i]);
-        s.dw = dws[i];
-    }
+    c.a.g[0] = operand(dq_out);
+    c.a.g[1] = operand(dk_out);
+    c.a.y[0] = operand(dq);
+    c.a.y[1] = operand(dk);
+    c.a.dw[0] = dq_weight;
+    c.a.dw[1] = dk_weight;
     c.a.partial = reinterpret_cast<float *>(workspace);
     deal(c, true);
     if (ns_status s = launch<true>(c, dtype, stream)) return s;
