@@ -28,20 +28,25 @@ namespace {
 // ---------------------------------------------------------------------------
 
 constexpr int kMaxExperts = 1024;
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxSortBlocks = 128;
+constexpr int kMaxSortBlocks = 256;
+constexpr int kSortRounds = 4;   // rounds of 64 slots that a wave ranks at once
+constexpr int kOneRounds = 4;    // most rounds of one workgroup by itself
 
 struct SortArgs {
     const void *ids;
     int64_t ids_ld;          // elements from a token's ids to the next one's
     int32_t id_bytes;
     int32_t slots, top_k, experts;
-    int32_t per;             // slots per workgroup: a multiple of 1024
+    int32_t per;             // slots per workgroup: a multiple of kSortThreads
     int32_t blocks;
     int32_t *offsets, *slot_of_row, *row_of_slot;
-    int32_t *hist;           // [blocks][experts + 1]
+    int32_t *hist;           // [blocks][hist_ld(experts)]: each workgroup's counts
 };
+
+// Counts of keys 0 .. experts in whole int4.
+__host__ __device__ inline int hist_ld(int experts) { return (experts + 1 + 3) & ~3; }
 
 // The sort key of a slot: its expert, or `experts` if dropped.
 __device__ inline int key_of(const SortArgs &A, uint32_t slot) {
@@ -55,16 +60,6 @@ __device__ inline int key_of(const SortArgs &A, uint32_t slot) {
     return id < 0 || id >= A.experts ? A.experts : (int)id;
 }
 
-// The lanes of the wave that hold the same key (`bits` bits of it) as this one.
-__device__ inline uint64_t same_key(int key, bool active, int bits) {
-    uint64_t m = __ballot(active);
-    for (int b = 0; b < bits; ++b) {
-        const uint64_t set = __ballot((key >> b) & 1);
-        m &= (key >> b) & 1 ? set : ~set;
-    }
-    return m;
-}
-
 // Counts of each key in one workgroup's slots.
 __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(SortArgs A) {
     __shared__ int32_t cnt[kMaxExperts + 1];
@@ -75,59 +70,117 @@ __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(SortArgs A) {
 #pragma unroll 4
     for (int64_t s = s0 + threadIdx.x; s < s1; s += kSortThreads) atomicAdd(&cnt[key_of(A, (uint32_t)s)], 1);
     __syncthreads();
-    for (int e = threadIdx.x; e <= A.experts; e += kSortThreads)
-        A.hist[(int64_t)blockIdx.x * (A.experts + 1) + e] = cnt[e];
+    for (int e = threadIdx.x; e < hist_ld(A.experts); e += kSortThreads)
+        A.hist[(int64_t)blockIdx.x * hist_ld(A.experts) + e] = e <= A.experts ? cnt[e] : 0;
 }
 
 // Rows of one workgroup's slots. Wave w holds the w-th run of per / 16 of
 // them; a slot's row is its key's first row, plus the same key's slots in
 // earlier workgroups, earlier waves, earlier rounds of this wave and lower
-// lanes. ONE: the only workgroup, which counts for itself.
+// lanes. A wave's LDS operations run in order, and none of a round's waits for
+// another round: the lanes of a key set their bits in its mask and read it, which
+// tells each the lower ones, then read the wave's count of the key, to which the
+// lowest adds the mask's bits. (Masks from one ballot for each of the key's bits
+// keep the vector units busy: 64 slots 4.2 us, so 3.2.) Runs of at most
+// kSortRounds rounds are ranked before the counts ahead of them are known,
+// longer ones after. ONE: the only workgroup, which counts for itself.
+//
+// Of 524288 slots and 256 experts (15.0 us with the counts, which stream 6 MB)
+// some 7 us go into reading every workgroup's counts in each; two to four
+// workgroups counted in one cost as much there as they save here.
 template <bool ONE>
 __global__ __launch_bounds__(kSortThreads) void moe_rank_kernel(SortArgs A) {
-    __shared__ int32_t cnt[kSortWaves][kMaxExperts + 1];
-    __shared__ int32_t before[kMaxExperts + 1], total[kMaxExperts + 1];
+    constexpr int kKeys = kSortWaves * (kMaxExperts + 1);   // [wave][key], K1 apart
+    __shared__ __attribute__((aligned(16))) int32_t cnt[kKeys];
+    __shared__ __attribute__((aligned(16))) uint64_t same[kKeys];
+    __shared__ int32_t before[kMaxExperts + 4], total[kMaxExperts + 4];
     __shared__ int32_t wave_total[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int E = A.experts, K1 = E + 1;
-    const int bits = 32 - __builtin_clz(E);   // keys 0 .. E
     for (int i = tid; i < K1; i += kSortThreads) before[i] = total[i] = 0;
-    for (int w = 0; w < kSortWaves; ++w)
-        for (int i = tid; i < K1; i += kSortThreads) cnt[w][i] = 0;
+    for (int i = tid * 4; i < kSortWaves * K1; i += kSortThreads * 4) {   // kSortWaves is a multiple of 4
+        *reinterpret_cast<int4 *>(&cnt[i]) = int4{0, 0, 0, 0};
+        *reinterpret_cast<int4 *>(&same[i]) = int4{0, 0, 0, 0};
+        *reinterpret_cast<int4 *>(&same[i + 2]) = int4{0, 0, 0, 0};
+    }
+    int32_t *const mine_cnt = cnt + wave * K1;
     __syncthreads();
     const int run = A.per / kSortWaves;
     const int64_t w0 = (int64_t)blockIdx.x * A.per + (int64_t)wave * run;
     const int64_t w1 = w0 + run < A.slots ? w0 + run : A.slots;
+    int key[kSortRounds], rank[kSortRounds];
+    const auto rank_rounds = [&](int64_t s0) {
+        uint64_t m[kSortRounds];
+#pragma unroll
+        for (int i = 0; i < kSortRounds; ++i) {
+            const int64_t s = s0 + i * 64 + lane;
+            key[i] = s < w1 ? key_of(A, (uint32_t)s) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kSortRounds; ++i) {
+            m[i] = 0;
+            if (key[i] < 0) continue;
+            uint64_t *const mask = &same[wave * K1 + key[i]];
+            __hip_atomic_fetch_or(mask, 1ull << lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            __builtin_amdgcn_wave_barrier();
+            m[i] = __hip_atomic_load(mask, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            __builtin_amdgcn_wave_barrier();
+            __hip_atomic_store(mask, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+#pragma unroll
+        for (int i = 0; i < kSortRounds; ++i) {
+            const int lower = __popcll(m[i] & ((1ull << lane) - 1));
+            rank[i] = 0;
+            if (key[i] < 0) continue;
+            int32_t *const count = &mine_cnt[key[i]];
+            rank[i] = lower + __hip_atomic_load(count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            __builtin_amdgcn_wave_barrier();
+            if (lower == 0) __hip_atomic_fetch_add(count, (int)__popcll(m[i]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+    };
+    const bool again = A.per > kSortRounds * kSortThreads;
+    if (again) {
 #pragma unroll 4
-    for (int64_t s = w0 + lane; s < w1; s += 64) atomicAdd(&cnt[wave][key_of(A, (uint32_t)s)], 1);
+        for (int64_t s = w0 + lane; s < w1; s += 64) atomicAdd(&mine_cnt[key_of(A, (uint32_t)s)], 1);
+    } else {
+        rank_rounds(w0);
+    }
     if constexpr (!ONE) {
-        const int step = min(kSortThreads, (K1 + 63) & ~63);   // threads for one workgroup's counts
-        const int group = tid / step, groups = kSortThreads / step;
-        for (int e = tid % step; group < groups && e < K1; e += step) {
-            int32_t b = 0, t = 0;
+        const int cols = hist_ld(E) / 4, groups = kSortThreads / cols, group = tid / cols, col = tid - group * cols;
+        if (group < groups) {
+            const int4 *hist = reinterpret_cast<const int4 *>(A.hist) + col;
+            int4 b = {0, 0, 0, 0}, t = {0, 0, 0, 0};
 #pragma unroll 8
             for (int c = group; c < A.blocks; c += groups) {
-                const int32_t v = A.hist[(int64_t)c * K1 + e];
-                t += v;
-                b += c < (int)blockIdx.x ? v : 0;
+                const int4 v = hist[(int64_t)c * cols];
+                const int earlier = c < (int)blockIdx.x ? -1 : 0;
+                t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+                b.x += v.x & earlier, b.y += v.y & earlier, b.z += v.z & earlier, b.w += v.w & earlier;
             }
-            atomicAdd(&before[e], b);   // integers: any order gives the same sum
-            atomicAdd(&total[e], t);
+            const int tv[4] = {t.x, t.y, t.z, t.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                atomicAdd(&before[col * 4 + i], bv[i]);   // integers: any order gives the same sum
+                atomicAdd(&total[col * 4 + i], tv[i]);
+            }
         }
     }
     __syncthreads();
     for (int e = tid; e < K1; e += kSortThreads) {   // counts to first ranks, wave by wave
         int32_t sum = 0;
         for (int w = 0; w < kSortWaves; ++w) {
-            const int32_t v = cnt[w][e];
-            cnt[w][e] = sum;
+            const int32_t v = cnt[w * K1 + e];
+            cnt[w * K1 + e] = sum;
             sum += v;
         }
         if constexpr (ONE) total[e] = sum;
     }
     __syncthreads();
     // first row of each expert: an exclusive sum over the (at most 1024) experts
-    const int32_t mine = tid < E ? total[tid] : 0;
+    constexpr int kEach = kMaxExperts / kSortThreads;
+    int32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) mine += tid * kEach + i < E ? total[tid * kEach + i] : 0;
     int32_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -141,31 +194,28 @@ __global__ __launch_bounds__(kSortThreads) void moe_rank_kernel(SortArgs A) {
         if (w < wave) first += wave_total[w];
         kept += wave_total[w];
     }
-    if (tid < E) before[tid] += first;
-    if (tid == 0) before[E] += kept;
-    if (blockIdx.x == 0) {
-        if (tid < E) A.offsets[tid] = first;
-        if (tid == 0) A.offsets[E] = kept;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int e = tid * kEach + i;
+        if (e >= E) break;
+        before[e] += first;
+        if (blockIdx.x == 0) A.offsets[e] = first;
+        first += total[e];
+    }
+    if (tid == 0) {
+        before[E] += kept;
+        if (blockIdx.x == 0) A.offsets[E] = kept;
     }
     __syncthreads();
-    volatile int32_t *mycnt = cnt[wave];
-    int key_next = w0 + lane < w1 ? key_of(A, (uint32_t)(w0 + lane)) : E;
-    for (int64_t s0 = w0; s0 < w1; s0 += 64) {
-        const int64_t s = s0 + lane;
-        const bool active = s < w1;
-        const int key = key_next;
-        if (s + 64 < w1) key_next = key_of(A, (uint32_t)(s + 64));
-        const uint64_t m = same_key(key, active, bits);
-        const int rank = __popcll(m & ((1ull << lane) - 1));
-        int32_t prior = 0;
-        if (active) prior = mycnt[key];
-        __builtin_amdgcn_wave_barrier();      // every lane has read before the first of each key writes
-        if (active && rank == 0) mycnt[key] = prior + __popcll(m);
-        __builtin_amdgcn_wave_barrier();
-        if (active) {
-            const int32_t row = before[key] + prior + rank, slot = (int32_t)s;
-            A.row_of_slot[slot] = key == E ? ~row : row;
-            A.slot_of_row[row] = key == E ? ~slot : slot;
+    for (int64_t s0 = w0; s0 < w1; s0 += 64 * kSortRounds) {
+        if (again) rank_rounds(s0);   // now from the counts before this wave on
+#pragma unroll
+        for (int i = 0; i < kSortRounds; ++i) {
+            if (key[i] < 0) continue;
+            const int32_t row = before[key[i]] + rank[i] + (again ? 0 : mine_cnt[key[i]]);
+            const int32_t slot = (int32_t)(s0 + i * 64 + lane);
+            A.row_of_slot[slot] = key[i] == E ? ~row : row;
+            A.slot_of_row[row] = key[i] == E ? ~slot : slot;
         }
     }
 }
@@ -452,7 +502,7 @@ extern "C" ns_status ns_moe_sort_workspace_bytes(int64_t tokens, int32_t top_k, 
     if (ns_status s = check_slots(tokens, top_k)) return s;
     if (experts < 1 || experts > kMaxExperts)
         return fail(NS_ERR_INVALID_ARG, "experts = %d outside [1, %d]", experts, kMaxExperts);
-    *bytes = (size_t)kMaxSortBlocks * (experts + 1) * sizeof(int32_t);
+    *bytes = (size_t)kMaxSortBlocks * hist_ld(experts) * sizeof(int32_t);
     return NS_OK;
 }
 
@@ -484,10 +534,10 @@ extern "C" ns_status ns_moe_sort(int64_t tokens, int32_t top_k, int32_t experts,
     a.slot_of_row = slot_of_row;
     a.row_of_slot = row_of_slot;
     a.hist = reinterpret_cast<int32_t *>(workspace);
-    // One workgroup up to 2 rounds of 1024 slots (2048 slots: 5.8 us, two launches 7.2; 4096: 8.6 and 7.4), past
-    // that two launches over up to 128 workgroups.
+    // One workgroup up to 4 rounds of 512 slots (2048 slots: 4.9 us; 4096: 9.3, two launches 6.4), past that two
+    // launches over up to 256 workgroups (524288 slots of 256 experts: 128 workgroups 15.5 us, 512 25).
     const int64_t rounds = (a.slots + kSortThreads - 1) / kSortThreads;
-    const bool one = rounds <= 2;
+    const bool one = rounds <= kOneRounds;
     const int64_t per = one ? (rounds > 0 ? rounds : 1) : (rounds + kMaxSortBlocks - 1) / kMaxSortBlocks;
     a.per = (int32_t)(per * kSortThreads);
     a.blocks = one ? 1 : (int32_t)((rounds + per - 1) / per);

@@ -294,7 +294,9 @@ def _sorted(ids, experts):
 
 @pytest.mark.parametrize("t,k,e,kind", [
     (1, 1, 1, "even"), (1, 8, 64, "even"), (0, 4, 8, "even"), (7, 3, 5, "drop"), (64, 1, 2, "one"), (65, 1, 3, "skew"),
-    (100, 4, 1024, "even"), (1000, 8, 64, "drop"), (1024, 8, 256, "even"),   # the largest in one workgroup
+    (100, 4, 1024, "even"), (1000, 8, 64, "drop"), (1024, 8, 256, "even"),
+    (256, 8, 256, "even"), (257, 8, 256, "even"),           # the largest in one workgroup, and one past it
+    (65536, 8, 31, "drop"), (70001, 8, 1024, "skew"), (300007, 7, 33, "drop"),   # runs ranked at once, and longer ones
     (1025, 8, 255, "skew"), (3000, 3, 17, "drop"), (9001, 7, 64, "one"), (20000, 8, 1023, "drop"),
     (40000, 8, 64, "skew"), (5000, 2, 6, "none"),
 ])
