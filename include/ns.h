@@ -443,8 +443,9 @@ typedef struct ns_heads {
  * head_dim 1 .. 1024; rope_dim even, 0 .. head_dim (0: no rotation, cos, sin
  * and pos unused).
  * q, k         inputs (either may have 0 heads); q_out, k_out: outputs with as
- *              many heads. An output may be its input with the same strides
- *              (in place); otherwise tensors must not overlap.
+ *              many heads, none of their strides below head_dim where its
+ *              dimension is longer than 1. An output may be its input with the
+ *              same strides (in place); otherwise tensors must not overlap.
  * q_weight,    [head_dim] of weight_dtype, or NULL for ones.
  * k_weight
  * cos, sin     [table_rows, rope_dim / 2] f32: the angles of position p in row

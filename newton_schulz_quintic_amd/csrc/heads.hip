@@ -435,9 +435,10 @@ __global__ __launch_bounds__(kJoinCols * kJoinRows) void qk_join_kernel(HeadArgs
 // host side
 // ---------------------------------------------------------------------------
 
-// One head tensor's checks. `out`: whether it is written.
+// One head tensor's checks. want_heads: the heads an output or its gradient has to
+// have. out: it is written, so no two of its heads may lie closer than their size.
 ns_status check_heads(const char *name, const ns_heads *h, int64_t batch, int64_t seq, int32_t D, int es,
-                      int32_t want_heads) {
+                      int32_t want_heads, bool out = false) {
     if (!h) return fail(NS_ERR_INVALID_ARG, "%s is NULL", name);
     if (h->heads < 0) return fail(NS_ERR_INVALID_ARG, "%s: heads = %d < 0", name, h->heads);
     if (h->heads > kMaxHeads) return fail(NS_ERR_OVERFLOW, "%s: more than %d heads", name, kMaxHeads);
@@ -448,6 +449,9 @@ ns_status check_heads(const char *name, const ns_heads *h, int64_t batch, int64_
     if (misaligned(h->data, es)) return fail(NS_ERR_INVALID_ARG, "%s: data not %d-byte aligned", name, es);
     if (h->batch_stride < 0 || h->token_stride < 0 || h->head_stride < 0)
         return fail(NS_ERR_INVALID_ARG, "%s: negative stride", name);
+    if (out && ((batch > 1 && h->batch_stride < D) || (seq > 1 && h->token_stride < D) ||
+                (h->heads > 1 && h->head_stride < D)))
+        return fail(NS_ERR_INVALID_ARG, "%s: an output's heads overlap (a stride below head_dim)", name);
     if (too_far(batch, h->batch_stride) || too_far(seq, h->token_stride) || too_far(h->heads, h->head_stride))
         return fail(NS_ERR_OVERFLOW, "%s: offsets overflow", name);
     if (batch * (double)h->batch_stride + seq * (double)h->token_stride + h->heads * (double)h->head_stride + D >
@@ -575,8 +579,8 @@ extern "C" ns_status ns_qk_norm_rope(int64_t batch, int64_t seq, int32_t head_di
     if (ns_status s = plan_heads(batch, seq, head_dim, dtype, q, k, q_weight, k_weight, weight_dtype, eps, cos, sin,
                                  table_rows, rope_dim, interleaved, pos, pos_bytes, pos_batch_stride, &c))
         return s;
-    if (ns_status s = check_heads("q_out", q_out, batch, seq, head_dim, c.es, q->heads)) return s;
-    if (ns_status s = check_heads("k_out", k_out, batch, seq, head_dim, c.es, k->heads)) return s;
+    if (ns_status s = check_heads("q_out", q_out, batch, seq, head_dim, c.es, q->heads, true)) return s;
+    if (ns_status s = check_heads("k_out", k_out, batch, seq, head_dim, c.es, k->heads, true)) return s;
     c.a.y[0] = operand(q_out);
     c.a.y[1] = operand(k_out);
     deal(c, false);
@@ -610,8 +614,8 @@ extern "C" ns_status ns_qk_norm_rope_backward(int64_t batch, int64_t seq, int32_
         return s;
     if (ns_status s = check_heads("dq_out", dq_out, batch, seq, head_dim, c.es, q->heads)) return s;
     if (ns_status s = check_heads("dk_out", dk_out, batch, seq, head_dim, c.es, k->heads)) return s;
-    if (ns_status s = check_heads("dq", dq, batch, seq, head_dim, c.es, q->heads)) return s;
-    if (ns_status s = check_heads("dk", dk, batch, seq, head_dim, c.es, k->heads)) return s;
+    if (ns_status s = check_heads("dq", dq, batch, seq, head_dim, c.es, q->heads, true)) return s;
+    if (ns_status s = check_heads("dk", dk, batch, seq, head_dim, c.es, k->heads, true)) return s;
     if (misaligned(dq_weight, 4) || misaligned(dk_weight, 4))
         return fail(NS_ERR_INVALID_ARG, "dq_weight / dk_weight not 4-byte aligned");
     const bool weights = dq_weight || dk_weight;

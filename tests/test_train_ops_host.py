@@ -73,6 +73,14 @@ def test_qk_backward_refusals_of_its_own():
     assert _qk_backward(QK, dk=None) == INVALID
 
 
+@pytest.mark.parametrize("short", [dict(b=0), dict(t=0), dict(h=0), dict(b=127), dict(t=127), dict(h=64)])
+def test_qk_outputs_with_overlapping_heads(short):
+    for name in ("qo", "ko"):
+        assert _qk_forward({**QK, name: _heads(**short)}) == INVALID
+    assert _qk_backward(QK, dq=_heads(**short)) == INVALID
+    assert _qk_backward(QK, dk=_heads(**short)) == INVALID
+
+
 def test_qk_nothing_to_do():
     none = _heads(data=None, n=0)
     assert _qk_forward({**QK, "batch": 0}) == OK
