@@ -18,7 +18,11 @@
 // pairs' q would lose all its digits where q_r is small.
 //
 // Bound by memory: loss and gradient in one call read the row once and write
-// its gradient once, the row staying in registers in between.
+// its gradient once, the row staying in registers in between. 4096 x 131072 bf16
+// with 64 pairs: 455 us, 4.7 TB/s, where a large copy here reaches 5.1: the
+// exponentials (two a value) overlap with the memory only as far as the CUs'
+// phases differ. 1025 x 50021 fp32, loss and then gradient in two calls: 119 us.
+// 4 rows are bound by two launches and their latency, 9.0 us.
 
 #include <algorithm>
 #include <type_traits>
@@ -575,11 +579,12 @@ __device__ inline RowSums row_sums(const DistillArgs &A, const PairLds<TOP> &L, 
 
 // Loss and gradient, the row in registers in between: kHeldVecs vectors and at
 // most one pair a thread, in the fewest threads that this takes (64 to 1024), so
-// that a CU's registers hold as many rows at once as they can. A workgroup takes rows in turn and loads each vector
-// of its next row as soon as it has written the one before. Loads return in
-// order, so what the next row needs besides (its tokens' logits, and the pairs
-// of the row after it, whose tokens those logits' addresses come from) is asked
-// for ahead of its vectors: its pairs are then weighed while its vectors come in.
+// that a CU's registers hold as many rows at once as they can. A workgroup takes
+// rows in turn and loads each vector of its next row as soon as it has written
+// the one before. Loads return in order, so what the next row needs besides (its
+// tokens' logits, and the pairs of the row after it, whose tokens those logits'
+// addresses come from) is asked for ahead of its vectors: its pairs are then
+// weighed while its vectors come in.
 // Vectors go through buffer descriptors: lanes past the row's last whole vector
 // read zeros (not used) and write nothing.
 template <typename T, int THREADS, bool REST>
