@@ -39,6 +39,8 @@ constexpr int kMaxChunks = 64;            // parts of a row that is split over w
 constexpr int kBitVocab = 1 << 18;        // tokens one workgroup marks in LDS (32 KiB)
 constexpr int kSplitThreads = 256;
 constexpr int kHeldVecs = 16;             // vectors of a row that a thread holds
+constexpr int kKeptVecs = 8;              // vectors a thread keeps of a row too long to hold
+static_assert(kKeptVecs <= kHeldVecs);
 constexpr int kAhead = 4;                 // vectors a thread of a split row loads ahead of everything else
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kNonTemporal = 2;           // a buffer store's cache policy
@@ -438,13 +440,12 @@ __device__ inline typename Vec16<T>::raw fast_grad(typename Vec16<T>::raw v, flo
     return o;
 }
 
-// The thread's part of a span's sum, read from memory, likewise.
-template <typename T, bool REST>
-__device__ inline float fast_span(const T *z, float zt, const Span<T> &S, const uint32_t *bits, float c, float hi) {
-    constexpr int B = 8;
+// The thread's part of a span's sum from the given vector on, read from memory, likewise.
+template <typename T, bool REST, int B>
+__device__ inline float fast_span(const T *z, float zt, const Span<T> &S, const uint32_t *bits, float c, float hi, int from) {
     const int threads = blockDim.x;
     float sum = 0.f;
-    int v = threadIdx.x;
+    int v = from + threadIdx.x;
     for (; v + (B - 1) * threads < S.vecs; v += B * threads) {
         typename Vec16<T>::raw r[B];
 #pragma unroll
@@ -727,35 +728,51 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
     }
 }
 
-// Loss, and with dlogits the gradient, of rows too long to hold: the row is
-// read a second time for the gradient.
-template <typename T, bool REST, bool NT>
-__global__ __launch_bounds__(kSplitThreads) void distill_row_kernel(DistillArgs A) {
+// Loss by itself, or (TRAIN) with the gradient of rows too long to hold. These
+// are read a second time for the gradient, except for the first kKept vectors of
+// each thread: one workgroup a CU, so that the 256 rows under way stay in the
+// last-level cache in between (2048 x 151936 bf16: 361 us with many workgroups of
+// 256 threads, 326 with 256 of 1024 threads, 279 with 8 vectors kept; 12 spill,
+// 287; 2000 x 100000 f32 448, 360 and 315).
+template <typename T, bool REST, bool TRAIN, int THREADS>
+__global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
     __shared__ __attribute__((aligned(16))) PairLds<kMaxTop> L;
+    constexpr int kKept = !TRAIN ? 0 : REST && sizeof(T) == 2 ? kKeptVecs - 2 : kKeptVecs;   // without spilling
     const Span<T> S(0, A.vocab);
     const float c = A.inv_tau * kLog2e;
     for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
         const T *z = reinterpret_cast<const T *>(A.logits) + row * A.ld;
+        typename Vec16<T>::raw kept[kKept + 1];   // a row too long to hold has kHeldVecs vectors a thread and more
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) kept[i] = load_vec<T>(z + (int64_t)(threadIdx.x + i * THREADS) * S.N);
         Pairs r = read_pairs<REST>(A, row, L, bits, (A.vocab + 31) >> 5);
         if (!r.some) {
             write_empty<T, REST>(A, row, S, true);
             __syncthreads();
             continue;
         }
-        for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) L.z[k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
+        for (int k = threadIdx.x; k < A.top_k; k += THREADS) L.z[k] = L.id[k] >= 0 ? (float)z[L.id[k]] : 0.f;
         const float zt = tail_of<T>(z, S);
         weigh_pairs<REST>(A, teacher_lse<REST>(A, row), L, r, bits, 0, A.vocab);
         const FastBase f = fast_base(A, L, c);
-        Lse rest = {f.m, block_sum<kSplitThreads>(fast_span<T, REST>(z, zt, S, bits, c, f.hi), L) * __builtin_amdgcn_exp2f(-f.lo)};
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+            sum += fast_sum<T, REST>(kept[i], REST ? vec_bits(bits, threadIdx.x + i * THREADS, S.N) : 0, c, f.hi);
+        sum += fast_span<T, REST, TRAIN && REST ? 4 : 8>(z, zt, S, bits, c, f.hi, kKept * THREADS);
+        Lse rest = {f.m, block_sum<THREADS>(sum, L) * __builtin_amdgcn_exp2f(-f.lo)};
         if (!fast_holds(rest)) {
             __syncthreads();
             rest = block_join(sum_span<T, REST>(z, zt, S, bits, c), L, c);
         }
-        const RowSums s = row_sums<REST>(A, L, r, A.dlogits ? A.grad_loss[row] : 0.f, rest, c);
-        if (A.dlogits) {
+        const RowSums s = row_sums<REST>(A, L, r, TRAIN ? A.grad_loss[row] : 0.f, rest, c);
+        if constexpr (TRAIN) {
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
-            grad_span<T, NT>(z, dz, S, s.others, c, s.g_others);
+#pragma unroll
+            for (int i = 0; i < kKept; ++i)
+                store_vec<T, true>(dz + (int64_t)(threadIdx.x + i * THREADS) * S.N, grad_vec<T>(kept[i], s.others, c, s.g_others));
+            grad_span<T, true>(z, dz, S, s.others, c, s.g_others, kKept * THREADS);
             finish_span<T>(A, L, [&](int j, T x) { dz[j] = x; }, S, zt, s.n, s.others, c, s.g, s.g_others);
         }
         write_loss<REST>(A, L, r, row, s.n, s.all, s.rest);
@@ -886,12 +903,13 @@ int64_t held_threads(const DistillArgs &a, int es) {
     return threads;
 }
 // Which calls split their rows over workgroups and run two kernels. Training
-// holds rows that it can from 256 on (one a CU; 600 x 131072 bf16: 81 us, split
-// 91); otherwise rows are read one to a workgroup of 256 threads once these fill
-// the GPU (600 x 131072 bf16 forward: split 38 us, a workgroup a row 44).
+// takes a row to a workgroup from 256 on (one a CU; 600 x 131072 bf16, held: 81 us,
+// split 91; 900 x 160000 bf16, not held: 140 us, split 181; 300 x 100001 f32 66 and
+// 79); loss alone reads rows one to a workgroup of 256 threads once these fill the
+// GPU (600 x 131072 bf16: split 38 us, a workgroup a row 44).
 bool split_rows(const DistillArgs &a, int es) {
     if (a.teacher_lse && a.vocab > kBitVocab) return true;
-    return a.rows < (a.dlogits && held_threads(a, es) <= 1024 ? 256 : 1024);
+    return a.rows < (a.dlogits ? 256 : 1024);
 }
 
 size_t distill_workspace(int64_t rows, int32_t top_k, bool split) {
@@ -969,8 +987,8 @@ ns_status launch_rows(const DistillArgs &a, hipStream_t st) {
     case 512: held(distill_held_kernel<T, 512, REST>, 512); break;
     case 1024: held(distill_held_kernel<T, 1024, REST>, 1024); break;
     default:
-        if (a.dlogits && past_cache(a, sizeof(T))) go(distill_row_kernel<T, REST, true>, kSplitThreads, 1 << 20);
-        else go(distill_row_kernel<T, REST, false>, kSplitThreads, 1 << 20);
+        if (a.dlogits) go(distill_row_kernel<T, REST, true, 1024>, 1024, 256);   // one a CU
+        else go(distill_row_kernel<T, REST, false, kSplitThreads>, kSplitThreads, 1 << 20);
     }
     NSQ_HIP(hipGetLastError());
     return NS_OK;

@@ -660,7 +660,7 @@ def test_distill_many_rows(dtype, n, v, k, kind, rest, form):
 
 
 @pytest.mark.parametrize("rest", [False, True])
-@pytest.mark.parametrize("dtype,v", [("bf16", 3001), ("f32", 20002)])
+@pytest.mark.parametrize("dtype,v", [("bf16", 3001), ("f32", 20002), ("bf16", 140011), ("f32", 66001)])
 def test_distill_rows_far_from_their_pairs(dtype, v, rest):
     """Rows whose sum does not fit relative to their pairs' largest logit: others far above it, all others far below
     it, masked by infinity or by the lowest value; next to ordinary rows."""
@@ -704,7 +704,7 @@ def test_distill_same_bits():
     import torch
     log("distill bits")
     rng = np.random.default_rng(0)
-    for n, v in ((3, 20000), (300, 9000)):
+    for n, v in ((3, 20000), (300, 9000), (260, 140011)):
         for rest in (False, True):
             c = _distill_case(rng, n, v, 11, "bf16", rest=rest, tau=1.3)
             for form in ("train", "step"):
