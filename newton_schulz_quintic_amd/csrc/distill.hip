@@ -36,6 +36,7 @@ constexpr int kMaxTop = 1024;
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kMaxRows = 1 << 24;
 constexpr int kMaxChunks = 64;            // parts of a row that is split over workgroups
+constexpr int kScanPairs = 128;           // up to so many pairs each one looks for its token in all others
 constexpr int kBitVocab = 1 << 18;        // tokens one workgroup marks in LDS (32 KiB)
 constexpr int kSplitThreads = 256;
 constexpr int kHeldVecs = 16;             // vectors of a row that a thread holds
@@ -113,6 +114,10 @@ struct PairLds {
     int32_t owner[TOP];        // the token, in the lowest of its pairs; -1 in the others
     Lse wave[16];
     float wave_sum[16];
+    // many pairs: marks of the tokens' hashes, seen and seen again, and the pairs whose hash was seen again
+    static constexpr int kMarks = TOP > kScanPairs ? TOP : 1;
+    uint32_t once[kMarks], again[kMarks];
+    int32_t listed[kMarks], listed_count;
 };
 
 struct Pairs {
@@ -173,7 +178,15 @@ __device__ inline void clear_pairs(const DistillArgs &A, PairLds<TOP> &L, uint32
     if (threadIdx.x < 4) L.id[A.top_k + threadIdx.x] = -1, L.p[A.top_k + threadIdx.x] = 0.f;
     if constexpr (REST)
         for (int i = threadIdx.x; i < words; i += blockDim.x) bits[i] = 0;
+    if constexpr (TOP > kScanPairs)
+        if (A.top_k > kScanPairs) {
+            for (int i = threadIdx.x; i < TOP; i += blockDim.x) L.once[i] = L.again[i] = 0;
+            if (threadIdx.x == 0) L.listed_count = 0;
+        }
 }
+
+// Where a token's mark is: 32 marks for each pair there is room for.
+template <int TOP> __device__ inline int mark_of(int id) { return (uint32_t)id * 2654435769u >> 17 & (TOP * 32 - 1); }
 
 // Brings the row's pairs into LDS; says whether the row has a loss. Ends with
 // every thread past the barrier.
@@ -195,11 +208,21 @@ __device__ inline float teacher_lse(const DistillArgs &A, int64_t row) {
 }
 
 // p of every pair, the tokens' lowest pairs, and with REST the tokens' bits
-// among [e0, e1). Ends with every thread past a barrier.
+// among [e0, e1). Ends with every thread past a barrier. Few pairs are compared
+// all with all. Of many, those whose token's hash no other has are alone; a wave
+// compares each of the rest with all (loss of 2048 x 32000 bf16 with 1024 pairs:
+// 562 us all with all, 78 by hashes; 50257 tokens, 256 pairs: 74 and 67).
 template <bool REST, int TOP>
 __device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds<TOP> &L, Pairs &r, uint32_t *bits, int e0,
                                    int e1) {
     const int lane = threadIdx.x & 63, threads = blockDim.x;
+    const bool many = TOP > kScanPairs && A.top_k > kScanPairs;
+    const auto settle = [&](int k, int id, bool lowest, float p) {
+        L.owner[k] = lowest ? id : -1;
+        L.p_token[k] = p;
+        if constexpr (REST)
+            if (lowest && id >= e0 && id < e1) atomicOr(&bits[(id - e0) >> 5], 1u << ((id - e0) & 31));
+    };
     if constexpr (REST) {
         if (r.t_max == kNegInf) r.t_max = 0.f;
         r.t_sub = fmaf(-r.t_max, A.inv_tau, lse);
@@ -214,25 +237,49 @@ __device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds<TOP>
         const float log_p = (L.t[k] - r.t_max) * A.inv_tau - r.t_sub;
         L.t[k] = log_p;
         L.p[k] = L.id[k] >= 0 ? __builtin_amdgcn_exp2f(log_p * kLog2e) : 0.f;
+        if (many && L.id[k] >= 0) {
+            const int at = mark_of<TOP>(L.id[k]);
+            const uint32_t bit = 1u << (at & 31);
+            if (atomicOr(&L.once[at >> 5], bit) & bit) atomicOr(&L.again[at >> 5], bit);
+        }
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < A.top_k; k += threads) {
-        const int id = L.id[k];
-        bool lowest = id >= 0;
-        float sum = 0.f;
-#pragma unroll 1
-        for (int j = 0; j < A.top_k; j += 4) {
-            const int4 other = *reinterpret_cast<const int4 *>(&L.id[j]);
-            const float4 p = *reinterpret_cast<const float4 *>(&L.p[j]);
-            lowest = lowest && !(other.x == id && j < k) && !(other.y == id && j + 1 < k) &&
-                     !(other.z == id && j + 2 < k) && !(other.w == id && j + 3 < k);
-            sum += (other.x == id ? p.x : 0.f) + (other.y == id ? p.y : 0.f) + (other.z == id ? p.z : 0.f) +
-                   (other.w == id ? p.w : 0.f);
+    if (many) {
+        for (int k = threadIdx.x; k < A.top_k; k += threads) {
+            const int id = L.id[k], at = mark_of<TOP>(id);
+            if (id >= 0 && (L.again[at >> 5] >> (at & 31) & 1)) L.listed[atomicAdd(&L.listed_count, 1)] = k;
+            else settle(k, id, id >= 0, L.p[k]);
         }
-        L.owner[k] = lowest ? id : -1;
-        L.p_token[k] = sum;
-        if constexpr (REST)
-            if (lowest && id >= e0 && id < e1) atomicOr(&bits[(id - e0) >> 5], 1u << ((id - e0) & 31));
+        __syncthreads();
+        for (int i = threadIdx.x >> 6; i < L.listed_count; i += threads >> 6) {   // a wave each
+            const int k = L.listed[i], id = L.id[k];
+            float sum = 0.f;
+            bool lower = false;
+            for (int j = lane; j < A.top_k; j += 64)
+                if (L.id[j] == id) {
+                    sum += L.p[j];
+                    lower |= j < k;
+                }
+            sum = wave_sum(sum);
+            const bool lowest = !__any(lower);
+            if (lane == 0) settle(k, id, lowest, sum);
+        }
+    } else {
+        for (int k = threadIdx.x; k < A.top_k; k += threads) {
+            const int id = L.id[k];
+            bool lowest = id >= 0;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < A.top_k; j += 4) {
+                const int4 other = *reinterpret_cast<const int4 *>(&L.id[j]);
+                const float4 p = *reinterpret_cast<const float4 *>(&L.p[j]);
+                lowest = lowest && !(other.x == id && j < k) && !(other.y == id && j + 1 < k) &&
+                         !(other.z == id && j + 2 < k) && !(other.w == id && j + 3 < k);
+                sum += (other.x == id ? p.x : 0.f) + (other.y == id ? p.y : 0.f) + (other.z == id ? p.z : 0.f) +
+                       (other.w == id ? p.w : 0.f);
+            }
+            settle(k, id, lowest, sum);
+        }
     }
     __syncthreads();
     if constexpr (REST) {
@@ -588,10 +635,10 @@ __device__ inline RowSums row_sums(const DistillArgs &A, const PairLds<TOP> &L, 
 // weighed while its vectors come in.
 // Vectors go through buffer descriptors: lanes past the row's last whole vector
 // read zeros (not used) and write nothing.
-template <typename T, int THREADS, bool REST>
+template <typename T, int THREADS, bool REST, int TOP>
 __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
-    __shared__ __attribute__((aligned(16))) PairLds<THREADS> L;
+    __shared__ __attribute__((aligned(16))) PairLds<TOP> L;
     typedef uint32_t dwords __attribute__((ext_vector_type(4)));
     typedef typename Vec16<T>::raw raw;
     const Span<T> S(0, A.vocab);
@@ -734,10 +781,10 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
 // last-level cache in between (2048 x 151936 bf16: 361 us with many workgroups of
 // 256 threads, 326 with 256 of 1024 threads, 279 with 8 vectors kept; 12 spill,
 // 287; 2000 x 100000 f32 448, 360 and 315).
-template <typename T, bool REST, bool TRAIN, int THREADS>
+template <typename T, bool REST, int TOP, bool TRAIN, int THREADS>
 __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
-    __shared__ __attribute__((aligned(16))) PairLds<kMaxTop> L;
+    __shared__ __attribute__((aligned(16))) PairLds<TOP> L;
     constexpr int kKept = !TRAIN ? 0 : REST && sizeof(T) == 2 ? kKeptVecs - 2 : kKeptVecs;   // without spilling
     const Span<T> S(0, A.vocab);
     const float c = A.inv_tau * kLog2e;
@@ -781,10 +828,10 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
 }
 
 // Few or very long rows: workgroup (chunk, row) sums its part of the row.
-template <typename T, bool REST>
+template <typename T, bool REST, int TOP>
 __global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
-    __shared__ __attribute__((aligned(16))) PairLds<kMaxTop> L;
+    __shared__ __attribute__((aligned(16))) PairLds<TOP> L;
     const float c = A.inv_tau * kLog2e;
     for (uint32_t b = blockIdx.x; b < (uint32_t)A.rows * A.chunks; b += gridDim.x) {
         const int64_t row = b / (uint32_t)A.chunks;
@@ -811,10 +858,10 @@ __global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillA
 
 // Workgroup (chunk, row) writes its part of the gradient, from the parts' sums
 // (LOSS: the first one also the loss) or from the logsumexps of a forward call.
-template <typename T, bool REST, bool LOSS, bool NT>
+template <typename T, bool REST, int TOP, bool LOSS, bool NT>
 __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArgs A, int32_t parts) {
     extern __shared__ uint32_t bits[];
-    __shared__ __attribute__((aligned(16))) PairLds<kMaxTop> L;
+    __shared__ __attribute__((aligned(16))) PairLds<TOP> L;
     const float c = A.inv_tau * kLog2e;
     for (uint32_t b = blockIdx.x; b < (uint32_t)A.rows * A.chunks; b += gridDim.x) {
         const int64_t row = b / (uint32_t)A.chunks;
@@ -972,7 +1019,7 @@ unsigned split_grid(const DistillArgs &a) { return (unsigned)std::min<int64_t>((
 // backward: 83 -> 67 us; 300 x 131072 bf16, 157 MB: no difference).
 bool past_cache(const DistillArgs &a, int es) { return 2.0 * a.rows * a.vocab * es > (double)kMallBytes; }
 
-template <typename T, bool REST>
+template <typename T, bool REST, int TOP>
 ns_status launch_rows(const DistillArgs &a, hipStream_t st) {
     const size_t lds = REST ? (size_t)((a.vocab + 31) / 32 + 1) * 4 : 0;   // lanes past the row read one byte behind it
     auto go = [&](auto kernel, int threads, int64_t most) {
@@ -981,39 +1028,52 @@ ns_status launch_rows(const DistillArgs &a, hipStream_t st) {
     // Held rows: as many workgroups as are resident at once, 16 waves a CU.
     const auto held = [&](auto kernel, int threads) { go(kernel, threads, 256 * (1024 / threads)); };
     switch (a.dlogits ? held_threads(a, sizeof(T)) : 2048) {
-    case 64: held(distill_held_kernel<T, 64, REST>, 64); break;
-    case 128: held(distill_held_kernel<T, 128, REST>, 128); break;
-    case 256: held(distill_held_kernel<T, 256, REST>, 256); break;
-    case 512: held(distill_held_kernel<T, 512, REST>, 512); break;
-    case 1024: held(distill_held_kernel<T, 1024, REST>, 1024); break;
+    case 64: held(distill_held_kernel<T, 64, REST, std::min(64, TOP)>, 64); break;
+    case 128: held(distill_held_kernel<T, 128, REST, std::min(128, TOP)>, 128); break;
+    case 256: held(distill_held_kernel<T, 256, REST, std::min(256, TOP)>, 256); break;
+    case 512: held(distill_held_kernel<T, 512, REST, std::min(512, TOP)>, 512); break;
+    case 1024: held(distill_held_kernel<T, 1024, REST, std::min(1024, TOP)>, 1024); break;
     default:
-        if (a.dlogits) go(distill_row_kernel<T, REST, true, 1024>, 1024, 256);   // one a CU
-        else go(distill_row_kernel<T, REST, false, kSplitThreads>, kSplitThreads, 1 << 20);
+        if (a.dlogits) go(distill_row_kernel<T, REST, TOP, true, 1024>, 1024, 256);   // one a CU
+        else go(distill_row_kernel<T, REST, TOP, false, kSplitThreads>, kSplitThreads, 1 << 20);
     }
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }
 
-template <typename T, bool REST>
+template <typename T, bool REST, int TOP>
 ns_status launch_split(DistillArgs a, hipStream_t st) {
     set_chunks(a);
     const size_t lds = REST ? (size_t)((a.chunk + 31) / 32) * 4 : 0;
-    hipLaunchKernelGGL((distill_partial_kernel<T, REST>), dim3(split_grid(a)), dim3(kSplitThreads), lds, st, a);
+    hipLaunchKernelGGL((distill_partial_kernel<T, REST, TOP>), dim3(split_grid(a)), dim3(kSplitThreads), lds, st, a);
     NSQ_HIP(hipGetLastError());
     const int32_t parts = a.chunks;
     if (!a.dlogits) a.chunks = 1, a.chunk = a.vocab;
-    hipLaunchKernelGGL((distill_apply_kernel<T, REST, true, false>), dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, parts);
+    hipLaunchKernelGGL((distill_apply_kernel<T, REST, TOP, true, false>), dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, parts);
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }
 
-template <typename T, bool REST>
+template <typename T, bool REST, int TOP>
 ns_status launch_backward(DistillArgs a, hipStream_t st) {
     set_chunks(a);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, 0); };
-    past_cache(a, sizeof(T)) ? go(distill_apply_kernel<T, REST, false, true>) : go(distill_apply_kernel<T, REST, false, false>);
+    past_cache(a, sizeof(T)) ? go(distill_apply_kernel<T, REST, TOP, false, true>) : go(distill_apply_kernel<T, REST, TOP, false, false>);
     NSQ_HIP(hipGetLastError());
     return NS_OK;
+}
+
+// go(T, teacher's rest, room for pairs) for a call's types and sizes.
+template <typename Go> ns_status by_type(const DistillArgs &a, int32_t dtype, const Go &go) {
+    const auto by_top = [&](auto t, auto rest) {
+        if (a.top_k <= kScanPairs) return go(t, rest, std::integral_constant<int, kScanPairs>());
+        return go(t, rest, std::integral_constant<int, kMaxTop>());
+    };
+    const auto by_rest = [&](auto t) {
+        if (a.teacher_lse) return by_top(t, std::true_type());
+        return by_top(t, std::false_type());
+    };
+    return dtype == NS_BF16 ? by_rest((__bf16)0.f) : by_rest(0.f);
 }
 
 }  // namespace
@@ -1041,7 +1101,7 @@ extern "C" ns_status ns_distill_topk(int64_t rows, int32_t vocab, int32_t top_k,
     if (rows > 0 && teacher_lse && !rest_lse) return fail(NS_ERR_INVALID_ARG, "teacher_lse needs rest_lse");
     if (misaligned(loss, 4) || misaligned(lse, 4) || misaligned(rest_lse, 4))
         return fail(NS_ERR_INVALID_ARG, "loss, lse or rest_lse not 4-byte aligned");
-    const bool rest = teacher_lse != nullptr, split = split_rows(a, dtype_bytes(dtype));
+    const bool split = split_rows(a, dtype_bytes(dtype));
     const size_t need = distill_workspace(rows, top_k, split);
     if (need && (!workspace || workspace_bytes < need))
         return fail(NS_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
@@ -1054,11 +1114,13 @@ extern "C" ns_status ns_distill_topk(int64_t rows, int32_t vocab, int32_t top_k,
     if (split) {
         a.partial = reinterpret_cast<float2 *>(workspace);
         a.top_z = reinterpret_cast<float *>(a.partial + rows * kMaxChunks);
-        if (dtype == NS_BF16) return rest ? launch_split<__bf16, true>(a, st) : launch_split<__bf16, false>(a, st);
-        return rest ? launch_split<float, true>(a, st) : launch_split<float, false>(a, st);
+        return by_type(a, dtype, [&](auto t, auto rest, auto top) {
+            return launch_split<decltype(t), decltype(rest)::value, decltype(top)::value>(a, st);
+        });
     }
-    if (dtype == NS_BF16) return rest ? launch_rows<__bf16, true>(a, st) : launch_rows<__bf16, false>(a, st);
-    return rest ? launch_rows<float, true>(a, st) : launch_rows<float, false>(a, st);
+    return by_type(a, dtype, [&](auto t, auto rest, auto top) {
+        return launch_rows<decltype(t), decltype(rest)::value, decltype(top)::value>(a, st);
+    });
 }
 
 extern "C" ns_status ns_distill_topk_backward(int64_t rows, int32_t vocab, int32_t top_k, ns_dtype dtype,
@@ -1078,6 +1140,7 @@ extern "C" ns_status ns_distill_topk_backward(int64_t rows, int32_t vocab, int32
     a.lse = const_cast<float *>(lse);
     a.rest_lse = const_cast<float *>(rest_lse);
     const hipStream_t st = as_stream(stream);
-    if (dtype == NS_BF16) return teacher_lse ? launch_backward<__bf16, true>(a, st) : launch_backward<__bf16, false>(a, st);
-    return teacher_lse ? launch_backward<float, true>(a, st) : launch_backward<float, false>(a, st);
+    return by_type(a, dtype, [&](auto t, auto rest, auto top) {
+        return launch_backward<decltype(t), decltype(rest)::value, decltype(top)::value>(a, st);
+    });
 }

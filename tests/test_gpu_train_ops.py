@@ -474,6 +474,12 @@ def _distill_case(rng, n, v, k, dtype, tdtype="f32", rest=False, tau=1.0, kind="
     z = rng.standard_normal((n, v)) * 2
     ids = np.stack([rng.permutation(max(v, k))[:k] for _ in range(n)]) if v <= 4096 else \
         (rng.integers(0, v, (n, 1)) + np.arange(k) * rng.integers(1, v // k, (n, 1))) % v
+    if kind == "twice":      # one token in all pairs, few tokens, tokens in several pairs, absent ones
+        from_pair = np.where(rng.random((n, k)) < 0.3, rng.integers(0, k, (n, k)), np.arange(k))
+        ids = np.take_along_axis(ids, from_pair, 1)
+        ids[0] = ids[0, 0] % v
+        ids[1] = rng.integers(0, min(v, 40), k)
+        ids[2:][rng.random((n - 2, k)) < 0.1] = v
     for i in range(n):
         ok = ids[i] < v
         z[i, ids[i][ok]] += rng.uniform(3, 9, ok.sum())
@@ -657,6 +663,20 @@ def test_distill_many_rows(dtype, n, v, k, kind, rest, form):
     rng = np.random.default_rng([n, v, k])
     c = _distill_case(rng, n, v, k, dtype, "f32", rest, 2.0, kind)
     _check_distill(c, _distill_run(c, form), rows=sorted(set(rng.integers(0, n, 5)) | {0, 1, 3, n - 1}))
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype,n,v,k", [
+    ("bf16", 4, 5000, 129), ("f32", 4, 40000, 1024), ("bf16", 5, 9001, 128), ("f32", 258, 3000, 300),
+    ("bf16", 257, 5000, 1024), ("bf16", 1030, 600, 200), ("f32", 1030, 300, 129), ("bf16", 256, 140003, 500),
+])
+def test_distill_many_pairs(dtype, n, v, k, rest, form):
+    """Pairs that are compared by their tokens' hashes first, tokens in many of them."""
+    log(f"distill many pairs {n} {v} {k} {dtype} {rest} {form}")
+    rng = np.random.default_rng([n, v, k])
+    c = _distill_case(rng, n, v, k, dtype, "f32", rest, 1.5, "twice")
+    _check_distill(c, _distill_run(c, form), rows=sorted(set(rng.integers(0, n, 4)) | {0, 1, 2, n - 1}))
 
 
 @pytest.mark.parametrize("rest", [False, True])
