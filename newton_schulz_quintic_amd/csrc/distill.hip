@@ -19,7 +19,7 @@
 //
 // Bound by memory: loss and gradient in one call read the row once and write
 // its gradient once, the row staying in registers in between. 4096 x 131072 bf16
-// with 64 pairs: 455 us, 4.7 TB/s, where a large copy here reaches 5.1: the
+// with 64 pairs: 454-459 us, 4.7 TB/s, where a large copy here reaches 5.1: the
 // exponentials (two a value) overlap with the memory only as far as the CUs'
 // phases differ. 1025 x 50021 fp32, loss and then gradient in two calls: 119 us.
 // 4 rows are bound by two launches and their latency, 9.0 us.
