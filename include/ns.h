@@ -539,6 +539,10 @@ ns_status ns_moe_combine_backward(int64_t tokens, int32_t top_k, int32_t hidden,
  * over its whole vocabulary) p_k = exp(teacher_k / temperature - teacher_lse),
  * and all tokens outside the pairs form one more class with p_r = max(0, 1 -
  * sum p_k) and q_r the sum of their q: loss += p_r (log p_r - log q_r).
+ * dlogits is the gradient of that loss wherever p_r was cut off, too: with P =
+ * sum p_k + p_r (1 unless the p_k exceed 1, or the pairs hold every token),
+ *   dloss / dlogits_j = (P q_j - sum of j's p_k) / temperature,
+ * for the tokens of the further class (P q_r - p_r) q_j / (q_r temperature).
  * Terms with p = 0 count as 0. Pairs whose id is outside [0, vocab) are
  * absent; several pairs may hold one token (their p add up). A row without
  * pairs, or without teacher_lse one whose teacher logits are all -inf, has

@@ -4,12 +4,16 @@
 // whose token is outside [0, V) are absent. At temperature tau:
 //   q = softmax(z / tau),  p_k = softmax over the row's pairs of t / tau,
 //   loss = sum_k p_k (log p_k - log q[token_k]),
-//   dz_j = g / tau (q_j - sum of p_k over the pairs of token j).
+//   dz_j = g / tau (P q_j - sum of p_k over the pairs of token j),
+// where P, all classes' p together, is 1.
 // With the teacher's logsumexp over its whole vocabulary (at tau), p_k =
 // exp(t_k / tau - lse_T) and all other tokens form one more class with
 // p_r = max(0, 1 - sum p_k) and q_r = the sum of their q:
-//   loss += p_r (log p_r - log q_r),  their dz_j = g / tau (q_r - p_r) q_j / q_r,
-// q_j / q_r being the softmax over them alone, finite however small q_r is.
+//   loss += p_r (log p_r - log q_r),  their dz_j = g / tau (P q_r - p_r) q_j / q_r,
+// q_j / q_r being the softmax over them alone, finite however small q_r is. P is
+// 1 again where p_r > 0, and the pairs' sum where p_r is 0: more than 1 where a
+// token is listed twice or lse_T is too small for the teacher's (rounded) logits,
+// less where the pairs hold every token.
 // Terms with p = 0 count as 0. A row without pairs (or, without lse_T, with
 // every teacher logit -inf) has loss and gradient 0 and its logits are not used.
 //
@@ -123,6 +127,7 @@ struct PairLds {
 struct Pairs {
     bool some;      // the row has a loss
     float t_max, t_sub, p_rest;
+    float mass;     // P
 };
 
 // One pair as it lies in memory (so that a load can be under way while other
@@ -169,6 +174,7 @@ __device__ inline Pairs look_at_pairs(const DistillArgs &A, const PairLds<TOP> &
     if (__any(nan)) r.t_max = __builtin_nanf("");
     r.some = __any(any) && (REST || r.t_max != kNegInf);
     r.t_sub = r.p_rest = 0.f;
+    r.mass = 1.f;
     return r;
 }
 
@@ -289,9 +295,11 @@ __device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds<TOP>
             sum += L.p[k];
             tokens += L.owner[k] >= 0;
         }
-        r.p_rest = 1.f - wave_sum(sum);
+        sum = wave_sum(sum);
+        r.p_rest = 1.f - sum;
         // nothing outside the pairs: no class to hold what rounding leaves
         if (r.p_rest < 0.f || (int)wave_sum((float)tokens) == A.vocab) r.p_rest = 0.f;
+        if (r.p_rest == 0.f) r.mass = sum;
     }
 }
 
@@ -525,7 +533,7 @@ __device__ inline void grad_span(const T *z, T *dz, const Span<T> &S, const Norm
 }
 
 // The tail's gradient, then that of the pairs' tokens, each written over the
-// other tokens' formula by the thread that wrote it.
+// other tokens' formula by the thread that wrote it. n: of the pairs' tokens, P q.
 template <typename T, typename Put, int TOP>
 __device__ inline void finish_span(const DistillArgs &A, const PairLds<TOP> &L, const Put &put, const Span<T> &S, float zt,
                                    const Norm &n, const Norm &others, float c, float g, float g_others) {
@@ -603,13 +611,13 @@ __device__ inline void write_empty(const DistillArgs &A, int64_t row, const Span
 // What the loss and the gradient of a row take from its sums.
 struct RowSums {
     Lse all, rest;
-    Norm n, others;    // q of any token, and what the others' gradient is g_others times
+    Norm n, others;    // P q of any token, and what the others' gradient is g_others times
     float g, g_others;
 };
 // The others' factor, from their share of the student's mass.
 template <bool REST>
 __device__ inline float others_factor(const Pairs &r, float g, float q_rest) {
-    return REST ? g * (q_rest - r.p_rest) : g;
+    return REST ? g * (r.mass * q_rest - r.p_rest) : g;
 }
 template <bool REST, int TOP>
 __device__ inline RowSums row_sums(const DistillArgs &A, const PairLds<TOP> &L, const Pairs &r, float grad_loss, Lse rest,
@@ -618,6 +626,7 @@ __device__ inline RowSums row_sums(const DistillArgs &A, const PairLds<TOP> &L, 
     s.rest = rest;
     s.all = REST ? join(rest, sum_tokens(A, L, c), c) : rest;
     s.n = norm_of(s.all);
+    if constexpr (REST) s.n.scale *= r.mass;
     s.others = norm_of(s.rest);
     if (REST && rest.s == 0.f && r.p_rest == 0.f) s.others.scale = 0.f;   // no others, or all masked: q is 0
     s.g = grad_loss * A.inv_tau;
@@ -906,6 +915,7 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
                 if (rest_lse == kNegInf) s.others = {0.f, r.p_rest == 0.f ? 0.f : __builtin_inff()};
                 else s.others = norm_of_lse(rest_lse, A.inv_tau);
                 s.g_others = others_factor<REST>(r, s.g, expf(rest_lse - lse));
+                s.n.scale *= r.mass;
             }
         }
         if (A.dlogits) {

@@ -130,6 +130,8 @@ def distill_row(z, ids, t, tau, teacher_lse=None, grad_loss=None):
             if p_rest > 0:
                 loss += p_rest * (np.log(p_rest) - log_q_rest)
                 dz[outside] = (np.exp(log_q_rest) - p_rest) * np.exp(log_q[outside] - log_q_rest)
+            else:
+                dz *= p.sum()        # what all classes' p add up to, here not 1
         for i, (j, _) in enumerate(here):
             dz[j] -= p[i]
         g = 1.0 if grad_loss is None else grad_loss

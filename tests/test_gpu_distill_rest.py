@@ -1,0 +1,128 @@
+"""GPU parity of ns_distill_topk with a teacher's logsumexp: how the pairs' and the rest's masses enter the gradient.
+
+Against the fp64 oracle (oracle/train_ops.py), with tolerances as in
+test_gpu_train_ops.py: U = 2^-24 is half a step of fp32, a bf16 result adds
+2^-8 of the value.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import train_ops as ops
+from tests.helpers import host_to_f64, log, to_device
+from tests.test_gpu_train_ops import HALF_STEP, U, _close, _distill_case, _distill_run, _f64
+from workloads import f32_to_bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+
+def _teacher(c, t, lse, tdtype="f32"):
+    """Puts teacher logits and logsumexps (rounded to fp32, as the call takes them) into a case."""
+    import torch
+    tb = f32_to_bf16_bits(t.astype(np.float32)) if tdtype == "bf16" else t.astype(np.float32)
+    c["t64"], c["t"] = host_to_f64(tb, tdtype), to_device(tb, tdtype)
+    c["lse64"] = lse.astype(np.float32).astype(np.float64)
+    c["lse_d"] = torch.from_numpy(lse.astype(np.float32)).cuda()
+    return c
+
+
+def _check(c, got, form, rows, p_steps=None):
+    """With F = P - p_r / q_r the gradient is g / tau (q_j F - sum of j's p). Relative errors: of q, (4 |z - m| / tau + 4 E
+    + 64) U as in _check_distill, and 2 |lse| U more where lse was rounded between two calls; of q_r likewise; of p,
+    p_steps U if given, else (4 (|t| / tau + |lse_T|) + 64) U, the rounding of fp32 exponents. P and p_r are off by dP, the
+    sum of the p's errors (and half a step of their own), which reaches others through F."""
+    loss, lse, rest, dz = got
+    tau, half = c["tau"], HALF_STEP[c["dtype"]]
+    for i in rows:
+        w = ops.distill_row(c["z64"][i], c["ids"][i], c["t64"][i], tau, c["lse64"][i], c["g64"][i])
+        g, z, v = c["g64"][i], c["z64"][i], len(c["z64"][i])
+        if not w["some"]:
+            assert loss[i] == 0 and lse[i] == 0 and rest[i] == 0 and not dz[i].float().abs().any()
+            continue
+        here = [(int(j), float(x)) for j, x in zip(c["ids"][i], c["t64"][i]) if 0 <= j < v]
+        at = np.array([j for j, _ in here])
+        t = np.array([x for _, x in here])
+        with np.errstate(all="ignore"):
+            q, p, p_rest = w["q"], w["p"], w["p_rest"]
+            arg = np.where(q > 0, np.abs(z - np.max(z)) / tau, 0.0)
+            E = np.sum(q * arg)
+            two = 2 * abs(w["lse"]) if form == "step" else 0.0
+            err_q = (4 * arg + 4 * E + 64 + two) * U
+            steps = 4 * (np.abs(t) / tau + abs(c["lse64"][i])) + 64 if p_steps is None else p_steps
+            err_p = np.where(p > 0, steps * U, 0.0)
+            P = p.sum() + p_rest
+            dP = np.sum(np.where(p > 0, p * err_p, 0.0)) + 2 * U * max(p_rest if p_steps else 1.0, 1e-9)
+            outside = np.ones(v, bool)
+            outside[at] = False
+            factor, err_factor = P, dP + 2 * U * P
+            err_rest = 0.0
+            if outside.any():
+                zr = z[outside]
+                qr = np.exp(w["rest_lse"] - w["lse"])
+                er = np.sum(np.where(zr > -np.inf, q[outside] * np.abs(zr - zr.max()) / tau, 0)) / max(qr, 1e-300)
+                err_rest = (4 * er + 64 + 4 * np.abs(zr.max() - np.max(z)) / tau + 4 * E
+                            + (2 * abs(w["lse"]) + 2 * abs(w["rest_lse"]) if form == "step" else 0.0)) * U
+                if p_rest > 0:
+                    factor = 1 - p_rest / qr
+                    err_factor = (dP + p_rest * (err_rest + 8 * U)) / qr
+                assert abs(float(rest[i]) - w["rest_lse"]) <= U * (4 * abs(zr.max()) / tau + 4 * er + 64 + 2 * abs(w["rest_lse"]))
+            size = q * ((err_q + err_rest) * (np.abs(factor) + P * (p_rest > 0)) + err_factor)
+            size[at] = (q * (err_q * P + err_factor if p_rest == 0 else err_q))[at]
+            for a, b in zip(at, p * err_p):
+                size[a] += b
+            used = p > 0
+            diff = np.abs(w["log_p"] - np.log(q[at]))
+            tol = np.sum((p * ((4 * arg[at] + 4 * E + 64) * U + err_p + (err_p + 64 * U) * diff
+                               + 2 * U * np.abs(w["log_p"])))[used])
+            if p_rest > 0:
+                log_qr = w["rest_lse"] - w["lse"]
+                tol += dP * (1 + abs(np.log(p_rest) - log_qr)) + p_rest * (err_rest + 8 * U * (1 + abs(np.log(p_rest)) + abs(log_qr)))
+        assert abs(float(loss[i]) - w["loss"]) <= tol + 4 * U * abs(w["loss"]), (i, float(loss[i]), w["loss"], tol)
+        want = np.where(np.abs(w["dlogits"]) < 2.0 ** -126, 0.0, w["dlogits"])
+        _close(_f64(dz[i]), want, half * np.abs(want) + g / tau * size + 8 * U * np.abs(want) + 2.0 ** -126, f"row {i}")
+
+
+# every form of the kernels: rows split over workgroups, held in 64 .. 1024 threads, too long to hold
+FORMS = [(3, 9001, 40), (260, 300, 20), (257, 3001, 300), (256, 33000, 24), (256, 66001, 64), (256, 140003, 16)]
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,v,k", FORMS)
+@pytest.mark.parametrize("kind", ["small logsumexp", "bf16 teacher", "listed twice"])
+def test_pairs_whose_mass_passes_one(kind, n, v, k, dtype, form):
+    """A logsumexp below the pairs' own, teacher logits rounded to bf16 after it was taken, tokens listed twice."""
+    log(f"distill mass {kind} {n} {v} {k} {dtype} {form}")
+    rng = np.random.default_rng([n, v, k])
+    tau = 1.5
+    c = _distill_case(rng, n, v, k, dtype, rest=True, tau=tau)
+    t = rng.uniform(3, 14, (n, k))
+    lse = np.array([ops._lse(r / tau) for r in t])
+    if kind == "small logsumexp":
+        lse -= rng.uniform(0.05, 0.8, n)
+    elif kind == "bf16 teacher":
+        lse += 1e-4
+    else:
+        c["ids"][:, k // 2:] = c["ids"][:, :k - k // 2]
+        t[:, k // 2:] = t[:, :k - k // 2]
+        lse = np.array([ops._lse(r[:k // 2] / tau) for r in t]) + 1e-3
+        import torch
+        c["ids_d"] = torch.from_numpy(c["ids"].astype(np.int32)).cuda()
+    _teacher(c, t, lse, "bf16" if kind == "bf16 teacher" else "f32")
+    mass = np.exp(c["t64"] / tau - c["lse64"][:, None]).sum(1)
+    rows = sorted(set(rng.integers(0, n, 4)) | {0, n - 1, int(np.argmax(mass))})
+    assert mass[rows].max() > 1
+    _check(c, _distill_run(c, form), form, rows)
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,v", [(4, 40), (260, 40), (258, 301), (3, 1), (256, 1024)])
+def test_pairs_that_hold_every_token(n, v, dtype, form):
+    """No class for the rest, whatever the pairs' mass adds up to."""
+    log(f"distill every token {n} {v} {dtype} {form}")
+    rng = np.random.default_rng([n, v])
+    c = _distill_case(rng, n, v, v, dtype, rest=True, tau=2.0)
+    t = rng.uniform(3, 9, (n, v))
+    _teacher(c, t, np.array([ops._lse(r / 2.0) for r in t]) + rng.uniform(-0.5, 0.5, n))
+    _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 4)) | {0, n - 1}))

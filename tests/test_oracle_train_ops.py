@@ -108,3 +108,24 @@ def test_distill_rows_without_teacher():
     z = np.zeros(3)
     assert ops.distill_row(z, [0, 1], [-np.inf, 0.0], 1.0)["loss"] == pytest.approx(np.log(3))
     assert ops.distill_row(np.array([-np.inf, 0.0]), [0], [0.0], 1.0)["loss"] == np.inf
+
+
+@pytest.mark.parametrize("z_size,ids,lse_off", [
+    (7, [3, 0, 5], -0.06),     # the pairs' p sum to more than 1: the teacher's logsumexp is too small
+    (7, [3, 0, 5], -0.6),
+    (7, [3, 5, 3], None),      # one token listed twice, the logsumexp over distinct tokens
+    (4, [3, 0, 2, 1], 0.4),    # every token paired: no class for the rest, whatever the sum
+    (3, [2, 0, 1, 1], -0.2),
+])
+def test_distill_gradient_where_the_pairs_mass_is_not_one(z_size, ids, lse_off):
+    rng = np.random.default_rng(8)
+    z, t = rng.standard_normal(z_size), rng.standard_normal(len(ids))
+    if lse_off is None:
+        t[2] = t[0]
+        lse = ops._lse(t[:2] / 1.7) + 0.01
+    else:
+        lse = ops._lse(t / 1.7) + lse_off
+    row = ops.distill_row(z, ids, t, 1.7, lse, 0.3)
+    want = _numeric(lambda v: 0.3 * ops.distill_row(v, ids, t, 1.7, lse)["loss"], z)
+    assert row["p_rest"] == 0 and abs(row["p"].sum() - 1) > 0.05
+    assert np.allclose(row["dlogits"], want, atol=1e-8)
