@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "op_util.h"
+#include "sort_split.h"
 
 namespace nsq {
 namespace {
@@ -31,11 +32,8 @@ namespace {
 // ---------------------------------------------------------------------------
 
 constexpr int kMaxExperts = 1024;
-constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxSortBlocks = 256;
 constexpr int kSortRounds = 4;   // rounds of 64 slots that a wave ranks at once
-constexpr int kOneRounds = 4;    // most rounds of one workgroup by itself
 
 struct SortArgs {
     const void *ids;
@@ -537,15 +535,11 @@ extern "C" ns_status ns_moe_sort(int64_t tokens, int32_t top_k, int32_t experts,
     a.slot_of_row = slot_of_row;
     a.row_of_slot = row_of_slot;
     a.hist = reinterpret_cast<int32_t *>(workspace);
-    // One workgroup up to 4 rounds of 512 slots (2048 slots: 4.9 us; 4096: 9.3, two launches 6.4), past that two
-    // launches over up to 256 workgroups (524288 slots of 256 experts: 128 workgroups 15.5 us, 512 25).
-    const int64_t rounds = (a.slots + kSortThreads - 1) / kSortThreads;
-    const bool one = rounds <= kOneRounds;
-    const int64_t per = one ? (rounds > 0 ? rounds : 1) : (rounds + kMaxSortBlocks - 1) / kMaxSortBlocks;
-    a.per = (int32_t)(per * kSortThreads);
-    a.blocks = one ? 1 : (int32_t)((rounds + per - 1) / per);
+    const SortSplit split = sort_split(a.slots);
+    a.per = split.per;
+    a.blocks = split.blocks;
     const hipStream_t st = as_stream(stream);
-    if (one) {
+    if (a.blocks == 1) {
         hipLaunchKernelGGL(moe_rank_kernel<true>, dim3(1), dim3(kSortThreads), 0, st, a);
     } else {
         hipLaunchKernelGGL(moe_count_kernel, dim3(a.blocks), dim3(kSortThreads), 0, st, a);
