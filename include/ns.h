@@ -485,9 +485,9 @@ ns_status ns_qk_norm_rope_backward(int64_t batch, int64_t seq, int32_t head_dim,
                                    size_t workspace_bytes, void *stream);
 
 /* Tokens sorted by expert. The tokens' top_k choices are tokens * top_k slots
- * (slot = token * top_k + choice, < 2^31), and every slot gets one of as many
- * rows: kept slots by expert, then by slot (stable). Slots whose expert id is
- * outside [0, experts) (a dropped choice, e.g. -1) take the rows behind them
+ * (slot = token * top_k + choice, < 2^31; top_k <= 2^30), and every slot gets
+ * one of as many rows: kept slots by expert, then by slot (stable). Slots whose
+ * expert id is outside [0, experts) (a dropped choice, e.g. -1) take the rows behind them
  * in slot order and appear complemented (~row, ~slot: negative).
  * experts      1 .. 1024.
  * expert_ids   int32 or int64 (id_bytes 4 or 8): choice k of token t is at

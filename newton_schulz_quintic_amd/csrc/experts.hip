@@ -396,7 +396,9 @@ __global__ __launch_bounds__(512) void moe_combine_backward_kernel(RowArgs A) {
 ns_status check_slots(int64_t tokens, int32_t top_k) {
     if (tokens < 0) return fail(NS_ERR_INVALID_ARG, "tokens < 0");
     if (top_k < 1) return fail(NS_ERR_INVALID_ARG, "top_k = %d < 1", top_k);
-    if (tokens >= (int64_t(1) << 31) / top_k) return fail(NS_ERR_OVERFLOW, "tokens x top_k does not fit in 31 bits");
+    // top_k: the kernels count choices in steps of 8 in 32 bits
+    if (tokens > INT32_MAX / top_k || (tokens > 0 && top_k > 1 << 30))
+        return fail(NS_ERR_OVERFLOW, "tokens x top_k does not fit in 31 bits, or top_k in 30");
     return NS_OK;
 }
 

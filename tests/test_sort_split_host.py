@@ -8,6 +8,8 @@ import subprocess
 
 import pytest
 
+import newton_schulz_quintic_amd as nsq
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -30,3 +32,19 @@ def test_every_slot_has_a_workgroup(tmp_path):
         assert per > 0 and per % 512 == 0 and 1 <= blocks <= 256, n
         assert per * blocks >= n and (blocks == 1 or per * (blocks - 1) < n), n   # all dealt, no workgroup without slots
         assert (blocks == 1) == (n <= 2048), n                                     # a single launch for few
+
+
+@pytest.mark.parametrize("top_k", [1, 2, 3, 5, 7, 8, 1000, 2 ** 30])
+def test_every_count_of_slots_below_two_to_the_31_is_taken(top_k):
+    most = (2 ** 31 - 1) // top_k
+    assert nsq.ns_moe_sort_workspace_bytes(most, top_k, 8) > 0
+    with pytest.raises(nsq.NSError) as e:
+        nsq.ns_moe_sort_workspace_bytes(most + 1, top_k, 8)
+    assert e.value.name == "NS_ERR_OVERFLOW"
+
+
+def test_choices_past_30_bits_are_refused():
+    assert nsq.ns_moe_sort_workspace_bytes(0, 2 ** 31 - 1, 8) > 0
+    with pytest.raises(nsq.NSError) as e:
+        nsq.ns_moe_sort_workspace_bytes(1, 2 ** 30 + 1, 8)
+    assert e.value.name == "NS_ERR_OVERFLOW"
