@@ -65,6 +65,7 @@ struct DistillArgs {
     int32_t id_bytes, teacher_f32;
     int32_t chunks, chunk;  // parts of a row, tokens of one
     float inv_tau;
+    double inv_tau64;
 };
 
 // ---------------------------------------------------------------------------
@@ -104,6 +105,20 @@ __device__ inline Norm norm_of_lse(float lse, float inv_tau) {
 }
 __device__ inline float q_of(float z, const Norm &n, float c) { return __builtin_amdgcn_exp2f((z - n.m) * c) * n.scale; }
 
+// exp(x) in 64 bits, off by 2^-44 of itself: x = n ln 2 + 256 r with |r| < 2^-9.4, the
+// series to r^4 (r^5 / 120 is below 2^-53), then eight squarings, each of which
+// doubles the relative error of the 2^-53 before it. Few constants and few
+// registers: the usual polynomial's made the kernels that hold a row spill.
+__device__ inline double exp64(double x) {
+    x = x < -800. ? -800. : x > 800. ? 800. : x;   // 0 and infinity; NaN stays
+    const float n = rintf((float)x * kLog2e);
+    const double r = fma(-(double)n, 0.69314718055994530942, x) * 0x1p-8;
+    double e = fma(r, fma(r, fma(r, fma(r, 1. / 24, 1. / 6), 0.5), 1.), 1.);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e *= e;
+    return ldexp(e, (int)n);
+}
+
 // ---------------------------------------------------------------------------
 // a row's pairs
 // ---------------------------------------------------------------------------
@@ -118,6 +133,7 @@ struct PairLds {
     int32_t owner[TOP];        // the token, in the lowest of its pairs; -1 in the others
     Lse wave[16];
     float wave_sum[16];
+    double wave_p[16];
     // many pairs: marks of the tokens' hashes, seen and seen again, and the pairs whose hash was seen again
     static constexpr int kMarks = TOP > kScanPairs ? TOP : 1;
     uint32_t once[kMarks], again[kMarks];
@@ -126,7 +142,8 @@ struct PairLds {
 
 struct Pairs {
     bool some;      // the row has a loss
-    float t_max, t_sub, p_rest;
+    float t_max, t_sub;   // without a rest: the largest teacher logit, and log of the sum relative to it
+    float p_rest;
     float mass;     // P
 };
 
@@ -214,7 +231,9 @@ __device__ inline float teacher_lse(const DistillArgs &A, int64_t row) {
 }
 
 // p of every pair, the tokens' lowest pairs, and with REST the tokens' bits
-// among [e0, e1). Ends with every thread past a barrier. Few pairs are compared
+// among [e0, e1). Ends with every thread past a barrier. With REST p and its sum
+// are found in 64 bits: p_r = 1 - sum is often 1e-3 to 1e-6, and all other
+// tokens' gradients hang on it, while an fp32 sum is off by some 1e-7. Few pairs are compared
 // all with all. Of many, those whose token's hash no other has are alone; a wave
 // compares each of the rest with all (loss of 2048 x 32000 bf16 with 1024 pairs:
 // 562 us all with all, 78 by hashes; 50257 tokens, 256 pairs: 74 and 67).
@@ -229,25 +248,35 @@ __device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds<TOP>
         if constexpr (REST)
             if (lowest && id >= e0 && id < e1) atomicOr(&bits[(id - e0) >> 5], 1u << ((id - e0) & 31));
     };
-    if constexpr (REST) {
-        if (r.t_max == kNegInf) r.t_max = 0.f;
-        r.t_sub = fmaf(-r.t_max, A.inv_tau, lse);
-    } else {
+    if constexpr (!REST) {
         float s = 0.f;
         for (int k = lane; k < A.top_k; k += 64)
             if (L.id[k] >= 0) s += __builtin_amdgcn_exp2f((L.t[k] - r.t_max) * (A.inv_tau * kLog2e));
         r.t_sub = logf(wave_sum(s));
     }
     __syncthreads();   // L.t has been read by every wave
+    double own = 0.;
     for (int k = threadIdx.x; k < A.top_k; k += threads) {
-        const float log_p = (L.t[k] - r.t_max) * A.inv_tau - r.t_sub;
+        float log_p, p;
+        if constexpr (REST) {
+            const double exact = L.t[k] * A.inv_tau64 - lse, p64 = L.id[k] >= 0 ? exp64(exact) : 0.;
+            own += p64;
+            log_p = (float)exact, p = (float)p64;
+        } else {
+            log_p = (L.t[k] - r.t_max) * A.inv_tau - r.t_sub;
+            p = L.id[k] >= 0 ? __builtin_amdgcn_exp2f(log_p * kLog2e) : 0.f;
+        }
         L.t[k] = log_p;
-        L.p[k] = L.id[k] >= 0 ? __builtin_amdgcn_exp2f(log_p * kLog2e) : 0.f;
+        L.p[k] = p;
         if (many && L.id[k] >= 0) {
             const int at = mark_of<TOP>(L.id[k]);
             const uint32_t bit = 1u << (at & 31);
             if (atomicOr(&L.once[at >> 5], bit) & bit) atomicOr(&L.again[at >> 5], bit);
         }
+    }
+    if constexpr (REST) {
+        own = wave_sum(own);
+        if (lane == 0) L.wave_p[threadIdx.x >> 6] = own;
     }
     __syncthreads();
     if (many) {
@@ -289,17 +318,14 @@ __device__ inline void weigh_pairs(const DistillArgs &A, float lse, PairLds<TOP>
     }
     __syncthreads();
     if constexpr (REST) {
-        float sum = 0.f;
+        double sum = 0.;
+        for (int w = 0; w < threads >> 6; ++w) sum += L.wave_p[w];
         int tokens = 0;
-        for (int k = lane; k < A.top_k; k += 64) {
-            sum += L.p[k];
-            tokens += L.owner[k] >= 0;
-        }
-        sum = wave_sum(sum);
-        r.p_rest = 1.f - sum;
+        for (int k = lane; k < A.top_k; k += 64) tokens += L.owner[k] >= 0;
+        r.p_rest = (float)(1. - sum);
         // nothing outside the pairs: no class to hold what rounding leaves
         if (r.p_rest < 0.f || (int)wave_sum((float)tokens) == A.vocab) r.p_rest = 0.f;
-        if (r.p_rest == 0.f) r.mass = sum;
+        if (r.p_rest == 0.f) r.mass = (float)sum;
     }
 }
 
@@ -789,9 +815,10 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
 // each thread: one workgroup a CU, so that the 256 rows under way stay in the
 // last-level cache in between (2048 x 151936 bf16: 361 us with many workgroups of
 // 256 threads, 326 with 256 of 1024 threads, 279 with 8 vectors kept; 12 spill,
-// 287; 2000 x 100000 f32 448, 360 and 315).
+// 287; 2000 x 100000 f32 448, 360 and 315). Loss alone with the rest: at most 72
+// registers, for 7 waves a SIMD (with 89 and 5 waves 8192 x 8192 bf16 took 65 us, not 53).
 template <typename T, bool REST, int TOP, bool TRAIN, int THREADS>
-__global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs A) {
+__global__ __launch_bounds__(THREADS, REST && !TRAIN && TOP <= kScanPairs ? 7 : 1) void distill_row_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
     __shared__ __attribute__((aligned(16))) PairLds<TOP> L;
     constexpr int kKept = !TRAIN ? 0 : REST && sizeof(T) == 2 ? kKeptVecs - 2 : kKeptVecs;   // without spilling
@@ -1018,6 +1045,7 @@ ns_status check_distill(int64_t rows, int32_t vocab, int32_t top_k, int32_t dtyp
     a->vocab = vocab;
     a->top_k = top_k;
     a->inv_tau = inv_tau;
+    a->inv_tau64 = 1. / temperature;
     return NS_OK;
 }
 

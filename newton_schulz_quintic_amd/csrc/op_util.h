@@ -67,6 +67,18 @@ __device__ inline float lanes_join(float v, const Op &op) {
     if constexpr (STEP < STEPS) return lanes_join<STEP + 1, STEPS>(op(v, partner<STEP>(v)), op);
     return v;
 }
+// The same of a double, in halves.
+template <int STEP>
+__device__ inline double partner(double v) {
+    typedef float halves __attribute__((ext_vector_type(2)));
+    halves h = __builtin_bit_cast(halves, v);
+    return __builtin_bit_cast(double, halves{partner<STEP>(h.x), partner<STEP>(h.y)});
+}
+template <int STEP = 0>
+__device__ inline double wave_sum(double v) {
+    if constexpr (STEP < 6) return wave_sum<STEP + 1>(v + partner<STEP>(v));
+    return v;
+}
 __device__ inline float wave_sum(float v) {
     return lanes_join<0, 6>(v, [](float a, float b) { return a + b; });
 }

@@ -26,11 +26,13 @@ def _teacher(c, t, lse, tdtype="f32"):
     return c
 
 
-def _check(c, got, form, rows, p_steps=None):
+def _check(c, got, form, rows, p_steps=None, mass64=False):
     """With F = P - p_r / q_r the gradient is g / tau (q_j F - sum of j's p). Relative errors: of q, (4 |z - m| / tau + 4 E
     + 64) U as in _check_distill, and 2 |lse| U more where lse was rounded between two calls; of q_r likewise; of p,
     p_steps U if given, else (4 (|t| / tau + |lse_T|) + 64) U, the rounding of fp32 exponents. P and p_r are off by dP, the
-    sum of the p's errors (and half a step of their own), which reaches others through F."""
+    sum of the p's errors (and half a step of their own), which reaches others through F. With mass64 they come from p in
+    64 bits and are rounded once: 2^-44 of the exponential, the exponent's roundings, 2^-53 of its parts each (4 of them
+    counted), and half a step of p_r."""
     loss, lse, rest, dz = got
     tau, half = c["tau"], HALF_STEP[c["dtype"]]
     for i in rows:
@@ -51,7 +53,9 @@ def _check(c, got, form, rows, p_steps=None):
             steps = 4 * (np.abs(t) / tau + abs(c["lse64"][i])) + 64 if p_steps is None else p_steps
             err_p = np.where(p > 0, steps * U, 0.0)
             P = p.sum() + p_rest
-            dP = np.sum(np.where(p > 0, p * err_p, 0.0)) + 2 * U * max(p_rest if p_steps else 1.0, 1e-9)
+            dP = np.sum(np.where(p > 0, p * err_p, 0.0)) + 2 * U
+            if mass64:
+                dP = P * (2.0 ** -44 + 2.0 ** -51 * (np.max(np.abs(t)) / tau + abs(c["lse64"][i]))) + U * p_rest
             outside = np.ones(v, bool)
             outside[at] = False
             factor, err_factor = P, dP + 2 * U * P
@@ -126,3 +130,22 @@ def test_pairs_that_hold_every_token(n, v, dtype, form):
     t = rng.uniform(3, 9, (n, v))
     _teacher(c, t, np.array([ops._lse(r / 2.0) for r in t]) + rng.uniform(-0.5, 0.5, n))
     _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 4)) | {0, n - 1}))
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tail", [1e-2, 1e-3, 1e-4, 1e-5, 1e-6])
+@pytest.mark.parametrize("n,v,k", FORMS)
+def test_small_tails_keep_their_digits(n, v, k, tail, dtype, form):
+    """Little mass left for the rest, and a student that gives it less still: 1 - sum p decides the others' gradient."""
+    log(f"distill tail {n} {v} {k} {tail} {dtype} {form}")
+    rng = np.random.default_rng([n, v, k])
+    tau = 1.5
+    c = _distill_case(rng, n, v, k, dtype, rest=True, tau=tau)
+    z = c["z64"].copy()
+    np.put_along_axis(z, c["ids"], np.take_along_axis(z, c["ids"], 1) + 30.0, 1)
+    bits = f32_to_bf16_bits(z.astype(np.float32)) if dtype == "bf16" else z.astype(np.float32)
+    c["z64"], c["z"] = host_to_f64(bits, dtype), to_device(bits, dtype)
+    t = rng.uniform(3, 14, (n, k)).astype(np.float32).astype(np.float64)
+    _teacher(c, t, np.array([ops._lse(r / tau) for r in t]) - np.log1p(-tail))
+    _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 3)) | {0, n - 1}), p_steps=4, mass64=True)
