@@ -543,6 +543,11 @@ ns_status ns_moe_combine_backward(int64_t tokens, int32_t top_k, int32_t hidden,
  * sum p_k + p_r (1 unless the p_k exceed 1, or the pairs hold every token),
  *   dloss / dlogits_j = (P q_j - sum of j's p_k) / temperature,
  * for the tokens of the further class (P q_r - p_r) q_j / (q_r temperature).
+ * p_k and p_r are found in 64 bits. Where q_r is 0 (every token outside the
+ * pairs masked) a p_r of no more than sum_k p_k ((|t_k| + |teacher_lse| + 4)
+ * 2^-22 + |t_k| h), t_k = teacher_k / temperature, h = 2^-7 for bf16 teacher
+ * logits and else 0, is what their rounding leaves and counts as 0; a larger
+ * one makes the loss infinite.
  * Terms with p = 0 count as 0. Pairs whose id is outside [0, vocab) are
  * absent; several pairs may hold one token (their p add up). A row without
  * pairs, or without teacher_lse one whose teacher logits are all -inf, has

@@ -13,7 +13,8 @@
 // q_j / q_r being the softmax over them alone, finite however small q_r is. P is
 // 1 again where p_r > 0, and the pairs' sum where p_r is 0: more than 1 where a
 // token is listed twice or lse_T is too small for the teacher's (rounded) logits,
-// less where the pairs hold every token.
+// less where the pairs hold every token. Where the student gives all others no
+// mass at all, a p_r that may be rounding of the teacher's side alone is 0.
 // Terms with p = 0 count as 0. A row without pairs (or, without lse_T, with
 // every teacher logit -inf) has loss and gradient 0 and its logits are not used.
 //
@@ -645,10 +646,30 @@ template <bool REST>
 __device__ inline float others_factor(const Pairs &r, float g, float q_rest) {
     return REST ? g * (r.mass * q_rest - r.p_rest) : g;
 }
+// For rows whose others have no mass in the student: a p_r no larger than what
+// rounding can leave of 1 - sum p becomes 0, or the loss of a student masked to
+// the pairs' tokens would be infinite for an lse_T over just these, half the
+// time. Rounded are teacher logits (bf16: by half a step, counted whole for the
+// exponential's sake) and lse_T, a logsumexp in fp32 (its parts by four half steps).
+template <int TOP>
+__device__ inline void drop_rounding(const DistillArgs &A, const PairLds<TOP> &L, Pairs &r, int64_t row) {
+    if (!(r.p_rest > 0.f)) return;
+    const float lse = A.teacher_lse[row];   // read again: seldom needed here
+    float left = 0.f;
+    for (int k = threadIdx.x & 63; k < A.top_k; k += 64)
+        if (L.p[k] > 0.f) {
+            const float size = fabsf(L.t[k] + lse);   // of t / tau
+            left += L.p[k] * (size * (A.teacher_f32 ? 0.f : 0x1p-7f) + 0x1p-22f * (size + fabsf(lse) + 4.f));
+        }
+    if (r.p_rest > wave_sum(left)) return;
+    r.mass = 1.f - r.p_rest;
+    r.p_rest = 0.f;
+}
 template <bool REST, int TOP>
-__device__ inline RowSums row_sums(const DistillArgs &A, const PairLds<TOP> &L, const Pairs &r, float grad_loss, Lse rest,
-                                   float c) {
+__device__ inline RowSums row_sums(const DistillArgs &A, const PairLds<TOP> &L, Pairs &r, int64_t row, float grad_loss,
+                                   Lse rest, float c) {
     RowSums s;
+    if (REST && rest.s == 0.f) drop_rounding(A, L, r, row);
     s.rest = rest;
     s.all = REST ? join(rest, sum_tokens(A, L, c), c) : rest;
     s.n = norm_of(s.all);
@@ -772,7 +793,7 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
             __syncthreads();
             rest = block_join(a, L, c);
         }
-        const RowSums s = row_sums<REST>(A, L, r, now.g, rest, c);
+        const RowSums s = row_sums<REST>(A, L, r, row, now.g, rest, c);
         // The next row: first what lies besides its vectors, and the pairs of the row after it.
         p = ahead;
         now = beside_of(next, p);
@@ -849,7 +870,7 @@ __global__ __launch_bounds__(THREADS, REST && !TRAIN && TOP <= kScanPairs ? 7 : 
             __syncthreads();
             rest = block_join(sum_span<T, REST>(z, zt, S, bits, c), L, c);
         }
-        const RowSums s = row_sums<REST>(A, L, r, TRAIN ? A.grad_loss[row] : 0.f, rest, c);
+        const RowSums s = row_sums<REST>(A, L, r, row, TRAIN ? A.grad_loss[row] : 0.f, rest, c);
         if constexpr (TRAIN) {
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
 #pragma unroll
@@ -932,15 +953,19 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
         weigh_pairs<REST>(A, t_lse, L, r, bits, 0, 0);
         RowSums s{};
         if constexpr (LOSS) {
-            s = row_sums<REST>(A, L, r, g, wave_join({part.x, part.y}, c), c);
+            s = row_sums<REST>(A, L, r, row, g, wave_join({part.x, part.y}, c), c);
         } else {
             const float lse = A.lse[row];
             s.n = s.others = norm_of_lse(lse, A.inv_tau);
             s.g = s.g_others = g * A.inv_tau;
             if constexpr (REST) {
                 const float rest_lse = A.rest_lse[row];
-                if (rest_lse == kNegInf) s.others = {0.f, r.p_rest == 0.f ? 0.f : __builtin_inff()};
-                else s.others = norm_of_lse(rest_lse, A.inv_tau);
+                if (rest_lse == kNegInf) {
+                    drop_rounding(A, L, r, row);
+                    s.others = {0.f, r.p_rest == 0.f ? 0.f : __builtin_inff()};
+                } else {
+                    s.others = norm_of_lse(rest_lse, A.inv_tau);
+                }
                 s.g_others = others_factor<REST>(r, s.g, expf(rest_lse - lse));
                 s.n.scale *= r.mass;
             }

@@ -103,8 +103,20 @@ def _lse(x):
     return m if not np.isfinite(m) else m + np.log(np.sum(np.exp(x - m)))
 
 
-def distill_row(z, ids, t, tau, teacher_lse=None, grad_loss=None):
-    """One row: dict(loss, lse, rest_lse, dlogits, p, p_rest, q) in fp64; z (V,), ids and t (K,)."""
+def _rounding_left(p, scaled, lse, teacher_bf16):
+    """What rounding of the teacher's logits (a step of bf16) and of an fp32 logsumexp of them can leave of 1 - sum p."""
+    with np.errstate(all="ignore"):
+        size = np.abs(scaled)
+        each = p * (size * (2.0 ** -7 if teacher_bf16 else 0.0) + 2.0 ** -22 * (size + abs(lse) + 4))
+    return np.sum(each[p > 0])
+
+
+def distill_row(z, ids, t, tau, teacher_lse=None, grad_loss=None, teacher_bf16=False):
+    """One row: dict(loss, lse, rest_lse, dlogits, p, p_rest, q) in fp64; z (V,), ids and t (K,).
+
+    teacher_bf16: the teacher's logits were rounded to bf16, which counts where all that is left of 1 - sum p may be
+    rounding.
+    """
     v = len(z)
     here = [(int(i), float(x)) for i, x in zip(ids, t) if 0 <= i < v]
     empty = {"loss": 0.0, "lse": 0.0, "rest_lse": 0.0, "dlogits": np.zeros(v), "some": False}
@@ -127,6 +139,8 @@ def distill_row(z, ids, t, tau, teacher_lse=None, grad_loss=None):
             outside[[j for j, _ in here]] = False
             rest_lse, log_q_rest = _lse(z[outside]), _lse(log_q[outside])
             p_rest = max(0.0, 1.0 - p.sum()) if outside.any() else 0.0
+            if log_q_rest == -np.inf and 0 < p_rest <= _rounding_left(p, tk, teacher_lse, teacher_bf16):
+                p_rest = 0.0
             if p_rest > 0:
                 loss += p_rest * (np.log(p_rest) - log_q_rest)
                 dz[outside] = (np.exp(log_q_rest) - p_rest) * np.exp(log_q[outside] - log_q_rest)

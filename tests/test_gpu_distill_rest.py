@@ -8,6 +8,7 @@ test_gpu_train_ops.py: U = 2^-24 is half a step of fp32, a bf16 result adds
 import numpy as np
 import pytest
 
+import newton_schulz_quintic_amd as nsq
 from oracle import train_ops as ops
 from tests.helpers import host_to_f64, log, to_device
 from tests.test_gpu_train_ops import HALF_STEP, U, _close, _distill_case, _distill_run, _f64
@@ -20,7 +21,7 @@ def _teacher(c, t, lse, tdtype="f32"):
     """Puts teacher logits and logsumexps (rounded to fp32, as the call takes them) into a case."""
     import torch
     tb = f32_to_bf16_bits(t.astype(np.float32)) if tdtype == "bf16" else t.astype(np.float32)
-    c["t64"], c["t"] = host_to_f64(tb, tdtype), to_device(tb, tdtype)
+    c["t64"], c["t"], c["tdtype"] = host_to_f64(tb, tdtype), to_device(tb, tdtype), tdtype
     c["lse64"] = lse.astype(np.float32).astype(np.float64)
     c["lse_d"] = torch.from_numpy(lse.astype(np.float32)).cuda()
     return c
@@ -36,7 +37,8 @@ def _check(c, got, form, rows, p_steps=None, mass64=False):
     loss, lse, rest, dz = got
     tau, half = c["tau"], HALF_STEP[c["dtype"]]
     for i in rows:
-        w = ops.distill_row(c["z64"][i], c["ids"][i], c["t64"][i], tau, c["lse64"][i], c["g64"][i])
+        w = ops.distill_row(c["z64"][i], c["ids"][i], c["t64"][i], tau, c["lse64"][i], c["g64"][i],
+                            teacher_bf16=c["tdtype"] == "bf16")
         g, z, v = c["g64"][i], c["z64"][i], len(c["z64"][i])
         if not w["some"]:
             assert loss[i] == 0 and lse[i] == 0 and rest[i] == 0 and not dz[i].float().abs().any()
@@ -60,7 +62,9 @@ def _check(c, got, form, rows, p_steps=None, mass64=False):
             outside[at] = False
             factor, err_factor = P, dP + 2 * U * P
             err_rest = 0.0
-            if outside.any():
+            if w["rest_lse"] == -np.inf:   # no others, or none with any mass
+                assert rest[i] == -np.inf
+            elif outside.any():
                 zr = z[outside]
                 qr = np.exp(w["rest_lse"] - w["lse"])
                 er = np.sum(np.where(zr > -np.inf, q[outside] * np.abs(zr - zr.max()) / tau, 0)) / max(qr, 1e-300)
@@ -149,3 +153,56 @@ def test_small_tails_keep_their_digits(n, v, k, tail, dtype, form):
     t = rng.uniform(3, 14, (n, k)).astype(np.float32).astype(np.float64)
     _teacher(c, t, np.array([ops._lse(r / tau) for r in t]) - np.log1p(-tail))
     _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 3)) | {0, n - 1}), p_steps=4, mass64=True)
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("dtype,tdtype", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("n,v,k", FORMS)
+def test_masked_others_and_a_logsumexp_of_the_pairs_alone(n, v, k, dtype, tdtype, form):
+    """The student gives every token outside the pairs no mass, and the teacher's logsumexp was taken over the pairs
+    alone, in fp32: what its rounding and the teacher logits' leave of 1 - sum p is no mass either. Some rows hold a
+    real remainder: their loss is infinite, as the formula says."""
+    import torch
+    log(f"distill masked others {n} {v} {k} {dtype} {tdtype} {form}")
+    rng = np.random.default_rng([n, v, k])
+    tau = 1.5
+    c = _distill_case(rng, n, v, k, dtype, rest=True, tau=tau)
+    z = c["z64"].copy()
+    dead = np.ones((n, v), bool)
+    np.put_along_axis(dead, c["ids"], False, 1)
+    z[dead] = -np.inf
+    bits = f32_to_bf16_bits(z.astype(np.float32)) if dtype == "bf16" else z.astype(np.float32)
+    c["z64"], c["z"] = host_to_f64(bits, dtype), to_device(bits, dtype)
+    t = rng.uniform(3, 14, (n, k)).astype(np.float32)
+    scaled = torch.from_numpy(t).cuda() * np.float32(1 / tau)
+    lse = torch.logsumexp(scaled, 1).cpu().numpy()
+    real = np.arange(n) % 5 == 2
+    lse[real] += 0.3
+    _teacher(c, t.astype(np.float64), lse, tdtype)
+    left = 1 - np.exp(c["t64"] / tau - c["lse64"][:, None]).sum(1)
+    if n > 100:
+        assert (left[~real] > 0).sum() > 10
+    got = _distill_run(c, form)
+    loss, dz = _f64(got[0]), _f64(got[3])
+    assert np.isposinf(loss[real]).all()
+    rows = [i for i in range(n) if not real[i]]
+    assert np.isfinite(loss[rows]).all() and np.isfinite(dz[rows]).all() and not dz[rows][dead[rows]].any()
+    _check(c, got, form, sorted(set(rng.choice(rows, min(5, len(rows)))) | {rows[0], rows[-1], rows[int(np.argmax(left[rows]))]}))
+
+
+def test_a_real_remainder_is_kept_where_the_student_gives_it_little_mass():
+    """The rule about rounding concerns others without any mass: where they have some, however little, p_r stays."""
+    import torch
+    log("distill little mass")
+    z = torch.full((3, 50), -60.0, device="cuda")
+    z[:, :2] = 0
+    ids = torch.tensor([[0, 1]] * 3, device="cuda", dtype=torch.int32)
+    t = torch.zeros(3, 2, device="cuda")
+    lse = torch.full((3,), float(np.log(2.0)) + 2e-7, device="cuda")
+    loss, l2, rest = (torch.empty(3, device="cuda") for _ in range(3))
+    dz = torch.empty_like(z)
+    nsq.ns_distill_topk(z, ids, t, loss, l2, teacher_lse=lse, rest_lse=rest, grad_loss=torch.ones(3, device="cuda"), dlogits=dz)
+    torch.cuda.synchronize()
+    w = ops.distill_row(z[0].cpu().numpy().astype(np.float64), [0, 1], [0.0, 0.0], 1.0, float(lse[0]))
+    assert w["p_rest"] > 0
+    assert np.allclose(_f64(dz)[:, 2:], w["dlogits"][2:], rtol=1e-4, atol=0) and np.allclose(_f64(loss), w["loss"], rtol=1e-3)
