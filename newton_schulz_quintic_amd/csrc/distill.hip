@@ -98,6 +98,13 @@ struct Norm {
     float m, scale;
 };
 __device__ inline Norm norm_of(Lse l) { return {l.m == kNegInf ? 0.f : l.m, 1.f / l.s}; }
+// The same from a large sum, relative to an m far below the largest x: m moves up
+// by log2(s) / c, rounded, which leaves the scale near 1 (the product of a small
+// factor and 1 / s could fall below the normal numbers).
+__device__ inline Norm norm_above(Lse l, float c) {
+    const float m = l.m + __builtin_amdgcn_logf(l.s) / c, d = m - l.m, e = d * c;
+    return {m, __builtin_amdgcn_exp2f(e) * __builtin_amdgcn_exp2f(fmaf(d, c, -e)) / l.s};
+}
 // From a logsumexp rounded to fp32: m is lse tau rounded, and the scale takes
 // up the rest of it, so q is off by no more than lse's own rounding.
 __device__ inline Norm norm_of_lse(float lse, float inv_tau) {
@@ -460,8 +467,9 @@ __device__ inline typename Vec16<T>::raw grad_vec(typename Vec16<T>::raw v, cons
 // The same two with exp((z - m) / tau) = 2^(z c + hi) 2^-lo, where m is the
 // pairs' largest logit: one fma a value, and no maximum to find. They serve
 // unless some logit lies so far above m that the sum overflows, or (REST) all
-// lie so far below that it is lost, or one is NaN or infinite; such a row is
-// summed again relative to its own largest.
+// lie so far below that it is lost, or one is NaN or infinite, or a held row's
+// gradient cannot be formed so (factor_holds); such a row is summed again
+// relative to its own largest.
 template <typename T, bool REST>
 __device__ inline float fast_sum(typename Vec16<T>::raw v, uint32_t skip, float c, float hi) {
     float s[2] = {0.f, 0.f};
@@ -496,13 +504,19 @@ __device__ inline FastBase fast_base(const DistillArgs &A, const PairLds<TOP> &L
 }
 __device__ inline bool fast_holds(const Lse &s) { return s.s > 1e-10f && s.s < 1e30f; }
 
-// factor 2^(z c + hi). For bf16 results log2 |factor| goes into the exponent
-// (its rounding, 2^-24 of a number below 100, is far under theirs) and the
-// sign is set afterwards.
+// factor 2^(z c + hi). For bf16 results log2 |factor| goes into the exponent and
+// the sign is set afterwards. That sum is rounded: with both parts below 1024 by
+// 2^-14, 4e-5 of the result or 1 % of a bf16 half step.
 struct FastFactor {
     float hi, factor;
     uint32_t sign;
 };
+// Whether a row's gradient can be formed so, from its sum s: the factor is g / s
+// without a rest, and with one g (P / (s + its tokens' sum) - p_r / s), 0 or no
+// smaller than 2^-25 of g over the larger sum, where it is to be a normal number.
+template <typename T> __device__ inline bool factor_holds(float s, float g, float hi) {
+    return (g == 0.f || fabsf(g) > (s + kMaxTop) * 0x1p-90f) && (sizeof(T) == 4 || fabsf(hi) < 1024.f);
+}
 template <typename T> __device__ inline FastFactor fast_factor(float factor, float hi) {
     const bool fold = sizeof(T) == 2;
     return {fold ? hi + __builtin_amdgcn_logf(fabsf(factor)) : hi, factor, fold && factor < 0.f ? 0x80008000u : 0u};
@@ -781,7 +795,7 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
         }
         sum += fast_tail<T, REST>(zt, S, bits, c, f0.hi);
         Lse rest = {f0.m, block_sum<THREADS>(sum, L) * __builtin_amdgcn_exp2f(-f0.lo)};
-        const bool fast = !r.some || fast_holds(rest);
+        const bool fast = !r.some || (fast_holds(rest) && factor_holds<T>(rest.s, now.g * A.inv_tau, f0.hi));
         if (!fast) {
             Lse a = {kNegInf, 0.f};
 #pragma unroll
@@ -870,8 +884,9 @@ __global__ __launch_bounds__(THREADS, REST && !TRAIN && TOP <= kScanPairs ? 7 : 
             __syncthreads();
             rest = block_join(sum_span<T, REST>(z, zt, S, bits, c), L, c);
         }
-        const RowSums s = row_sums<REST>(A, L, r, row, TRAIN ? A.grad_loss[row] : 0.f, rest, c);
+        RowSums s = row_sums<REST>(A, L, r, row, TRAIN ? A.grad_loss[row] : 0.f, rest, c);
         if constexpr (TRAIN) {
+            if (s.rest.s > 0x1p20f) s.others = norm_above(s.rest, c);
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
 #pragma unroll
             for (int i = 0; i < kKept; ++i)

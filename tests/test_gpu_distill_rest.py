@@ -1,4 +1,5 @@
-"""GPU parity of ns_distill_topk with a teacher's logsumexp: how the pairs' and the rest's masses enter the gradient.
+"""GPU parity of ns_distill_topk's masses and gradients where they take most care: pairs whose mass is not 1, small
+remainders, masked others, students far above their pairs, large logits.
 
 Against the fp64 oracle (oracle/train_ops.py), with tolerances as in
 test_gpu_train_ops.py: U = 2^-24 is half a step of fp32, a bf16 result adds
@@ -37,11 +38,12 @@ def _check(c, got, form, rows, p_steps=None, mass64=False):
     loss, lse, rest, dz = got
     tau, half = c["tau"], HALF_STEP[c["dtype"]]
     for i in rows:
-        w = ops.distill_row(c["z64"][i], c["ids"][i], c["t64"][i], tau, c["lse64"][i], c["g64"][i],
+        tl = None if c["lse64"] is None else c["lse64"][i]
+        w = ops.distill_row(c["z64"][i], c["ids"][i], c["t64"][i], tau, tl, c["g64"][i],
                             teacher_bf16=c["tdtype"] == "bf16")
         g, z, v = c["g64"][i], c["z64"][i], len(c["z64"][i])
         if not w["some"]:
-            assert loss[i] == 0 and lse[i] == 0 and rest[i] == 0 and not dz[i].float().abs().any()
+            assert loss[i] == 0 and lse[i] == 0 and (tl is None or rest[i] == 0) and not dz[i].float().abs().any()
             continue
         here = [(int(j), float(x)) for j, x in zip(c["ids"][i], c["t64"][i]) if 0 <= j < v]
         at = np.array([j for j, _ in here])
@@ -52,17 +54,20 @@ def _check(c, got, form, rows, p_steps=None, mass64=False):
             E = np.sum(q * arg)
             two = 2 * abs(w["lse"]) if form == "step" else 0.0
             err_q = (4 * arg + 4 * E + 64 + two) * U
-            steps = 4 * (np.abs(t) / tau + abs(c["lse64"][i])) + 64 if p_steps is None else p_steps
+            steps = 4 * (np.abs(t - np.max(t)) / tau if tl is None else np.abs(t) / tau + abs(tl)) + 64
+            steps = steps if p_steps is None else p_steps
             err_p = np.where(p > 0, steps * U, 0.0)
             P = p.sum() + p_rest
             dP = np.sum(np.where(p > 0, p * err_p, 0.0)) + 2 * U
             if mass64:
-                dP = P * (2.0 ** -44 + 2.0 ** -51 * (np.max(np.abs(t)) / tau + abs(c["lse64"][i]))) + U * p_rest
+                dP = P * (2.0 ** -44 + 2.0 ** -51 * (np.max(np.abs(t)) / tau + abs(tl))) + U * p_rest
             outside = np.ones(v, bool)
             outside[at] = False
             factor, err_factor = P, dP + 2 * U * P
             err_rest = 0.0
-            if w["rest_lse"] == -np.inf:   # no others, or none with any mass
+            if tl is None:
+                factor, err_factor = 1.0, 0.0
+            elif w["rest_lse"] == -np.inf:   # no others, or none with any mass
                 assert rest[i] == -np.inf
             elif outside.any():
                 zr = z[outside]
@@ -75,7 +80,7 @@ def _check(c, got, form, rows, p_steps=None, mass64=False):
                     err_factor = (dP + p_rest * (err_rest + 8 * U)) / qr
                 assert abs(float(rest[i]) - w["rest_lse"]) <= U * (4 * abs(zr.max()) / tau + 4 * er + 64 + 2 * abs(w["rest_lse"]))
             size = q * ((err_q + err_rest) * (np.abs(factor) + P * (p_rest > 0)) + err_factor)
-            size[at] = (q * (err_q * P + err_factor if p_rest == 0 else err_q))[at]
+            size[at] = (q * (err_q * P + err_factor if p_rest == 0 and tl is not None else err_q))[at]
             for a, b in zip(at, p * err_p):
                 size[a] += b
             used = p > 0
@@ -206,3 +211,53 @@ def test_a_real_remainder_is_kept_where_the_student_gives_it_little_mass():
     w = ops.distill_row(z[0].cpu().numpy().astype(np.float64), [0, 1], [0.0, 0.0], 1.0, float(lse[0]))
     assert w["p_rest"] > 0
     assert np.allclose(_f64(dz)[:, 2:], w["dlogits"][2:], rtol=1e-4, atol=0) and np.allclose(_f64(loss), w["loss"], rtol=1e-3)
+
+
+def _student(c, z, g):
+    import torch
+    bits = f32_to_bf16_bits(z.astype(np.float32)) if c["dtype"] == "bf16" else z.astype(np.float32)
+    c["z64"], c["z"] = host_to_f64(bits, c["dtype"]), to_device(bits, c["dtype"])
+    c["g64"] = np.asarray(g, np.float32).astype(np.float64)
+    c["g"] = torch.from_numpy(np.asarray(g, np.float32)).cuda()
+    c["tdtype"] = "f32"
+    return c
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,v,k", [(3, 9001, 40), (260, 300, 20), (257, 9001, 30), (256, 66001, 64), (256, 140003, 16)])
+def test_others_far_above_the_pairs_and_small_loss_gradients(n, v, k, dtype, rest, form):
+    """Sums relative to the pairs' logits near 1e30 and loss gradients down to 1e-14: their quotient is below fp32's
+    normal numbers, the gradients are not."""
+    log(f"distill far above {n} {v} {k} {dtype} {rest} {form}")
+    rng = np.random.default_rng([n, v, k])
+    c = _distill_case(rng, n, v, k, dtype, rest=rest, tau=1.0)
+    z = c["z64"].copy()
+    np.put_along_axis(z, c["ids"], np.take_along_axis(z, c["ids"], 1) - rng.uniform(30, 66 - np.log(v), (n, 1)) - 9, 1)
+    g = 10.0 ** rng.uniform(-14, -7, n)
+    _student(c, z, g)
+    _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 5)) | {0, n - 1, int(np.argmin(g))}))
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [300.0, 3e4, 1e6])
+@pytest.mark.parametrize("n,v,k", [(3, 9001, 40), (260, 300, 20), (257, 9001, 30), (256, 140003, 16)])
+def test_large_logits(n, v, k, scale, dtype, rest, form):
+    """Logits of some `scale` temperatures, many of them tied at the largest value (as bf16 ones are)."""
+    log(f"distill large logits {n} {v} {k} {scale} {dtype} {rest} {form}")
+    rng = np.random.default_rng([n, v, k])
+    tau = float(np.float32(1024.0 / scale))
+    c = _distill_case(rng, n, v, k, dtype, rest=rest, tau=tau)
+    steps = rng.integers(0, 4, (n, v)) * (rng.random((n, v)) < 0.9) * (rng.random((n, 1)) < 0.8)
+    z = rng.uniform(1000, 1400, (n, 1)) - 8.0 * steps
+    g = rng.uniform(0.1, 1, n)
+    _student(c, z, g)
+    t = rng.uniform(3, 9, (n, k)) * tau
+    lse = np.array([ops._lse(r.astype(np.float32).astype(np.float64) / tau) for r in t]) + 0.2
+    _teacher(c, t, lse)
+    if not rest:
+        c["lse64"] = c["lse_d"] = None
+    _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 5)) | {0, n - 1}))
