@@ -1031,7 +1031,7 @@ int64_t held_threads(const DistillArgs &a, int es) {
 // split 91; 900 x 160000 bf16, not held: 140 us, split 181; 300 x 100001 f32 66 and
 // 79); loss alone reads rows one to a workgroup of 256 threads once these fill the
 // GPU (600 x 131072 bf16: split 38 us, a workgroup a row 44).
-bool split_rows(const DistillArgs &a, int es) {
+bool split_rows(const DistillArgs &a) {
     if (a.teacher_lse && a.vocab > kBitVocab) return true;
     return a.rows < (a.dlogits ? 256 : 1024);
 }
@@ -1179,7 +1179,7 @@ extern "C" ns_status ns_distill_topk(int64_t rows, int32_t vocab, int32_t top_k,
     if (rows > 0 && teacher_lse && !rest_lse) return fail(NS_ERR_INVALID_ARG, "teacher_lse needs rest_lse");
     if (misaligned(loss, 4) || misaligned(lse, 4) || misaligned(rest_lse, 4))
         return fail(NS_ERR_INVALID_ARG, "loss, lse or rest_lse not 4-byte aligned");
-    const bool split = split_rows(a, dtype_bytes(dtype));
+    const bool split = split_rows(a);
     const size_t need = distill_workspace(rows, top_k, split);
     if (need && (!workspace || workspace_bytes < need))
         return fail(NS_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);

@@ -261,3 +261,35 @@ def test_large_logits(n, v, k, scale, dtype, rest, form):
     if not rest:
         c["lse64"] = c["lse_d"] = None
     _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 5)) | {0, n - 1}))
+
+
+@pytest.mark.parametrize("dtype,n,v,k", [
+    ("bf16", 3, 262144, 8), ("f32", 3, 262145, 300), ("bf16", 1, 1 << 24, 40),
+    ("bf16", 256, 262144, 8), ("bf16", 256, 262144, 300), ("f32", 256, 262144, 1024), ("bf16", 256, 262145, 8),
+    ("f32", 256, 262145, 300), ("bf16", 300, 300001, 129), ("bf16", 1030, 262144, 300), ("f32", 1030, 262143, 128),
+    ("bf16", 1030, 262145, 300), ("bf16", 1024, 1 << 20, 300), ("bf16", 1025, 786432, 8),
+])
+def test_vocabularies_around_what_one_workgroup_marks(dtype, n, v, k):
+    """With a rest, up to 2^18 tokens are marked in one workgroup's LDS (32 KiB beside up to 37 KiB of pairs) and longer
+    rows are split at any row count; both forms, few and many pairs."""
+    import torch
+    log(f"distill vocabulary {dtype} {n} {v} {k}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(v + n)
+    type_ = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    z = torch.randn(n, v, device="cuda", generator=gen, dtype=type_)
+    ids = (torch.randint(0, v, (n, 1), device="cuda", generator=gen)
+           + torch.arange(k, device="cuda") * (v // k) // 2 * 2 + torch.arange(k, device="cuda") % 2) % v
+    ids[:, 0], ids[:, -1] = 0, v - 1
+    ids[:, k // 2] = ids[:, k // 2 - 1]                # one token twice
+    z.scatter_(1, ids, (torch.rand(n, k, device="cuda", generator=gen) * 6 + 5).to(type_))
+    t = torch.rand(n, k, device="cuda", generator=gen) * 6 + 3
+    tl = torch.logsumexp(t / 1.5, 1) + 0.01
+    g = torch.rand(n, device="cuda", generator=gen) + 0.1
+    c = {"tau": 1.5, "dtype": dtype, "tdtype": "f32", "z": z, "ids_d": ids.to(torch.int32), "t": t, "g": g, "lse_d": tl}
+    rows = sorted({0, n // 2, n - 1}) if v < 1 << 20 else [n - 1]
+    pick = torch.tensor(rows, device="cuda")
+    c64 = dict(c, z64=_f64(z[pick]), ids=ids[pick].cpu().numpy(), t64=_f64(t[pick]), g64=_f64(g[pick]), lse64=_f64(tl[pick]))
+    for form in ("train", "step"):
+        got = _distill_run(c, form)
+        _check(c64, tuple(x[pick] for x in got), form, range(len(rows)))
