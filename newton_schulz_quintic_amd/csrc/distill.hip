@@ -752,10 +752,11 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
     // descriptors end before them), and the first row's loads go out like the others': in order, each behind a store
     // (to a descriptor of length zero).
     // With one workgroup a CU and equal rows the CUs stay in step: all load, then all compute while memory rests.
-    // Over many bf16 rows those of four neighbouring XCDs start a quarter of a row apart (4096 x 131072: 480 us
-    // become 459, 1024 rows 132 become 138 if they do; f32 rows, with half the work a byte, 224 become 227).
-    if (THREADS == 1024 && sizeof(T) == 2 && A.rows >= 8 * (int)gridDim.x)
-        for (uint32_t i = 0; i < (blockIdx.x & 3) * 2; ++i) __builtin_amdgcn_s_sleep(127);
+    // Over many bf16 rows of a length that needs a CU's registers those of four neighbouring XCDs start a quarter of
+    // a row apart, 1024 cycles for 1024 vectors (4096 x 131072: 472 us become 456, 4096 x 70000: 307 become 300; 1024
+    // rows of 131072 132 become 138 if they do; f32 rows, with half the work a byte, 224 become 227).
+    if (THREADS == 1024 && sizeof(T) == 2 && S.vecs > kHeldVecs * THREADS / 2 && A.rows >= 8 * (int)gridDim.x)
+        for (int i = 0; i < (int)(blockIdx.x & 3) * S.vecs / 1024; ++i) __builtin_amdgcn_s_sleep(16);
     dwords held[kHeldVecs];
     int64_t row = blockIdx.x;
     RawPair p = pair_of(row), ahead = pair_of(row + gridDim.x);
