@@ -6,7 +6,8 @@
 //
 // Every tensor must be on the current GPU. Work goes to `stream` (default:
 // torch's current one) without waiting for it. Tensors that torch allocated on
-// another stream are the caller's to order and to record on it.
+// another stream are the caller's to order and to record on it. Autograd records
+// nothing of a call; the versions of the tensors that it writes move on.
 
 #include <Python.h>
 
@@ -231,6 +232,12 @@ PyObject *workspace(PyObject *given, const Size &size, PyObject *like, PyObject 
     return w;
 }
 
+// Tells autograd that a call has written these: a backward pass that saved one of them, written in place, then says so.
+void wrote(std::initializer_list<const at::Tensor *> outputs) {
+    for (const at::Tensor *t : outputs)
+        if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // Drops a reference on the way out, unless it is given away.
 struct Held {
     PyObject *o;
@@ -336,6 +343,7 @@ PyObject *norm_rope(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *k
         check(ns_qk_norm_rope(h.batch, h.seq, h.dim, h.dtype, &h.q, &h.k, h.wq, h.wk, h.w_dtype, (float)a.number(9, 1e-6),
                               h.cos, h.sin, h.rows, h.rope, a.flag(10), h.pos, h.pos_bytes, h.pos_stride, &oq, &ok,
                               a.stream(11, device)));
+        wrote({a.tensor(2), a.tensor(3)});
         Py_RETURN_NONE;
     });
 }
@@ -362,6 +370,7 @@ PyObject *norm_rope_backward(PyObject *, PyObject *const *args, Py_ssize_t n, Py
         check(ns_qk_norm_rope_backward(h.batch, h.seq, h.dim, h.dtype, &h.q, &h.k, &gq, &gk, h.wq, h.wk, h.w_dtype,
                                        (float)a.number(13, 1e-6), h.cos, h.sin, h.rows, h.rope, a.flag(14), h.pos,
                                        h.pos_bytes, h.pos_stride, &oq, &ok, wq, wk, p, bytes, a.stream(16, device)));
+        wrote({a.tensor(4), a.tensor(5), a.tensor(6), a.tensor(7)});
         if (ws.o) return ws.give();
         Py_RETURN_NONE;
     });
@@ -393,6 +402,7 @@ PyObject *moe_sort(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw
                           a.v[0], a.v[6], &p, &bytes)};
         check(ns_moe_sort(t, (int32_t)k, (int32_t)e, ids.data_ptr(), id_bytes, ld, offsets, slot_of_row, row_of_slot, p, bytes,
                           a.stream(6, device)));
+        wrote({a.tensor(2), a.tensor(3), a.tensor(4)});
         return ws.give();
     });
 }
@@ -428,6 +438,7 @@ PyObject *moe_dispatch(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject
         const RowCall c(x, "x", a.must(1));
         const int64_t ld = c.token_rows(x, "x"), out_ld = c.sorted_rows(xs, "xs");
         check(ns_moe_dispatch(c.t, c.k, c.h, c.dtype, x.data_ptr(), ld, c.rows, xs.data_ptr(), out_ld, a.stream(3, device)));
+        wrote({&xs});
         Py_RETURN_NONE;
     });
 }
@@ -442,6 +453,7 @@ PyObject *moe_dispatch_backward(PyObject *, PyObject *const *args, Py_ssize_t n,
         const int64_t ld = c.sorted_rows(dxs, "dxs"), out_ld = c.token_rows(dx, "dx");
         check(ns_moe_dispatch_backward(c.t, c.k, c.h, c.dtype, dxs.data_ptr(), ld, c.rows, dx.data_ptr(), out_ld,
                                        a.stream(3, device)));
+        wrote({&dx});
         Py_RETURN_NONE;
     });
 }
@@ -456,6 +468,7 @@ PyObject *moe_combine(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         const int64_t ld = c.sorted_rows(y, "y"), out_ld = c.token_rows(out, "out");
         const float *w = array<float>(a.tensor(2), "weights", {c.t, c.k}, at::kFloat);
         check(ns_moe_combine(c.t, c.k, c.h, c.dtype, y.data_ptr(), ld, c.rows, w, out.data_ptr(), out_ld, a.stream(4, device)));
+        wrote({&out});
         Py_RETURN_NONE;
     });
 }
@@ -474,6 +487,7 @@ PyObject *moe_combine_backward(PyObject *, PyObject *const *args, Py_ssize_t n, 
         float *dw = array<float>(a.tensor(5), "dweights", {c.t, c.k}, at::kFloat);
         check(ns_moe_combine_backward(c.t, c.k, c.h, c.dtype, dout.data_ptr(), dout_ld, y.data_ptr(), y_ld, c.rows, w,
                                       dy.data_ptr(), dy_ld, dw, a.stream(6, device)));
+        wrote({&dy, a.tensor(5)});
         Py_RETURN_NONE;
     });
 }
@@ -533,6 +547,7 @@ PyObject *distill(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw)
         check(ns_distill_topk(c.rows, c.v, c.k, c.dtype, z.data_ptr(), c.ld, ids.data_ptr(), c.id_bytes, teacher.data_ptr(),
                               c.t_dtype, c.teacher_lse, (float)a.number(7, 1.0), grad, loss, lse, rest_lse,
                               dz ? dz->data_ptr() : nullptr, dld, p, bytes, a.stream(11, device)));
+        wrote({a.tensor(3), a.tensor(4), rest, dz});
         return ws.give();
     });
 }
@@ -556,6 +571,7 @@ PyObject *distill_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyOb
         check(ns_distill_topk_backward(c.rows, c.v, c.k, c.dtype, z.data_ptr(), c.ld, ids.data_ptr(), c.id_bytes,
                                        teacher.data_ptr(), c.t_dtype, c.teacher_lse, (float)a.number(8, 1.0), lse, rest_lse,
                                        grad, dz.data_ptr(), dld, a.stream(9, device)));
+        wrote({&dz});
         Py_RETURN_NONE;
     });
 }
