@@ -322,10 +322,12 @@ struct HeadArgs {
         }
         if (p) {
             pos_bytes = int_bytes(*p, "pos");
-            if (p->dim() == 2 && p->size(0) == batch && p->size(1) == seq) pos_stride = seq;
-            else if (p->dim() != 1 || p->size(0) != seq)
-                raise(PyExc_ValueError, "pos must have shape " + text({seq}) + " or " + text({batch, seq}) + ", not " + text(*p));
-            if (!p->is_contiguous()) raise(PyExc_ValueError, "pos must be contiguous");
+            const int64_t last = p->dim() - 1;   // one row for all sequences (a stride of 0), or a row each
+            if (last < 0 || last > 1 || p->size(last) != seq || (last == 1 && p->size(0) != batch && p->size(0) != 1))
+                raise(PyExc_ValueError, "pos must have shape " + text({seq}) + ", " + text({1, seq}) + " or " + text({batch, seq}) +
+                                            ", not " + text(*p));
+            if (p->stride(last) != 1 && seq > 1 && batch) raise(PyExc_ValueError, "pos must have contiguous rows");
+            if (last == 1 && p->size(0) > 1) pos_stride = p->stride(0);
             pos = p->data_ptr();
         }
     }
@@ -591,7 +593,8 @@ PyMethodDef methods[] = {
                "RMS norm of each head of q and k, its weight and the position rotation (see ns.h).\n\n"
                "q, k: (batch, seq, heads, head_dim) or (seq, heads, head_dim) views with contiguous heads, bf16 or f32;\n"
                "k (or q) and its output may be None. cos, sin: (positions, rope_dim / 2) f32, or None for no rotation.\n"
-               "pos: (seq,) or (batch, seq) int32 or int64, or None for 0, 1, ... Outputs may be the inputs."),
+               "pos: (seq,), (1, seq) or (batch, seq) int32 or int64 with contiguous rows, or None for 0, 1, ... Outputs may be\n"
+               "the inputs."),
     NSQ_METHOD("ns_qk_norm_rope_backward", norm_rope_backward,
                "ns_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight=None, dk_weight=None, q_weight=None, "
                "k_weight=None, cos=None, sin=None, pos=None, eps=1e-06, interleaved=False, workspace=None, stream=None)\n--\n\n"

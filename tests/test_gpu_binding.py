@@ -66,3 +66,31 @@ def test_backward_notices_a_saved_tensor_written_in_place():
     nsq.ns_distill_topk(z.detach(), ids, t, _new(4), _new(4), grad_loss=one, dlogits=z.detach())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         z.sum().backward()
+
+
+@pytest.mark.parametrize("dtype", ["int32", "int64"])
+def test_positions_shared_by_the_batch_and_in_wider_rows(dtype):
+    """(1, seq) for a batch, an expanded row, rows of a wider tensor: the bits of whole (batch, seq) positions."""
+    import torch
+    log(f"positions {dtype}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    b, s = 3, 7
+    q, g = (torch.randn(b, s, 2, 64, device="cuda", generator=gen) for _ in "qg")
+    cos, sin = torch.rand(40, 32, device="cuda", generator=gen), torch.rand(40, 32, device="cuda", generator=gen)
+    line = torch.randint(0, 40, (1, s), device="cuda", generator=gen).to(getattr(torch, dtype))
+    rows = torch.randint(0, 40, (b, s + 5), device="cuda", generator=gen).to(getattr(torch, dtype))
+    shared = line.expand(b, s).contiguous()
+    for whole, forms in ((shared, [line, line[0], line.expand(b, s)]), (rows[:, 2:2 + s].contiguous(), [rows[:, 2:2 + s]])):
+        want, dwant = torch.empty_like(q), torch.empty_like(q)
+        nsq.ns_qk_norm_rope(q, None, want, None, cos=cos, sin=sin, pos=whole)
+        nsq.ns_qk_norm_rope_backward(q, None, g, None, dwant, None, cos=cos, sin=sin, pos=whole)
+        for pos in forms:
+            got, dgot = torch.empty_like(q), torch.empty_like(q)
+            nsq.ns_qk_norm_rope(q, None, got, None, cos=cos, sin=sin, pos=pos)
+            nsq.ns_qk_norm_rope_backward(q, None, g, None, dgot, None, cos=cos, sin=sin, pos=pos)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want) and torch.equal(dgot, dwant)
+    for bad in (rows[:, ::2][:, :s], line[:, :s - 1], line.expand(b + 1, s), line.t()):
+        with pytest.raises(ValueError, match="pos must"):
+            nsq.ns_qk_norm_rope(q, None, want, None, cos=cos, sin=sin, pos=bad)
