@@ -1005,8 +1005,9 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
 // host side
 // ---------------------------------------------------------------------------
 
-// Parts of a row for the split kernels: enough workgroups to fill the GPU, of
-// at least 8192 tokens (and no more than one workgroup marks in LDS).
+// Parts of a row for the split kernels: 512 workgroups over few rows if parts of
+// 2048 tokens give as many, up to 4096 of parts of 16384 (and no part longer than
+// one workgroup marks in LDS).
 void set_chunks(DistillArgs &a) {
     const auto deal = [&](int64_t workgroups, int64_t tokens) {
         return std::min((workgroups + a.rows - 1) / a.rows, (a.vocab + tokens - 1) / tokens);

@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(SortArgs A) {
         A.hist[(int64_t)blockIdx.x * hist_ld(A.experts) + e] = e <= A.experts ? cnt[e] : 0;
 }
 
-// Rows of one workgroup's slots. Wave w holds the w-th run of per / 16 of
+// Rows of one workgroup's slots. Wave w holds the w-th run of per / 8 of
 // them; a slot's row is its key's first row, plus the same key's slots in
 // earlier workgroups, earlier waves, earlier rounds of this wave and lower
 // lanes. A wave's LDS operations run in order, and none of a round's waits for

@@ -11,12 +11,12 @@
 // r is computed again from x, so the forward pass saves nothing.
 //
 // Layout: a group of G lanes (a power of two) holds one head, each lane two
-// 16-byte pieces of it that the rotation pairs up (pieces at 8i and 8i + R/2 of
-// bf16, or two neighbours for (2i, 2i + 1) pairs), so a rotation needs no other
+// pieces of 8 elements of it that the rotation pairs up (pieces at 8i and 8i +
+// R/2, or two neighbours for (2i, 2i + 1) pairs), so a rotation needs no other
 // lane and the sums need log2 G exchanges. A wave holds 64 / G heads of one
-// token at a time and takes U such rounds with all their loads in flight. Heads
-// whose size or rotated part does not split into such pieces take the same code
-// with pieces of one element (VEC = 1).
+// token at a time and loads its next token's while it computes. Heads whose size
+// or rotated part does not split into such pieces take the same code with pieces
+// of 4 elements or of one (VEC), a lane then holding up to eight pairs of them.
 //
 // Bound by memory: each input is read once and each output written once.
 
