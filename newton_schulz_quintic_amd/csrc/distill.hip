@@ -87,6 +87,14 @@ __device__ inline Lse join(Lse a, Lse b, float c) {
     const float m = fmaxf(a.m, b.m);
     return {m, a.s * shifted(a.m, m, c) + b.s * shifted(b.m, m, c)};
 }
+// The same sum relative to an m that lies log2(s) / c, rounded, further: s is then
+// near 1. (Relative to an m far above the largest x the exponentials fall below
+// the normal numbers where q does not; far below it 1 / s times a small factor
+// does, and log s loses digits that m takes up again.)
+__device__ inline Lse near(Lse l, float c) {
+    const float m = l.m + __builtin_amdgcn_logf(l.s) / c, d = m - l.m, e = d * c;
+    return {m, l.s * __builtin_amdgcn_exp2f(-e) * __builtin_amdgcn_exp2f(-fmaf(d, c, -e))};
+}
 template <int STEP = 0>
 __device__ inline Lse wave_join(Lse v, float c) {
     if constexpr (STEP < 6) return wave_join<STEP + 1>(join(v, {partner<STEP>(v.m), partner<STEP>(v.s)}, c), c);
@@ -98,13 +106,6 @@ struct Norm {
     float m, scale;
 };
 __device__ inline Norm norm_of(Lse l) { return {l.m == kNegInf ? 0.f : l.m, 1.f / l.s}; }
-// The same from a large sum, relative to an m far below the largest x: m moves up
-// by log2(s) / c, rounded, which leaves the scale near 1 (the product of a small
-// factor and 1 / s could fall below the normal numbers).
-__device__ inline Norm norm_above(Lse l, float c) {
-    const float m = l.m + __builtin_amdgcn_logf(l.s) / c, d = m - l.m, e = d * c;
-    return {m, __builtin_amdgcn_exp2f(e) * __builtin_amdgcn_exp2f(fmaf(d, c, -e)) / l.s};
-}
 // From a logsumexp rounded to fp32: m is lse tau rounded, and the scale takes
 // up the rest of it, so q is off by no more than lse's own rounding.
 __device__ inline Norm norm_of_lse(float lse, float inv_tau) {
@@ -467,9 +468,9 @@ __device__ inline typename Vec16<T>::raw grad_vec(typename Vec16<T>::raw v, cons
 // The same two with exp((z - m) / tau) = 2^(z c + hi) 2^-lo, where m is the
 // pairs' largest logit: one fma a value, and no maximum to find. They serve
 // unless some logit lies so far above m that the sum overflows, or (REST) all
-// lie so far below that it is lost, or one is NaN or infinite, or a held row's
-// gradient cannot be formed so (factor_holds); such a row is summed again
-// relative to its own largest.
+// lie so far below that it is lost, or one is NaN or infinite, or (bf16) m lies
+// where the gradient's exponent is too coarse; such a row is summed again relative
+// to its own largest.
 template <typename T, bool REST>
 __device__ inline float fast_sum(typename Vec16<T>::raw v, uint32_t skip, float c, float hi) {
     float s[2] = {0.f, 0.f};
@@ -511,14 +512,12 @@ struct FastFactor {
     float hi, factor;
     uint32_t sign;
 };
-// Whether a row's gradient can be formed so, from its sum s: the factor is g / s
-// without a rest, and with one g (P / (s + its tokens' sum) - p_r / s), 0 or no
-// smaller than 2^-25 of g over the larger sum, where it is to be a normal number.
-template <typename T> __device__ inline bool factor_holds(float s, float g, float hi) {
-    return (g == 0.f || fabsf(g) > (s + kMaxTop) * 0x1p-90f) && (sizeof(T) == 4 || fabsf(hi) < 1024.f);
-}
-template <typename T> __device__ inline FastFactor fast_factor(float factor, float hi) {
+// Whether hi stays below that, given the offset of the sum that m moves by.
+template <typename T> __device__ inline bool offset_holds(float hi) { return sizeof(T) == 4 || fabsf(hi) < 900.f; }
+// g q of any logit, from a norm near its row's logsumexp.
+template <typename T> __device__ inline FastFactor fast_factor(const Norm &n, float g, float c) {
     const bool fold = sizeof(T) == 2;
+    const float hi = -n.m * c, factor = g * n.scale * __builtin_amdgcn_exp2f(-fmaf(n.m, c, hi));
     return {fold ? hi + __builtin_amdgcn_logf(fabsf(factor)) : hi, factor, fold && factor < 0.f ? 0x80008000u : 0u};
 }
 template <typename T>
@@ -796,7 +795,8 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
         }
         sum += fast_tail<T, REST>(zt, S, bits, c, f0.hi);
         Lse rest = {f0.m, block_sum<THREADS>(sum, L) * __builtin_amdgcn_exp2f(-f0.lo)};
-        const bool fast = !r.some || (fast_holds(rest) && factor_holds<T>(rest.s, now.g * A.inv_tau, f0.hi));
+        const bool fast = !r.some || (fast_holds(rest) && offset_holds<T>(f0.hi));
+        rest = near(rest, c);
         if (!fast) {
             Lse a = {kNegInf, 0.f};
 #pragma unroll
@@ -814,7 +814,7 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
         now = beside_of(next, p);
         ahead = pair_of(next + gridDim.x);
         const auto dz = vecs_of(A.dlogits, row, A.dld, true), z = vecs_of(A.logits, next, A.ld, next < A.rows);
-        const FastFactor f = fast_factor<T>(s.g_others * s.others.scale * __builtin_amdgcn_exp2f(-f0.lo), f0.hi);
+        const FastFactor f = fast_factor<T>(s.others, s.g_others, c);
         const auto turn = [&](auto value) {
 #pragma unroll
             for (int i = 0; i < kHeldVecs; ++i) {
@@ -851,10 +851,11 @@ __global__ __launch_bounds__(THREADS, 4) void distill_held_kernel(DistillArgs A)
 // each thread: one workgroup a CU, so that the 256 rows under way stay in the
 // last-level cache in between (2048 x 151936 bf16: 361 us with many workgroups of
 // 256 threads, 326 with 256 of 1024 threads, 279 with 8 vectors kept; 12 spill,
-// 287; 2000 x 100000 f32 448, 360 and 315). Loss alone with the rest: at most 72
-// registers, for 7 waves a SIMD (with 89 and 5 waves 8192 x 8192 bf16 took 65 us, not 53).
+// 287; 2000 x 100000 f32 448, 360 and 315). Loss alone keeps 8 waves a SIMD, with
+// the rest 7 (8192 x 8192 bf16: 5 waves of 91 registers 54 us, 8 waves 40; with the
+// rest 5 waves 65, 7 waves 53; 4096 x 131072: 5 waves 183, 8 waves 188).
 template <typename T, bool REST, int TOP, bool TRAIN, int THREADS>
-__global__ __launch_bounds__(THREADS, REST && !TRAIN && TOP <= kScanPairs ? 7 : 1) void distill_row_kernel(DistillArgs A) {
+__global__ __launch_bounds__(THREADS, TRAIN || TOP > kScanPairs ? 1 : REST ? 7 : 8) void distill_row_kernel(DistillArgs A) {
     extern __shared__ uint32_t bits[];
     __shared__ __attribute__((aligned(16))) PairLds<TOP> L;
     constexpr int kKept = !TRAIN ? 0 : REST && sizeof(T) == 2 ? kKeptVecs - 2 : kKeptVecs;   // without spilling
@@ -881,13 +882,14 @@ __global__ __launch_bounds__(THREADS, REST && !TRAIN && TOP <= kScanPairs ? 7 : 
             sum += fast_sum<T, REST>(kept[i], REST ? vec_bits(bits, threadIdx.x + i * THREADS, S.N) : 0, c, f.hi);
         sum += fast_span<T, REST, TRAIN && REST ? 4 : 8>(z, zt, S, bits, c, f.hi, kKept * THREADS);
         Lse rest = {f.m, block_sum<THREADS>(sum, L) * __builtin_amdgcn_exp2f(-f.lo)};
-        if (!fast_holds(rest)) {
+        if (fast_holds(rest)) {
+            rest = near(rest, c);
+        } else {
             __syncthreads();
             rest = block_join(sum_span<T, REST>(z, zt, S, bits, c), L, c);
         }
-        RowSums s = row_sums<REST>(A, L, r, row, TRAIN ? A.grad_loss[row] : 0.f, rest, c);
+        const RowSums s = row_sums<REST>(A, L, r, row, TRAIN ? A.grad_loss[row] : 0.f, rest, c);
         if constexpr (TRAIN) {
-            if (s.rest.s > 0x1p20f) s.others = norm_above(s.rest, c);
             T *dz = reinterpret_cast<T *>(A.dlogits) + row * A.dld;
 #pragma unroll
             for (int i = 0; i < kKept; ++i)

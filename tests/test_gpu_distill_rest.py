@@ -293,3 +293,27 @@ def test_vocabularies_around_what_one_workgroup_marks(dtype, n, v, k):
     for form in ("train", "step"):
         got = _distill_run(c, form)
         _check(c64, tuple(x[pick] for x in got), form, range(len(rows)))
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("below", [0.0, 1.5, 3.0])
+@pytest.mark.parametrize("n,v,k", [(3, 9001, 40), (260, 300, 20), (257, 2602, 9), (256, 33001, 24), (256, 140003, 16)])
+def test_others_below_the_pairs_over_a_wide_range(n, v, k, below, dtype, form):
+    """At a low temperature the others' shares of their class run from 1 down to 1e-40, and the class lies up to 1e-9
+    below the pairs: shares of 1e-30 are numbers of either type."""
+    log(f"distill wide range {n} {v} {k} {below} {dtype} {form}")
+    rng = np.random.default_rng([n, v, k])
+    tau = 0.125
+    c = _distill_case(rng, n, v, k, dtype, rest=True, tau=tau)
+    z = rng.standard_normal((n, v)) * 2 - 8.0 - below
+    for i in range(n):
+        z[i, c["ids"][i]] = rng.uniform(0, 0.5, k)
+    z[:, v - 2:] = z.max(1, keepdims=True) - 9.0 - below     # the last ones, too
+    c["ids"] = c["ids"] % (v - 2)
+    import torch
+    c["ids_d"] = torch.from_numpy(c["ids"].astype(np.int32)).cuda()
+    _student(c, z, rng.uniform(0.01, 0.1, n))
+    t = rng.uniform(3, 9, (n, k)) * tau
+    _teacher(c, t, np.array([ops._lse(r / tau) for r in t]) + rng.uniform(0.01, 0.5, n))
+    _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 5)) | {0, n - 1}))
