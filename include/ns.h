@@ -577,7 +577,9 @@ ns_status ns_distill_topk(int64_t rows, int32_t vocab, int32_t top_k, ns_dtype d
 
 /* The gradient by itself, from the lse (and rest_lse) of an earlier
  * ns_distill_topk on the same inputs: dlogits of sum(grad_loss * loss). In
- * place allowed as above. One launch.
+ * place allowed as above. Rows whose lse or rest_lse passes 1024 in magnitude,
+ * and would give q to fewer digits, are summed again. One launch, in place two
+ * for few or long rows.
  * Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
 ns_status ns_distill_topk_backward(int64_t rows, int32_t vocab, int32_t top_k, ns_dtype dtype, const void *logits,
                                    int64_t logits_ld, const void *ids, int32_t id_bytes, const void *teacher,

@@ -66,8 +66,12 @@ struct DistillArgs {
     int32_t id_bytes, teacher_f32;
     int32_t chunks, chunk;  // parts of a row, tokens of one
     float inv_tau;
+    int32_t large;          // gradient alone: which rows, by their logsumexp (too_large)
     double inv_tau64;
 };
+
+// Rows with a large logsumexp: with the others, left out, by themselves.
+enum { kLargeToo = 0, kLargeNone = 1, kLargeOnly = 2 };
 
 // ---------------------------------------------------------------------------
 // sums of exponentials
@@ -112,6 +116,9 @@ __device__ inline Norm norm_of_lse(float lse, float inv_tau) {
     const float m = lse / inv_tau, rest = fmaf(m, inv_tau, -lse);
     return {m, expf(rest)};
 }
+// Whether q from that logsumexp is too far off: by 2^-24 of it, 1.2e-4 at the bound,
+// what a quotient z / tau of the size is off by itself.
+__device__ inline bool too_large(float lse) { return fabsf(lse) > 1024.f; }
 __device__ inline float q_of(float z, const Norm &n, float c) { return __builtin_amdgcn_exp2f((z - n.m) * c) * n.scale; }
 
 // exp(x) in 64 bits, off by 2^-44 of itself: x = n ln 2 + 256 r with |r| < 2^-9.4, the
@@ -393,9 +400,8 @@ __device__ inline void add_tail(Lse &a, float x, const Span<T> &S, const uint32_
 }
 
 // The sum over a span of a row in memory, joined over the workgroup.
-template <typename T, bool REST>
+template <typename T, bool REST, int B = 4>
 __device__ inline Lse sum_span(const T *z, float zt, const Span<T> &S, const uint32_t *bits, float c) {
-    constexpr int B = 4;
     const int threads = blockDim.x;
     Lse a = {kNegInf, 0.f};
     int v = threadIdx.x;
@@ -931,10 +937,57 @@ __global__ __launch_bounds__(kSplitThreads) void distill_partial_kernel(DistillA
     }
 }
 
+// The others' sum of a whole row (its pairs are in LDS and weighed), in parts
+// whose marks fit: the largest logit, then the sum relative to it. One vector at
+// a time: few registers, for a kernel that seldom needs it.
+template <typename T, bool REST, int TOP>
+__device__ inline Lse sum_row(const DistillArgs &A, PairLds<TOP> &L, const T *z, float c) {
+    constexpr int N = Vec16<T>::N, kPart = kSplitThreads * N;   // a vector a thread
+    __shared__ uint32_t marks[REST ? kPart / 32 : 1];
+    float m = kNegInf, s = 0.f;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        if (pass) {
+            m = wave_max(m);
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) L.wave_sum[threadIdx.x >> 6] = m;
+            __syncthreads();
+            m = fmaxf(fmaxf(L.wave_sum[0], L.wave_sum[1]), fmaxf(L.wave_sum[2], L.wave_sum[3]));
+            __syncthreads();
+        }
+        const float base = m == kNegInf ? 0.f : m;
+#pragma unroll 1
+        for (int e0 = 0; e0 < A.vocab; e0 += kPart) {
+            if constexpr (REST) {
+                __syncthreads();   // the part before has been read
+                for (int i = threadIdx.x; i < kPart / 32; i += kSplitThreads) marks[i] = 0;
+                __syncthreads();
+                for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) {
+                    const int at = L.owner[k] - e0;
+                    if (L.owner[k] >= 0 && at >= 0 && at < kPart) atomicOr(&marks[at >> 5], 1u << (at & 31));
+                }
+                __syncthreads();
+            }
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                const int at = threadIdx.x + i * kSplitThreads;
+                if (e0 + at >= A.vocab || (REST && (marks[at >> 5] >> (at & 31) & 1))) continue;
+                const float x = (float)z[e0 + at];
+                if (pass) s += __builtin_amdgcn_exp2f((x - base) * c);
+                else m = fmaxf(m, x);
+            }
+        }
+    }
+    __syncthreads();
+    return {m, block_sum<kSplitThreads>(s, L)};
+}
+
 // Workgroup (chunk, row) writes its part of the gradient, from the parts' sums
-// (LOSS: the first one also the loss) or from the logsumexps of a forward call.
+// (LOSS: the first one also the loss) or from the logsumexps of a forward call:
+// each a whole row's sum again where they are too large. The gradient alone with
+// the rest keeps 5 waves a SIMD (8192 x 8192 bf16: 4 waves 90 us, 5 waves 82).
 template <typename T, bool REST, int TOP, bool LOSS, bool NT>
-__global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArgs A, int32_t parts) {
+__global__ __launch_bounds__(kSplitThreads, !LOSS && REST && TOP <= kScanPairs ? 5 : 1) void distill_apply_kernel(DistillArgs A, int32_t parts) {
     extern __shared__ uint32_t bits[];
     __shared__ __attribute__((aligned(16))) PairLds<TOP> L;
     const float c = A.inv_tau * kLog2e;
@@ -963,29 +1016,32 @@ __global__ __launch_bounds__(kSplitThreads) void distill_apply_kernel(DistillArg
             __syncthreads();
             continue;
         }
+        const float lse = LOSS ? 0.f : A.lse[row], rest_lse = !LOSS && REST ? A.rest_lse[row] : 0.f;
+        const bool again = !LOSS && (too_large(lse) || too_large(rest_lse));   // -inf too: no others, or below fp32's range
+        if (!LOSS && A.large != (again ? kLargeOnly : kLargeNone) && A.large != kLargeToo) {   // the other launch's row
+            __syncthreads();
+            continue;
+        }
         if (!LOSS)
             for (int k = threadIdx.x; k < A.top_k; k += kSplitThreads) {
                 const int id = L.id[k];
-                L.z[k] = id >= e0 && id < e1 ? (float)z[id] : 0.f;
+                L.z[k] = id >= (again ? 0 : e0) && id < (again ? A.vocab : e1) ? (float)z[id] : 0.f;
             }
         weigh_pairs<REST>(A, t_lse, L, r, bits, 0, 0);
         RowSums s{};
         if constexpr (LOSS) {
             s = row_sums<REST>(A, L, r, row, g, wave_join({part.x, part.y}, c), c);
         } else {
-            const float lse = A.lse[row];
-            s.n = s.others = norm_of_lse(lse, A.inv_tau);
-            s.g = s.g_others = g * A.inv_tau;
-            if constexpr (REST) {
-                const float rest_lse = A.rest_lse[row];
-                if (rest_lse == kNegInf) {
-                    drop_rounding(A, L, r, row);
-                    s.others = {0.f, r.p_rest == 0.f ? 0.f : __builtin_inff()};
-                } else {
+            if (again) {
+                s = row_sums<REST>(A, L, r, row, g, sum_row<T, REST>(A, L, z, c), c);
+            } else {
+                s.n = s.others = norm_of_lse(lse, A.inv_tau);
+                s.g = s.g_others = g * A.inv_tau;
+                if constexpr (REST) {
                     s.others = norm_of_lse(rest_lse, A.inv_tau);
+                    s.g_others = others_factor<REST>(r, s.g, expf(rest_lse - lse));
+                    s.n.scale *= r.mass;
                 }
-                s.g_others = others_factor<REST>(r, s.g, expf(rest_lse - lse));
-                s.n.scale *= r.mass;
             }
         }
         if (A.dlogits) {
@@ -1136,12 +1192,26 @@ ns_status launch_split(DistillArgs a, hipStream_t st) {
     return NS_OK;
 }
 
+// The gradient in place of the logits leaves rows that are summed again to a
+// second launch, in which one workgroup takes all of a row (parts of it would read
+// what others have written).
 template <typename T, bool REST, int TOP>
 ns_status launch_backward(DistillArgs a, hipStream_t st) {
     set_chunks(a);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(split_grid(a)), dim3(kSplitThreads), 0, st, a, 0); };
-    past_cache(a, sizeof(T)) ? go(distill_apply_kernel<T, REST, TOP, false, true>) : go(distill_apply_kernel<T, REST, TOP, false, false>);
+    const auto rows = [&](int32_t large) {
+        a.large = large;
+        past_cache(a, sizeof(T)) ? go(distill_apply_kernel<T, REST, TOP, false, true>) : go(distill_apply_kernel<T, REST, TOP, false, false>);
+    };
+    const bool place = a.dlogits == a.logits && a.chunks > 1;
+    rows(place ? kLargeNone : kLargeToo);
     NSQ_HIP(hipGetLastError());
+    if (place) {
+        a.chunks = 1;
+        a.chunk = a.vocab;
+        rows(kLargeOnly);
+        NSQ_HIP(hipGetLastError());
+    }
     return NS_OK;
 }
 

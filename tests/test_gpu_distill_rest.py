@@ -28,13 +28,13 @@ def _teacher(c, t, lse, tdtype="f32"):
     return c
 
 
-def _check(c, got, form, rows, p_steps=None, mass64=False):
+def _check(c, got, form, rows, p_steps=None, mass64=False, most=np.inf):
     """With F = P - p_r / q_r the gradient is g / tau (q_j F - sum of j's p). Relative errors: of q, (4 |z - m| / tau + 4 E
     + 64) U as in _check_distill, and 2 |lse| U more where lse was rounded between two calls; of q_r likewise; of p,
     p_steps U if given, else (4 (|t| / tau + |lse_T|) + 64) U, the rounding of fp32 exponents. P and p_r are off by dP, the
     sum of the p's errors (and half a step of their own), which reaches others through F. With mass64 they come from p in
     64 bits and are rounded once: 2^-44 of the exponential, the exponent's roundings, 2^-53 of its parts each (4 of them
-    counted), and half a step of p_r."""
+    counted), and half a step of p_r. `most`: the largest logsumexp that the second call takes q from."""
     loss, lse, rest, dz = got
     tau, half = c["tau"], HALF_STEP[c["dtype"]]
     for i in rows:
@@ -52,7 +52,7 @@ def _check(c, got, form, rows, p_steps=None, mass64=False):
             q, p, p_rest = w["q"], w["p"], w["p_rest"]
             arg = np.where(q > 0, np.abs(z - np.max(z)) / tau, 0.0)
             E = np.sum(q * arg)
-            two = 2 * abs(w["lse"]) if form == "step" else 0.0
+            two = 2 * min(abs(w["lse"]), most) if form == "step" else 0.0
             err_q = (4 * arg + 4 * E + 64 + two) * U
             steps = 4 * (np.abs(t - np.max(t)) / tau if tl is None else np.abs(t) / tau + abs(tl)) + 64
             steps = steps if p_steps is None else p_steps
@@ -74,7 +74,7 @@ def _check(c, got, form, rows, p_steps=None, mass64=False):
                 qr = np.exp(w["rest_lse"] - w["lse"])
                 er = np.sum(np.where(zr > -np.inf, q[outside] * np.abs(zr - zr.max()) / tau, 0)) / max(qr, 1e-300)
                 err_rest = (4 * er + 64 + 4 * np.abs(zr.max() - np.max(z)) / tau + 4 * E
-                            + (2 * abs(w["lse"]) + 2 * abs(w["rest_lse"]) if form == "step" else 0.0)) * U
+                            + (two + 2 * min(abs(w["rest_lse"]), most) if form == "step" else 0.0)) * U
                 if p_rest > 0:
                     factor = 1 - p_rest / qr
                     err_factor = (dP + p_rest * (err_rest + 8 * U)) / qr
@@ -317,3 +317,62 @@ def test_others_below_the_pairs_over_a_wide_range(n, v, k, below, dtype, form):
     t = rng.uniform(3, 9, (n, k)) * tau
     _teacher(c, t, np.array([ops._lse(r / tau) for r in t]) + rng.uniform(0.01, 0.5, n))
     _check(c, _distill_run(c, form), form, sorted(set(rng.integers(0, n, 5)) | {0, n - 1}))
+
+
+@pytest.mark.parametrize("place", [False, True])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [900.0, 3e3, 1e5, 1e7])
+@pytest.mark.parametrize("n,v,k", [(3, 9001, 40), (260, 300, 20), (257, 20003, 300), (5, 140003, 16)])
+def test_gradient_alone_where_the_logsumexp_is_large(n, v, k, scale, dtype, rest, place):
+    """An fp32 logsumexp of 1e5 is 4e-3 off: from 1024 on the second call sums such rows again, next to ordinary ones."""
+    log(f"distill gradient alone {n} {v} {k} {scale} {dtype} {rest} {place}")
+    rng = np.random.default_rng([n, v, k])
+    tau = float(np.float32(1000.0 / scale))
+    c = _distill_case(rng, n, v, k, dtype, rest=rest, tau=tau)
+    z = 8.0 * rng.integers(-2, 2, (n, v)) * (rng.random((n, 1)) < 0.7) + rng.choice([-1024.0, 0.0, 1024.0], (n, 1))
+    _student(c, z, rng.uniform(0.1, 1, n))
+    t = rng.uniform(3, 9, (n, k)) * tau
+    _teacher(c, t, np.array([ops._lse(r.astype(np.float32).astype(np.float64) / tau) for r in t]) + 0.2)
+    if not rest:
+        c["lse64"] = c["lse_d"] = None
+    got = _distill_run(c, "step", place=place)
+    _check(c, got, "step", sorted(set(rng.integers(0, n, 6)) | {0, n - 1}), most=1024.0)
+
+
+@pytest.mark.parametrize("form", ["train", "step"])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [0.3, 1.0, 1.7])
+@pytest.mark.parametrize("n,v,k", [(4, 5003, 6), (260, 300, 20), (257, 9001, 200)])
+def test_rows_masked_whole_by_the_lowest_value(n, v, k, tau, dtype, rest, form):
+    """Every logit the type's lowest value, or all but the pairs': the shares are equal, whatever the temperature makes
+    of the logsumexp (its quotient by a temperature below 1 is -inf)."""
+    log(f"distill lowest rows {n} {v} {k} {tau} {dtype} {rest} {form}")
+    rng = np.random.default_rng([n, v, k])
+    tau = float(np.float32(tau))
+    c = _distill_case(rng, n, v, k, dtype, rest=rest, tau=tau)
+    z = c["z64"].copy()
+    low = -3.3895313892515355e38 if dtype == "bf16" else -3.4028234663852886e38
+    inside = np.zeros((n, v), bool)
+    np.put_along_axis(inside, c["ids"], True, 1)
+    z[0::3] = low
+    z[1::3] = np.where(inside[1::3], z[1::3], low)
+    _student(c, z, rng.uniform(0.1, 1, n))
+    t = rng.uniform(3, 9, (n, k)) * tau
+    _teacher(c, t, np.array([ops._lse(r.astype(np.float32).astype(np.float64) / tau) for r in t]) + 0.2)
+    if not rest:
+        c["lse64"] = c["lse_d"] = None
+    loss, lse, rest_lse, dz = _distill_run(c, form)
+    dz, loss = _f64(dz), _f64(loss)
+    assert np.isfinite(dz).all()
+    for i in (0, 1, 2, 3, n - 1):
+        tl = None if not rest else c["lse64"][i]
+        w = ops.distill_row(c["z64"][i], c["ids"][i], c["t64"][i], tau, tl, c["g64"][i])
+        if i % 3 == 0:   # q is 1 / v: p from fp32 exponents of t / tau up to 9, sums of 9001 equal terms
+            size = c["g64"][i] / tau * (1 / v + np.bincount(c["ids"][i], w["p"], v))
+            _close(dz[i], w["dlogits"], (HALF_STEP[dtype] + 8 * U) * np.abs(w["dlogits"]) + 256 * U * size, f"row {i}")
+            assert abs(loss[i] - w["loss"]) <= 256 * U * (1 + np.log(v))
+        elif i % 3 == 1 and rest:   # the others share g p_r / tau equally; their q is 0 in 64 bits, too
+            others = -c["g64"][i] / tau * w["p_rest"] / (v - k)
+            _close(dz[i][~inside[i]], np.full(v - k, others), (HALF_STEP[dtype] + 256 * U) * abs(others), f"row {i} others")
