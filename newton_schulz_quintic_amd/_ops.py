@@ -4,6 +4,10 @@ The operators themselves are functions of the compiled module ``_binding``
 (``csrc/python/binding.cpp``), under the C entry points' names; ``operator`` finds
 them on first use, so that importing the package loads neither torch nor the
 library. The workspace sizes come through ctypes like the rest of the library.
+
+Autograd records nothing of a call: ``examples/moe_distill_step.py`` wraps them in
+autograd functions. A call moves the versions of the tensors it writes, so that a
+backward pass which saved one of them raises.
 """
 
 from __future__ import annotations

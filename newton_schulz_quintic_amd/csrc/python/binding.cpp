@@ -631,7 +631,8 @@ PyMethodDef methods[] = {
                "Gradient of ns_distill_topk by itself, from the lse (and rest_lse) it gave (see ns.h)."),
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Training-step operators of the library.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Training-step operators of the library. Autograd records nothing of a call (see the\n"
+                      "example's autograd functions); the versions of the tensors that a call writes move on.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 bool import_name(const char *from, const char *name, PyObject **to) {
