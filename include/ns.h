@@ -587,6 +587,140 @@ ns_status ns_distill_topk_backward(int64_t rows, int32_t vocab, int32_t top_k, n
                                    const float *lse, const float *rest_lse, const float *grad_loss,
                                    void *dlogits, int64_t dlogits_ld, void *stream);
 
+/* A (rows, hidden) tensor: value j of row i is at data[i * ld + j]. A tensor
+ * that a call takes or leaves may be given as NULL or with data NULL. */
+typedef struct ns_rows {
+    void *data;
+    int64_t ld;
+} ns_rows;
+
+/* The norms before and after a block with its gate and residual scale, in one
+ * pass. For each row, with x the residual stream and y the block's output:
+ *   z     = y / sqrt(mean(y^2) + eps) * post_weight     (post_norm = 0: z = y)
+ *   x_out = alpha * x + scale * gate * z                (no y: alpha * x, not written)
+ *   h     = r / sqrt(mean(r^2) + eps) * pre_weight      r: x_out before rounding
+ * x_out is the new residual, h what the next block reads; either may be left
+ * out. Without y the call is the norm in front of the first block.
+ * hidden 1 .. 16384, rows 0 .. 2^31 - 1. residual_dtype is that of x and x_out,
+ * dtype that of y and h; an f32 dtype needs an f32 residual.
+ * post_weight,  [hidden] of weight_dtype, or NULL for ones.
+ * pre_weight
+ * gate          (gate_rows, hidden) of gate_dtype or left out (ones): gate row
+ *               g holds for rows g * rows / gate_rows and on: 1 gate row (a
+ *               value per channel), one per sequence, or one per token.
+ *               gate_rows divides rows.
+ * x_out may be x, and h may be y, with the same ld (in place); otherwise
+ * outputs overlap nothing. One launch. Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
+ns_status ns_block_norm(int64_t rows, int32_t hidden, ns_dtype residual_dtype, ns_dtype dtype, const ns_rows *x,
+                        const ns_rows *y, const void *post_weight, const void *pre_weight, ns_dtype weight_dtype,
+                        int32_t post_norm, const ns_rows *gate, int64_t gate_rows, ns_dtype gate_dtype, float alpha,
+                        float scale, float eps, const ns_rows *x_out, const ns_rows *h, void *stream);
+
+/* Workspace of ns_block_norm_backward (needed for dpost_weight, dpre_weight and
+ * a dgate with fewer rows than x). Errors: INVALID_ARG. */
+ns_status ns_block_norm_workspace_bytes(int64_t rows, int32_t hidden, size_t *bytes);
+
+/* The gradient of ns_block_norm: from the forward's inputs and the gradients
+ * dx_out and dh of its outputs (one may be left out: zeros) writes, where
+ * given, dx, dy, dpost_weight and dpre_weight ([hidden] f32, summed over rows)
+ * and dgate (like gate, summed over the rows of each gate row). Sums are not
+ * added to what is there. dx may be dx_out or x, and dy may be dh or y, with
+ * the same ld (in place). One launch, or two with sums over rows. Other
+ * arguments as for ns_block_norm.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
+ns_status ns_block_norm_backward(int64_t rows, int32_t hidden, ns_dtype residual_dtype, ns_dtype dtype, const ns_rows *x,
+                                 const ns_rows *y, const void *post_weight, const void *pre_weight,
+                                 ns_dtype weight_dtype, int32_t post_norm, const ns_rows *gate, int64_t gate_rows,
+                                 ns_dtype gate_dtype, float alpha, float scale, float eps, const ns_rows *dx_out,
+                                 const ns_rows *dh, const ns_rows *dx, const ns_rows *dy, float *dpost_weight,
+                                 float *dpre_weight, const ns_rows *dgate, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* 8-bit matrix products with a scale for each block of 128 values along the
+ * reduction. Values are e4m3 (4 exponent bits, 3 mantissa bits, largest 448,
+ * no infinities); a scale is a power of two, held as its exponent + 127 in
+ * one byte. A row of such a matrix has whole blocks: its width is rounded up
+ * to a multiple of 128 and the values behind the last column are zeros. Rows
+ * are 16-byte aligned: addresses and row strides (in bytes) are multiples of 16,
+ * a stride is at most 2^22.
+ *
+ * ns_quantize writes x (batch x rows x cols, x_ld and x_batch elements apart) in
+ * that form: e is the smallest whole number (at least -126) for which the largest
+ * finite magnitude of a block is at most 448 * 2^e (0 for a block of zeros), and
+ * each value is x / 2^e rounded to nearest even; infinities and NaN become NaN.
+ * block_rows   1: a block is 128 values of one row (batch must be 1), or 128:
+ *              128 rows x 128 columns (weights: the same scales serve the
+ *              matrix and its transpose).
+ * q, scales    batch x rows x cols' (cols' = cols rounded up to 128), and batch x
+ *              ceil(rows / block_rows) x cols' / 128 bytes, contiguous.
+ * qt, scales_t the transpose in the same form, blocks along the rows: batch x cols
+ *              x rows' and batch x ceil(cols / block_rows) x rows' / 128 bytes.
+ *              Either pair may be NULL.
+ * offsets      NULL, or [groups + 1] on the GPU (as ns_moe_sort leaves them), which
+ *              divides the rows into groups: in qt each group then starts at a
+ *              whole block, rows' = (rows / 128 + groups) * 128 (rounded down
+ *              first), and rows behind the last group have no place; blocks
+ *              behind the last group's are left as they were. Needs block_rows 1.
+ * rows 0 .. 2^30, cols 1 .. 2^22, batch 0 .. 65535, groups 1 .. 1024; with qt or
+ * square blocks at most 65534 blocks of rows. One launch.
+ * Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
+ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_dtype dtype, const void *x, int64_t x_ld,
+                      int64_t x_batch, int32_t block_rows, const int32_t *offsets, int32_t groups, void *q,
+                      int64_t q_ld, int64_t q_batch, uint8_t *scales, void *qt, int64_t qt_ld, int64_t qt_batch,
+                      uint8_t *scales_t, void *stream);
+
+/* out = a b^T for such matrices a (m x k) and b (n x k), k a multiple of 128 up to
+ * 2^22: out[i, j] = the sum over blocks of 2^(sa + sb - 254) times the block's sum
+ * of products, added in fp32 and rounded once.
+ * a_scales     [m, k / 128].
+ * b_scales     [n, k / 128] (b_block_rows 1) or [ceil(n / 128), k / 128] (128).
+ * out          (m, n) of out_dtype (BF16 or F32), rows out_ld elements apart.
+ * offsets      NULL, or [groups + 1] on the GPU. With reduce = 0 they divide a's
+ *              rows: those of group e are multiplied by b + e * b_batch bytes with
+ *              the scales of its own behind each other; rows behind the last
+ *              group are left as they were. With reduce = 1 they divide `rows`
+ *              rows that both a and b hold transposed, as ns_quantize lays them
+ *              out, and each group has a product of its own, out + e * out_batch
+ *              elements (zeros for a group without rows); k = (rows / 128 +
+ *              groups) * 128. Without reduce `rows` is not used.
+ * Offsets outside the rows or out of order give wrong results and no fault.
+ * workspace from ns_scaled_matmul_workspace_bytes (may be NULL if it says 0).
+ * m, n 0 .. 2^30, groups up to 1024. Nothing may overlap out.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
+ns_status ns_scaled_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t *bytes);
+ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, int64_t a_ld, const uint8_t *a_scales,
+                           const void *b, int64_t b_ld, int64_t b_batch, const uint8_t *b_scales,
+                           int32_t b_block_rows, const int32_t *offsets, int32_t groups, int32_t reduce, int64_t rows,
+                           ns_dtype out_dtype, void *out, int64_t out_ld, int64_t out_batch, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Norm of many gradients together: over n tensors of counts[i] contiguous
+ * values of grad_dtypes[i] (ns_dtype values) each,
+ *   *sum_sq = the sum of all squares (f64),  *norm = its square root (f32),
+ * either of which may be NULL. Squares are added in 64 bits. Gradients that lie
+ * on several GPUs: add their sum_sq and take the root. n 0 .. 2^20; all arrays
+ * are host memory that the call has read when it returns. workspace from
+ * ns_grad_workspace_bytes (any values; 256-byte aligned).
+ * Launches: one up to 256 KiB of gradients, else two; and one more for each 96
+ * tensors of a list of more than 96.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
+ns_status ns_grad_workspace_bytes(int32_t n, size_t *bytes);
+ns_status ns_grad_norm(int32_t n, const int64_t *counts, const void *const *grads, const int32_t *grad_dtypes,
+                       float *norm, double *sum_sq, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients clipped by their norm on the way into the momentum:
+ *   c = min(1, max_norm / (*norm + eps)),  outs[i] = beta * momenta[i] + c * grads[i]
+ * norm: on the GPU (as ns_grad_norm left it), or NULL for c = 1 (max_norm and
+ * eps unused). A norm that is not finite makes c 0 or NaN, by the formula. beta =
+ * 0: momenta are not read and may be NULL. outs[i] and momenta[i] are of
+ * out_dtypes[i]; outs[i] may be momenta[i], or grads[i] of the same type;
+ * otherwise tensors must not overlap. One launch, and one more for each 96
+ * tensors of a list of more than 96. Other arguments as for ns_grad_norm.
+ * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
+ns_status ns_grad_clip(int32_t n, const int64_t *counts, const void *const *grads, const int32_t *grad_dtypes,
+                       const void *const *momenta, void *const *outs, const int32_t *out_dtypes, const float *norm,
+                       float max_norm, float eps, float beta, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------------ *
  * Measurement support
  * ------------------------------------------------------------------------ */

@@ -42,9 +42,12 @@ from ._lib import (  # noqa: F401
 )
 from ._ops import (  # noqa: F401
     OPERATORS as _OPERATORS,
+    ns_block_norm_workspace_bytes,
     ns_distill_workspace_bytes,
+    ns_grad_workspace_bytes,
     ns_moe_sort_workspace_bytes,
     ns_qk_norm_rope_workspace_bytes,
+    ns_scaled_matmul_workspace_bytes,
 )
 
 

@@ -34,6 +34,9 @@ EXPORTS = [
     "ns_moe_sort_workspace_bytes", "ns_moe_sort", "ns_moe_dispatch", "ns_moe_dispatch_backward", "ns_moe_combine",
     "ns_moe_combine_backward",
     "ns_distill_workspace_bytes", "ns_distill_topk", "ns_distill_topk_backward",
+    "ns_block_norm", "ns_block_norm_workspace_bytes", "ns_block_norm_backward",
+    "ns_quantize", "ns_scaled_matmul_workspace_bytes", "ns_scaled_matmul",
+    "ns_grad_workspace_bytes", "ns_grad_norm", "ns_grad_clip",
 ]
 
 
@@ -98,6 +101,19 @@ _SIGS = {
                                _P, _SZ, _P]),
     "ns_distill_topk_backward": (_I32, [_I64, _I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I32, _P, _F32, _P, _P, _P, _P,
                                         _I64, _P]),
+    "ns_block_norm": (_I32, [_I64, _I32, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _F32, _F32, _F32, _P, _P,
+                             _P]),
+    "ns_block_norm_workspace_bytes": (_I32, [_I64, _I32, _P]),
+    "ns_block_norm_backward": (_I32, [_I64, _I32, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _F32, _F32, _F32,
+                                      _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ns_quantize": (_I32, [_I64, _I64, _I64, _I32, _P, _I64, _I64, _I32, _P, _I32, _P, _I64, _I64, _P, _P, _I64, _I64, _P,
+                           _P]),
+    "ns_scaled_matmul_workspace_bytes": (_I32, [_I64, _I64, _I64, _I32, _P]),
+    "ns_scaled_matmul": (_I32, [_I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _I32, _P, _I32, _I32, _I64, _I32, _P,
+                                _I64, _I64, _P, _SZ, _P]),
+    "ns_grad_workspace_bytes": (_I32, [_I32, _P]),
+    "ns_grad_norm": (_I32, [_I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ns_grad_clip": (_I32, [_I32, _P, _P, _P, _P, _P, _P, _P, _F32, _F32, _F32, _P, _SZ, _P]),
 }
 
 _lock = threading.Lock()

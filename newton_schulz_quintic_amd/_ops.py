@@ -22,12 +22,19 @@ OPERATORS = (
     "ns_qk_norm_rope", "ns_qk_norm_rope_backward",
     "ns_moe_sort", "ns_moe_dispatch", "ns_moe_dispatch_backward", "ns_moe_combine", "ns_moe_combine_backward",
     "ns_distill_topk", "ns_distill_topk_backward",
+    "ns_block_norm", "ns_block_norm_backward",
+    "ns_quantize", "ns_scaled_matmul",
+    "ns_grad_norm", "ns_grad_clip",
 )
 
 
 class ns_heads(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
+
+class ns_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
 
 
 def operator(name: str):
@@ -55,4 +62,22 @@ def ns_moe_sort_workspace_bytes(tokens: int, top_k: int, num_experts: int) -> in
 def ns_distill_workspace_bytes(rows: int, vocab: int, top_k: int) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().ns_distill_workspace_bytes(rows, vocab, top_k, ctypes.byref(n)))
+    return n.value
+
+
+def ns_block_norm_workspace_bytes(rows: int, hidden: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().ns_block_norm_workspace_bytes(rows, hidden, ctypes.byref(n)))
+    return n.value
+
+
+def ns_scaled_matmul_workspace_bytes(m: int, n: int, k: int, groups: int = 0) -> int:
+    size = ctypes.c_size_t(0)
+    _check(lib().ns_scaled_matmul_workspace_bytes(m, n, k, groups, ctypes.byref(size)))
+    return size.value
+
+
+def ns_grad_workspace_bytes(tensors: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().ns_grad_workspace_bytes(tensors, ctypes.byref(n)))
     return n.value

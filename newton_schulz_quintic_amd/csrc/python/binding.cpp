@@ -17,6 +17,7 @@
 #include <cstring>
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "ns.h"
 
@@ -122,8 +123,8 @@ struct Args {
         if (x == -1 && PyErr_Occurred()) throw Raised{};
         return x;
     }
-    bool flag(int i) const {
-        if (v[i] == Py_None) return false;
+    bool flag(int i, bool otherwise = false) const {
+        if (v[i] == Py_None) return otherwise;
         const int x = PyObject_IsTrue(v[i]);
         if (x < 0) throw Raised{};
         return x;
@@ -579,6 +580,341 @@ PyObject *distill_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyOb
 }
 
 // ---------------------------------------------------------------------------
+// norms around a block
+// ---------------------------------------------------------------------------
+
+// A (rows, hidden) tensor of one type with contiguous rows, or an absent one.
+ns_rows rows(const at::Tensor *t, const char *name, int64_t n, int64_t hidden, at::ScalarType type) {
+    if (!t) return ns_rows{nullptr, 0};
+    const int64_t ld = row_stride(*t, name, n, hidden, type);
+    return ns_rows{t->data_ptr(), ld};
+}
+
+struct BlockCall {
+    int64_t n, hidden, gate_rows = 1;
+    ns_dtype x_dtype, y_dtype, w_dtype = NS_F32, g_dtype = NS_F32;
+    at::ScalarType x_type, y_type;
+    ns_rows x, y, gate;
+    const void *wp = nullptr, *wn = nullptr;
+
+    // like: a tensor of the block's own type (y, h or dh), if there is any
+    BlockCall(const at::Tensor &tx, const at::Tensor *ty, const at::Tensor *like, const at::Tensor *post, const at::Tensor *pre,
+              const at::Tensor *g) {
+        if (tx.dim() != 2) raise(PyExc_ValueError, "x must be (rows, hidden)");
+        n = tx.size(0);
+        hidden = tx.size(1);
+        if (hidden > INT32_MAX) raise(PyExc_ValueError, "hidden out of range");
+        x_type = tx.scalar_type();
+        y_type = ty ? ty->scalar_type() : like ? like->scalar_type() : x_type;
+        x_dtype = code(tx, "x");
+        y_dtype = code(ty ? *ty : like ? *like : tx, "y and h");
+        x = rows(&tx, "x", n, hidden, x_type);
+        y = rows(ty, "y", n, hidden, y_type);
+        if (const at::Tensor *w = post ? post : pre) {
+            w_dtype = code(*w, "weights");
+            for (const at::Tensor *t : {post, pre})
+                if (t && (t->scalar_type() != w->scalar_type() || t->dim() != 1 || t->size(0) != hidden || !t->is_contiguous()))
+                    raise(PyExc_ValueError, "weights must share one dtype and be contiguous of shape " + text({hidden}));
+            wp = post ? post->data_ptr() : nullptr;
+            wn = pre ? pre->data_ptr() : nullptr;
+        }
+        gate = ns_rows{nullptr, 0};
+        if (g) {
+            if (g->dim() != 2) raise(PyExc_ValueError, "gate must be (gate_rows, hidden)");
+            g_dtype = code(*g, "gate");
+            gate_rows = g->size(0);
+            gate = rows(g, "gate", gate_rows, hidden, g->scalar_type());
+        }
+    }
+};
+
+Signature s_block_norm = {"ns_block_norm", 12, 4,
+                          {"x", "y", "x_out", "h", "post_weight", "pre_weight", "gate", "post_norm", "alpha", "scale", "eps",
+                           "stream"}};
+PyObject *block_norm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw) {
+    return guarded([&]() -> PyObject * {
+        const Args a(s_block_norm, args, n, kw);
+        const int64_t device = a.device(7);
+        const at::Tensor *y = a.tensor(1), *x_out = a.tensor(2), *h = a.tensor(3);
+        const BlockCall c(a.must(0), y, h, a.tensor(4), a.tensor(5), a.tensor(6));
+        const ns_rows o = rows(x_out, "x_out", c.n, c.hidden, c.x_type), oh = rows(h, "h", c.n, c.hidden, c.y_type);
+        if (!x_out && !h) raise(PyExc_ValueError, "x_out or h is required");
+        if (x_out && !y) raise(PyExc_ValueError, "x_out goes with y");
+        check(ns_block_norm(c.n, (int32_t)c.hidden, c.x_dtype, c.y_dtype, &c.x, y ? &c.y : nullptr, c.wp, c.wn, c.w_dtype,
+                            a.flag(7, y != nullptr), a.tensor(6) ? &c.gate : nullptr, c.gate_rows, c.g_dtype,
+                            (float)a.number(8, 1.0), (float)a.number(9, 1.0), (float)a.number(10, 1e-6), &o, &oh,
+                            a.stream(11, device)));
+        wrote({x_out, h});
+        Py_RETURN_NONE;
+    });
+}
+
+Signature s_block_norm_backward = {"ns_block_norm_backward", 18, 6,
+                                   {"x", "y", "dx_out", "dh", "dx", "dy", "dpost_weight", "dpre_weight", "dgate", "post_weight",
+                                    "pre_weight", "gate", "post_norm", "alpha", "scale", "eps", "workspace", "stream"}};
+PyObject *block_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw) {
+    return guarded([&]() -> PyObject * {
+        const Args a(s_block_norm_backward, args, n, kw);
+        const int64_t device = a.device(17);
+        const at::Tensor *y = a.tensor(1), *dx_out = a.tensor(2), *dh = a.tensor(3), *dx = a.tensor(4), *dy = a.tensor(5);
+        const at::Tensor *dgate = a.tensor(8), *gate = a.tensor(11);
+        const BlockCall c(a.must(0), y, dh ? dh : dy, a.tensor(9), a.tensor(10), gate);
+        if (!dx_out && !dh) raise(PyExc_ValueError, "dx_out or dh is required");
+        if ((dx_out || dy) && !y) raise(PyExc_ValueError, "dx_out and dy go with y");
+        if (dgate && !gate) raise(PyExc_ValueError, "dgate goes with gate");
+        const ns_rows gx = rows(dx_out, "dx_out", c.n, c.hidden, c.x_type), gh = rows(dh, "dh", c.n, c.hidden, c.y_type);
+        const ns_rows ox = rows(dx, "dx", c.n, c.hidden, c.x_type), oy = rows(dy, "dy", c.n, c.hidden, c.y_type);
+        const ns_rows og = dgate ? rows(dgate, "dgate", c.gate_rows, c.hidden, gate->scalar_type()) : ns_rows{nullptr, 0};
+        float *wp = array<float>(a.tensor(6), "dpost_weight", {c.hidden}, at::kFloat);
+        float *wn = array<float>(a.tensor(7), "dpre_weight", {c.hidden}, at::kFloat);
+        void *p = nullptr;
+        size_t bytes = 0;
+        Held ws{nullptr};
+        if (wp || wn || dgate || a.v[16] != Py_None)
+            ws.o = workspace(a.v[16], [&](size_t *need) { return ns_block_norm_workspace_bytes(c.n, (int32_t)c.hidden, need); },
+                             a.v[0], a.v[17], &p, &bytes);
+        check(ns_block_norm_backward(c.n, (int32_t)c.hidden, c.x_dtype, c.y_dtype, &c.x, y ? &c.y : nullptr, c.wp, c.wn,
+                                     c.w_dtype, a.flag(12, y != nullptr), gate ? &c.gate : nullptr, c.gate_rows, c.g_dtype,
+                                     (float)a.number(13, 1.0), (float)a.number(14, 1.0), (float)a.number(15, 1e-6), &gx, &gh,
+                                     &ox, &oy, wp, wn, dgate ? &og : nullptr, p, bytes, a.stream(17, device)));
+        wrote({dx, dy, a.tensor(6), a.tensor(7), dgate});
+        if (ws.o) return ws.give();
+        Py_RETURN_NONE;
+    });
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit products
+// ---------------------------------------------------------------------------
+
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+// An e4m3 tensor of (batch,) rows x cols with contiguous rows: address, row and batch stride (NULL for None).
+struct Bytes {
+    void *p = nullptr;
+    int64_t ld = 0, batch = 0;
+    Bytes(const at::Tensor *t, const char *name, bool batched, int64_t n, int64_t rows, int64_t cols) {
+        if (!t) return;
+        want_type(*t, name, at::kFloat8_e4m3fn);
+        const int64_t d = batched ? 1 : 0;
+        if (t->dim() != 2 + d || (batched && t->size(0) != n) || t->size(d) != rows || t->size(d + 1) != cols)
+            raise(PyExc_ValueError, std::string(name) + " must have shape " +
+                                        (batched ? text({n, rows, cols}) : text({rows, cols})) + ", not " + text(*t));
+        if (t->stride(d + 1) != 1 && cols > 1 && t->numel()) raise(PyExc_ValueError, std::string("each row of ") + name + " must be contiguous");
+        p = t->data_ptr();
+        ld = rows > 1 ? t->stride(d) : (cols + 15) / 16 * 16;
+        batch = batched ? t->stride(0) : 0;
+    }
+};
+
+const int32_t *group_offsets(const at::Tensor *t, int64_t *groups) {
+    if (!t) return nullptr;
+    if (t->dim() != 1 || t->size(0) < 2) raise(PyExc_ValueError, "offsets must be (groups + 1,)");
+    *groups = t->size(0) - 1;
+    if (*groups > INT32_MAX) raise(PyExc_ValueError, "too many groups");
+    return array<int32_t>(t, "offsets", {*groups + 1}, at::kInt);
+}
+
+Signature s_quantize = {"ns_quantize", 8, 3, {"x", "q", "scales", "qt", "scales_t", "block_rows", "offsets", "stream"}};
+PyObject *quantize(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw) {
+    return guarded([&]() -> PyObject * {
+        const Args a(s_quantize, args, n, kw);
+        const int64_t device = a.device(7);
+        const at::Tensor &x = a.must(0);
+        const bool batched = x.dim() == 3;
+        if (x.dim() != 2 && !batched) raise(PyExc_ValueError, "x must be (rows, cols) or (batch, rows, cols)");
+        const int64_t d = batched, batch = batched ? x.size(0) : 1, r = x.size(d), c = x.size(d + 1);
+        const int64_t block = a.v[5] == Py_None ? 1 : a.integer(5);
+        if (block != 1 && block != 128) raise(PyExc_ValueError, "block_rows must be 1 or 128");
+        const ns_dtype dtype = code(x, "x");
+        if (x.numel() && x.stride(d + 1) != 1 && c > 1) raise(PyExc_ValueError, "each row of x must be contiguous");
+        int64_t groups = 0;
+        const int32_t *offsets = group_offsets(a.tensor(6), &groups);
+        const int64_t cb = blocks(c), rb = offsets ? r / 128 + groups : blocks(r);
+        const Bytes q(a.tensor(1), "q", batched, batch, r, cb * 128), qt(a.tensor(3), "qt", batched, batch, c, rb * 128);
+        const int64_t sr = block == 1 ? r : blocks(r), sc = block == 1 ? c : blocks(c);
+        uint8_t *s = batched ? array<uint8_t>(a.tensor(2), "scales", {batch, sr, cb}, at::kByte)
+                             : array<uint8_t>(a.tensor(2), "scales", {sr, cb}, at::kByte);
+        uint8_t *st = batched ? array<uint8_t>(a.tensor(4), "scales_t", {batch, sc, rb}, at::kByte)
+                              : array<uint8_t>(a.tensor(4), "scales_t", {sc, rb}, at::kByte);
+        if (!a.tensor(1) != !a.tensor(2) || !a.tensor(3) != !a.tensor(4))
+            raise(PyExc_ValueError, "q goes with scales, and qt with scales_t");
+        if (!a.tensor(1) && !a.tensor(3)) raise(PyExc_ValueError, "q or qt is required");
+        if (!x.numel() && !offsets) Py_RETURN_NONE;
+        check(ns_quantize(batch, r, c, dtype, x.data_ptr(), r > 1 ? x.stride(d) : c, batched ? x.stride(0) : 0, (int32_t)block,
+                          offsets, (int32_t)groups, q.p, q.ld, q.batch, s, qt.p, qt.ld, qt.batch, st, a.stream(7, device)));
+        wrote({a.tensor(1), a.tensor(2), a.tensor(3), a.tensor(4)});
+        Py_RETURN_NONE;
+    });
+}
+
+Signature s_scaled_matmul = {"ns_scaled_matmul", 9, 5,
+                             {"a", "a_scales", "b", "b_scales", "out", "offsets", "reduce", "workspace", "stream"}};
+PyObject *scaled_matmul(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw) {
+    return guarded([&]() -> PyObject * {
+        const Args a(s_scaled_matmul, args, n, kw);
+        const int64_t device = a.device(8);
+        const at::Tensor &ta = a.must(0), &tsa = a.must(1), &tb = a.must(2), &tsb = a.must(3), &out = a.must(4);
+        int64_t groups = 0;
+        const int32_t *offsets = group_offsets(a.tensor(5), &groups);
+        const bool reduce = a.flag(6), batched = offsets && !reduce;
+        if (ta.dim() != 2 || tb.dim() != (batched ? 3 : 2))
+            raise(PyExc_ValueError, batched ? "a must be (m, k) and b (groups, n, k)" : "a must be (m, k) and b (n, k)");
+        const int64_t m = ta.size(0), k = ta.size(1), cols = tb.size(batched ? 1 : 0);
+        if (k % 128) raise(PyExc_ValueError, "k = " + std::to_string(k) + " is not a multiple of 128");
+        const Bytes qa(&ta, "a", false, 1, m, k), qb(&tb, "b", batched, groups, cols, k);
+        const uint8_t *sa = array<uint8_t>(&tsa, "a_scales", {m, k / 128}, at::kByte);
+        const int64_t given = tsb.dim() == (batched ? 3 : 2) ? tsb.size(batched ? 1 : 0) : -1;
+        const int32_t block = given == cols ? 1 : 128;
+        const int64_t want = block == 1 ? cols : blocks(cols);
+        const uint8_t *sb = batched ? array<uint8_t>(&tsb, "b_scales", {groups, want, k / 128}, at::kByte)
+                                    : array<uint8_t>(&tsb, "b_scales", {want, k / 128}, at::kByte);
+        const ns_dtype out_dtype = code(out, "out");
+        int64_t ld, out_batch = 0, tokens = 0;
+        if (reduce) {
+            if (!offsets) raise(PyExc_ValueError, "reduce goes with offsets");
+            if (k / 128 < groups) raise(PyExc_ValueError, "k must be (rows / 128 + groups) * 128");
+            tokens = (k / 128 - groups) * 128 + 127;   // the most that this k has room for
+            if (out.dim() != 3 || out.size(0) != groups || out.size(1) != m || out.size(2) != cols)
+                raise(PyExc_ValueError, "out must have shape " + text({groups, m, cols}) + ", not " + text(out));
+            if (out.stride(2) != 1 && cols > 1 && out.numel()) raise(PyExc_ValueError, "each row of out must be contiguous");
+            ld = m > 1 ? out.stride(1) : std::max<int64_t>(cols, 1);
+            out_batch = out.stride(0);
+        } else {
+            ld = row_stride(out, "out", m, cols, out.scalar_type());
+        }
+        void *p = nullptr;
+        size_t bytes = 0;
+        Held ws{nullptr};
+        size_t need = 0;
+        check(ns_scaled_matmul_workspace_bytes(m, cols, k, (int32_t)groups, &need));
+        if (need || a.v[7] != Py_None)
+            ws.o = workspace(a.v[7], [&](size_t *to) { *to = need; return NS_OK; }, a.v[0], a.v[8], &p, &bytes);
+        check(ns_scaled_matmul(m, cols, k, qa.p, qa.ld, sa, qb.p, qb.ld, qb.batch, sb, block, offsets, (int32_t)groups, reduce,
+                               tokens, out_dtype, out.data_ptr(), ld, out_batch, p, bytes, a.stream(8, device)));
+        wrote({&out});
+        if (ws.o) return ws.give();
+        Py_RETURN_NONE;
+    });
+}
+
+// ---------------------------------------------------------------------------
+// gradients together
+// ---------------------------------------------------------------------------
+
+// The contiguous bf16 and f32 tensors of a list or tuple: addresses, sizes, types.
+struct TensorList {
+    std::vector<const at::Tensor *> t;
+    std::vector<void *> p;
+    std::vector<int64_t> count;
+    std::vector<int32_t> dtype;
+    PyObject *seq;
+
+    TensorList(PyObject *list, const char *name, const TensorList *like, int64_t *device) {
+        seq = PySequence_Fast(list, (std::string(name) + " must be a list of tensors").c_str());
+        if (!seq) throw Raised{};
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+        try {
+            if (n > INT32_MAX) raise(PyExc_ValueError, std::string(name) + " is too long");
+            if (like && like->t.size() != (size_t)n)
+                raise(PyExc_ValueError, std::string(name) + " must hold " + std::to_string(like->t.size()) + " tensors, not " + std::to_string(n));
+            for (Py_ssize_t i = 0; i < n; ++i) {
+                PyObject *o = PySequence_Fast_GET_ITEM(seq, i);
+                if (!THPVariable_Check(o)) raise(PyExc_TypeError, std::string(name) + " must hold tensors");
+                const at::Tensor &x = THPVariable_Unpack(o);
+                const int64_t at = x.is_cuda() ? x.get_device() : -1;
+                if (*device < 0 && at >= 0) {
+                    PyObject *d = PyObject_CallNoArgs(g_get_device);
+                    if (!d) throw Raised{};
+                    *device = PyLong_AsLongLong(d);
+                    Py_DECREF(d);
+                }
+                if (at < 0 || at != *device)
+                    raise(PyExc_ValueError, std::string(name) + "[" + std::to_string(i) + "] is on " + x.device().str() + ", not on the current GPU");
+                if (!x.is_contiguous()) raise(PyExc_ValueError, std::string(name) + "[" + std::to_string(i) + "] must be contiguous");
+                if (like && x.numel() != like->count[i])
+                    raise(PyExc_ValueError, std::string(name) + "[" + std::to_string(i) + "] must have " + std::to_string(like->count[i]) +
+                                                " values, not " + std::to_string(x.numel()));
+                t.push_back(&x);
+                p.push_back(x.data_ptr());
+                count.push_back(x.numel());
+                dtype.push_back(code(x, name));
+            }
+        } catch (...) {
+            Py_DECREF(seq);
+            throw;
+        }
+    }
+    ~TensorList() { Py_DECREF(seq); }
+    TensorList(const TensorList &) = delete;
+    int32_t n() const { return (int32_t)t.size(); }
+};
+
+// One f32 (or f64) value on the GPU.
+template <typename P>
+P *one_value(const at::Tensor *t, const char *name, at::ScalarType type) {
+    if (!t) return nullptr;
+    want_type(*t, name, type);
+    if (t->numel() != 1) raise(PyExc_ValueError, std::string(name) + " must hold one value, not " + text(*t));
+    return static_cast<P *>(t->data_ptr());
+}
+
+Signature s_grad_norm = {"ns_grad_norm", 5, 2, {"grads", "norm", "sum_sq", "workspace", "stream"}};
+PyObject *grad_norm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw) {
+    return guarded([&]() -> PyObject * {
+        const Args a(s_grad_norm, args, n, kw);
+        int64_t device = a.device(4);
+        const TensorList g(a.v[0], "grads", nullptr, &device);
+        float *norm = one_value<float>(a.tensor(1), "norm", at::kFloat);
+        double *sum_sq = one_value<double>(a.tensor(2), "sum_sq", at::kDouble);
+        if (!norm && !sum_sq) raise(PyExc_ValueError, "norm or sum_sq is required");
+        void *p;
+        size_t bytes;
+        Held ws{workspace(a.v[3], [&](size_t *need) { return ns_grad_workspace_bytes(g.n(), need); },
+                          norm ? a.v[1] : a.v[2], a.v[4], &p, &bytes)};
+        check(ns_grad_norm(g.n(), g.count.data(), g.p.data(), g.dtype.data(), norm, sum_sq, p, bytes, a.stream(4, device)));
+        wrote({a.tensor(1), a.tensor(2)});
+        return ws.give();
+    });
+}
+
+Signature s_grad_clip = {"ns_grad_clip", 9, 2,
+                         {"grads", "outs", "norm", "max_norm", "eps", "momenta", "beta", "workspace", "stream"}};
+PyObject *grad_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw) {
+    return guarded([&]() -> PyObject * {
+        const Args a(s_grad_clip, args, n, kw);
+        int64_t device = a.device(8);
+        const TensorList g(a.v[0], "grads", nullptr, &device), o(a.v[1], "outs", &g, &device);
+        const float *norm = one_value<float>(a.tensor(2), "norm", at::kFloat);
+        if (norm && a.v[3] == Py_None) raise(PyExc_ValueError, "norm goes with max_norm");
+        const float beta = (float)a.number(6, 0.0);
+        const bool given = a.v[5] != Py_None;
+        if (beta != 0.f && !given) raise(PyExc_ValueError, "beta goes with momenta");
+        PyObject *none = nullptr;
+        if (!given) {
+            none = PyTuple_New(0);
+            if (!none) throw Raised{};
+        }
+        Held held{none};
+        const TensorList m(given ? a.v[5] : none, "momenta", given ? &g : nullptr, &device);
+        if (given && m.dtype != o.dtype) raise(PyExc_ValueError, "momenta must have the dtypes of outs");
+        if (!g.n()) {   // nothing to take a device from
+            if (a.v[7] == Py_None) Py_RETURN_NONE;
+            return Py_NewRef(a.v[7]);
+        }
+        void *p;
+        size_t bytes;
+        Held ws{workspace(a.v[7], [&](size_t *need) { return ns_grad_workspace_bytes(g.n(), need); },
+                          PySequence_Fast_GET_ITEM(g.seq, 0), a.v[8], &p, &bytes)};
+        check(ns_grad_clip(g.n(), g.count.data(), g.p.data(), g.dtype.data(), given ? m.p.data() : nullptr, o.p.data(),
+                           o.dtype.data(), norm, (float)a.number(3, 0.0), (float)a.number(4, 1e-6), beta, p, bytes,
+                           a.stream(8, device)));
+        for (const at::Tensor *t : o.t) wrote({t});
+        return ws.give();
+    });
+}
+
+// ---------------------------------------------------------------------------
 // module
 // ---------------------------------------------------------------------------
 
@@ -629,6 +965,44 @@ PyMethodDef methods[] = {
                "ns_distill_topk_backward(logits, ids, teacher, lse, grad_loss, dlogits, teacher_lse=None, rest_lse=None, "
                "temperature=1.0, stream=None)\n--\n\n"
                "Gradient of ns_distill_topk by itself, from the lse (and rest_lse) it gave (see ns.h)."),
+    NSQ_METHOD("ns_block_norm", block_norm,
+               "ns_block_norm(x, y, x_out, h, post_weight=None, pre_weight=None, gate=None, post_norm=True, alpha=1.0, "
+               "scale=1.0, eps=1e-06, stream=None)\n--\n\n"
+               "Norms before and after a block with its gate and residual scale (see ns.h):\n"
+               "x_out = alpha x + scale gate norm(y), h = norm(x_out).\n\n"
+               "x, y, x_out, h: (rows, hidden) with contiguous rows, bf16 or f32 (x and x_out f32 if y and h are). y, x_out\n"
+               "or h may be None. gate: (gate_rows, hidden), a row for each rows / gate_rows rows. x_out may be x, h may be y."),
+    NSQ_METHOD("ns_block_norm_backward", block_norm_backward,
+               "ns_block_norm_backward(x, y, dx_out, dh, dx, dy, dpost_weight=None, dpre_weight=None, dgate=None, "
+               "post_weight=None, pre_weight=None, gate=None, post_norm=True, alpha=1.0, scale=1.0, eps=1e-06, workspace=None, "
+               "stream=None)\n--\n\n"
+               "Gradient of ns_block_norm (see ns.h): x and y are the forward's inputs; dx_out or dh, and any output, may be\n"
+               "None. dpost_weight, dpre_weight: (hidden,) f32; dgate like gate. Returns the workspace (None if no sum over\n"
+               "rows is wanted and none given)."),
+    NSQ_METHOD("ns_quantize", quantize,
+               "ns_quantize(x, q, scales, qt=None, scales_t=None, block_rows=1, offsets=None, stream=None)\n--\n\n"
+               "x as e4m3 values with a power-of-two scale for each 1 x 128 (block_rows 128: 128 x 128) block (see ns.h).\n\n"
+               "x: (rows, cols), or (batch, rows, cols) with block_rows 128; bf16 or f32 with contiguous rows.\n"
+               "q: (..., rows, cols') float8_e4m3fn, cols' = cols rounded up to 128; scales (..., rows or blocks of rows,\n"
+               "cols' / 128) uint8. qt, scales_t: the same of the transpose. q and scales, or qt and scales_t, may be None.\n"
+               "offsets: (groups + 1,) int32, each group of rows starts a block of qt, (cols, (rows // 128 + groups) * 128)."),
+    NSQ_METHOD("ns_scaled_matmul", scaled_matmul,
+               "ns_scaled_matmul(a, a_scales, b, b_scales, out, offsets=None, reduce=False, workspace=None, stream=None)\n--\n\n"
+               "out = a b^T of e4m3 matrices with their scales (see ns.h).\n\n"
+               "a: (m, k), a_scales (m, k / 128); b: (n, k), b_scales (n or blocks of n, k / 128); out: (m, n) bf16 or f32.\n"
+               "offsets: (groups + 1,) int32; b is then (groups, n, k) and a's rows offsets[e] .. offsets[e + 1] take b[e], or\n"
+               "with reduce a and b are transposes by group (ns_quantize with offsets) and out is (groups, m, n).\n"
+               "Returns the workspace (None if it takes none)."),
+    NSQ_METHOD("ns_grad_norm", grad_norm,
+               "ns_grad_norm(grads, norm, sum_sq=None, workspace=None, stream=None)\n--\n\n"
+               "Root of the sum of all squares of a list of contiguous bf16 and f32 tensors (see ns.h).\n\n"
+               "norm: one f32 value, or None with sum_sq, one f64 value. Returns the workspace."),
+    NSQ_METHOD("ns_grad_clip", grad_clip,
+               "ns_grad_clip(grads, outs, norm=None, max_norm=None, eps=1e-06, momenta=None, beta=0.0, workspace=None, "
+               "stream=None)\n--\n\n"
+               "outs[i] = beta momenta[i] + min(1, max_norm / (norm + eps)) grads[i] (see ns.h).\n\n"
+               "norm: one f32 value as ns_grad_norm leaves it, or None for no clipping. outs may be momenta, or grads.\n"
+               "Returns the workspace."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Training-step operators of the library. Autograd records nothing of a call (see the\n"
@@ -654,7 +1028,8 @@ PyMODINIT_FUNC PyInit__binding() {
     g_str_device = PyUnicode_InternFromString("device");
     g_str_cuda_stream = PyUnicode_InternFromString("cuda_stream");
     for (Signature *s : {&s_norm_rope, &s_norm_rope_backward, &s_moe_sort, &s_moe_dispatch, &s_moe_dispatch_backward,
-                         &s_moe_combine, &s_moe_combine_backward, &s_distill, &s_distill_backward})
+                         &s_moe_combine, &s_moe_combine_backward, &s_distill, &s_distill_backward, &s_block_norm,
+                         &s_block_norm_backward, &s_quantize, &s_scaled_matmul, &s_grad_norm, &s_grad_clip})
         for (int i = 0; i < s->count; ++i) {
             s->interned[i] = PyUnicode_InternFromString(s->names[i]);
             if (!s->interned[i]) return nullptr;

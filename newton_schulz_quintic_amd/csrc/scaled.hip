@@ -1,0 +1,716 @@
+// 8-bit matrix products with a power-of-two scale for each block of 128 along the
+// reduction, and the quantization that makes their operands.
+//
+// A value v of a block is held as e4m3(v / 2^e), with e the smallest whole number
+// for which the block's largest magnitude over 2^e is at most 448 (e4m3's
+// largest), and e + 127 in one byte. Dividing by a power of two is exact, so a
+// value is rounded once. Product, for a block index kb and its 128 values of k:
+//   out[m, n] = sum over kb of 2^(sa[m, kb] - 127) 2^(sb[n, kb] - 127) sum over k of a[m, k] b[n, k].
+// bf16 outputs: the scales go into the matrix instruction
+// (v_mfma_scale_f32_16x16x128_f8f6f4), which takes such a byte for each row of both
+// operands: a block of 128 is one instruction, its sum is added to the fp32
+// accumulator scaled, and no value is touched outside it.
+// fp32 outputs: the 8-bit instructions (all three shapes alike) align the products
+// of a block to the largest and drop bits below some 2^-13 of it; measured against
+// 64 bits, sums come out 1.4e-5 of their rms off where the values of a block are
+// normally distributed, 7e-5 where they spread over 2^12. Next to bf16's rounding
+// (1.7e-3) that is nothing; where fp32 is asked for it is not. There the values are
+// widened to bf16, scale included (exact: one conversion for two values), and go
+// through v_mfma_f32_16x16x32_bf16, whose sums are as good as fp32 adds (2e-8 to
+// 1e-7 here), at half the peak.
+
+#include <algorithm>
+
+#include "elems.h"
+
+namespace nsq {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+#define NSQ_LDS __attribute__((address_space(3)))
+
+constexpr int kBlock = 128;        // values of one scale
+constexpr int kMaxGroups = 1024;
+constexpr int kNumXcd = 8;
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxCols = 1 << 22;
+
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Groups of rows ---------------------------------------------------------------
+
+// Row group e is offsets[e] .. offsets[e + 1], cut to [0, rows).
+__device__ inline int edge(const int32_t *offsets, int e, int rows) { return min(max(offsets[e], 0), rows); }
+
+// The groups' rows in blocks of `unit`, numbered through: the group and the place
+// in it of block `target` (group -1: there are no more than `total` blocks), or with
+// by_group the number of group `target`'s first block. A wave's lanes take a run of
+// groups each, so this is a short chain of loads and one scan.
+struct GroupBlock {
+    int group, index, total;
+};
+template <bool BY_GROUP>
+__device__ inline GroupBlock find_block(const int32_t *offsets, int groups, int rows, int unit, int target) {
+    const int lane = threadIdx.x & 63, per = (groups + 63) / 64;
+    const int from = min(lane * per, groups), to = min(from + per, groups);
+    int sum = 0;
+    for (int e = from; e < to; ++e) sum += (max(edge(offsets, e + 1, rows) - edge(offsets, e, rows), 0) + unit - 1) / unit;
+    int upto = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+    }
+    GroupBlock r;
+    r.total = uniform(__shfl(upto, 63));
+    const bool mine = BY_GROUP ? target >= from && target < to : target >= upto - sum && target < upto;
+    int group = -1, index = 0;
+    if (mine) {
+        int before = upto - sum;
+        for (int e = from; e < to; ++e) {
+            const int n = (max(edge(offsets, e + 1, rows) - edge(offsets, e, rows), 0) + unit - 1) / unit;
+            if (BY_GROUP ? e == target : target < before + n) {
+                group = e;
+                index = BY_GROUP ? before : target - before;
+                break;
+            }
+            before += n;
+        }
+    }
+    const uint64_t who = __ballot(mine);
+    const int at = who ? __ffsll((unsigned long long)who) - 1 : 0;
+    r.group = uniform(__shfl(group, at));
+    r.index = uniform(__shfl(index, at));
+    if (!who) r.group = -1;
+    return r;
+}
+
+// ---------------------------------------------------------------------------
+// quantization
+// ---------------------------------------------------------------------------
+
+struct QuantArgs {
+    const char *x;
+    uint8_t *q, *s, *qt, *st;
+    const int32_t *offsets;
+    int64_t x_ld, x_batch, q_ld, q_batch, s_batch, qt_ld, qt_batch, st_batch;
+    int rows, cols, groups;
+    int nb, nbt;          // blocks of a row of q, of qt
+};
+
+// Magnitudes of the finite values; the others count as 0 and become e4m3's NaN.
+__device__ inline float size_of(float x) {
+    const float m = fabsf(x);
+    return m <= 3.402823466e38f ? m : 0.f;
+}
+// The exponent's byte for a block's largest magnitude, and 1 / scale.
+__device__ inline int scale_byte(float largest) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, largest);
+    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFF) > 0x600000);   // 448 = 1.75 x 2^8
+    return largest > 0.f ? max(e, -126) + 127 : 127;
+}
+__device__ inline float inverse_scale(int byte) { return __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23); }
+
+// Four values as e4m3, rounded to nearest even.
+__device__ inline uint32_t pack4(float a, float b, float c, float d) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+// A value over its scale; what is not finite as NaN.
+__device__ inline float scaled(float x, float inv) { return fabsf(x) <= 3.402823466e38f ? x * inv : __builtin_nanf(""); }
+
+// Eight elements of a row from column c, zeros behind the last column.
+template <typename T>
+__device__ inline void load8(const T *row, int c, int cols, float (&v)[8]) {
+    if (c + 8 <= cols) {
+        if constexpr (sizeof(T) == 2) {
+            Elems<T, 8>::widen(Elems<T, 8>::load(row + c), v);
+        } else {
+            float lo[4], hi[4];
+            Elems<T, 4>::widen(Elems<T, 4>::load(row + c), lo);
+            Elems<T, 4>::widen(Elems<T, 4>::load(row + c + 4), hi);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? (float)row[c + k] : 0.f;
+    }
+}
+
+__device__ inline float max16(float v) {   // over 16 neighbouring lanes
+    return lanes_join<0, 4>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// Rows only: 16 lanes take a block of 128 values, four blocks at a time.
+template <typename T, int AT_ONCE>
+__global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
+    const int64_t units = (int64_t)a.rows * a.nb;
+    const int lane = threadIdx.x & 15;
+    const int64_t first = (int64_t)blockIdx.x * 16 * AT_ONCE + (threadIdx.x >> 4);
+    float v[AT_ONCE][8];
+    int64_t row[AT_ONCE];
+    int kb[AT_ONCE];
+#pragma unroll
+    for (int n = 0; n < AT_ONCE; ++n) {
+        const int64_t u = min(first + 16 * n, units - 1);
+        row[n] = u / a.nb;
+        kb[n] = (int)(u - row[n] * a.nb);
+        load8<T>(reinterpret_cast<const T *>(a.x) + row[n] * a.x_ld, kb[n] * kBlock + lane * 8, a.cols, v[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < AT_ONCE; ++n) {
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(v[n][k]));
+        const int byte = scale_byte(max16(m));
+        const float inv = inverse_scale(byte);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[n][k] = scaled(v[n][k], inv);
+        if (first + 16 * n >= units) return;
+        uint2 out = {pack4(v[n][0], v[n][1], v[n][2], v[n][3]), pack4(v[n][4], v[n][5], v[n][6], v[n][7])};
+        *reinterpret_cast<uint2 *>(a.q + row[n] * a.q_ld + kb[n] * kBlock + lane * 8) = out;
+        if (lane == 0) a.s[row[n] * a.nb + kb[n]] = (uint8_t)byte;
+    }
+}
+
+// A tile of 128 x 128: a thread holds 8 x 8 values of it. SQUARE: one scale for
+// the tile, for q and for qt; else one for each row (q) and one for each column (qt).
+constexpr int kTurnPitch = kBlock + 16;
+template <typename T, bool SQUARE>
+__global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
+    __shared__ float part[16][kBlock];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock * kTurnPitch];
+    const int cb = blockIdx.x;
+    const int lane = threadIdx.x & 15, down = threadIdx.x >> 4;
+    // rows [r0, end) go to columns t0 and on of qt
+    int r0 = blockIdx.y * kBlock, end = min(r0 + kBlock, a.rows), t0 = r0;
+    bool turn = a.qt != nullptr;
+    if (a.offsets) {
+        const GroupBlock g = find_block<false>(a.offsets, a.groups, a.rows, kBlock, blockIdx.y);
+        if (g.group >= 0) {
+            r0 = edge(a.offsets, g.group, a.rows) + g.index * kBlock;
+            end = min(r0 + kBlock, edge(a.offsets, g.group + 1, a.rows));
+            turn = turn && t0 < a.nbt * kBlock;
+        } else {   // rows behind the last group: they have no place in qt
+            r0 = edge(a.offsets, a.groups, a.rows) + ((int)blockIdx.y - g.total) * kBlock;
+            end = min(r0 + kBlock, a.rows);
+            turn = false;
+            if (r0 >= end || !a.q) return;
+        }
+    }
+    const T *x = reinterpret_cast<const T *>(a.x) + blockIdx.z * a.x_batch;
+    const int c0 = cb * kBlock + lane * 8;
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + down * 8 + i;
+        if (r < end) {
+            load8<T>(x + (int64_t)r * a.x_ld, c0, a.cols, v[i]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+        }
+    }
+    int byte = 0;
+    if constexpr (SQUARE) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(v[i][k]));
+        m = wave_max(m);
+        if ((threadIdx.x & 63) == 0) part[0][threadIdx.x >> 6] = m;
+        __syncthreads();
+        byte = scale_byte(fmaxf(fmaxf(part[0][0], part[0][1]), fmaxf(part[0][2], part[0][3])));
+        const float inv = inverse_scale(byte);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = scaled(v[i][k], inv);
+        if (threadIdx.x == 0) {
+            if (a.s) a.s[blockIdx.z * a.s_batch + (int64_t)blockIdx.y * a.nb + cb] = (uint8_t)byte;
+            if (a.st) a.st[blockIdx.z * a.st_batch + (int64_t)cb * a.nbt + blockIdx.y] = (uint8_t)byte;
+        }
+    }
+    if (a.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + down * 8 + i;
+            float inv = 1.f;
+            if constexpr (!SQUARE) {
+                float m = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(v[i][k]));
+                const int b = scale_byte(max16(m));
+                inv = inverse_scale(b);
+                if (lane == 0 && r < end) a.s[(int64_t)r * a.nb + cb] = (uint8_t)b;
+            }
+            if (r >= end) continue;
+            float u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = SQUARE ? v[i][k] : scaled(v[i][k], inv);
+            uint2 out = {pack4(u[0], u[1], u[2], u[3]), pack4(u[4], u[5], u[6], u[7])};
+            *reinterpret_cast<uint2 *>(a.q + blockIdx.z * a.q_batch + r * a.q_ld + c0) = out;
+        }
+    }
+    if (!turn) return;
+    float inv[8];
+    if constexpr (!SQUARE) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, size_of(v[i][k]));
+            part[down][lane * 8 + k] = m;
+        }
+        __syncthreads();
+        float m[8] = {};
+#pragma unroll
+        for (int d = 0; d < 16; ++d)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m[k] = fmaxf(m[k], part[d][lane * 8 + k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int b = scale_byte(m[k]);
+            inv[k] = inverse_scale(b);
+            if (down == 0 && c0 + k < a.cols) a.st[(int64_t)(c0 + k) * a.nbt + t0 / kBlock] = (uint8_t)b;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = SQUARE ? v[i][k] : scaled(v[i][k], inv[k]);
+        uint2 out = {pack4(u[0], u[1], u[2], u[3]), pack4(u[4], u[5], u[6], u[7])};
+        *reinterpret_cast<uint2 *>(turned + (lane * 8 + k) * kTurnPitch + down * 8) = out;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int col = p * 32 + (threadIdx.x >> 3), piece = (threadIdx.x & 7) * 16;
+        if (cb * kBlock + col >= a.cols) continue;
+        const uint4 out = *reinterpret_cast<const uint4 *>(turned + col * kTurnPitch + piece);
+        *reinterpret_cast<uint4 *>(a.qt + blockIdx.z * a.qt_batch + (int64_t)(cb * kBlock + col) * a.qt_ld + t0 + piece) = out;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+
+enum Grouping { kDense = 0, kRows = 1, kReduce = 2 };
+
+struct MatArgs {
+    const uint8_t *a, *as, *b, *bs;
+    char *out;
+    const int32_t *offsets;
+    int64_t lda, ldb, ldo, b_batch, bs_batch, out_batch;
+    int m, n, nkb;                 // rows of a, rows of b, blocks along the reduction
+    int groups, rows;              // rows: what the groups divide (a's rows, or kReduce: tokens)
+    int b_square, out_f32;
+    int tiles_m, tiles_n;
+};
+
+// Tile of BM x BN computed by WM x WN waves; stages of one block (128 bytes a row) of both operands in two LDS buffers.
+template <int BM_, int BN_, int WM_, int WN_> struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    static constexpr int NM = BM / WM / 16, NN = BN / WN / 16;
+    static constexpr int PANEL_A = BM * kBlock, PANEL_B = BN * kBlock, STAGE = PANEL_A + PANEL_B;
+    static constexpr int LOADS_A = BM / WAVES / 8, LOADS_B = BN / WAVES / 8;   // 8 rows a wave load
+};
+
+// Panel row r sits at r * 128 bytes, its 16-byte chunk c at slot c ^ swz(r): the 16
+// lanes of a fragment read (16 rows, one chunk each) hit distinct banks.
+__device__ inline int swz(int r) { return (r >> 1) & 7; }
+
+// Four blocks' scale bytes of one row, from block 4 j. Never reads outside the row.
+__device__ inline uint32_t scale_word(const uint8_t *row, int j, int nkb) {
+    if (nkb >= 4) {
+        const int at = min(4 * j, nkb - 4);
+        typedef uint32_t word_u __attribute__((aligned(1)));
+        return *reinterpret_cast<const word_u *>(row + at) >> (8 * (4 * j - at));
+    }
+    uint32_t w = 0;
+    for (int k = 0; k < nkb; ++k) w |= (uint32_t)row[k] << (8 * k);
+    return w;
+}
+
+__device__ inline float scale_of(uint32_t word) { return __builtin_bit_cast(float, (word & 255) << 23); }
+
+// Eight e4m3 values, bytes of two words, times a power of two, as bf16.
+__device__ inline bf16x8 widen8(int lo, int hi, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+template <int N> __device__ inline void wait_vmcnt() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
+// Workgroup id -> tile such that an XCD's workgroups (ids congruent mod 8) get a contiguous run.
+__device__ inline int xcd_remap(int b, int g) {
+    const int xcd = b % kNumXcd, local = b / kNumXcd, per = g / kNumXcd, rem = g % kNumXcd;
+    return xcd < rem ? xcd * (per + 1) + local : rem * (per + 1) + (xcd - rem) * per + local;
+}
+
+// Tiles in runs of up to 8 rows of tiles, columns of tiles outside, so that neighbours share panels.
+__device__ inline void place(int t, int tiles_m, int tiles_n, int *tm, int *tn) {
+    constexpr int RUN = 8;
+    const int band = t / (RUN * tiles_n), in = t - band * RUN * tiles_n;
+    const int height = min(RUN, tiles_m - band * RUN);
+    *tm = band * RUN + in % height;
+    *tn = in / height;
+}
+
+// WIDE: fp32 output through bf16 products.
+template <int GROUPING, bool WIDE, class C>
+__device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / C::WN, wn = wave % C::WN;
+    // the tile: rows [row0, row_end) of a, rows col0 .. of b, blocks [kb0, kb0 + nk)
+    int tm, tn, group = 0, row0, row_end = p.m, kb0 = 0, nk = p.nkb;
+    if constexpr (GROUPING == kRows) {
+        const GroupBlock all = find_block<false>(p.offsets, p.groups, p.rows, C::BM, 0);
+        const int total = all.total * p.tiles_n;
+        if ((int)blockIdx.x >= total) return;
+        // a group's tiles one after the other, its rows of tiles inside
+        const int t = xcd_remap(blockIdx.x, total);
+        const GroupBlock g = find_block<false>(p.offsets, p.groups, p.rows, C::BM, t / p.tiles_n);
+        const int first = t / p.tiles_n - g.index;                              // the group's first row of tiles
+        const int begin = edge(p.offsets, g.group, p.rows);
+        row_end = edge(p.offsets, g.group + 1, p.rows);
+        const int height = (row_end - begin + C::BM - 1) / C::BM;
+        place(t - first * p.tiles_n, height, p.tiles_n, &tm, &tn);
+        group = g.group;
+        row0 = begin + tm * C::BM;
+    } else {
+        const int per = p.tiles_m * p.tiles_n;
+        const int t = xcd_remap(blockIdx.x, gridDim.x);
+        group = t / per;
+        place(t - group * per, p.tiles_m, p.tiles_n, &tm, &tn);
+        row0 = tm * C::BM;
+        if constexpr (GROUPING == kReduce) {
+            kb0 = find_block<true>(p.offsets, p.groups, p.rows, kBlock, group).index;
+            const int rows = edge(p.offsets, group + 1, p.rows) - edge(p.offsets, group, p.rows);
+            nk = max(0, min((max(rows, 0) + kBlock - 1) / kBlock, p.nkb - kb0));
+        }
+    }
+    const int col0 = tn * C::BN;
+    const uint8_t *pa = p.a + row0 * p.lda + (int64_t)kb0 * kBlock;
+    const uint8_t *pb = p.b + (GROUPING == kRows ? group * p.b_batch : 0) + col0 * p.ldb + (int64_t)kb0 * kBlock;
+    const uint8_t *psb = p.bs + (GROUPING == kRows ? group * p.bs_batch : 0) + kb0;
+    // rows past the tile's last one are read as that one: their results are not stored
+    const int ra = row_end - row0 - 1, rb = p.n - col0 - 1;
+    const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(pa), (short)0, -1, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(pb), (short)0, -1, 0x00020000);
+    int off_a[C::LOADS_A], off_b[C::LOADS_B];
+#pragma unroll
+    for (int i = 0; i < C::LOADS_A; ++i) {
+        const int r = (wave * C::LOADS_A + i) * 8 + (lane >> 3);
+        off_a[i] = min(r, ra) * (int)p.lda + (((lane & 7) ^ swz(r)) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < C::LOADS_B; ++i) {
+        const int r = (wave * C::LOADS_B + i) * 8 + (lane >> 3);
+        off_b[i] = min(r, rb) * (int)p.ldb + (((lane & 7) ^ swz(r)) << 4);
+    }
+    const auto load_stage = [&](int kb, int buf) {
+        char *base = lds + buf * C::STAGE;
+#pragma unroll
+        for (int i = 0; i < C::LOADS_A; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (NSQ_LDS void *)(base + (wave * C::LOADS_A + i) * 1024), 16, off_a[i],
+                                                     kb * kBlock, 0, 0);
+#pragma unroll
+        for (int i = 0; i < C::LOADS_B; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (NSQ_LDS void *)(base + C::PANEL_A + (wave * C::LOADS_B + i) * 1024),
+                                                     16, off_b[i], kb * kBlock, 0, 0);
+    };
+    // scale rows of this lane's fragments
+    const uint8_t *sa_row[C::NM], *sb_row[C::NN];
+#pragma unroll
+    for (int i = 0; i < C::NM; ++i) {
+        const int r = min((wm * C::NM + i) * 16 + (lane & 15), ra);
+        sa_row[i] = p.as + (int64_t)(row0 + r) * p.nkb + kb0;
+    }
+#pragma unroll
+    for (int j = 0; j < C::NN; ++j) {
+        const int r = col0 + min((wn * C::NN + j) * 16 + (lane & 15), rb);
+        sb_row[j] = psb + (int64_t)(p.b_square ? r / kBlock : r) * p.nkb;
+    }
+    uint32_t sa[C::NM], sb[C::NN];
+    f32x4 acc[C::NN][C::NM];
+#pragma unroll
+    for (int j = 0; j < C::NN; ++j)
+#pragma unroll
+        for (int i = 0; i < C::NM; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int frag = (lane & 15) * kBlock, fsw = swz(lane & 15);
+    const int c0 = ((lane >> 4) ^ fsw) << 4, c1 = ((4 + (lane >> 4)) ^ fsw) << 4;
+    const auto read = [&](const char *panel, int block) {
+        const char *q = panel + block * 16 * kBlock + frag;
+        const i32x4 lo = *reinterpret_cast<const i32x4 *>(q + c0), hi = *reinterpret_cast<const i32x4 *>(q + c1);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    if (nk > 0) load_stage(0, 0);
+    for (int kb = 0; kb < nk; ++kb) {
+        if ((kb & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < C::NM; ++i) sa[i] = scale_word(sa_row[i], kb >> 2, nk);
+#pragma unroll
+            for (int j = 0; j < C::NN; ++j) sb[j] = scale_word(sb_row[j], kb >> 2, nk);
+        }
+        wait_vmcnt<0>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (kb + 1 < nk) load_stage(kb + 1, (kb + 1) & 1);
+        const char *panel_a = lds + (kb & 1) * C::STAGE + wm * C::NM * 16 * kBlock;
+        const char *panel_b = lds + (kb & 1) * C::STAGE + C::PANEL_A + wn * C::NN * 16 * kBlock;
+        // b first: a lane then holds four consecutive columns of one row
+        if constexpr (WIDE) {
+            bf16x8 fb[C::NN][4];
+#pragma unroll
+            for (int j = 0; j < C::NN; ++j) {
+                const i32x8 f = read(panel_b, j);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) fb[j][g] = widen8(f[2 * g], f[2 * g + 1], scale_of(sb[j]));
+            }
+#pragma unroll
+            for (int i = 0; i < C::NM; ++i) {
+                const i32x8 f = read(panel_a, i);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const bf16x8 fa = widen8(f[2 * g], f[2 * g + 1], scale_of(sa[i]));
+#pragma unroll
+                    for (int j = 0; j < C::NN; ++j)
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j][g], fa, acc[j][i], 0, 0, 0);
+                }
+            }
+        } else {
+            i32x8 fb[C::NN];
+#pragma unroll
+            for (int j = 0; j < C::NN; ++j) fb[j] = read(panel_b, j);
+#pragma unroll
+            for (int i = 0; i < C::NM; ++i) {
+                const i32x8 fa = read(panel_a, i);
+#pragma unroll
+                for (int j = 0; j < C::NN; ++j)
+                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa, acc[j][i], 0, 0, 0, (int)sb[j], 0, (int)sa[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < C::NM; ++i) sa[i] >>= 8;
+#pragma unroll
+        for (int j = 0; j < C::NN; ++j) sb[j] >>= 8;
+    }
+    // lane l of block (j, i): row l % 16 of block i, columns 4 (l / 16) .. + 4 of block j
+    char *out = p.out + (GROUPING == kReduce ? group * p.out_batch * (WIDE ? 4 : 2) : 0);
+#pragma unroll
+    for (int i = 0; i < C::NM; ++i) {
+        const int r = (wm * C::NM + i) * 16 + (lane & 15);
+        if (r > ra) continue;
+#pragma unroll
+        for (int j = 0; j < C::NN; ++j) {
+            const int c = col0 + (wn * C::NN + j) * 16 + 4 * (lane >> 4);
+            float v[4] = {acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3]};
+            const int64_t at = (row0 + r) * p.ldo + c;
+            if (c + 4 <= p.n) {
+                if constexpr (WIDE) Elems<float, 4>::store(reinterpret_cast<float *>(out) + at, v);
+                else Elems<__bf16, 4>::store(reinterpret_cast<__bf16 *>(out) + at, v);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (c + k >= p.n) break;
+                    if constexpr (WIDE) reinterpret_cast<float *>(out)[at + k] = v[k];
+                    else reinterpret_cast<__bf16 *>(out)[at + k] = (__bf16)v[k];
+                }
+            }
+        }
+    }
+}
+
+template <int GROUPING, bool WIDE, class C>
+__global__ __launch_bounds__(C::THREADS) void scaled_tile_kernel(MatArgs p) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    scaled_tile<GROUPING, WIDE, C>(p, lds);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+// e4m3 rows: 16-byte aligned, whole blocks.
+ns_status check_bytes(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t batch, int64_t batch_stride) {
+    if (!p) return fail(NS_ERR_INVALID_ARG, "%s is NULL", name);
+    if (misaligned(p, 16)) return fail(NS_ERR_INVALID_ARG, "%s not 16-byte aligned", name);
+    if (ld < cols || ld % 16 || ld > (int64_t(1) << 22))
+        return fail(NS_ERR_INVALID_ARG, "%s: rows %lld apart (a multiple of 16, at least %lld, at most 2^22)", name, (long long)ld,
+                    (long long)cols);
+    if (batch > 1 && (batch_stride < 0 || batch_stride % 16)) return fail(NS_ERR_INVALID_ARG, "%s: batch stride not a multiple of 16", name);
+    if (batch > 1 && too_far(batch, batch_stride)) return fail(NS_ERR_OVERFLOW, "%s: offsets overflow", name);
+    return NS_OK;
+}
+
+template <int GROUPING, class C> ns_status launch_tile(const MatArgs &p, int64_t grid, hipStream_t st) {
+    const dim3 blocks((unsigned)grid), threads(C::THREADS);
+    if (p.out_f32) hipLaunchKernelGGL((scaled_tile_kernel<GROUPING, true, C>), blocks, threads, 2 * C::STAGE, st, p);
+    else hipLaunchKernelGGL((scaled_tile_kernel<GROUPING, false, C>), blocks, threads, 2 * C::STAGE, st, p);
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
+}  // namespace
+}  // namespace nsq
+
+using namespace nsq;
+
+extern "C" ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_dtype dtype, const void *x, int64_t x_ld,
+                                 int64_t x_batch, int32_t block_rows, const int32_t *offsets, int32_t groups, void *q,
+                                 int64_t q_ld, int64_t q_batch, uint8_t *scales, void *qt, int64_t qt_ld, int64_t qt_batch,
+                                 uint8_t *scales_t, void *stream) {
+    const int es = dtype_bytes(dtype);
+    if (!es) return fail(NS_ERR_DTYPE, "dtype %d is not NS_BF16 or NS_F32", dtype);
+    if (batch < 0 || batch > 65535) return fail(NS_ERR_INVALID_ARG, "batch outside [0, 65535]");
+    if (rows < 0 || rows > kMaxRows) return fail(NS_ERR_INVALID_ARG, "rows outside [0, 2^30]");
+    if (cols < 1 || cols > kMaxCols) return fail(NS_ERR_INVALID_ARG, "cols outside [1, 2^22]");
+    if (block_rows != 1 && block_rows != kBlock) return fail(NS_ERR_INVALID_ARG, "block_rows must be 1 or 128");
+    if (block_rows == 1 && batch > 1) return fail(NS_ERR_INVALID_ARG, "a batch needs block_rows = 128");
+    if (!q != !scales || !qt != !scales_t || (!q && !qt))
+        return fail(NS_ERR_INVALID_ARG, "q and scales, or qt and scales_t, or both pairs are required");
+    if (!batch || (!rows && !offsets)) return NS_OK;
+    if (rows && !x) return fail(NS_ERR_INVALID_ARG, "x is NULL");
+    if (misaligned(x, es)) return fail(NS_ERR_INVALID_ARG, "x not aligned to its type");
+    if (x_ld < 0 || (batch > 1 && x_batch < 0)) return fail(NS_ERR_INVALID_ARG, "negative stride");
+    if (too_far(rows, x_ld) || too_far(batch, x_batch) || rows * (double)x_ld + batch * (double)x_batch > 4.6e18 / es)
+        return fail(NS_ERR_OVERFLOW, "x: offsets overflow");
+    const int64_t nb = blocks_of(cols);
+    int64_t nbt = blocks_of(rows);
+    if (offsets) {
+        if (block_rows != 1) return fail(NS_ERR_INVALID_ARG, "offsets need block_rows = 1");
+        if (groups < 1 || groups > kMaxGroups) return fail(NS_ERR_INVALID_ARG, "groups = %d outside [1, %d]", groups, kMaxGroups);
+        if (misaligned(offsets, 4)) return fail(NS_ERR_INVALID_ARG, "offsets not 4-byte aligned");
+        nbt = rows / kBlock + groups;
+    }
+    if (q)
+        if (ns_status s = check_bytes("q", q, rows, nb * kBlock, q_ld, batch, q_batch)) return s;
+    if (qt)
+        if (ns_status s = check_bytes("qt", qt, cols, nbt * kBlock, qt_ld, batch, qt_batch)) return s;
+    QuantArgs a{};
+    a.x = reinterpret_cast<const char *>(x);
+    a.x_ld = x_ld;
+    a.x_batch = x_batch;
+    a.q = reinterpret_cast<uint8_t *>(q);
+    a.q_ld = q_ld;
+    a.q_batch = q_batch;
+    a.s = scales;
+    a.s_batch = blocks_of(rows) * nb;
+    a.qt = reinterpret_cast<uint8_t *>(qt);
+    a.qt_ld = qt_ld;
+    a.qt_batch = qt_batch;
+    a.st = scales_t;
+    a.st_batch = nb * nbt;
+    a.offsets = qt ? offsets : nullptr;
+    a.groups = groups;
+    a.rows = (int)rows;
+    a.cols = (int)cols;
+    a.nb = (int)nb;
+    a.nbt = (int)nbt;
+    hipStream_t st = as_stream(stream);
+    if (block_rows == 1 && !qt) {
+        const int64_t units = rows * nb;
+        if (!units) return NS_OK;
+        // four blocks a group of lanes, one where that would leave CUs idle
+        const bool few = units < 16 * 4 * 1024;
+        const int64_t grid = (units + (few ? 16 : 64) - 1) / (few ? 16 : 64);
+        if (grid > INT32_MAX) return fail(NS_ERR_OVERFLOW, "rows x cols too large");
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, st, a); };
+        if (dtype == NS_BF16) few ? go(quant_rows_kernel<__bf16, 1>) : go(quant_rows_kernel<__bf16, 4>);
+        else few ? go(quant_rows_kernel<float, 1>) : go(quant_rows_kernel<float, 4>);
+    } else {
+        // with groups a row of tiles more, for the rows behind the last one
+        const int64_t down = a.offsets ? nbt + 1 : nbt;
+        if (down > 65535) return fail(NS_ERR_OVERFLOW, "rows too many for qt or square blocks");
+        const dim3 grid((unsigned)nb, (unsigned)down, (unsigned)batch);
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a); };
+        if (dtype == NS_BF16) block_rows == 1 ? go(quant_tile_kernel<__bf16, false>) : go(quant_tile_kernel<__bf16, true>);
+        else block_rows == 1 ? go(quant_tile_kernel<float, false>) : go(quant_tile_kernel<float, true>);
+    }
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
+extern "C" ns_status ns_scaled_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t *bytes) {
+    if (!bytes) return fail(NS_ERR_INVALID_ARG, "bytes is NULL");
+    if (m < 0 || m > kMaxRows || n < 0 || n > kMaxRows) return fail(NS_ERR_INVALID_ARG, "m or n outside [0, 2^30]");
+    if (k < 0 || k % kBlock || k > kMaxCols) return fail(NS_ERR_INVALID_ARG, "k must be a multiple of 128 up to 2^22");
+    if (groups < 0 || groups > kMaxGroups) return fail(NS_ERR_INVALID_ARG, "groups = %d outside [0, %d]", groups, kMaxGroups);
+    *bytes = 0;
+    return NS_OK;
+}
+
+extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, int64_t a_ld, const uint8_t *a_scales,
+                                      const void *b, int64_t b_ld, int64_t b_batch, const uint8_t *b_scales,
+                                      int32_t b_block_rows, const int32_t *offsets, int32_t groups, int32_t reduce,
+                                      int64_t rows, ns_dtype out_dtype, void *out, int64_t out_ld, int64_t out_batch,
+                                      void *workspace, size_t workspace_bytes, void *stream) {
+    const int es = dtype_bytes(out_dtype);
+    if (!es) return fail(NS_ERR_DTYPE, "out_dtype %d is not NS_BF16 or NS_F32", out_dtype);
+    size_t need;
+    if (ns_status s = ns_scaled_matmul_workspace_bytes(m, n, k, groups, &need)) return s;
+    if (b_block_rows != 1 && b_block_rows != kBlock) return fail(NS_ERR_INVALID_ARG, "b_block_rows must be 1 or 128");
+    if (reduce != 0 && reduce != 1) return fail(NS_ERR_INVALID_ARG, "reduce must be 0 or 1");
+    if (!offsets != !groups) return fail(NS_ERR_INVALID_ARG, "offsets and groups go together");
+    if (reduce && !offsets) return fail(NS_ERR_INVALID_ARG, "reduce needs offsets");
+    if (misaligned(offsets, 4)) return fail(NS_ERR_INVALID_ARG, "offsets not 4-byte aligned");
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(NS_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    if (misaligned(workspace, 256)) return fail(NS_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    if (!m || !n) return NS_OK;
+    if (!out || misaligned(out, es)) return fail(NS_ERR_INVALID_ARG, "out is NULL or not aligned to its type");
+    if (out_ld < n || too_far(m, out_ld) || m * (double)out_ld > 1e18 || (reduce && groups > 1 && (out_batch < 0 || too_far(groups, out_batch * es))))
+        return fail(NS_ERR_INVALID_ARG, "out: bad strides");
+    if (k) {
+        if (ns_status s = check_bytes("a", a, m, k, a_ld, 1, 0)) return s;
+        if (ns_status s = check_bytes("b", b, n, k, b_ld, offsets && !reduce ? groups : 1, b_batch)) return s;
+        if (!a_scales || !b_scales) return fail(NS_ERR_INVALID_ARG, "a_scales and b_scales are required");
+    }
+    if (reduce && (rows < 0 || rows / kBlock + groups < 0 || k < (rows / kBlock) * kBlock))
+        return fail(NS_ERR_INVALID_ARG, "rows = %lld do not fit k", (long long)rows);
+    MatArgs p{};
+    p.a = reinterpret_cast<const uint8_t *>(a);
+    p.as = a_scales;
+    p.b = reinterpret_cast<const uint8_t *>(b);
+    p.bs = b_scales;
+    p.out = reinterpret_cast<char *>(out);
+    p.offsets = offsets;
+    p.lda = a_ld;
+    p.ldb = b_ld;
+    p.ldo = out_ld;
+    p.b_batch = b_batch;
+    p.m = (int)m;
+    p.n = (int)n;
+    p.nkb = (int)(k / kBlock);
+    p.bs_batch = (b_block_rows == 1 ? n : blocks_of(n)) * p.nkb;
+    p.out_batch = out_batch;
+    p.groups = groups;
+    p.rows = (int)(reduce ? rows : m);
+    p.b_square = b_block_rows == kBlock;
+    p.out_f32 = out_dtype == NS_F32;
+    hipStream_t st = as_stream(stream);
+    typedef Tile<128, 128, 2, 2> Small;
+    p.tiles_m = (int)((m + Small::BM - 1) / Small::BM);
+    p.tiles_n = (int)((n + Small::BN - 1) / Small::BN);
+    int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
+    if (offsets && !reduce) grid = (m / Small::BM + groups) * p.tiles_n;
+    if (reduce) grid *= groups;
+    if (grid > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
+    if (!offsets) return launch_tile<kDense, Small>(p, grid, st);
+    return reduce ? launch_tile<kReduce, Small>(p, grid, st) : launch_tile<kRows, Small>(p, grid, st);
+}
