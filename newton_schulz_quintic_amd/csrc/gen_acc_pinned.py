@@ -1,4 +1,4 @@
-"""Writes acc_pinned.h and pinned_stage.inc beside this script.
+"""Writes acc_pinned.h, pinned_stage.inc, acc_scaled.h and scaled_stage.inc beside this script.
 
 The 4-wave 256-tile product keeps each wave's 128 x 128 accumulator tile in
 the AGPRs a0..a255, block (i, j) of its 8 x 8 blocks of 16 x 16 in
@@ -8,6 +8,11 @@ register allocator, a tile of this size is moved between registers inside the
 loop). pinned_stage.inc is the unrolled schedule of one K stage (two k-groups of
 32): MFMAs in pairs, with the fragment reads, operand loads and the stage
 barrier spread between the pairs.
+
+acc_scaled.h has the 8-bit products' MFMA for the same registers (one instruction
+for a block's 128 k, with both operands' scales), and scaled_stage.inc their K
+stage: the A fragments pass through four registers sets, the next stage's B
+fragments are read meanwhile.
 
 Run: python3 gen_acc_pinned.py  (the outputs are committed).
 """
@@ -119,9 +124,55 @@ def stage():
     return "\n".join(body) + "\n"
 
 
+def scaled_header():
+    out = ["// Generated by gen_acc_pinned.py: do not edit by hand.",
+           "// The 8-bit products' MFMA on block q of the accumulators of acc_pinned.h: a's and b's",
+           "// scales are the low bytes of sa and sb. Included by scaled.hip inside its namespace.",
+           "#pragma once", "", "namespace pinned {", ""]
+    for q in range(64):
+        r = reg(q)
+        out.append(f"__device__ __forceinline__ void scaled{q}(i32x8 a, i32x8 b, uint32_t sa, uint32_t sb) {{")
+        out.append(f'    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 a[{r}:{r + 3}], %0, %1, a[{r}:{r + 3}], %2, %3 op_sel_hi:[0,0,0]"')
+        out.append(f'                 :: "v"(a), "v"(b), "v"(sa), "v"(sb) : "a{r}", "a{r + 1}", "a{r + 2}", "a{r + 3}");')
+        out.append("}")
+    out += ["", "}  // namespace pinned", ""]
+    return "\n".join(out)
+
+
+def scaled_stage():
+    body = ["// Generated by gen_acc_pinned.py: one K stage of the 8-bit 256-tile product.",
+            "// In scope: FA[4], FB[2][8] fragments (FA[0] .. FA[2] and FB[PAR] hold this stage's),",
+            "// ra(slot, i), rb(slot, j) (read a fragment of this stage's A, of the next stage's B),",
+            "// rna(slot, i) (of the next stage's A), la(n), lb(n) (loads n < 8 of the A and the B panel",
+            "// three stages on; n < 4 of A: the first halves of both wave rows), sa[8], sb(j), PAR."]
+    slots = [[] for _ in range(64)]   # the operations after each MFMA
+    slots[17].append("lds_barrier();     // every wave has the next stage's B")
+    slots[47] += ["wait_vmcnt<16>();  // this wave's loads of the next A panel and the B panel after the next",
+                  "lds_barrier();     // ... and every wave's; this stage's A is read"]
+    for i, k in enumerate((1, 9, 17, 25, 33)):      # as soon as the slot's last fragment has been used
+        slots[k].append(f"ra({(i + 3) & 3}, {i + 3});")
+    for n, k in enumerate((49, 51, 57)):
+        slots[k].append(f"rna({n}, {n});")
+    for n, k in enumerate((1, 3, 3, 5, 5, 7, 7, 9)):
+        slots[k].append(f"rb(PAR ^ 1, {n});")
+    for n, k in enumerate((17, 19, 21, 23, 27, 29, 31, 35)):
+        slots[k].append(f"lb({n});")
+    for n, k in enumerate((49, 51, 53, 55, 57, 59, 61, 63)):
+        slots[k].append(f"la({n});")
+    for q in range(64):
+        i, j = q >> 3, q & 7
+        body.append(f"pinned::scaled{q}(FB[PAR][{j}], FA[{i & 3}], sb({j}), sa[{i}]);")
+        body += slots[q]
+    return "\n".join(body) + "\n"
+
+
 if __name__ == "__main__":
     with open(os.path.join(HERE, "acc_pinned.h"), "w") as f:
         f.write(header())
     with open(os.path.join(HERE, "pinned_stage.inc"), "w") as f:
         f.write(stage())
-    print("wrote acc_pinned.h, pinned_stage.inc")
+    with open(os.path.join(HERE, "acc_scaled.h"), "w") as f:
+        f.write(scaled_header())
+    with open(os.path.join(HERE, "scaled_stage.inc"), "w") as f:
+        f.write(scaled_stage())
+    print("wrote acc_pinned.h, pinned_stage.inc, acc_scaled.h, scaled_stage.inc")

@@ -328,18 +328,6 @@ template <int BM_, int BN_, int WM_, int WN_> struct Tile {
 // lanes of a fragment read (16 rows, one chunk each) hit distinct banks.
 __device__ inline int swz(int r) { return (r >> 1) & 7; }
 
-// Four blocks' scale bytes of one row, from block 4 j. Never reads outside the row.
-__device__ inline uint32_t scale_word(const uint8_t *row, int j, int nkb) {
-    if (nkb >= 4) {
-        const int at = min(4 * j, nkb - 4);
-        typedef uint32_t word_u __attribute__((aligned(1)));
-        return *reinterpret_cast<const word_u *>(row + at) >> (8 * (4 * j - at));
-    }
-    uint32_t w = 0;
-    for (int k = 0; k < nkb; ++k) w |= (uint32_t)row[k] << (8 * k);
-    return w;
-}
-
 __device__ inline float scale_of(uint32_t word) { return __builtin_bit_cast(float, (word & 255) << 23); }
 
 // Eight e4m3 values, bytes of two words, times a power of two, as bf16.
@@ -371,42 +359,79 @@ __device__ inline void place(int t, int tiles_m, int tiles_n, int *tm, int *tn) 
     *tn = in / height;
 }
 
+// A workgroup's tile: rows [row0, row_end) of a (the tile's first row and the end of its
+// group's), rows col0 .. of b, blocks [kb0, kb0 + nk) of the reduction.
+struct Spot {
+    int group, row0, row_end, col0, kb0, nk;
+    bool any;
+};
+template <int GROUPING, int BM, int BN>
+__device__ inline Spot locate(const MatArgs &p) {
+    Spot s = {0, 0, p.m, 0, 0, p.nkb, true};
+    int tm, tn;
+    if constexpr (GROUPING == kRows) {
+        const int total = find_block<false>(p.offsets, p.groups, p.rows, BM, 0).total * p.tiles_n;
+        s.any = (int)blockIdx.x < total;
+        if (!s.any) return s;
+        const int t = xcd_remap(blockIdx.x, total);
+        const GroupBlock g = find_block<false>(p.offsets, p.groups, p.rows, BM, t / p.tiles_n);
+        const int first = t / p.tiles_n - g.index;   // the group's first row of tiles
+        const int begin = edge(p.offsets, g.group, p.rows);
+        s.group = g.group;
+        s.row_end = edge(p.offsets, g.group + 1, p.rows);
+        place(t - first * p.tiles_n, (s.row_end - begin + BM - 1) / BM, p.tiles_n, &tm, &tn);
+        s.row0 = begin + tm * BM;
+    } else {
+        const int per = p.tiles_m * p.tiles_n;
+        const int t = xcd_remap(blockIdx.x, gridDim.x);
+        s.group = t / per;
+        place(t - s.group * per, p.tiles_m, p.tiles_n, &tm, &tn);
+        s.row0 = tm * BM;
+        if constexpr (GROUPING == kReduce) {
+            s.kb0 = find_block<true>(p.offsets, p.groups, p.rows, kBlock, s.group).index;
+            const int rows = max(edge(p.offsets, s.group + 1, p.rows) - edge(p.offsets, s.group, p.rows), 0);
+            s.nk = max(0, min((rows + kBlock - 1) / kBlock, p.nkb - s.kb0));
+        }
+    }
+    s.col0 = tn * BN;
+    return s;
+}
+
+// Scale words: the bytes of blocks 4 j .. 4 j + 3 of one row (nk of them in all). The
+// last word of a row is loaded from four bytes before the row's end, never past it,
+// and shifted by `tail_bits` when it is used. Rows at `base` + row[i].
+__device__ inline int word_at(int j, int nk) { return min(4 * j, nk - 4); }
+__device__ inline int tail_bits(int j, int nk) { return min(8 * (4 * j - word_at(j, nk)), 31); }
+template <int N>
+__device__ inline void load_words(const uint8_t *base, const int (&row)[N], int j, int nk, uint32_t (&w)[N]) {
+    typedef uint32_t word_u __attribute__((aligned(1)));
+    const int at = word_at(j, nk);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const word_u *>(base + (uint32_t)(row[i] + at));
+}
+// The first words, also of rows of fewer than four blocks.
+template <int N>
+__device__ inline void first_words(const uint8_t *base, const int (&row)[N], int nk, uint32_t (&w)[N]) {
+    if (nk >= 4) return load_words(base, row, 0, nk, w);
+    uint32_t b[3][N];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) b[k][i] = base[(uint32_t)(row[i] + min(k, nk - 1))];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = b[0][i] | b[1][i] << 8 | b[2][i] << 16;
+}
+
 // WIDE: fp32 output through bf16 products.
 template <int GROUPING, bool WIDE, class C>
 __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / C::WN, wn = wave % C::WN;
-    // the tile: rows [row0, row_end) of a, rows col0 .. of b, blocks [kb0, kb0 + nk)
-    int tm, tn, group = 0, row0, row_end = p.m, kb0 = 0, nk = p.nkb;
-    if constexpr (GROUPING == kRows) {
-        const GroupBlock all = find_block<false>(p.offsets, p.groups, p.rows, C::BM, 0);
-        const int total = all.total * p.tiles_n;
-        if ((int)blockIdx.x >= total) return;
-        // a group's tiles one after the other, its rows of tiles inside
-        const int t = xcd_remap(blockIdx.x, total);
-        const GroupBlock g = find_block<false>(p.offsets, p.groups, p.rows, C::BM, t / p.tiles_n);
-        const int first = t / p.tiles_n - g.index;                              // the group's first row of tiles
-        const int begin = edge(p.offsets, g.group, p.rows);
-        row_end = edge(p.offsets, g.group + 1, p.rows);
-        const int height = (row_end - begin + C::BM - 1) / C::BM;
-        place(t - first * p.tiles_n, height, p.tiles_n, &tm, &tn);
-        group = g.group;
-        row0 = begin + tm * C::BM;
-    } else {
-        const int per = p.tiles_m * p.tiles_n;
-        const int t = xcd_remap(blockIdx.x, gridDim.x);
-        group = t / per;
-        place(t - group * per, p.tiles_m, p.tiles_n, &tm, &tn);
-        row0 = tm * C::BM;
-        if constexpr (GROUPING == kReduce) {
-            kb0 = find_block<true>(p.offsets, p.groups, p.rows, kBlock, group).index;
-            const int rows = edge(p.offsets, group + 1, p.rows) - edge(p.offsets, group, p.rows);
-            nk = max(0, min((max(rows, 0) + kBlock - 1) / kBlock, p.nkb - kb0));
-        }
-    }
-    const int col0 = tn * C::BN;
+    const Spot at = locate<GROUPING, C::BM, C::BN>(p);
+    if (!at.any) return;
+    const int row0 = at.row0, row_end = at.row_end, col0 = at.col0, kb0 = at.kb0, nk = at.nk, group = at.group;
     const uint8_t *pa = p.a + row0 * p.lda + (int64_t)kb0 * kBlock;
     const uint8_t *pb = p.b + (GROUPING == kRows ? group * p.b_batch : 0) + col0 * p.ldb + (int64_t)kb0 * kBlock;
-    const uint8_t *psb = p.bs + (GROUPING == kRows ? group * p.bs_batch : 0) + kb0;
+    const uint8_t *psb = p.bs + (GROUPING == kRows ? group * p.bs_batch : 0) + (int64_t)(p.b_square ? col0 / kBlock : col0) * p.nkb + kb0;
     // rows past the tile's last one are read as that one: their results are not stored
     const int ra = row_end - row0 - 1, rb = p.n - col0 - 1;
     const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(pa), (short)0, -1, 0x00020000);
@@ -434,18 +459,17 @@ __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
                                                      16, off_b[i], kb * kBlock, 0, 0);
     };
     // scale rows of this lane's fragments
-    const uint8_t *sa_row[C::NM], *sb_row[C::NN];
+    static_assert(C::BN % kBlock == 0, "whole square blocks");
+    const uint8_t *psa = p.as + (int64_t)row0 * p.nkb + kb0;
+    int sa_row[C::NM], sb_row[C::NN];
 #pragma unroll
-    for (int i = 0; i < C::NM; ++i) {
-        const int r = min((wm * C::NM + i) * 16 + (lane & 15), ra);
-        sa_row[i] = p.as + (int64_t)(row0 + r) * p.nkb + kb0;
-    }
+    for (int i = 0; i < C::NM; ++i) sa_row[i] = min((wm * C::NM + i) * 16 + (lane & 15), ra) * p.nkb;
 #pragma unroll
     for (int j = 0; j < C::NN; ++j) {
-        const int r = col0 + min((wn * C::NN + j) * 16 + (lane & 15), rb);
-        sb_row[j] = psb + (int64_t)(p.b_square ? r / kBlock : r) * p.nkb;
+        const int r = min((wn * C::NN + j) * 16 + (lane & 15), rb);
+        sb_row[j] = (p.b_square ? r / kBlock : r) * p.nkb;
     }
-    uint32_t sa[C::NM], sb[C::NN];
+    uint32_t sa[C::NM], sb[C::NN], next_a[C::NM], next_b[C::NN];
     f32x4 acc[C::NN][C::NM];
 #pragma unroll
     for (int j = 0; j < C::NN; ++j)
@@ -458,13 +482,21 @@ __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
         const i32x4 lo = *reinterpret_cast<const i32x4 *>(q + c0), hi = *reinterpret_cast<const i32x4 *>(q + c1);
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
-    if (nk > 0) load_stage(0, 0);
+    if (nk > 0) {
+        first_words(psa, sa_row, nk, next_a);
+        first_words(psb, sb_row, nk, next_b);
+        load_stage(0, 0);
+    }
     for (int kb = 0; kb < nk; ++kb) {
-        if ((kb & 3) == 0) {
+        if ((kb & 3) == 0) {   // four blocks' scales at a time, loaded four blocks ahead
 #pragma unroll
-            for (int i = 0; i < C::NM; ++i) sa[i] = scale_word(sa_row[i], kb >> 2, nk);
+            for (int i = 0; i < C::NM; ++i) sa[i] = next_a[i] >> (kb ? tail_bits(kb >> 2, nk) : 0);
 #pragma unroll
-            for (int j = 0; j < C::NN; ++j) sb[j] = scale_word(sb_row[j], kb >> 2, nk);
+            for (int j = 0; j < C::NN; ++j) sb[j] = next_b[j] >> (kb ? tail_bits(kb >> 2, nk) : 0);
+            if (kb + 4 < nk) {
+                load_words(psa, sa_row, (kb >> 2) + 1, nk, next_a);
+                load_words(psb, sb_row, (kb >> 2) + 1, nk, next_b);
+            }
         }
         wait_vmcnt<0>();
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -538,6 +570,201 @@ template <int GROUPING, bool WIDE, class C>
 __global__ __launch_bounds__(C::THREADS) void scaled_tile_kernel(MatArgs p) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     scaled_tile<GROUPING, WIDE, C>(p, lds);
+}
+
+// --- 256 x 256 tiles on four waves, accumulators in fixed registers -------------
+// For bf16 outputs of calls with enough tiles to fill the GPU. Four waves of 128 x
+// 128, one a SIMD, hold their 8 x 8 blocks of 16 x 16 in the AGPRs a0..a255 (the
+// register allocator moves a tile of that size about inside the loop), and every
+// MFMA is an inline-asm statement on its block's registers (acc_scaled.h). A block
+// of 128 k is one stage, 32 KB a panel. The next stage's B fragments (64 registers)
+// are read at the start of a stage, A fragments pass through four register sets as
+// they are used. LDS holds three A panels and two B panels; with a barrier once the
+// next B is read and one once this A is, panels three stages on are loaded as soon
+// as their place is free, and have two (A) and 1.5 (B) stages to land
+// (scaled_stage.inc). Stages past the last one are loaded and read as the last one
+// and not used, so that the loop has one form.
+#include "acc_pinned.h"
+#include "acc_scaled.h"
+
+constexpr int kQuadThreads = 256, kQuadTile = 256;
+constexpr int kQuadPanel = kQuadTile * kBlock;
+constexpr int kQuadLds = 5 * kQuadPanel;
+constexpr int kQuadPitch = kQuadTile * 2 + 16;   // of the output tile in LDS: rows on different banks
+
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <int GROUPING, bool SQUARE>
+__device__ __forceinline__ void scaled_quad(const MatArgs &__restrict__ p, char *lds) {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+    const Spot at = locate<GROUPING, kQuadTile, kQuadTile>(p);
+    if (!at.any) return;
+    const int ra_last = at.row_end - at.row0 - 1, rb_last = p.n - at.col0 - 1, nk = at.nk;
+    const uint8_t *pa = p.a + at.row0 * p.lda + (int64_t)at.kb0 * kBlock;
+    const uint8_t *pb = p.b + (GROUPING == kRows ? at.group * p.b_batch : 0) + at.col0 * p.ldb + (int64_t)at.kb0 * kBlock;
+    // a wave's 128 columns have one square block's scales, or each its own
+    constexpr int NSB = SQUARE ? 1 : 8;
+    const uint8_t *psa = p.as + (int64_t)at.row0 * p.nkb + at.kb0;
+    const uint8_t *psb = p.bs + (GROUPING == kRows ? at.group * p.bs_batch : 0) +
+                         (int64_t)(SQUARE ? at.col0 / kBlock : at.col0) * p.nkb + at.kb0;
+    const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(pa), (short)0, -1, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(pb), (short)0, -1, 0x00020000);
+    // Load n of a panel brings 8 rows: n < 4 the first halves of the two wave rows (rows 0 .. 63 and 128 .. 191), n >= 4 the others.
+    const auto load_row = [&](int n) { return (wave >> 1) * 128 + (n >> 2) * 64 + ((wave & 1) * 4 + (n & 3)) * 8; };
+    int off_a[8], off_b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = load_row(i) + (lane >> 3), chunk = ((lane & 7) ^ swz(r)) << 4;
+        off_a[i] = min(r, ra_last) * (int)p.lda + chunk;
+        off_b[i] = min(r, rb_last) * (int)p.ldb + chunk;
+    }
+    // this lane's rows in a's and b's scales
+    struct Places {
+        int a[8], b[NSB];
+    };
+    const auto places = [&]() {
+        Places w;
+        int l = lane & 15;
+        asm volatile("" : "+v"(l));   // found again for each use: kept, they would take 16 registers
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w.a[i] = min(wm * 128 + i * 16 + l, ra_last) * p.nkb;
+#pragma unroll
+        for (int i = 0; i < NSB; ++i) w.b[i] = (SQUARE ? min(wn, rb_last / kBlock) : min(wn * 128 + i * 16 + l, rb_last)) * p.nkb;
+        return w;
+    };
+    char *const panel_b = lds + 3 * kQuadPanel;
+    const auto load_a = [&](int n, int kb, int ring) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (NSQ_LDS void *)(lds + ring * kQuadPanel + load_row(n) * kBlock), 16, off_a[n],
+                                                 uniform(min(kb, nk - 1) * kBlock), 0, 0);
+    };
+    const auto load_b = [&](int n, int kb) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (NSQ_LDS void *)(panel_b + (kb & 1) * kQuadPanel + load_row(n) * kBlock), 16,
+                                                 off_b[n], uniform(min(kb, nk - 1) * kBlock), 0, 0);
+    };
+    const int fsw = swz(lane & 15), c0 = ((lane >> 4) ^ fsw) << 4, c1 = ((4 + (lane >> 4)) ^ fsw) << 4;
+    const int frag_a = (wm * 128 + (lane & 15)) * kBlock, frag_b = (wn * 128 + (lane & 15)) * kBlock;
+    const auto read = [&](const char *row, int block) {
+        const i32x4 lo = *reinterpret_cast<const i32x4 *>(row + block * 16 * kBlock + c0);
+        const i32x4 hi = *reinterpret_cast<const i32x4 *>(row + block * 16 * kBlock + c1);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    if (nk > 0) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) load_a(n, 0, 0), load_b(n, 0);
+        uint32_t sa[8], sb_word[NSB], next_a[8], next_b[NSB];
+        {
+            const Places w = places();
+            first_words(psa, w.a, nk, sa);
+            first_words(psb, w.b, nk, sb_word);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) next_a[i] = sa[i];
+#pragma unroll
+            for (int j = 0; j < NSB; ++j) next_b[j] = sb_word[j];
+            if (nk > 4) {
+                load_words(psa, w.a, 1, nk, next_a);
+                load_words(psb, w.b, 1, nk, next_b);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) load_b(n, 1);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) load_a(n, 1, 1);
+        pinned::zero();
+        wait_vmcnt<8>();   // all but A's stage 1
+        lds_barrier();
+        i32x8 FA[4], FB[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) FB[0][j] = read(panel_b + frag_b, j);
+        FA[0] = read(lds + frag_a, 0);
+        FA[1] = read(lds + frag_a, 1);
+        FA[2] = read(lds + frag_a, 2);
+        lds_barrier();   // every wave has stage 0's B fragments
+#pragma unroll
+        for (int n = 0; n < 8; ++n) load_b(n, 2);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) load_a(n, 2, 2);
+        int ring = 0;   // where stage kb's A panel is, and stage kb + 3's will be
+        const auto stage = [&](auto par, int kb) {
+            constexpr int PAR = decltype(par)::value;
+            const int then = ring == 2 ? 0 : ring + 1;
+            const char *now_a = lds + ring * kQuadPanel + frag_a, *then_a = lds + then * kQuadPanel + frag_a;
+            const char *next_panel_b = panel_b + (PAR ^ 1) * kQuadPanel + frag_b;
+            const auto sb = [&](int j) { return sb_word[SQUARE ? 0 : j]; };
+            const auto ra = [&](int slot, int i) { FA[slot] = read(now_a, i); };
+            const auto rna = [&](int slot, int i) { FA[slot] = read(then_a, i); };
+            const auto rb = [&](int slot, int j) { FB[slot][j] = read(next_panel_b, j); };
+            const auto la = [&](int n) { load_a(n, kb + 3, ring); };
+            const auto lb = [&](int n) { load_b(n, kb + 3); };
+#include "scaled_stage.inc"
+            if ((kb & 3) == 3) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sa[i] = next_a[i] >> tail_bits((kb + 1) >> 2, nk);
+#pragma unroll
+                for (int j = 0; j < NSB; ++j) sb_word[j] = next_b[j] >> tail_bits((kb + 1) >> 2, nk);
+                if (kb + 5 < nk) {
+                    const Places w = places();
+                    load_words(psa, w.a, (kb + 5) >> 2, nk, next_a);
+                    load_words(psb, w.b, (kb + 5) >> 2, nk, next_b);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sa[i] >>= 8;
+#pragma unroll
+                for (int j = 0; j < NSB; ++j) sb_word[j] >>= 8;
+            }
+            ring = then;
+        };
+        int kb = 0;
+        for (; kb + 1 < nk; kb += 2) {
+            stage(std::integral_constant<int, 0>{}, kb);
+            stage(std::integral_constant<int, 1>{}, kb + 1);
+        }
+        if (kb < nk) stage(std::integral_constant<int, 0>{}, kb);
+        wait_vmcnt<0>();   // loads past the last stage
+        pinned::drain();
+    } else {
+        pinned::zero();
+    }
+    lds_barrier();
+    // Block q = 8 i + j: lane l has row l % 16 of row block i, columns 4 (l / 16) .. + 4 of column block j. The tile
+    // goes through LDS and leaves in whole rows.
+    typedef uint16_t h4 __attribute__((ext_vector_type(4)));
+    pinned::each_block([&](auto qc, f32x4 v) {
+        constexpr int i = decltype(qc)::value >> 3, j = decltype(qc)::value & 7;
+        h4 h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = __builtin_bit_cast(uint16_t, (__bf16)v[k]);
+        *reinterpret_cast<h4 *>(lds + (wm * 128 + i * 16 + (lane & 15)) * kQuadPitch + (wn * 128 + j * 16 + 4 * (lane >> 4)) * 2) = h;
+    });
+    lds_barrier();
+    __bf16 *out = reinterpret_cast<__bf16 *>(p.out) + (GROUPING == kReduce ? at.group * p.out_batch : 0);
+    const int c = (threadIdx.x & 31) * 8, rows = min(ra_last + 1, kQuadTile);
+    typedef Elems<__bf16, 8> Out;
+    __bf16 *to = out + (int64_t)at.row0 * p.ldo + at.col0 + c;
+    if (rows == kQuadTile && at.col0 + kQuadTile <= p.n) {
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+            const int r = i * 8 + (threadIdx.x >> 5);
+            *reinterpret_cast<Out::raw_u *>(to + r * p.ldo) = *reinterpret_cast<const Out::raw *>(lds + r * kQuadPitch + c * 2);
+        }
+        return;
+    }
+    for (int r = threadIdx.x >> 5; r < rows; r += 8) {
+        const Out::raw v = *reinterpret_cast<const Out::raw *>(lds + r * kQuadPitch + c * 2);
+        if (at.col0 + c + 8 <= p.n) {
+            *reinterpret_cast<Out::raw_u *>(to + r * p.ldo) = v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (at.col0 + c + k < p.n) to[r * p.ldo + k] = __builtin_bit_cast(__bf16, (uint16_t)v[k]);
+        }
+    }
+}
+
+template <int GROUPING, bool SQUARE>
+__global__ __launch_bounds__(kQuadThreads, 1) void scaled_quad_kernel(MatArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[kQuadLds];
+    scaled_quad<GROUPING, SQUARE>(p, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -704,6 +931,21 @@ extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const voi
     p.b_square = b_block_rows == kBlock;
     p.out_f32 = out_dtype == NS_F32;
     hipStream_t st = as_stream(stream);
+    if (!p.out_f32 && k && !(reduce && p.b_square)) {
+        p.tiles_m = (int)((m + kQuadTile - 1) / kQuadTile);
+        p.tiles_n = (int)((n + kQuadTile - 1) / kQuadTile);
+        const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * (reduce ? groups : 1);
+        if (tiles >= 192) {
+            const int64_t quads = offsets && !reduce ? (m / kQuadTile + groups) * p.tiles_n : tiles;
+            if (quads > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
+            auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)quads), dim3(kQuadThreads), 0, st, p); };
+            if (!offsets) p.b_square ? go(scaled_quad_kernel<kDense, true>) : go(scaled_quad_kernel<kDense, false>);
+            else if (!reduce) p.b_square ? go(scaled_quad_kernel<kRows, true>) : go(scaled_quad_kernel<kRows, false>);
+            else go(scaled_quad_kernel<kReduce, false>);
+            NSQ_HIP(hipGetLastError());
+            return NS_OK;
+        }
+    }
     typedef Tile<128, 128, 2, 2> Small;
     p.tiles_m = (int)((m + Small::BM - 1) / Small::BM);
     p.tiles_n = (int)((n + Small::BN - 1) / Small::BN);
