@@ -101,91 +101,202 @@ struct QuantArgs {
     int nb, nbt;          // blocks of a row of q, of qt
 };
 
-// Magnitudes of the finite values; the others count as 0 and become e4m3's NaN.
-__device__ inline float size_of(float x) {
-    const float m = fabsf(x);
-    return m <= 3.402823466e38f ? m : 0.f;
-}
-// The exponent's byte for a block's largest magnitude, and 1 / scale.
+// The exponent's byte for a block's largest magnitude, and the scale itself.
 __device__ inline int scale_byte(float largest) {
     const uint32_t b = __builtin_bit_cast(uint32_t, largest);
     const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFF) > 0x600000);   // 448 = 1.75 x 2^8
     return largest > 0.f ? max(e, -126) + 127 : 127;
 }
-__device__ inline float inverse_scale(int byte) { return __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23); }
+__device__ inline float scale_of(uint32_t byte) { return __builtin_bit_cast(float, (byte & 255) << 23); }
 
-// Four values as e4m3, rounded to nearest even.
-__device__ inline uint32_t pack4(float a, float b, float c, float d) {
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
-}
-// A value over its scale; what is not finite as NaN.
-__device__ inline float scaled(float x, float inv) { return fabsf(x) <= 3.402823466e38f ? x * inv : __builtin_nanf(""); }
-
-// Eight elements of a row from column c, zeros behind the last column.
-template <typename T>
-__device__ inline void load8(const T *row, int c, int cols, float (&v)[8]) {
-    if (c + 8 <= cols) {
-        if constexpr (sizeof(T) == 2) {
-            Elems<T, 8>::widen(Elems<T, 8>::load(row + c), v);
+// Eight consecutive elements of a row. Magnitudes are taken of the finite ones: where
+// any is not (a wave finds out at once), `strange` forms leave those out and turn
+// infinities into NaN, which e4m3 has. Conversion divides by the scale and rounds to
+// nearest even, two values an instruction.
+template <typename T> struct Eight;
+template <> struct Eight<__bf16> {
+    uint32_t p[4];   // pairs
+    __device__ inline void load(const __bf16 *row, int c, int cols) {
+        if (c + 8 <= cols) {
+            typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+            const u4 v = __builtin_bit_cast(u4, load_vec(row + c));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = v[k];
         } else {
-            float lo[4], hi[4];
-            Elems<T, 4>::widen(Elems<T, 4>::load(row + c), lo);
-            Elems<T, 4>::widen(Elems<T, 4>::load(row + c + 4), hi);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint16_t *q = reinterpret_cast<const uint16_t *>(row);
+                const uint32_t lo = c + 2 * k < cols ? q[c + 2 * k] : 0, hi = c + 2 * k + 1 < cols ? q[c + 2 * k + 1] : 0;
+                p[k] = lo | hi << 16;
+            }
+        }
+    }
+    __device__ inline void clear() { p[0] = p[1] = p[2] = p[3] = 0; }
+    typedef uint16_t pair __attribute__((ext_vector_type(2)));
+    // the pair's magnitudes as 16-bit integers, which order as the values do
+    __device__ inline pair size(int k, bool strange) const {
+        pair m = __builtin_bit_cast(pair, p[k] & 0x7FFF7FFFu);
+        if (strange) m = pair{(uint16_t)(m.x >= 0x7F80 ? 0 : m.x), (uint16_t)(m.y >= 0x7F80 ? 0 : m.y)};
+        return m;
+    }
+    __device__ inline bool odd() const {
+        const pair m = __builtin_elementwise_max(__builtin_elementwise_max(size(0, false), size(1, false)),
+                                                 __builtin_elementwise_max(size(2, false), size(3, false)));
+        return max(m.x, m.y) >= 0x7F80;
+    }
+    __device__ inline void mend() {   // infinities to NaN
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if ((p[k] & 0x7FFFu) == 0x7F80u) p[k] |= 0x7Fu;
+            if ((p[k] & 0x7FFF0000u) == 0x7F800000u) p[k] |= 0x7F0000u;
+        }
+    }
+    __device__ inline float largest(bool strange) const {
+        const pair m = __builtin_elementwise_max(__builtin_elementwise_max(size(0, strange), size(1, strange)),
+                                                 __builtin_elementwise_max(size(2, strange), size(3, strange)));
+        return __builtin_bit_cast(float, (uint32_t)max(m.x, m.y) << 16);
+    }
+    static __device__ inline uint32_t four(uint32_t a, uint32_t b, float scale) {
+        typedef short s2 __attribute__((ext_vector_type(2)));
+        s2 v = {0, 0};
+        v = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v, __builtin_bit_cast(bf16x2, a), scale, false);
+        v = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v, __builtin_bit_cast(bf16x2, b), scale, true);
+        return __builtin_bit_cast(uint32_t, v);
+    }
+    __device__ inline uint2 bytes(float scale) const { return {four(p[0], p[1], scale), four(p[2], p[3], scale)}; }
+    // largest magnitudes of the columns of eight rows, and column k's bytes
+    static __device__ inline void columns(const Eight (&v)[8], bool strange, float (&m)[8]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            pair c = v[0].size(k, strange);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) c = __builtin_elementwise_max(c, v[i].size(k, strange));
+            m[2 * k] = __builtin_bit_cast(float, (uint32_t)c.x << 16);
+            m[2 * k + 1] = __builtin_bit_cast(float, (uint32_t)c.y << 16);
+        }
+    }
+    static __device__ inline uint2 column(const Eight (&v)[8], int k, float scale) {
+        uint32_t two[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            two[i] = __builtin_amdgcn_perm(v[2 * i + 1].p[k / 2], v[2 * i].p[k / 2], k & 1 ? 0x07060302 : 0x05040100);
+        return {four(two[0], two[1], scale), four(two[2], two[3], scale)};
+    }
+};
+template <> struct Eight<float> {
+    float v[8];
+    __device__ inline void load(const float *row, int c, int cols) {
+        if (c + 8 <= cols) {
+            const auto lo = load_vec(row + c), hi = load_vec(row + c + 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? (float)row[c + k] : 0.f;
+            for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? row[c + k] : 0.f;
+        }
     }
-}
+    __device__ inline void clear() {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    }
+    __device__ inline float size(int k, bool strange) const {
+        const float m = fabsf(v[k]);
+        return !strange || m <= 3.402823466e38f ? m : 0.f;
+    }
+    __device__ inline bool odd() const {
+        float m = 0.f;   // 0 x (infinity or NaN) is NaN
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaf(0.f, v[k], m);
+        return m != m;
+    }
+    __device__ inline void mend() {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (!(fabsf(v[k]) <= 3.402823466e38f)) v[k] = __builtin_nanf("");
+    }
+    __device__ inline float largest(bool strange) const {
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, size(k, strange));
+        return m;
+    }
+    static __device__ inline uint32_t four(float a, float b, float c, float d, float scale) {
+        typedef short s2 __attribute__((ext_vector_type(2)));
+        s2 r = {0, 0};
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
+        return __builtin_bit_cast(uint32_t, r);
+    }
+    __device__ inline uint2 bytes(float scale) const {
+        return {four(v[0], v[1], v[2], v[3], scale), four(v[4], v[5], v[6], v[7], scale)};
+    }
+    static __device__ inline void columns(const Eight (&v)[8], bool strange, float (&m)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            m[k] = v[0].size(k, strange);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m[k] = fmaxf(m[k], v[i].size(k, strange));
+        }
+    }
+    static __device__ inline uint2 column(const Eight (&v)[8], int k, float scale) {
+        return {four(v[0].v[k], v[1].v[k], v[2].v[k], v[3].v[k], scale), four(v[4].v[k], v[5].v[k], v[6].v[k], v[7].v[k], scale)};
+    }
+};
 
 __device__ inline float max16(float v) {   // over 16 neighbouring lanes
     return lanes_join<0, 4>(v, [](float a, float b) { return fmaxf(a, b); });
 }
+__device__ inline float max_rows(float v) {   // over the wave's four rows of 16 lanes
+    uint32_t x = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = max(a[0], a[1]);   // magnitudes order as their bits
+    const auto b = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return __builtin_bit_cast(float, max(b[0], b[1]));
+}
 
-// Rows only: 16 lanes take a block of 128 values, four blocks at a time.
+// Rows only: 16 lanes take a block of 128 values, AT_ONCE blocks at a time.
 template <typename T, int AT_ONCE>
 __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
     const int64_t units = (int64_t)a.rows * a.nb;
     const int lane = threadIdx.x & 15;
     const int64_t first = (int64_t)blockIdx.x * 16 * AT_ONCE + (threadIdx.x >> 4);
-    float v[AT_ONCE][8];
+    Eight<T> v[AT_ONCE];
     int64_t row[AT_ONCE];
     int kb[AT_ONCE];
+    bool odd = false;
 #pragma unroll
     for (int n = 0; n < AT_ONCE; ++n) {
         const int64_t u = min(first + 16 * n, units - 1);
-        row[n] = u / a.nb;
+        row[n] = units >> 32 ? u / a.nb : (uint32_t)u / (uint32_t)a.nb;
         kb[n] = (int)(u - row[n] * a.nb);
-        load8<T>(reinterpret_cast<const T *>(a.x) + row[n] * a.x_ld, kb[n] * kBlock + lane * 8, a.cols, v[n]);
+        v[n].load(reinterpret_cast<const T *>(a.x) + row[n] * a.x_ld, kb[n] * kBlock + lane * 8, a.cols);
+    }
+#pragma unroll
+    for (int n = 0; n < AT_ONCE; ++n) odd |= v[n].odd();
+    const bool strange = __any(odd);
+    if (strange) {
+#pragma unroll
+        for (int n = 0; n < AT_ONCE; ++n) v[n].mend();
     }
 #pragma unroll
     for (int n = 0; n < AT_ONCE; ++n) {
-        float m = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(v[n][k]));
-        const int byte = scale_byte(max16(m));
-        const float inv = inverse_scale(byte);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[n][k] = scaled(v[n][k], inv);
+        const int byte = scale_byte(max16(v[n].largest(strange)));
         if (first + 16 * n >= units) return;
-        uint2 out = {pack4(v[n][0], v[n][1], v[n][2], v[n][3]), pack4(v[n][4], v[n][5], v[n][6], v[n][7])};
-        *reinterpret_cast<uint2 *>(a.q + row[n] * a.q_ld + kb[n] * kBlock + lane * 8) = out;
+        *reinterpret_cast<uint2 *>(a.q + row[n] * a.q_ld + kb[n] * kBlock + lane * 8) = v[n].bytes(scale_of(byte));
         if (lane == 0) a.s[row[n] * a.nb + kb[n]] = (uint8_t)byte;
     }
 }
 
 // A tile of 128 x 128: a thread holds 8 x 8 values of it. SQUARE: one scale for
 // the tile, for q and for qt; else one for each row (q) and one for each column (qt).
-constexpr int kTurnPitch = kBlock + 16;
+// The transpose goes through LDS, eight bytes (of a column) at a time: unit u of
+// column c at u ^ (c / 8 & 14), which spreads a wave's writes over the banks.
 template <typename T, bool SQUARE>
 __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
-    __shared__ float part[16][kBlock];
-    __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock * kTurnPitch];
+    __shared__ __attribute__((aligned(16))) float part[4][kBlock];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock * kBlock];
     const int cb = blockIdx.x;
-    const int lane = threadIdx.x & 15, down = threadIdx.x >> 4;
+    const int lane = threadIdx.x & 15, down = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     // rows [r0, end) go to columns t0 and on of qt
     int r0 = blockIdx.y * kBlock, end = min(r0 + kBlock, a.rows), t0 = r0;
     bool turn = a.qt != nullptr;
@@ -204,33 +315,31 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
     }
     const T *x = reinterpret_cast<const T *>(a.x) + blockIdx.z * a.x_batch;
     const int c0 = cb * kBlock + lane * 8;
-    float v[8][8];
+    Eight<T> v[8];
+    bool odd = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + down * 8 + i;
-        if (r < end) {
-            load8<T>(x + (int64_t)r * a.x_ld, c0, a.cols, v[i]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
-        }
+        if (r < end) v[i].load(x + (int64_t)r * a.x_ld, c0, a.cols);
+        else v[i].clear();
     }
-    int byte = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) odd |= v[i].odd();
+    const bool strange = __any(odd);
+    if (strange) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i].mend();
+    }
+    float square = 1.f;
     if constexpr (SQUARE) {
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(v[i][k]));
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i].largest(strange));
         m = wave_max(m);
-        if ((threadIdx.x & 63) == 0) part[0][threadIdx.x >> 6] = m;
+        if ((threadIdx.x & 63) == 0) part[0][wave] = m;
         __syncthreads();
-        byte = scale_byte(fmaxf(fmaxf(part[0][0], part[0][1]), fmaxf(part[0][2], part[0][3])));
-        const float inv = inverse_scale(byte);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = scaled(v[i][k], inv);
+        const int byte = scale_byte(fmaxf(fmaxf(part[0][0], part[0][1]), fmaxf(part[0][2], part[0][3])));
+        square = scale_of(byte);
         if (threadIdx.x == 0) {
             if (a.s) a.s[blockIdx.z * a.s_batch + (int64_t)blockIdx.y * a.nb + cb] = (uint8_t)byte;
             if (a.st) a.st[blockIdx.z * a.st_batch + (int64_t)cb * a.nbt + blockIdx.y] = (uint8_t)byte;
@@ -240,60 +349,47 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = r0 + down * 8 + i;
-            float inv = 1.f;
+            float scale = square;
             if constexpr (!SQUARE) {
-                float m = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(v[i][k]));
-                const int b = scale_byte(max16(m));
-                inv = inverse_scale(b);
+                const int b = scale_byte(max16(v[i].largest(strange)));
+                scale = scale_of(b);
                 if (lane == 0 && r < end) a.s[(int64_t)r * a.nb + cb] = (uint8_t)b;
             }
-            if (r >= end) continue;
-            float u[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = SQUARE ? v[i][k] : scaled(v[i][k], inv);
-            uint2 out = {pack4(u[0], u[1], u[2], u[3]), pack4(u[4], u[5], u[6], u[7])};
-            *reinterpret_cast<uint2 *>(a.q + blockIdx.z * a.q_batch + r * a.q_ld + c0) = out;
+            if (r < end) *reinterpret_cast<uint2 *>(a.q + blockIdx.z * a.q_batch + r * a.q_ld + c0) = v[i].bytes(scale);
         }
     }
     if (!turn) return;
-    float inv[8];
-    if constexpr (!SQUARE) {
+    float scale[8];
+    if constexpr (SQUARE) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float m = 0.f;
+        for (int k = 0; k < 8; ++k) scale[k] = square;
+    } else {
+        float m[8];
+        Eight<T>::columns(v, strange, m);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, size_of(v[i][k]));
-            part[down][lane * 8 + k] = m;
+        for (int k = 0; k < 8; ++k) m[k] = max_rows(m[k]);
+        if ((threadIdx.x & 63) < 16) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) part[wave][lane * 8 + k] = m[k];
         }
         __syncthreads();
-        float m[8] = {};
-#pragma unroll
-        for (int d = 0; d < 16; ++d)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m[k] = fmaxf(m[k], part[d][lane * 8 + k]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int b = scale_byte(m[k]);
-            inv[k] = inverse_scale(b);
-            if (down == 0 && c0 + k < a.cols) a.st[(int64_t)(c0 + k) * a.nbt + t0 / kBlock] = (uint8_t)b;
+            const int c = lane * 8 + k;
+            const int b = scale_byte(fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c])));
+            scale[k] = scale_of(b);
+            if (down == 0 && cb * kBlock + c < a.cols) a.st[(int64_t)(cb * kBlock + c) * a.nbt + t0 / kBlock] = (uint8_t)b;
         }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = SQUARE ? v[i][k] : scaled(v[i][k], inv[k]);
-        uint2 out = {pack4(u[0], u[1], u[2], u[3]), pack4(u[4], u[5], u[6], u[7])};
-        *reinterpret_cast<uint2 *>(turned + (lane * 8 + k) * kTurnPitch + down * 8) = out;
-    }
+    for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint2 *>(turned + (lane * 8 + k) * kBlock + (down ^ (lane & 14)) * 8) = Eight<T>::column(v, k, scale[k]);
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const int col = p * 32 + (threadIdx.x >> 3), piece = (threadIdx.x & 7) * 16;
         if (cb * kBlock + col >= a.cols) continue;
-        const uint4 out = *reinterpret_cast<const uint4 *>(turned + col * kTurnPitch + piece);
+        const uint4 out = *reinterpret_cast<const uint4 *>(turned + col * kBlock + (piece ^ ((col >> 3 & 14) * 8)));
         *reinterpret_cast<uint4 *>(a.qt + blockIdx.z * a.qt_batch + (int64_t)(cb * kBlock + col) * a.qt_ld + t0 + piece) = out;
     }
 }
@@ -327,8 +423,6 @@ template <int BM_, int BN_, int WM_, int WN_> struct Tile {
 // Panel row r sits at r * 128 bytes, its 16-byte chunk c at slot c ^ swz(r): the 16
 // lanes of a fragment read (16 rows, one chunk each) hit distinct banks.
 __device__ inline int swz(int r) { return (r >> 1) & 7; }
-
-__device__ inline float scale_of(uint32_t word) { return __builtin_bit_cast(float, (word & 255) << 23); }
 
 // Eight e4m3 values, bytes of two words, times a power of two, as bf16.
 __device__ inline bf16x8 widen8(int lo, int hi, float scale) {
