@@ -409,6 +409,8 @@ struct MatArgs {
     int groups, rows;              // rows: what the groups divide (a's rows, or kReduce: tokens)
     int b_square, out_f32;
     int tiles_m, tiles_n;
+    float *partial;                // with several splits of the reduction: [split][group][m][n]
+    int splits;
 };
 
 // Tile of BM x BN computed by WM x WN waves; stages of one block (128 bytes a row) of both operands in two LDS buffers.
@@ -516,13 +518,42 @@ __device__ inline void first_words(const uint8_t *base, const int (&row)[N], int
     for (int i = 0; i < N; ++i) w[i] = b[0][i] | b[1][i] << 8 | b[2][i] << 16;
 }
 
+// acc += the products of a block of 128 of 16 rows each, b's first; scales are the words' low bytes.
+template <bool WIDE>
+__device__ inline f32x4 multiply(i32x8 b, i32x8 a, f32x4 acc, uint32_t sb, uint32_t sa) {
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(b[2 * g], b[2 * g + 1], scale_of(sb)),
+                                                          widen8(a[2 * g], a[2 * g + 1], scale_of(sa)), acc, 0, 0, 0);
+        return acc;
+    } else {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc, 0, 0, 0, (int)sb, 0, (int)sa);
+    }
+}
+
+// Up to four consecutive values of a row of the output.
+template <bool WIDE>
+__device__ inline void store4(char *out, int64_t at, f32x4 x, int left) {
+    typedef typename std::conditional<WIDE, float, __bf16>::type O;
+    O *to = reinterpret_cast<O *>(out) + at;
+    float v[4] = {x[0], x[1], x[2], x[3]};
+    if (left >= 4) return Elems<O, 4>::store(to, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < left) to[k] = (O)v[k];
+}
+
 // WIDE: fp32 output through bf16 products.
 template <int GROUPING, bool WIDE, class C>
 __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / C::WN, wn = wave % C::WN;
     const Spot at = locate<GROUPING, C::BM, C::BN>(p);
     if (!at.any) return;
-    const int row0 = at.row0, row_end = at.row_end, col0 = at.col0, kb0 = at.kb0, nk = at.nk, group = at.group;
+    const int row0 = at.row0, row_end = at.row_end, col0 = at.col0, group = at.group;
+    // this workgroup's part of the reduction
+    const int skip = (int)((int64_t)at.nk * blockIdx.y / p.splits), nk = (int)((int64_t)at.nk * (blockIdx.y + 1) / p.splits) - skip;
+    const int kb0 = at.kb0 + skip;
     const uint8_t *pa = p.a + row0 * p.lda + (int64_t)kb0 * kBlock;
     const uint8_t *pb = p.b + (GROUPING == kRows ? group * p.b_batch : 0) + col0 * p.ldb + (int64_t)kb0 * kBlock;
     const uint8_t *psb = p.bs + (GROUPING == kRows ? group * p.bs_batch : 0) + (int64_t)(p.b_square ? col0 / kBlock : col0) * p.nkb + kb0;
@@ -636,6 +667,7 @@ __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
     }
     // lane l of block (j, i): row l % 16 of block i, columns 4 (l / 16) .. + 4 of block j
     char *out = p.out + (GROUPING == kReduce ? group * p.out_batch * (WIDE ? 4 : 2) : 0);
+    const int64_t part = ((int64_t)blockIdx.y * max(p.groups, 1) + group) * p.m * p.n;
 #pragma unroll
     for (int i = 0; i < C::NM; ++i) {
         const int r = (wm * C::NM + i) * 16 + (lane & 15);
@@ -643,19 +675,37 @@ __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
 #pragma unroll
         for (int j = 0; j < C::NN; ++j) {
             const int c = col0 + (wn * C::NN + j) * 16 + 4 * (lane >> 4);
-            float v[4] = {acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3]};
-            const int64_t at = (row0 + r) * p.ldo + c;
-            if (c + 4 <= p.n) {
-                if constexpr (WIDE) Elems<float, 4>::store(reinterpret_cast<float *>(out) + at, v);
-                else Elems<__bf16, 4>::store(reinterpret_cast<__bf16 *>(out) + at, v);
-            } else {
+            if (p.splits > 1) store4<true>(reinterpret_cast<char *>(p.partial + part), (int64_t)(row0 + r) * p.n + c, acc[j][i], p.n - c);
+            else store4<WIDE>(out, (row0 + r) * p.ldo + c, acc[j][i], p.n - c);
+        }
+    }
+}
+
+// Adds the splits' sums in order: four values of a row a thread.
+template <typename O>
+__global__ __launch_bounds__(256) void scaled_join_kernel(MatArgs p) {
+    const int64_t all = (int64_t)max(p.groups, 1) * p.m * p.n;
+    const int per = (p.n + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / per;   // over all groups
+    const int c = (int)(i - row * per) * 4;
+    if (row >= (int64_t)max(p.groups, 1) * p.m) return;
+    const int64_t at = row * p.n + c, group = row / p.m;
+    O *out = reinterpret_cast<O *>(p.out) + group * p.out_batch + (row - group * p.m) * p.ldo + c;
+    if (c + 4 <= p.n) {
+        float v[4] = {};
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) {
+            const auto x = load_vec(p.partial + s * all + at);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (c + k >= p.n) break;
-                    if constexpr (WIDE) reinterpret_cast<float *>(out)[at + k] = v[k];
-                    else reinterpret_cast<__bf16 *>(out)[at + k] = (__bf16)v[k];
-                }
-            }
+            for (int k = 0; k < 4; ++k) v[k] += x[k];
+        }
+        Elems<O, 4>::store(out, v);
+    } else {
+        for (int k = 0; c + k < p.n; ++k) {
+            float v = 0.f;
+            for (int s = 0; s < p.splits; ++s) v += p.partial[s * all + at + k];
+            out[k] = (O)v;
         }
     }
 }
@@ -664,6 +714,85 @@ template <int GROUPING, bool WIDE, class C>
 __global__ __launch_bounds__(C::THREADS) void scaled_tile_kernel(MatArgs p) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     scaled_tile<GROUPING, WIDE, C>(p, lds);
+}
+
+// --- few rows ---------------------------------------------------------------------
+// Up to 32 rows, as of tokens being decoded: bound by b's bytes, so every CU has to
+// be reading. A workgroup takes NB blocks of 16 rows of b and all of a (MB blocks of
+// 16 rows), its W waves a run of blocks of the reduction each, straight from memory
+// to registers (a wave's two loads of a block bring 128 bytes of each row); the
+// waves' sums meet in LDS. a comes from the caches NB times less often than with
+// one block of b.
+template <bool WIDE, int MB, int NB, int W>
+__global__ __launch_bounds__(64 * W) void scaled_rows_kernel(MatArgs p) {
+    constexpr int AT_ONCE = MB + NB <= 2 ? 4 : MB + NB <= 4 ? 2 : 1;   // blocks of the reduction whose loads are under way together
+    __shared__ f32x4 part[W][MB * NB][64];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), low = lane & 15;
+    const int col0 = blockIdx.x * 16 * NB;
+    const int k0 = p.nkb * wave / W, k1 = p.nkb * (wave + 1) / W, last = max(p.nkb - 1, 0);
+    const uint8_t *a[MB], *sa[MB], *b[NB], *sb[NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int r = min(i * 16 + low, p.m - 1);
+        a[i] = p.a + r * p.lda + (lane >> 4) * 16;
+        sa[i] = p.as + (int64_t)r * p.nkb;
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const int r = min(col0 + j * 16 + low, p.n - 1);
+        b[j] = p.b + r * p.ldb + (lane >> 4) * 16;
+        sb[j] = p.bs + (int64_t)(p.b_square ? r / kBlock : r) * p.nkb;
+    }
+    f32x4 acc[NB][MB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = k0; k < k1; k += AT_ONCE) {
+        i32x4 fb[AT_ONCE][NB][2], fa[AT_ONCE][MB][2];
+        uint32_t wb[AT_ONCE][NB], wa[AT_ONCE][MB];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const int at = min(k + u, last);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                fb[u][j][0] = *reinterpret_cast<const i32x4 *>(b[j] + (int64_t)at * kBlock);
+                fb[u][j][1] = *reinterpret_cast<const i32x4 *>(b[j] + (int64_t)at * kBlock + 64);
+                wb[u][j] = sb[j][at];
+            }
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                fa[u][i][0] = *reinterpret_cast<const i32x4 *>(a[i] + (int64_t)at * kBlock);
+                fa[u][i][1] = *reinterpret_cast<const i32x4 *>(a[i] + (int64_t)at * kBlock + 64);
+                wa[u][i] = sa[i][at];
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // every load before the first product
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            if (k + u >= k1) break;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+                    acc[j][i] = multiply<WIDE>(__builtin_shufflevector(fb[u][j][0], fb[u][j][1], 0, 1, 2, 3, 4, 5, 6, 7),
+                                               __builtin_shufflevector(fa[u][i][0], fa[u][i][1], 0, 1, 2, 3, 4, 5, 6, 7),
+                                               acc[j][i], wb[u][j], wa[u][i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) part[wave][j * MB + i][lane] = acc[j][i];
+    __syncthreads();
+    static_assert(MB * NB <= W, "a wave for each block");
+    if (wave < MB * NB) {
+        const int r = wave % MB * 16 + low, c = col0 + wave / MB * 16 + 4 * (lane >> 4);
+        f32x4 sum = part[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += part[w][wave][lane];
+        if (r < p.m) store4<WIDE>(p.out, (int64_t)r * p.ldo + c, sum, p.n - c);
+    }
 }
 
 // --- 256 x 256 tiles on four waves, accumulators in fixed registers -------------
@@ -867,6 +996,16 @@ __global__ __launch_bounds__(kQuadThreads, 1) void scaled_quad_kernel(MatArgs p)
 
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
 
+constexpr int kFewRows = 32;   // the most that scaled_rows_kernel takes
+constexpr int kQuadTiles = 192;   // with fewer 256-tiles than this, 128-tiles fill the GPU better
+// Into how many parts the reduction is cut where 128-tiles are too few for the GPU: two workgroups a CU, and at
+// least four blocks each (a workgroup takes some 0.6 us a block when it is alone on its CU).
+int splits_of(int64_t m, int64_t n, int64_t nkb, int32_t groups) {
+    const int64_t tiles = blocks_of(m) * blocks_of(n) * std::max(groups, 1);
+    if (tiles == 0 || tiles >= 192 || (!groups && m <= kFewRows) || nkb / std::max(groups, 1) < 16) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({nkb / std::max(groups, 1) / 4, 512 / tiles, 32}));
+}
+
 // e4m3 rows: 16-byte aligned, whole blocks.
 ns_status check_bytes(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t batch, int64_t batch_stride) {
     if (!p) return fail(NS_ERR_INVALID_ARG, "%s is NULL", name);
@@ -879,11 +1018,39 @@ ns_status check_bytes(const char *name, const void *p, int64_t rows, int64_t col
     return NS_OK;
 }
 
+ns_status launch_rows(const MatArgs &p, hipStream_t st) {
+    // as many blocks of 16 rows of b to a workgroup as leave one for most CUs, and twice the waves where even one does not
+    const int nb = p.n >= 4 * 16 * 208 ? 4 : p.n >= 2 * 16 * 208 ? 2 : 1;
+    const dim3 grid((p.n + 16 * nb - 1) / (16 * nb));
+    auto go = [&](auto kernel, int waves) { hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, p); };
+    auto pick = [&](auto wide, auto mb) {
+        constexpr bool WIDE = decltype(wide)::value;
+        constexpr int MB = decltype(mb)::value;
+        if (nb == 4) go(scaled_rows_kernel<WIDE, MB, 4, 8>, 8);
+        else if (nb == 2) go(scaled_rows_kernel<WIDE, MB, 2, 8>, 8);
+        else if (grid.x >= 208) go(scaled_rows_kernel<WIDE, MB, 1, 8>, 8);
+        else go(scaled_rows_kernel<WIDE, MB, 1, 16>, 16);
+    };
+    typedef std::integral_constant<int, 1> One;
+    typedef std::integral_constant<int, 2> Two;
+    if (p.out_f32) p.m <= 16 ? pick(std::true_type{}, One{}) : pick(std::true_type{}, Two{});
+    else p.m <= 16 ? pick(std::false_type{}, One{}) : pick(std::false_type{}, Two{});
+    NSQ_HIP(hipGetLastError());
+    return NS_OK;
+}
+
 template <int GROUPING, class C> ns_status launch_tile(const MatArgs &p, int64_t grid, hipStream_t st) {
-    const dim3 blocks((unsigned)grid), threads(C::THREADS);
+    const dim3 blocks((unsigned)grid, p.splits), threads(C::THREADS);
     if (p.out_f32) hipLaunchKernelGGL((scaled_tile_kernel<GROUPING, true, C>), blocks, threads, 2 * C::STAGE, st, p);
     else hipLaunchKernelGGL((scaled_tile_kernel<GROUPING, false, C>), blocks, threads, 2 * C::STAGE, st, p);
     NSQ_HIP(hipGetLastError());
+    if (p.splits > 1) {
+        const int64_t threads_in_all = (int64_t)std::max(p.groups, 1) * p.m * ((p.n + 3) / 4);
+        const dim3 join((unsigned)((threads_in_all + 255) / 256));
+        if (p.out_f32) hipLaunchKernelGGL(scaled_join_kernel<float>, join, dim3(256), 0, st, p);
+        else hipLaunchKernelGGL(scaled_join_kernel<__bf16>, join, dim3(256), 0, st, p);
+        NSQ_HIP(hipGetLastError());
+    }
     return NS_OK;
 }
 
@@ -972,7 +1139,8 @@ extern "C" ns_status ns_scaled_matmul_workspace_bytes(int64_t m, int64_t n, int6
     if (m < 0 || m > kMaxRows || n < 0 || n > kMaxRows) return fail(NS_ERR_INVALID_ARG, "m or n outside [0, 2^30]");
     if (k < 0 || k % kBlock || k > kMaxCols) return fail(NS_ERR_INVALID_ARG, "k must be a multiple of 128 up to 2^22");
     if (groups < 0 || groups > kMaxGroups) return fail(NS_ERR_INVALID_ARG, "groups = %d outside [0, %d]", groups, kMaxGroups);
-    *bytes = 0;
+    const int splits = splits_of(m, n, k / kBlock, groups);
+    *bytes = splits > 1 ? (size_t)splits * std::max(groups, 1) * m * n * sizeof(float) : 0;
     return NS_OK;
 }
 
@@ -1025,11 +1193,12 @@ extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const voi
     p.b_square = b_block_rows == kBlock;
     p.out_f32 = out_dtype == NS_F32;
     hipStream_t st = as_stream(stream);
+    if (!offsets && m <= kFewRows) return launch_rows(p, st);
     if (!p.out_f32 && k && !(reduce && p.b_square)) {
         p.tiles_m = (int)((m + kQuadTile - 1) / kQuadTile);
         p.tiles_n = (int)((n + kQuadTile - 1) / kQuadTile);
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * (reduce ? groups : 1);
-        if (tiles >= 192) {
+        if (tiles >= kQuadTiles) {
             const int64_t quads = offsets && !reduce ? (m / kQuadTile + groups) * p.tiles_n : tiles;
             if (quads > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
             auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)quads), dim3(kQuadThreads), 0, st, p); };
@@ -1046,6 +1215,8 @@ extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const voi
     int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
     if (offsets && !reduce) grid = (m / Small::BM + groups) * p.tiles_n;
     if (reduce) grid *= groups;
+    p.splits = offsets && !reduce ? 1 : splits_of(m, n, p.nkb, groups);
+    p.partial = reinterpret_cast<float *>(workspace);
     if (grid > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
     if (!offsets) return launch_tile<kDense, Small>(p, grid, st);
     return reduce ? launch_tile<kReduce, Small>(p, grid, st) : launch_tile<kRows, Small>(p, grid, st);
