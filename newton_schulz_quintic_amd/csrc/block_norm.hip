@@ -30,7 +30,7 @@ namespace {
 constexpr int kMaxHidden = 16384;
 // Teams of a launch, for teams of one wave, of four and more waves.
 constexpr int teams_for(int waves, bool backward) {
-    return backward ? (waves == 1 ? 1024 : waves == 4 ? 512 : 256) : (waves == 1 ? 4096 : waves == 4 ? 1024 : 512);
+    return backward ? (waves == 1 ? 1024 : waves == 4 ? 512 : 256) : (waves == 1 ? 16384 : waves == 4 ? 4096 : 2048);
 }
 
 struct Rows {
@@ -43,11 +43,12 @@ struct BlockArgs {
     Rows dx, dy, dgate;
     const void *w_post, *w_pre;
     float *dw_post, *dw_pre;
-    float *partial;                    // [team][set][hidden]: dw_pre, dw_post, dgate
+    float *partial;                    // [team][sets][hidden]: sums of dh n; of a u (many gate rows: gate a u); of a u
     int64_t rows, gate_span;           // rows of one gate row
     int32_t hidden, teams;
     int32_t per, gate_teams;           // rows of a team; teams of one gate row (1: a team has whole gate rows)
-    int32_t post_norm, w_f32, gate_f32, has_y, has_gate, many_gates, nt, sets;
+    int32_t post_norm, w_f32, gate_f32, has_y, has_gate, many_gates, nt;
+    int32_t join_u, sets, whole_gates; // the second partial row is wanted; partial rows of a team; a team has whole gate rows and writes their gradients itself
     float alpha, scale, eps, inv_hidden;
 };
 
@@ -318,7 +319,7 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_backward_kernel(BlockAr
         ++row;
         if (HAS_Y && (--left == 0 || row == end)) {   // the gate row, or this team's part of it, ends
             NSQ_EACH(i, k) sum_post[i][k] = fmaf(gate[i][k], sum_gate[i][k], sum_post[i][k]);
-            if (a.dgate.p && a.gate_teams == 1 && a.many_gates) {
+            if (a.dgate.p && a.whole_gates) {
                 NSQ_EACH(i, k) sum_gate[i][k] *= wp[i][k];
                 if (a.gate_f32) {
                     float *to = reinterpret_cast<float *>(a.dgate.p) + g * a.dgate.ld;
@@ -327,50 +328,53 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_backward_kernel(BlockAr
                     const Rows to = {a.dgate.p, a.dgate.ld};
                     store_row<F, __bf16>(to, g, pc, sum_gate, a.nt);
                 }
-                NSQ_EACH(i, k) sum_gate[i][k] = 0.f;
             }
             if (row < end) {
-                if (!(a.dgate.p && a.gate_teams == 1)) {
-                    NSQ_EACH(i, k) sum_gate[i][k] = 0.f;
-                }
+                NSQ_EACH(i, k) sum_gate[i][k] = 0.f;
                 load_row<F>(gate_at(++g), a.gate_f32, pc, gate);
                 left = a.gate_span;
             }
         }
     }
     if (a.dw_pre) store_partial<F>(a, team, 0, pc, sum_pre);
-    if (HAS_Y && a.dw_post) store_partial<F>(a, team, 1, pc, sum_post);
-    if (HAS_Y && a.sets == 3) {
-        NSQ_EACH(i, k) sum_gate[i][k] *= wp[i][k];
-        store_partial<F>(a, team, 2, pc, sum_gate);
-    }
+    if (HAS_Y && a.join_u) store_partial<F>(a, team, 1, pc, a.many_gates ? sum_post : sum_gate);
+    if (HAS_Y && a.sets == 3) store_partial<F>(a, team, 2, pc, sum_gate);
 }
 
-// Adds the teams' partial rows: 64 columns a workgroup, 16 teams at a time. blockIdx.y: dw_pre, dw_post, then the gate rows.
-constexpr int kJoinCols = 64, kJoinRows = 16;
+// Adds the teams' partial rows: 32 columns a workgroup, 32 teams at a time. blockIdx.y
+// 0: dw_pre. 1: dw_post, from the sums of gate a u or, with a single gate row, of a u;
+// and that gate row's gradient. From 2 on: the gate rows' gradients, from their teams.
+constexpr int kJoinCols = 32, kJoinRows = 32;
+__device__ inline float value_at(const void *p, int f32, int64_t i) {
+    return f32 ? reinterpret_cast<const float *>(p)[i] : (float)reinterpret_cast<const __bf16 *>(p)[i];
+}
 __global__ __launch_bounds__(kJoinCols * kJoinRows) void block_norm_join_kernel(BlockArgs a) {
     __shared__ float part[kJoinRows][kJoinCols];
     const int col = threadIdx.x % kJoinCols, down = threadIdx.x / kJoinCols, j = blockIdx.x * kJoinCols + col;
-    const int set = min((int)blockIdx.y, 2), gate_row = (int)blockIdx.y - 2;
-    int from = 0, to = a.teams;
-    if (set == 2 && a.many_gates) from = gate_row * a.gate_teams, to = from + a.gate_teams;
-    float *out = set == 0 ? a.dw_pre : a.dw_post;
-    if (set < 2 && !out) return;
+    const int set = min((int)blockIdx.y, 2), gate_row = blockIdx.y < 2 ? 0 : (int)blockIdx.y - 2;
+    if (set == 0 && !a.dw_pre) return;
+    const int from = set == 2 ? gate_row * a.gate_teams : 0, to = set == 2 ? from + a.gate_teams : a.teams;
     float sum = 0.f;
     if (j < a.hidden) {
         const float *p = a.partial + (int64_t)set * a.hidden + j;
+        const int64_t ld = (int64_t)a.sets * a.hidden;
 #pragma unroll 8
-        for (int r = from + down; r < to; r += kJoinRows) sum += p[(int64_t)r * a.sets * a.hidden];
+        for (int r = from + down; r < to; r += kJoinRows) sum += p[r * ld];
     }
     part[down][col] = sum;
     __syncthreads();
-    if (down == 0 && j < a.hidden) {
-        sum = 0.f;
+    if (down != 0 || j >= a.hidden) return;
+    sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kJoinRows; ++i) sum += part[i][col];
-        if (set < 2) out[j] = sum;
-        else if (a.gate_f32) reinterpret_cast<float *>(a.dgate.p)[gate_row * a.dgate.ld + j] = sum;
-        else reinterpret_cast<__bf16 *>(a.dgate.p)[gate_row * a.dgate.ld + j] = (__bf16)sum;
+    for (int i = 0; i < kJoinRows; ++i) sum += part[i][col];
+    float sum_gate = sum;
+    if (set == 1 && a.has_gate && !a.many_gates) sum *= value_at(a.gate.p, a.gate_f32, j);
+    if (blockIdx.y == 0) a.dw_pre[j] = sum;
+    if (blockIdx.y == 1 && a.dw_post) a.dw_post[j] = sum;
+    if (blockIdx.y >= 2 || (blockIdx.y == 1 && a.dgate.p && !a.many_gates)) {
+        if (a.w_post) sum_gate *= value_at(a.w_post, a.w_f32, j);
+        if (a.gate_f32) reinterpret_cast<float *>(a.dgate.p)[gate_row * a.dgate.ld + j] = sum_gate;
+        else reinterpret_cast<__bf16 *>(a.dgate.p)[gate_row * a.dgate.ld + j] = (__bf16)sum_gate;
     }
 }
 
@@ -398,7 +402,7 @@ struct BlockCall {
 
 // The form of a call by its width: the fewest waves whose lanes hold the row in 8 or 16 elements each.
 void pick_form(BlockCall &c, int32_t hidden) {
-    const int cap[6][3] = {{512, 1, 8}, {1024, 1, 16}, {2048, 4, 8}, {4096, 4, 16}, {8192, 8, 16}, {16384, 16, 16}};
+    const int cap[6][3] = {{512, 1, 8}, {1024, 1, 16}, {2048, 4, 8}, {4096, 8, 8}, {8192, 8, 16}, {16384, 16, 16}};
     for (const auto &f : cap)
         if (hidden <= f[0]) {
             c.waves = f[1];
@@ -502,8 +506,8 @@ template <bool BWD, typename TX, typename TY> void pick(const BlockCall &c, hipS
     if (c.single) go<BWD, Form<TX, TY, 1, 1, 1>>(c, st);
     else if (c.waves == 1 && c.lane_elems == 8) go<BWD, Form<TX, TY, V, 1, 8>>(c, st);
     else if (c.waves == 1) go<BWD, Form<TX, TY, V, 1, 16>>(c, st);
-    else if (c.waves == 4 && c.lane_elems == 8) go<BWD, Form<TX, TY, V, 4, 8>>(c, st);
-    else if (c.waves == 4) go<BWD, Form<TX, TY, V, 4, 16>>(c, st);
+    else if (c.waves == 4) go<BWD, Form<TX, TY, V, 4, 8>>(c, st);
+    else if (c.waves == 8 && c.lane_elems == 8) go<BWD, Form<TX, TY, V, 8, 8>>(c, st);
     else if (c.waves == 8) go<BWD, Form<TX, TY, V, 8, 16>>(c, st);
     else go<BWD, Form<TX, TY, V, 16, 16>>(c, st);
 }
@@ -596,9 +600,11 @@ extern "C" ns_status ns_block_norm_backward(int64_t rows, int32_t hidden, ns_dty
     const double moved = (double)rows * hidden * ((a.x_out.p ? 3 : 2) * c.xs + ((a.has_y ? 2 : 0) + (a.h.p ? 1 : 0)) * c.ys);
     a.nt = moved > (double)kMallBytes;
     deal(c, true);
-    const bool join_gate = a.dgate.p && (!a.many_gates || a.gate_teams > 1);
-    a.sets = join_gate ? 3 : 2;
-    const bool join = a.dw_pre || a.dw_post || join_gate;
+    a.whole_gates = a.many_gates && a.gate_teams == 1;
+    const bool join_gate = a.dgate.p && !a.whole_gates;
+    a.join_u = a.dw_post || join_gate;
+    a.sets = join_gate && a.many_gates ? 3 : 2;
+    const bool join = a.dw_pre || a.join_u;
     if (join) {
         const size_t need = workspace_bytes_of(rows, hidden);
         if (need && (!workspace || workspace_bytes < need))
@@ -609,8 +615,8 @@ extern "C" ns_status ns_block_norm_backward(int64_t rows, int32_t hidden, ns_dty
     hipStream_t st = as_stream(stream);
     if (ns_status s = launch<true>(c, st)) return s;
     if (join) {
-        const int gates = join_gate ? (a.many_gates ? (int)gate_rows : 1) : 0;
-        hipLaunchKernelGGL(block_norm_join_kernel, dim3((hidden + kJoinCols - 1) / kJoinCols, 2 + gates),
+        const int gates = join_gate && a.many_gates ? (int)gate_rows : 0;
+        hipLaunchKernelGGL(block_norm_join_kernel, dim3((hidden + kJoinCols - 1) / kJoinCols, a.join_u ? 2 + gates : 1),
                            dim3(kJoinCols * kJoinRows), 0, st, a);
         NSQ_HIP(hipGetLastError());
     }
