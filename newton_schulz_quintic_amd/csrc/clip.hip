@@ -113,7 +113,7 @@ __device__ inline void each_chunk(const ClipArgs &a, int part, int parts, const 
 // Adds the squares of elements [begin, end), a chunk, dealt to `WIDTH` lanes.
 template <typename T, int WIDTH>
 __device__ inline void add_squares(const T *g, int64_t begin, int64_t end, int lane, double &sum) {
-    constexpr int V = Vec16<T>::N, AT_ONCE = WIDTH == 64 ? 4 : 2;
+    constexpr int V = Vec16<T>::N, AT_ONCE = WIDTH == 64 ? 8 : 2;
     const int whole = (int)(end - begin) / V;
     const T *p = g + begin;
     const int tail = whole * V + lane;   // fewer than V, so lanes 0 .. V - 1
