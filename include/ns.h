@@ -608,7 +608,7 @@ typedef struct ns_rows {
  * gate          (gate_rows, hidden) of gate_dtype or left out (ones): gate row
  *               g holds for rows g * rows / gate_rows and on: 1 gate row (a
  *               value per channel), one per sequence, or one per token.
- *               gate_rows divides rows.
+ *               gate_rows divides rows (without rows: at most 65533).
  * x_out may be x, and h may be y, with the same ld (in place); otherwise
  * outputs overlap nothing. One launch. Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
 ns_status ns_block_norm(int64_t rows, int32_t hidden, ns_dtype residual_dtype, ns_dtype dtype, const ns_rows *x,

@@ -28,6 +28,7 @@ namespace nsq {
 namespace {
 
 constexpr int kMaxHidden = 16384;
+constexpr int kMaxEmptyGates = 65533;   // gate rows of a call without rows, whose gradients are only cleared
 // Teams of a launch, for teams of one wave, of four and more waves.
 constexpr int teams_for(int waves, bool backward) {
     return backward ? (waves == 1 ? 1024 : waves == 4 ? 512 : 256) : (waves == 1 ? 16384 : waves == 4 ? 4096 : 2048);
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(kJoinCols * kJoinRows) void block_norm_join_kernel(
     const int col = threadIdx.x % kJoinCols, down = threadIdx.x / kJoinCols, j = blockIdx.x * kJoinCols + col;
     const int set = min((int)blockIdx.y, 2), gate_row = blockIdx.y < 2 ? 0 : (int)blockIdx.y - 2;
     if (set == 0 && !a.dw_pre) return;
-    const int from = set == 2 ? gate_row * a.gate_teams : 0, to = set == 2 ? from + a.gate_teams : a.teams;
+    const int from = set == 2 ? gate_row * a.gate_teams : 0, to = min(set == 2 ? from + a.gate_teams : a.teams, a.teams);
     float sum = 0.f;
     if (j < a.hidden) {
         const float *p = a.partial + (int64_t)set * a.hidden + j;
@@ -453,7 +454,7 @@ ns_status plan_block(int64_t rows, int32_t hidden, int32_t residual_dtype, int32
     if (!(eps >= 0.f) || eps > 3.4e38f) return fail(NS_ERR_INVALID_ARG, "eps must be finite and >= 0");
     if (!(alpha >= -3.4e38f && alpha <= 3.4e38f) || !(scale >= -3.4e38f && scale <= 3.4e38f))
         return fail(NS_ERR_INVALID_ARG, "alpha and scale must be finite");
-    const bool has_y = y && (y->data || !rows), has_gate = gate && (gate->data || !rows);
+    const bool has_y = y && (y->data || !rows), has_gate = gate && (gate->data || !rows) && (rows || gate_rows);
     if (rows && (!x || !x->data)) return fail(NS_ERR_INVALID_ARG, "x is NULL");
     if (!has_y && (has_gate || post_weight)) return fail(NS_ERR_INVALID_ARG, "gate and post_weight need y");
     if (!post_norm && post_weight) return fail(NS_ERR_INVALID_ARG, "post_weight without post_norm");
@@ -463,7 +464,7 @@ ns_status plan_block(int64_t rows, int32_t hidden, int32_t residual_dtype, int32
     if (ns_status s = check_rows("y", y, rows, hidden, c->ys)) return s;
     if (has_gate) {
         if (!dtype_bytes(gate_dtype)) return fail(NS_ERR_DTYPE, "gate_dtype %d is not NS_BF16 or NS_F32", gate_dtype);
-        if (gate_rows < 1 || rows % gate_rows)
+        if (gate_rows < 0 || (rows ? gate_rows < 1 || rows % gate_rows : gate_rows > kMaxEmptyGates))
             return fail(NS_ERR_INVALID_ARG, "gate_rows = %lld does not divide rows", (long long)gate_rows);
         if (ns_status s = check_rows("gate", gate, gate_rows, hidden, dtype_bytes(gate_dtype))) return s;
     }
@@ -600,7 +601,7 @@ extern "C" ns_status ns_block_norm_backward(int64_t rows, int32_t hidden, ns_dty
     const double moved = (double)rows * hidden * ((a.x_out.p ? 3 : 2) * c.xs + ((a.has_y ? 2 : 0) + (a.h.p ? 1 : 0)) * c.ys);
     a.nt = moved > (double)kMallBytes;
     deal(c, true);
-    a.whole_gates = a.many_gates && a.gate_teams == 1;
+    a.whole_gates = a.many_gates && a.gate_teams == 1 && rows;   // without rows the second launch clears the gradients
     const bool join_gate = a.dgate.p && !a.whole_gates;
     a.join_u = a.dw_post || join_gate;
     a.sets = join_gate && a.many_gates ? 3 : 2;

@@ -871,7 +871,7 @@ __device__ __forceinline__ void scaled_quad(const MatArgs &__restrict__ p, char 
         const i32x4 hi = *reinterpret_cast<const i32x4 *>(row + block * 16 * kBlock + c1);
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
-    if (nk > 0) {
+    if (GROUPING != kReduce || nk > 0) {   // only a group of rows may be empty
 #pragma unroll
         for (int n = 0; n < 8; ++n) load_a(n, 0, 0), load_b(n, 0);
         uint32_t sa[8], sb_word[NSB], next_a[8], next_b[NSB];
