@@ -77,11 +77,77 @@ class Combine(torch.autograd.Function):
         return dy, None, dweights
 
 
+class BlockNorm(torch.autograd.Function):
+    """(x + scale gate norm(y), its norm), or (x, norm of x) where y is None."""
+
+    @staticmethod
+    def forward(ctx, x, y, post_weight, pre_weight, gate, scale):
+        h = torch.empty_like(x if y is None else y)
+        x_out = None if y is None else torch.empty_like(x)
+        ctx.scale = scale
+        ctx.save_for_backward(x, y, post_weight, pre_weight, gate)
+        nsq.ns_block_norm(x, y, x_out, h, post_weight=post_weight, pre_weight=pre_weight, gate=gate, scale=scale)
+        return (x.view_as(x) if y is None else x_out), h
+
+    @staticmethod
+    def backward(ctx, dx_out, dh):
+        x, y, post_weight, pre_weight, gate = ctx.saved_tensors
+        new = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+        dx, dy, dpost, dpre, dgate = new(x), new(y), new(post_weight), new(pre_weight), new(gate)
+        nsq.ns_block_norm_backward(x, y, None if y is None else dx_out.contiguous(), dh.contiguous(), dx, dy,
+                                   dpost_weight=dpost, dpre_weight=dpre, dgate=dgate, post_weight=post_weight,
+                                   pre_weight=pre_weight, gate=gate, scale=ctx.scale)
+        return (dx + dx_out if y is None else dx), dy, dpost, dpre, dgate, None
+
+
+def eight_bit(shape, rows: int = 1, device="cuda"):
+    """Room for the 8-bit form of a (..., rows, cols) tensor: values and scales."""
+    *lead, n, cols = shape
+    blocks = -(-cols // 128)
+    return (torch.empty(*lead, n, 128 * blocks, dtype=torch.float8_e4m3fn, device=device),
+            torch.empty(*lead, -(-n // rows), blocks, dtype=torch.uint8, device=device))
+
+
+class ExpertProducts(torch.autograd.Function):
+    """Rows offsets[e] .. offsets[e + 1] of xs times w[e]^T in 8 bits; xs (rows, k), w (experts, n, k)."""
+
+    @staticmethod
+    def forward(ctx, xs, w, offsets):
+        e, n, k = w.shape
+        q, s = eight_bit(xs.shape)
+        nsq.ns_quantize(xs, q, s)
+        wq, ws = eight_bit(w.shape, 128)
+        wqt, wst = eight_bit((e, k, n), 128)
+        nsq.ns_quantize(w, wq, ws, wqt, wst, block_rows=128)
+        y = xs.new_zeros(xs.shape[0], n)
+        nsq.ns_scaled_matmul(q, s, wq, ws, y, offsets=offsets)
+        ctx.save_for_backward(xs, wqt, wst, offsets)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        xs, wqt, wst, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        (rows, n), k, e = dy.shape, xs.shape[1], offsets.numel() - 1
+        tall = (rows // 128 + e) * 128
+        q, s = eight_bit(dy.shape)
+        qt, st = eight_bit((n, tall))
+        xt, xst = eight_bit((k, tall))
+        nsq.ns_quantize(dy, q, s, qt, st, offsets=offsets)
+        nsq.ns_quantize(xs, None, None, xt, xst, offsets=offsets)
+        dx = torch.zeros_like(xs)
+        nsq.ns_scaled_matmul(q, s, wqt, wst, dx, offsets=offsets)
+        dw = torch.empty(e, n, k, dtype=xs.dtype, device=xs.device)
+        nsq.ns_scaled_matmul(qt, st, xt, xst, dw, offsets=offsets, reduce=True)
+        return dx, dw, None
+
+
 class Student:
     """The block's parameters; matrices in the step's dtype, norm weights and the router in fp32."""
 
     def __init__(self, vocab=1000, hidden=256, heads=4, kv_heads=2, experts=8, top_k=2, ffn=128, dtype=torch.bfloat16,
-                 seed=0, device="cuda"):
+                 seed=0, device="cuda", norms=False, eight_bit=False):
+        self.norms, self.eight_bit = norms, eight_bit
         self.heads, self.kv_heads, self.dim, self.top_k, self.experts = heads, kv_heads, hidden // heads, top_k, experts
         gen = torch.Generator(device=device)
         gen.manual_seed(seed)
@@ -99,12 +165,17 @@ class Student:
         self.up = [matrix(ffn, hidden) for _ in range(experts)]
         self.down = [matrix(hidden, ffn) for _ in range(experts)]
         self.head = matrix(vocab, hidden)
+        if norms:   # before and after the attention and the experts, before the head; a gate per channel after each
+            ones = lambda: torch.ones(hidden, device=device).requires_grad_()  # noqa: E731
+            self.norm_weights = [ones() for _ in range(5)]
+            self.gates = [torch.full((1, hidden), 0.5, device=device).requires_grad_() for _ in range(2)]
 
     def muon_matrices(self):
         return [self.q, self.k, self.v, self.o, *self.up, *self.down]
 
     def others(self):
-        return [self.embed, self.q_weight, self.k_weight, self.router, self.head]
+        more = [*self.norm_weights, *self.gates] if self.norms else []
+        return [self.embed, self.q_weight, self.k_weight, self.router, self.head, *more]
 
 
 def angles(positions: int, dim: int, device="cuda"):
@@ -124,23 +195,37 @@ def attention(q, k, v):
     return torch.matmul(p, v).transpose(1, 2).reshape(b, s, h * d).to(q.dtype)
 
 
-def logits_of(m: Student, tokens, cos, sin):
-    b, s = tokens.shape
-    x = m.embed[tokens]
-    q, k, v = ((x @ w.t()).view(b, s, -1, m.dim) for w in (m.q, m.k, m.v))
-    q, k = QkNormRope.apply(q, k, m.q_weight, m.k_weight, cos, sin)
-    x = (x + attention(q, k, v) @ m.o.t()).reshape(b * s, -1)
-    # the router's choices, sorted by expert
+def experts(m: Student, x):
+    """The experts' layer of the rows x, sorted by the router's choices and back."""
     top, ids = torch.topk(x.float() @ m.router.t(), m.top_k, dim=1)
     offsets = torch.empty(m.experts + 1, dtype=torch.int32, device=x.device)
     slot_of_row = torch.empty(ids.numel(), dtype=torch.int32, device=x.device)
     row_of_slot = torch.empty(ids.shape, dtype=torch.int32, device=x.device)
     nsq.ns_moe_sort(ids, m.experts, offsets, slot_of_row, row_of_slot)
     xs = Dispatch.apply(x, row_of_slot)
-    at = offsets.tolist()
-    ys = [torch.nn.functional.silu(xs[a:z] @ up.t()) @ down.t() for a, z, up, down in zip(at, at[1:], m.up, m.down)]
-    x = x + Combine.apply(torch.cat(ys), row_of_slot, torch.softmax(top, 1))
-    return x @ m.head.t()
+    if m.eight_bit:
+        up = torch.nn.functional.silu(ExpertProducts.apply(xs, torch.stack(m.up), offsets))
+        ys = ExpertProducts.apply(up, torch.stack(m.down), offsets)
+    else:
+        at = offsets.tolist()
+        ys = torch.cat([torch.nn.functional.silu(xs[a:z] @ up.t()) @ down.t() for a, z, up, down in zip(at, at[1:], m.up, m.down)])
+    return Combine.apply(ys, row_of_slot, torch.softmax(top, 1))
+
+
+def logits_of(m: Student, tokens, cos, sin):
+    b, s = tokens.shape
+    x = m.embed[tokens].reshape(b * s, -1)
+    before_attention, after_attention, before_experts, after_experts, before_head = m.norm_weights if m.norms else 5 * [None]
+    h = BlockNorm.apply(x, None, None, before_attention, None, 1.0)[1] if m.norms else x
+    q, k, v = ((h @ w.t()).view(b, s, -1, m.dim) for w in (m.q, m.k, m.v))
+    q, k = QkNormRope.apply(q, k, m.q_weight, m.k_weight, cos, sin)
+    y = (attention(q, k, v) @ m.o.t()).reshape(b * s, -1)
+    if not m.norms:
+        x = x + y
+        return (x + experts(m, x)) @ m.head.t()
+    x, h = BlockNorm.apply(x, y, after_attention, before_experts, m.gates[0], 1.0)
+    x, h = BlockNorm.apply(x, experts(m, h), after_experts, before_head, m.gates[1], 1.0)
+    return h @ m.head.t()
 
 
 def backward(m: Student, tokens, ids, teacher, teacher_lse, temperature, cos, sin):
@@ -156,12 +241,23 @@ def backward(m: Student, tokens, ids, teacher, teacher_lse, temperature, cos, si
     return loss.mean()
 
 
-def muon_update(m: Student, momenta, lr: float, beta: float = 0.9):
-    """Momentum, its orthogonalization by Newton-Schulz, and the step on every Muon matrix; plain SGD on the rest."""
+def muon_update(m: Student, momenta, lr: float, beta: float = 0.9, max_norm: float | None = None):
+    """Momentum, its orthogonalization by Newton-Schulz, and the step on every Muon matrix; plain SGD on the rest.
+    With max_norm all gradients are clipped by their common norm; returns that norm (None without)."""
     weights = m.muon_matrices()
+    norm = None
     with torch.no_grad():
-        for w, mu in zip(weights, momenta):
-            mu.mul_(beta).add_(w.grad)
+        if max_norm is not None:
+            grads, rest = ([p.grad.contiguous() for p in ps] for ps in (weights, m.others()))
+            norm = torch.empty(1, device=grads[0].device)
+            workspace = nsq.ns_grad_norm(grads + rest, norm)
+            nsq.ns_grad_clip(grads, momenta, norm=norm, max_norm=max_norm, momenta=momenta, beta=beta, workspace=workspace)
+            nsq.ns_grad_clip(rest, rest, norm=norm, max_norm=max_norm, workspace=workspace)
+            for p, g in zip(m.others(), rest):
+                p.grad = g
+        else:
+            for w, mu in zip(weights, momenta):
+                mu.mul_(beta).add_(w.grad)
         updates = [torch.empty_like(mu) for mu in momenta]
         order = nsq.ns_plan([tuple(w.shape) for w in weights])["order"]
         nsq.ns_orthogonalize_batched(momenta, updates, order=order)
@@ -171,12 +267,13 @@ def muon_update(m: Student, momenta, lr: float, beta: float = 0.9):
         for p in m.others():
             p.sub_(p.grad, alpha=lr)
             p.grad = None
+    return norm
 
 
 def main(steps: int = 20, dtype=torch.bfloat16, batch: int = 4, seq: int = 64, top: int = 32, temperature: float = 2.0,
-         quiet: bool = False):
+         quiet: bool = False, norms: bool = False, eight_bit: bool = False, max_norm: float | None = None):
     """Trains a student on one teacher's top logits; returns the loss of each step."""
-    student, teacher = Student(dtype=dtype, seed=0), Student(dtype=dtype, seed=1)
+    student, teacher = Student(dtype=dtype, seed=0, norms=norms, eight_bit=eight_bit), Student(dtype=dtype, seed=1)
     cos, sin = angles(seq, student.dim)
     momenta = [torch.zeros_like(w) for w in student.muon_matrices()]
     gen = torch.Generator(device="cuda")
@@ -189,7 +286,7 @@ def main(steps: int = 20, dtype=torch.bfloat16, batch: int = 4, seq: int = 64, t
     losses = []
     for step in range(steps):
         loss = backward(student, tokens, ids, values, teacher_lse, temperature, cos, sin)
-        muon_update(student, momenta, lr=0.02)
+        muon_update(student, momenta, lr=0.02, max_norm=max_norm)
         losses.append(loss.item())
         if not quiet:
             print(f"step {step}: loss {losses[-1]:.4f}", flush=True)
@@ -200,5 +297,9 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--dtype", choices=("bf16", "f32"), default="bf16")
+    ap.add_argument("--norms", action="store_true")
+    ap.add_argument("--eight-bit", action="store_true")
+    ap.add_argument("--max-norm", type=float)
     a = ap.parse_args()
-    main(a.steps, {"bf16": torch.bfloat16, "f32": torch.float32}[a.dtype])
+    main(a.steps, {"bf16": torch.bfloat16, "f32": torch.float32}[a.dtype], norms=a.norms, eight_bit=a.eight_bit,
+         max_norm=a.max_norm)
