@@ -552,7 +552,7 @@ __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
     if (!at.any) return;
     const int row0 = at.row0, row_end = at.row_end, col0 = at.col0, group = at.group;
     // this workgroup's part of the reduction
-    const int skip = (int)((int64_t)at.nk * blockIdx.y / p.splits), nk = (int)((int64_t)at.nk * (blockIdx.y + 1) / p.splits) - skip;
+    const int skip = at.nk * (int)blockIdx.y / p.splits, nk = at.nk * ((int)blockIdx.y + 1) / p.splits - skip;
     const int kb0 = at.kb0 + skip;
     const uint8_t *pa = p.a + row0 * p.lda + (int64_t)kb0 * kBlock;
     const uint8_t *pb = p.b + (GROUPING == kRows ? group * p.b_batch : 0) + col0 * p.ldb + (int64_t)kb0 * kBlock;
