@@ -29,9 +29,12 @@ namespace {
 
 constexpr int kMaxHidden = 16384;
 constexpr int kMaxEmptyGates = 65533;   // gate rows of a call without rows, whose gradients are only cleared
-// Teams of a launch, for teams of one wave, of four and more waves.
+// The most teams of a launch, for teams of one wave, of four and more waves. Backward: one round of workgroups, whose
+// partial rows are few to add (16384 x 4096 bf16 173 us; half as many 272, twice as many 178). Forward: several rounds,
+// so that one's stores go out under another's loads (16384 x 4096 bf16 with half as many 109, 106, with twice as many
+// 111 us; 8192 x 4096 fp32 129, 120, 115).
 constexpr int teams_for(int waves, bool backward) {
-    return backward ? (waves == 1 ? 1024 : waves == 4 ? 512 : 256) : (waves == 1 ? 16384 : waves == 4 ? 4096 : 2048);
+    return backward ? (waves == 1 ? 1024 : waves == 4 ? 512 : 256) : (waves == 1 ? 32768 : waves == 4 ? 8192 : 4096);
 }
 
 struct Rows {
@@ -48,7 +51,7 @@ struct BlockArgs {
     int64_t rows, gate_span;           // rows of one gate row
     int32_t hidden, teams;
     int32_t per, gate_teams;           // rows of a team; teams of one gate row (1: a team has whole gate rows)
-    int32_t post_norm, w_f32, gate_f32, has_y, has_gate, many_gates, nt;
+    int32_t post_norm, w_f32, gate_f32, has_y, has_gate, many_gates;
     int32_t join_u, sets, whole_gates; // the second partial row is wanted; partial rows of a team; a team has whole gate rows and writes their gradients itself
     float alpha, scale, eps, inv_hidden;
 };
@@ -102,25 +105,19 @@ __device__ inline void load_row(const void *p, int f32, const Pieces<F> &pc, flo
 }
 
 template <class F, typename T, typename R>
-__device__ inline void load_raw(const Rows &t, int64_t row, const Pieces<F> &pc, R (&v)[F::NP], bool nt) {
+__device__ inline void load_raw(const Rows &t, int64_t row, const Pieces<F> &pc, R (&v)[F::NP]) {
     const T *p = reinterpret_cast<const T *>(t.p) + row * t.ld;
-    if (nt) {
 #pragma unroll
-        for (int i = 0; i < F::NP; ++i) v[i] = Elems<T, F::V>::template load<F::V != 1>(p + pc.at[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < F::NP; ++i) v[i] = Elems<T, F::V>::load(p + pc.at[i]);
-    }
+    for (int i = 0; i < F::NP; ++i) v[i] = Elems<T, F::V>::load(p + pc.at[i]);
 }
 
 template <class F, typename T>
-__device__ inline void store_row(const Rows &t, int64_t row, const Pieces<F> &pc, const float (&v)[F::NP][F::V], bool nt) {
+__device__ inline void store_row(const Rows &t, int64_t row, const Pieces<F> &pc, const float (&v)[F::NP][F::V]) {
     T *p = reinterpret_cast<T *>(t.p) + row * t.ld;
 #pragma unroll
     for (int i = 0; i < F::NP; ++i) {
         if (pc.skip[i] == 0) {
-            if (nt) Elems<T, F::V>::template store<F::V != 1>(p + pc.at[i], v[i]);
-            else Elems<T, F::V>::store(p + pc.at[i], v[i]);
+            Elems<T, F::V>::store(p + pc.at[i], v[i]);
         } else if (pc.has(i)) {   // in place, overlapped elements may have been read after their own lane wrote them
 #pragma unroll
             for (int k = 1; k < F::V; ++k)
@@ -185,8 +182,8 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_kernel(BlockArgs a) {
     }
     typename F::RX x[F::NP];
     typename F::RY y[F::NP];
-    load_raw<F, X>(a.x, row, pc, x, a.nt);
-    if (HAS_Y) load_raw<F, Y>(a.y, row, pc, y, a.nt);
+    load_raw<F, X>(a.x, row, pc, x);
+    if (HAS_Y) load_raw<F, Y>(a.y, row, pc, y);
     for (int odd = 0;; odd ^= 2) {
         float r[F::NP][F::V], z[F::NP][F::V];
         NSQ_EACH(i, k) r[i][k] = a.alpha * EX::at(x[i], k);
@@ -195,8 +192,8 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_kernel(BlockArgs a) {
         }
         const int64_t next = row + 1;
         if (next < end) {
-            load_raw<F, X>(a.x, next, pc, x, a.nt);
-            if (HAS_Y) load_raw<F, Y>(a.y, next, pc, y, a.nt);
+            load_raw<F, X>(a.x, next, pc, x);
+            if (HAS_Y) load_raw<F, Y>(a.y, next, pc, y);
         }
         if (HAS_Y) {
             float ry = 1.f;
@@ -207,7 +204,7 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_kernel(BlockArgs a) {
                 ry = 1.f / sqrtf(s * a.inv_hidden + a.eps);
             }
             NSQ_EACH(i, k) r[i][k] = fmaf(gate[i][k], z[i][k] * ry * wp[i][k], r[i][k]);
-            if (a.x_out.p) store_row<F, X>(a.x_out, row, pc, r, a.nt);
+            if (a.x_out.p) store_row<F, X>(a.x_out, row, pc, r);
         }
         if (a.h.p) {
             float s = 0.f;
@@ -215,7 +212,7 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_kernel(BlockArgs a) {
             s = team_sum<F>(s, lds, odd + 1);
             const float rr = 1.f / sqrtf(s * a.inv_hidden + a.eps);
             NSQ_EACH(i, k) r[i][k] = r[i][k] * rr * wn[i][k];
-            store_row<F, Y>(a.h, row, pc, r, a.nt);
+            store_row<F, Y>(a.h, row, pc, r);
         }
         if (next >= end) return;
         row = next;
@@ -259,10 +256,10 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_backward_kernel(BlockAr
     typename F::RX x[F::NP], gx[F::NP];
     typename F::RY y[F::NP], gh[F::NP];
     const auto load_all = [&](int64_t at) {
-        load_raw<F, X>(a.x, at, pc, x, a.nt);
-        if (HAS_Y) load_raw<F, Y>(a.y, at, pc, y, a.nt);
-        if (a.x_out.p) load_raw<F, X>(a.x_out, at, pc, gx, a.nt);
-        if (a.h.p) load_raw<F, Y>(a.h, at, pc, gh, a.nt);
+        load_raw<F, X>(a.x, at, pc, x);
+        if (HAS_Y) load_raw<F, Y>(a.y, at, pc, y);
+        if (a.x_out.p) load_raw<F, X>(a.x_out, at, pc, gx);
+        if (a.h.p) load_raw<F, Y>(a.h, at, pc, gh);
     };
     if (row < end) load_all(row);
     for (int odd = 0; row < end; odd ^= 4) {
@@ -313,10 +310,10 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_backward_kernel(BlockAr
                 s = team_sum<F>(s, lds, odd + 3) * a.inv_hidden;
                 NSQ_EACH(i, k) du[i][k] = ry * (du[i][k] - u[i][k] * s);
             }
-            if (a.dy.p) store_row<F, Y>(a.dy, row, pc, du, a.nt);
+            if (a.dy.p) store_row<F, Y>(a.dy, row, pc, du);
         }
         NSQ_EACH(i, k) dr[i][k] *= a.alpha;
-        if (a.dx.p) store_row<F, X>(a.dx, row, pc, dr, a.nt);
+        if (a.dx.p) store_row<F, X>(a.dx, row, pc, dr);
         ++row;
         if (HAS_Y && (--left == 0 || row == end)) {   // the gate row, or this team's part of it, ends
             NSQ_EACH(i, k) sum_post[i][k] = fmaf(gate[i][k], sum_gate[i][k], sum_post[i][k]);
@@ -327,7 +324,7 @@ __global__ __launch_bounds__(F::THREADS) void block_norm_backward_kernel(BlockAr
                     NSQ_EACH(i, k) if (k >= pc.skip[i]) to[pc.at[i] + k] = sum_gate[i][k];
                 } else {
                     const Rows to = {a.dgate.p, a.dgate.ld};
-                    store_row<F, __bf16>(to, g, pc, sum_gate, a.nt);
+                    store_row<F, __bf16>(to, g, pc, sum_gate);
                 }
             }
             if (row < end) {
@@ -550,8 +547,6 @@ extern "C" ns_status ns_block_norm(int64_t rows, int32_t hidden, ns_dtype residu
     c.a.h = rows_at(h);
     if (rows && !c.a.x_out.p && !c.a.h.p) return fail(NS_ERR_INVALID_ARG, "x_out or h is required");
     if (rows && c.a.x_out.p && !c.a.has_y) return fail(NS_ERR_INVALID_ARG, "x_out needs y");
-    const double moved = (double)rows * hidden * (c.xs + (c.a.has_y ? c.ys : 0) + (c.a.x_out.p ? c.xs : 0) + (c.a.h.p ? c.ys : 0));
-    c.a.nt = moved > (double)kMallBytes;
     deal(c, false);
     return launch<false>(c, as_stream(stream));
 }
@@ -598,8 +593,6 @@ extern "C" ns_status ns_block_norm_backward(int64_t rows, int32_t hidden, ns_dty
     }
     a.dw_post = dpost_weight;
     a.dw_pre = dpre_weight;
-    const double moved = (double)rows * hidden * ((a.x_out.p ? 3 : 2) * c.xs + ((a.has_y ? 2 : 0) + (a.h.p ? 1 : 0)) * c.ys);
-    a.nt = moved > (double)kMallBytes;
     deal(c, true);
     a.whole_gates = a.many_gates && a.gate_teams == 1 && rows;   // without rows the second launch clears the gradients
     const bool join_gate = a.dgate.p && !a.whole_gates;
