@@ -57,7 +57,7 @@ __device__ inline GroupBlock find_block(const int32_t *offsets, int groups, int 
     const int lane = threadIdx.x & 63, per = (groups + 63) / 64;
     const int from = min(lane * per, groups), to = min(from + per, groups);
     int sum = 0;
-    for (int e = from; e < to; ++e) sum += (max(edge(offsets, e + 1, rows) - edge(offsets, e, rows), 0) + unit - 1) / unit;
+    for (int e = from; e < to; ++e) sum = min(sum + (max(edge(offsets, e + 1, rows) - edge(offsets, e, rows), 0) + unit - 1) / unit, 1 << 24);
     int upto = sum;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -466,11 +466,14 @@ __device__ inline Spot locate(const MatArgs &p) {
     Spot s = {0, 0, p.m, 0, 0, p.nkb, true};
     int tm, tn;
     if constexpr (GROUPING == kRows) {
-        const int total = find_block<false>(p.offsets, p.groups, p.rows, BM, 0).total * p.tiles_n;
+        const int blocks = find_block<false>(p.offsets, p.groups, p.rows, BM, 0).total;
+        const int total = min(blocks, (int)gridDim.x / p.tiles_n) * p.tiles_n;
         s.any = (int)blockIdx.x < total;
         if (!s.any) return s;
         const int t = xcd_remap(blockIdx.x, total);
         const GroupBlock g = find_block<false>(p.offsets, p.groups, p.rows, BM, t / p.tiles_n);
+        s.any = g.group >= 0;
+        if (!s.any) return s;
         const int first = t / p.tiles_n - g.index;   // the group's first row of tiles
         const int begin = edge(p.offsets, g.group, p.rows);
         s.group = g.group;
@@ -725,11 +728,12 @@ __global__ __launch_bounds__(C::THREADS) void scaled_tile_kernel(MatArgs p) {
 // one block of b.
 template <bool WIDE, int MB, int NB, int W>
 __global__ __launch_bounds__(64 * W) void scaled_rows_kernel(MatArgs p) {
-    constexpr int AT_ONCE = MB + NB <= 2 ? 4 : MB + NB <= 4 ? 2 : 1;   // blocks of the reduction whose loads are under way together
+    // blocks of the reduction whose loads a wave has under way together (four: 16 x 6144 -> 6144 15.4 -> 19.0 us)
+    constexpr int AT_ONCE = MB + NB <= 4 ? 2 : 1;
     __shared__ f32x4 part[W][MB * NB][64];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), low = lane & 15;
     const int col0 = blockIdx.x * 16 * NB;
-    const int k0 = p.nkb * wave / W, k1 = p.nkb * (wave + 1) / W, last = max(p.nkb - 1, 0);
+    const int k0 = p.nkb * wave / W, k1 = p.nkb * (wave + 1) / W;
     const uint8_t *a[MB], *sa[MB], *b[NB], *sb[NB];
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
@@ -753,7 +757,7 @@ __global__ __launch_bounds__(64 * W) void scaled_rows_kernel(MatArgs p) {
         uint32_t wb[AT_ONCE][NB], wa[AT_ONCE][MB];
 #pragma unroll
         for (int u = 0; u < AT_ONCE; ++u) {
-            const int at = min(k + u, last);
+            const int at = min(k + u, k1 - 1);
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 fb[u][j][0] = *reinterpret_cast<const i32x4 *>(b[j] + (int64_t)at * kBlock);
@@ -785,12 +789,12 @@ __global__ __launch_bounds__(64 * W) void scaled_rows_kernel(MatArgs p) {
 #pragma unroll
         for (int i = 0; i < MB; ++i) part[wave][j * MB + i][lane] = acc[j][i];
     __syncthreads();
-    static_assert(MB * NB <= W, "a wave for each block");
-    if (wave < MB * NB) {
-        const int r = wave % MB * 16 + low, c = col0 + wave / MB * 16 + 4 * (lane >> 4);
-        f32x4 sum = part[0][wave][lane];
 #pragma unroll
-        for (int w = 1; w < W; ++w) sum += part[w][wave][lane];
+    for (int q = wave; q < MB * NB; q += W) {
+        const int r = q % MB * 16 + low, c = col0 + q / MB * 16 + 4 * (lane >> 4);
+        f32x4 sum = part[0][q][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += part[w][q][lane];
         if (r < p.m) store4<WIDE>(p.out, (int64_t)r * p.ldo + c, sum, p.n - c);
     }
 }
@@ -996,14 +1000,32 @@ __global__ __launch_bounds__(kQuadThreads, 1) void scaled_quad_kernel(MatArgs p)
 
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
 
-constexpr int kFewRows = 32;   // the most that scaled_rows_kernel takes
-constexpr int kQuadTiles = 192;   // with fewer 256-tiles than this, 128-tiles fill the GPU better
-// Into how many parts the reduction is cut where 128-tiles are too few for the GPU: two workgroups a CU, and at
-// least four blocks each (a workgroup takes some 0.6 us a block when it is alone on its CU).
+// Whether scaled_rows_kernel takes a dense call. It has no second launch and no more workgroups than n gives; a long
+// reduction over few columns, and over most with a second block of rows, is better cut into parts (splits_of). Cold
+// weights, this kernel against the parts: 16 x 4096 -> 14336 15.1, 18.1 us; 16 x 8192 -> 4096 12.1, 14.1; 16 x 14336 ->
+// 1024 19, 11.9; 32 x 4096 -> 14336 17.8, 19.5; 32 x 8192 -> 4096 17.1, 15.2; 32 x 14336 -> 4096 24.6, 18.8; 32 x 8192 ->
+// 28672 46.8, 66.
+bool few_rows(int64_t m, int64_t n, int64_t nkb) {
+    return m <= 16 ? nkb <= 64 || n > 2048 : m <= 32 && (nkb <= 48 || n > 16384);
+}
+
+// Into how many parts the reduction is cut where 128-tiles are too few for the GPU: two workgroups a CU, and at least
+// four blocks each (a workgroup takes some 0.6 us a block when it is alone on its CU, the second launch 3 us). Without
+// and with: 128 x 14336 -> 4096 82, 26 us; 256 x 65536 -> 256 (fp32) 561, 29; 1024 x 8192 -> 1024 (fp32) 74, 32. One
+// tile for most CUs is cut in two where the reduction is long: 768 x 8192 -> 4096 49, 43 us; 896 x 14336 -> 4096 81, 67;
+// but 896 x 4096 -> 4096 28, 32.
 int splits_of(int64_t m, int64_t n, int64_t nkb, int32_t groups) {
-    const int64_t tiles = blocks_of(m) * blocks_of(n) * std::max(groups, 1);
-    if (tiles == 0 || tiles >= 192 || (!groups && m <= kFewRows) || nkb / std::max(groups, 1) < 16) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({nkb / std::max(groups, 1) / 4, 512 / tiles, 32}));
+    const int64_t tiles = blocks_of(m) * blocks_of(n) * std::max(groups, 1), depth = nkb / std::max(groups, 1);
+    if (tiles == 0 || tiles > 256 || (tiles >= 192 && depth < 64) || (!groups && few_rows(m, n, nkb)) || depth < 16) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({depth / 4, 512 / tiles, 32}));
+}
+
+// 256-tiles or 128-tiles, for bf16. Up to 512 of the smaller are resident at once, and on a CU two of them take less
+// time than one of the larger; beyond, a larger tile's fewer reads of its panels win: 2048 x 4096 -> 4096 37 us with
+// 128-tiles, 51 with 256-tiles; -> 4352 60, 53; -> 8192 70, 56; 8192 x 4096 -> 14336 490, 393. Groups of up to 128 rows
+// leave half of a 256-tile empty: 64 groups of 128 rows, 4096 -> 4096 241 us with 128-tiles, 279 with 256-tiles; of 187 365, 293.
+bool quad_tiles(int64_t m, int64_t n, int32_t groups, int32_t reduce) {
+    return blocks_of(m) * blocks_of(n) * (reduce ? groups : 1) > 512 && (reduce || m > int64_t(kBlock) * groups);
 }
 
 // e4m3 rows: 16-byte aligned, whole blocks.
@@ -1018,23 +1040,40 @@ ns_status check_bytes(const char *name, const void *p, int64_t rows, int64_t col
     return NS_OK;
 }
 
+// Blocks of 16 rows of b to a workgroup of scaled_rows_kernel. A CU brings some 27 bytes a ns to its registers, of a
+// as of b, and a call ends with its busiest CU.
+int row_blocks(int64_t n, int mb) {
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int nb = 1; nb <= 8; ++nb) {
+        const int64_t groups = (n + 16 * nb - 1) / (16 * nb), cost = (groups + 255) / 256 * (nb + mb);
+        if (cost < least) least = cost, best = nb;
+    }
+    return best;
+}
+
 ns_status launch_rows(const MatArgs &p, hipStream_t st) {
-    // as many blocks of 16 rows of b to a workgroup as leave one for most CUs, and twice the waves where even one does not
-    const int nb = p.n >= 4 * 16 * 208 ? 4 : p.n >= 2 * 16 * 208 ? 2 : 1;
+    const int mb = p.m <= 16 ? 1 : 2, nb = row_blocks(p.n, mb);
     const dim3 grid((p.n + 16 * nb - 1) / (16 * nb));
     auto go = [&](auto kernel, int waves) { hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, p); };
     auto pick = [&](auto wide, auto mb) {
         constexpr bool WIDE = decltype(wide)::value;
         constexpr int MB = decltype(mb)::value;
-        if (nb == 4) go(scaled_rows_kernel<WIDE, MB, 4, 8>, 8);
-        else if (nb == 2) go(scaled_rows_kernel<WIDE, MB, 2, 8>, 8);
-        else if (grid.x >= 208) go(scaled_rows_kernel<WIDE, MB, 1, 8>, 8);
-        else go(scaled_rows_kernel<WIDE, MB, 1, 16>, 16);
+        switch (nb) {
+            case 1: return grid.x >= 208 ? go(scaled_rows_kernel<WIDE, MB, 1, 8>, 8) : go(scaled_rows_kernel<WIDE, MB, 1, 16>, 16);
+            case 2: return go(scaled_rows_kernel<WIDE, MB, 2, 8>, 8);
+            case 3: return go(scaled_rows_kernel<WIDE, MB, 3, 8>, 8);
+            case 4: return go(scaled_rows_kernel<WIDE, MB, 4, 8>, 8);
+            case 5: return go(scaled_rows_kernel<WIDE, MB, 5, 8>, 8);
+            case 6: return go(scaled_rows_kernel<WIDE, MB, 6, 8>, 8);
+            case 7: return go(scaled_rows_kernel<WIDE, MB, 7, 8>, 8);
+            default: return go(scaled_rows_kernel<WIDE, MB, 8, 8>, 8);
+        }
     };
     typedef std::integral_constant<int, 1> One;
     typedef std::integral_constant<int, 2> Two;
-    if (p.out_f32) p.m <= 16 ? pick(std::true_type{}, One{}) : pick(std::true_type{}, Two{});
-    else p.m <= 16 ? pick(std::false_type{}, One{}) : pick(std::false_type{}, Two{});
+    if (p.out_f32) mb == 1 ? pick(std::true_type{}, One{}) : pick(std::true_type{}, Two{});
+    else mb == 1 ? pick(std::false_type{}, One{}) : pick(std::false_type{}, Two{});
     NSQ_HIP(hipGetLastError());
     return NS_OK;
 }
@@ -1114,8 +1153,9 @@ extern "C" ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_d
     if (block_rows == 1 && !qt) {
         const int64_t units = rows * nb;
         if (!units) return NS_OK;
-        // four blocks a group of lanes, one where that would leave CUs idle
-        const bool few = units < 16 * 4 * 1024;
+        // One block a group of lanes, four in large calls: 2048 x 4096 bf16 6.6 and 7.0 us, 8192 x 4096 18.4 both, 65536
+        // x 7168 259 and 248.
+        const bool few = units < 16 * 4 * 4096;
         const int64_t grid = (units + (few ? 16 : 64) - 1) / (few ? 16 : 64);
         if (grid > INT32_MAX) return fail(NS_ERR_OVERFLOW, "rows x cols too large");
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, st, a); };
@@ -1193,21 +1233,20 @@ extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const voi
     p.b_square = b_block_rows == kBlock;
     p.out_f32 = out_dtype == NS_F32;
     hipStream_t st = as_stream(stream);
-    if (!offsets && m <= kFewRows) return launch_rows(p, st);
-    if (!p.out_f32 && k && !(reduce && p.b_square)) {
+    if (!offsets && few_rows(m, n, p.nkb)) return launch_rows(p, st);
+    if (!p.out_f32 && k && !(reduce && p.b_square) && quad_tiles(m, n, groups, reduce)) {
         p.tiles_m = (int)((m + kQuadTile - 1) / kQuadTile);
         p.tiles_n = (int)((n + kQuadTile - 1) / kQuadTile);
-        const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * (reduce ? groups : 1);
-        if (tiles >= kQuadTiles) {
-            const int64_t quads = offsets && !reduce ? (m / kQuadTile + groups) * p.tiles_n : tiles;
-            if (quads > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
-            auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)quads), dim3(kQuadThreads), 0, st, p); };
-            if (!offsets) p.b_square ? go(scaled_quad_kernel<kDense, true>) : go(scaled_quad_kernel<kDense, false>);
-            else if (!reduce) p.b_square ? go(scaled_quad_kernel<kRows, true>) : go(scaled_quad_kernel<kRows, false>);
-            else go(scaled_quad_kernel<kReduce, false>);
-            NSQ_HIP(hipGetLastError());
-            return NS_OK;
-        }
+        int64_t quads = (int64_t)p.tiles_m * p.tiles_n;
+        if (offsets && !reduce) quads = (m / kQuadTile + groups) * p.tiles_n;
+        if (reduce) quads *= groups;
+        if (quads > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)quads), dim3(kQuadThreads), 0, st, p); };
+        if (!offsets) p.b_square ? go(scaled_quad_kernel<kDense, true>) : go(scaled_quad_kernel<kDense, false>);
+        else if (!reduce) p.b_square ? go(scaled_quad_kernel<kRows, true>) : go(scaled_quad_kernel<kRows, false>);
+        else go(scaled_quad_kernel<kReduce, false>);
+        NSQ_HIP(hipGetLastError());
+        return NS_OK;
     }
     typedef Tile<128, 128, 2, 2> Small;
     p.tiles_m = (int)((m + Small::BM - 1) / Small::BM);

@@ -213,6 +213,40 @@ def test_products(m, n, k, tall, dtype):
     assert _beside(out)
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("n", [4000, 4100, 8200, 12300, 16400, 20500, 24600, 28700, 33000])
+@pytest.mark.parametrize("m,k", [(1, 1152), (16, 256), (17, 384), (32, 1152)])
+def test_products_of_few_rows(m, k, n, dtype):
+    """A workgroup takes one to eight blocks of 16 rows of b, by their number."""
+    import torch
+    log(f"few rows {m} {n} {k} {dtype}")
+    rng = np.random.default_rng([m, n, k])
+    a, sa, a64 = _operand(rng, m, k, 1)
+    b, sb, b64 = _operand(rng, n, k, 128)
+    out = _out(m, n, dtype)
+    nsq.ns_scaled_matmul(a, sa, b, sb, out)
+    torch.cuda.synchronize()
+    _check(out, a64, b64, "few rows")
+    assert _beside(out)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n,k", [(20, 500, 7000 // 128 * 128), (16, 1900, 8448), (900, 2950, 8192)])
+def test_products_of_long_reductions(m, n, k, dtype):
+    """Few rows whose reduction is cut into parts, and a tile for most CUs, cut in two."""
+    import torch
+    log(f"long {m} {n} {k} {dtype}")
+    rng = np.random.default_rng([m, n, k])
+    a, sa, a64 = _operand(rng, m, k, 1)
+    b, sb, b64 = _operand(rng, n, k, 128)
+    out = _out(m, n, dtype)
+    nsq.ns_scaled_matmul(a, sa, b, sb, out)
+    torch.cuda.synchronize()
+    rows = np.unique(rng.integers(0, m, 60))
+    _check(out[torch.from_numpy(rows).cuda()], a64[rows], b64, "long")
+    assert _beside(out)
+
+
 @pytest.mark.parametrize("tall", [1, 128])
 @pytest.mark.parametrize("m,n,k", [(3600, 3500, 128), (3600, 3500, 384), (3584, 3584, 512), (3590, 3599, 640), (3333, 4001, 1152)])
 def test_products_of_many_tiles(m, n, k, tall):
