@@ -968,11 +968,14 @@ __device__ __forceinline__ void scaled_quad(const MatArgs &__restrict__ p, char 
     const int c = (threadIdx.x & 31) * 8, rows = min(ra_last + 1, kQuadTile);
     typedef Elems<__bf16, 8> Out;
     __bf16 *to = out + (int64_t)at.row0 * p.ldo + at.col0 + c;
+    // Stored past the caches, whose room a's and b's panels have use for: 256 groups of 256 rows, 7168 -> 2048 1035 -> 989
+    // us, 32768 x 1024 -> 4096 171 -> 162.
     if (rows == kQuadTile && at.col0 + kQuadTile <= p.n) {
 #pragma unroll 8
         for (int i = 0; i < 32; ++i) {
             const int r = i * 8 + (threadIdx.x >> 5);
-            *reinterpret_cast<Out::raw_u *>(to + r * p.ldo) = *reinterpret_cast<const Out::raw *>(lds + r * kQuadPitch + c * 2);
+            __builtin_nontemporal_store(*reinterpret_cast<const Out::raw *>(lds + r * kQuadPitch + c * 2),
+                                        reinterpret_cast<Out::raw_u *>(to + r * p.ldo));
         }
         return;
     }
