@@ -109,17 +109,19 @@ __device__ inline int scale_byte(float largest) {
 }
 __device__ inline float scale_of(uint32_t byte) { return __builtin_bit_cast(float, (byte & 255) << 23); }
 
-// Eight consecutive elements of a row. Magnitudes are taken of the finite ones: where
-// any is not (a wave finds out at once), `strange` forms leave those out and turn
-// infinities into NaN, which e4m3 has. Conversion divides by the scale and rounds to
-// nearest even, two values an instruction.
+// Eight consecutive elements of a row. Those that reach past its end are loaded from
+// its last eight and shifted into place by trim(), so that no load waits in a branch
+// (14589 x 335 bf16, both ways: 16.0 us with loads one by one, 12.2). Magnitudes are
+// taken of the finite ones: where any is not (a wave finds out at once), `strange`
+// forms leave those out and turn infinities into NaN, which e4m3 has. Conversion
+// divides by the scale and rounds to nearest even, two values an instruction.
 template <typename T> struct Eight;
 template <> struct Eight<__bf16> {
     uint32_t p[4];   // pairs
     __device__ inline void load(const __bf16 *row, int c, int cols) {
-        if (c + 8 <= cols) {
+        if (cols >= 8) {
             typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-            const u4 v = __builtin_bit_cast(u4, load_vec(row + c));
+            const u4 v = __builtin_bit_cast(u4, load_vec(row + min(c, cols - 8)));
 #pragma unroll
             for (int k = 0; k < 4; ++k) p[k] = v[k];
         } else {
@@ -130,6 +132,17 @@ template <> struct Eight<__bf16> {
                 p[k] = lo | hi << 16;
             }
         }
+    }
+    __device__ inline void trim(int c, int cols) {
+        const int by = cols >= 8 ? c - (cols - 8) : 0;
+        if (by <= 0) return;
+        if (by & 4) p[0] = p[2], p[1] = p[3], p[2] = p[3] = 0;
+        if (by & 2) p[0] = p[1], p[1] = p[2], p[2] = p[3], p[3] = 0;
+        if (by & 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = p[k] >> 16 | (k < 3 ? p[k + 1] << 16 : 0);
+        }
+        if (by >= 8) clear();
     }
     __device__ inline void clear() { p[0] = p[1] = p[2] = p[3] = 0; }
     typedef uint16_t pair __attribute__((ext_vector_type(2)));
@@ -186,14 +199,26 @@ template <> struct Eight<__bf16> {
 template <> struct Eight<float> {
     float v[8];
     __device__ inline void load(const float *row, int c, int cols) {
-        if (c + 8 <= cols) {
-            const auto lo = load_vec(row + c), hi = load_vec(row + c + 4);
+        if (cols >= 8) {
+            const int at = min(c, cols - 8);
+            const auto lo = load_vec(row + at), hi = load_vec(row + at + 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? row[c + k] : 0.f;
         }
+    }
+    __device__ inline void trim(int c, int cols) {
+        const int by = cols >= 8 ? c - (cols - 8) : 0;
+        if (by <= 0) return;
+#pragma unroll
+        for (int step = 4; step; step >>= 1)
+            if (by & step) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = k + step < 8 ? v[k + step] : 0.f;
+            }
+        if (by >= 8) clear();
     }
     __device__ inline void clear() {
 #pragma unroll
@@ -272,7 +297,10 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
         v[n].load(reinterpret_cast<const T *>(a.x) + row[n] * a.x_ld, kb[n] * kBlock + lane * 8, a.cols);
     }
 #pragma unroll
-    for (int n = 0; n < AT_ONCE; ++n) odd |= v[n].odd();
+    for (int n = 0; n < AT_ONCE; ++n) {
+        v[n].trim(kb[n] * kBlock + lane * 8, a.cols);
+        odd |= v[n].odd();
+    }
     const bool strange = __any(odd);
     if (strange) {
 #pragma unroll
@@ -324,7 +352,10 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
         else v[i].clear();
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) odd |= v[i].odd();
+    for (int i = 0; i < 8; ++i) {
+        v[i].trim(c0, a.cols);
+        odd |= v[i].odd();
+    }
     const bool strange = __any(odd);
     if (strange) {
 #pragma unroll
@@ -670,7 +701,7 @@ __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
     }
     // lane l of block (j, i): row l % 16 of block i, columns 4 (l / 16) .. + 4 of block j
     char *out = p.out + (GROUPING == kReduce ? group * p.out_batch * (WIDE ? 4 : 2) : 0);
-    const int64_t part = ((int64_t)blockIdx.y * max(p.groups, 1) + group) * p.m * p.n;
+    const int64_t part = (GROUPING == kReduce ? (int64_t)blockIdx.y * p.groups + group : blockIdx.y) * p.m * p.n;
 #pragma unroll
     for (int i = 0; i < C::NM; ++i) {
         const int r = (wm * C::NM + i) * 16 + (lane & 15);
@@ -684,15 +715,18 @@ __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
     }
 }
 
-// Adds the splits' sums in order: four values of a row a thread.
-template <typename O>
+// Adds the splits' sums in order: four values of a row a thread. (A split to each wave of a workgroup and a sum over
+// LDS took 1 us less for 32 splits of 256 x 256 values, 2 to 3 us more for few splits of more.)
+template <int GROUPING, typename O>
 __global__ __launch_bounds__(256) void scaled_join_kernel(MatArgs p) {
-    const int64_t all = (int64_t)max(p.groups, 1) * p.m * p.n;
+    const int parts = GROUPING == kReduce ? p.groups : 1;
+    const int64_t all = (int64_t)parts * p.m * p.n;
     const int per = (p.n + 3) / 4;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t row = i / per;   // over all groups
     const int c = (int)(i - row * per) * 4;
-    if (row >= (int64_t)max(p.groups, 1) * p.m) return;
+    if (row >= (int64_t)parts * p.m) return;
+    if (GROUPING == kRows && (row < edge(p.offsets, 0, p.rows) || row >= edge(p.offsets, p.groups, p.rows))) return;
     const int64_t at = row * p.n + c, group = row / p.m;
     O *out = reinterpret_cast<O *>(p.out) + group * p.out_batch + (row - group * p.m) * p.ldo + c;
     if (c + 4 <= p.n) {
@@ -715,7 +749,7 @@ __global__ __launch_bounds__(256) void scaled_join_kernel(MatArgs p) {
 
 template <int GROUPING, bool WIDE, class C>
 __global__ __launch_bounds__(C::THREADS) void scaled_tile_kernel(MatArgs p) {
-    extern __shared__ __attribute__((aligned(16))) char lds[];
+    __shared__ __attribute__((aligned(16))) char lds[2 * C::STAGE];
     scaled_tile<GROUPING, WIDE, C>(p, lds);
 }
 
@@ -1013,14 +1047,23 @@ bool few_rows(int64_t m, int64_t n, int64_t nkb) {
 }
 
 // Into how many parts the reduction is cut where 128-tiles are too few for the GPU: two workgroups a CU, and at least
-// four blocks each (a workgroup takes some 0.6 us a block when it is alone on its CU, the second launch 3 us). Without
-// and with: 128 x 14336 -> 4096 82, 26 us; 256 x 65536 -> 256 (fp32) 561, 29; 1024 x 8192 -> 1024 (fp32) 74, 32. One
-// tile for most CUs is cut in two where the reduction is long: 768 x 8192 -> 4096 49, 43 us; 896 x 14336 -> 4096 81, 67;
-// but 896 x 4096 -> 4096 28, 32.
-int splits_of(int64_t m, int64_t n, int64_t nkb, int32_t groups) {
-    const int64_t tiles = blocks_of(m) * blocks_of(n) * std::max(groups, 1), depth = nkb / std::max(groups, 1);
-    if (tiles == 0 || tiles > 256 || (tiles >= 192 && depth < 64) || (!groups && few_rows(m, n, nkb)) || depth < 16) return 1;
+// four blocks each (a workgroup takes some 0.6 us a block for bf16, 1 us for fp32, however many stages of loads are under
+// way; the second launch 3 us and the parts' traffic). Without and with: 128 x 14336 -> 4096 82, 25 us; 256 x 65536 -> 256
+// (fp32) 561, 28; 1024 x 8192 -> 1024 (fp32) 74, 31; 512 x 2048 -> 512 14, 11; but 1024 x 2048 -> 1024 14, 18. One tile
+// for most CUs is cut in two where the reduction is long: 768 x 8192 -> 4096 49, 42 us; 896 x 14336 -> 4096 81, 67; but
+// 896 x 4096 -> 4096 28, 32. With groups of rows there are at most m / 128 + groups tiles of rows, and no more than rows:
+// 2 rows of 4 groups, 7808 -> 320 (fp32) 66, 13 us. Over groups of rows the longest group counts, taken as twice the average.
+int splits_of(int64_t m, int64_t n, int64_t nkb, int32_t groups, int32_t reduce) {
+    int64_t tiles = blocks_of(m) * blocks_of(n), depth = nkb;
+    if (reduce) tiles *= groups, depth = 2 * nkb / groups;
+    else if (groups) tiles = std::min(m, m / kBlock + groups) * blocks_of(n);
+    else if (few_rows(m, n, nkb)) return 1;
+    if (tiles == 0 || tiles > 256 || depth < (tiles >= 192 ? 64 : tiles > 48 ? 24 : 16)) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>({depth / 4, 512 / tiles, 32}));
+}
+size_t partial_bytes(int64_t m, int64_t n, int64_t nkb, int32_t groups, int32_t reduce) {
+    const int splits = splits_of(m, n, nkb, groups, reduce);
+    return splits > 1 ? (size_t)splits * (reduce ? groups : 1) * m * n * sizeof(float) : 0;
 }
 
 // 256-tiles or 128-tiles, for bf16. Up to 512 of the smaller are resident at once, and on a CU two of them take less
@@ -1081,16 +1124,17 @@ ns_status launch_rows(const MatArgs &p, hipStream_t st) {
     return NS_OK;
 }
 
-template <int GROUPING, class C> ns_status launch_tile(const MatArgs &p, int64_t grid, hipStream_t st) {
-    const dim3 blocks((unsigned)grid, p.splits), threads(C::THREADS);
-    if (p.out_f32) hipLaunchKernelGGL((scaled_tile_kernel<GROUPING, true, C>), blocks, threads, 2 * C::STAGE, st, p);
-    else hipLaunchKernelGGL((scaled_tile_kernel<GROUPING, false, C>), blocks, threads, 2 * C::STAGE, st, p);
+template <int GROUPING> ns_status launch_tile(const MatArgs &p, int64_t grid, hipStream_t st) {
+    typedef Tile<128, 128, 2, 2> T;
+    const dim3 blocks((unsigned)grid, p.splits), threads(T::THREADS);
+    if (p.out_f32) hipLaunchKernelGGL((scaled_tile_kernel<GROUPING, true, T>), blocks, threads, 0, st, p);
+    else hipLaunchKernelGGL((scaled_tile_kernel<GROUPING, false, T>), blocks, threads, 0, st, p);
     NSQ_HIP(hipGetLastError());
     if (p.splits > 1) {
-        const int64_t threads_in_all = (int64_t)std::max(p.groups, 1) * p.m * ((p.n + 3) / 4);
-        const dim3 join((unsigned)((threads_in_all + 255) / 256));
-        if (p.out_f32) hipLaunchKernelGGL(scaled_join_kernel<float>, join, dim3(256), 0, st, p);
-        else hipLaunchKernelGGL(scaled_join_kernel<__bf16>, join, dim3(256), 0, st, p);
+        const int64_t join_threads = (int64_t)(GROUPING == kReduce ? p.groups : 1) * p.m * ((p.n + 3) / 4);
+        const dim3 join((unsigned)((join_threads + 255) / 256));
+        if (p.out_f32) hipLaunchKernelGGL((scaled_join_kernel<GROUPING, float>), join, dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((scaled_join_kernel<GROUPING, __bf16>), join, dim3(256), 0, st, p);
         NSQ_HIP(hipGetLastError());
     }
     return NS_OK;
@@ -1182,8 +1226,8 @@ extern "C" ns_status ns_scaled_matmul_workspace_bytes(int64_t m, int64_t n, int6
     if (m < 0 || m > kMaxRows || n < 0 || n > kMaxRows) return fail(NS_ERR_INVALID_ARG, "m or n outside [0, 2^30]");
     if (k < 0 || k % kBlock || k > kMaxCols) return fail(NS_ERR_INVALID_ARG, "k must be a multiple of 128 up to 2^22");
     if (groups < 0 || groups > kMaxGroups) return fail(NS_ERR_INVALID_ARG, "groups = %d outside [0, %d]", groups, kMaxGroups);
-    const int splits = splits_of(m, n, k / kBlock, groups);
-    *bytes = splits > 1 ? (size_t)splits * std::max(groups, 1) * m * n * sizeof(float) : 0;
+    *bytes = partial_bytes(m, n, k / kBlock, groups, 0);
+    if (groups) *bytes = std::max(*bytes, partial_bytes(m, n, k / kBlock, groups, 1));
     return NS_OK;
 }
 
@@ -1251,15 +1295,14 @@ extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const voi
         NSQ_HIP(hipGetLastError());
         return NS_OK;
     }
-    typedef Tile<128, 128, 2, 2> Small;
-    p.tiles_m = (int)((m + Small::BM - 1) / Small::BM);
-    p.tiles_n = (int)((n + Small::BN - 1) / Small::BN);
+    p.tiles_m = (int)blocks_of(m);
+    p.tiles_n = (int)blocks_of(n);
     int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
-    if (offsets && !reduce) grid = (m / Small::BM + groups) * p.tiles_n;
+    if (offsets && !reduce) grid = std::min(m, m / kBlock + groups) * p.tiles_n;
     if (reduce) grid *= groups;
-    p.splits = offsets && !reduce ? 1 : splits_of(m, n, p.nkb, groups);
+    p.splits = splits_of(m, n, p.nkb, groups, reduce);
     p.partial = reinterpret_cast<float *>(workspace);
     if (grid > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
-    if (!offsets) return launch_tile<kDense, Small>(p, grid, st);
-    return reduce ? launch_tile<kReduce, Small>(p, grid, st) : launch_tile<kRows, Small>(p, grid, st);
+    if (!offsets) return launch_tile<kDense>(p, grid, st);
+    return reduce ? launch_tile<kReduce>(p, grid, st) : launch_tile<kRows>(p, grid, st);
 }

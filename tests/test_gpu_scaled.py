@@ -120,6 +120,30 @@ def test_quantize_views_and_batches(dtype):
             _same(got, ref)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [5, 7, 8, 9, 14, 15, 63, 121, 125, 134, 135])
+def test_quantize_ends_of_rows(cols, dtype):
+    """Widths that end inside a lane's eight elements, in rows that other values follow."""
+    import torch
+    log(f"quantize ends {cols} {dtype}")
+    x, x64 = _values(np.random.default_rng(cols), 40, cols + 9, dtype, "strange" if cols == 63 else "normal")
+    x, x64 = x[:, :cols], x64[:, :cols]
+    for tall in (1, 128):
+        want = ops.quantize(x64, tall) + ops.quantize(x64.T, tall)
+        q, s = _new8(40, _up(cols)), _bytes(40 if tall == 1 else 1, _up(cols) // 128)
+        qt, st = _new8(cols, 128), _bytes(cols if tall == 1 else -(-cols // 128), 1)
+        nsq.ns_quantize(x, q, s, qt, st, block_rows=tall)
+        torch.cuda.synchronize()
+        for got, ref in ((q, want[0]), (s, want[1]), (qt, want[2]), (st, want[3])):
+            _same(got, ref)
+    q, s = _new8(40, _up(cols)), _bytes(40, _up(cols) // 128)
+    nsq.ns_quantize(x, q, s)
+    torch.cuda.synchronize()
+    want = ops.quantize(x64, 1)
+    _same(q, want[0])
+    _same(s, want[1])
+
+
 GROUPS = [[0, 5], [0, 0, 130, 130, 131, 300], [3, 100, 228, 228, 290], [0, 128, 256, 300], [0] * 70 + [300], [0, 0, 0]]
 
 
@@ -323,6 +347,53 @@ def test_products_over_groups(at, dtype):
     nsq.ns_scaled_matmul(yq, ys, xq, xs, out, offsets=offsets, reduce=True)
     torch.cuda.synchronize()
     for e in range(groups):
+        if at[e + 1] == at[e]:
+            assert not out[e].any()
+            continue
+        a = ops.value(*ops.quantize(y64[at[e]:at[e + 1]].T, 1))
+        b = ops.value(*ops.quantize(x64[at[e]:at[e + 1]].T, 1))
+        _check(out[e], a, b, f"group {e}")
+    assert _beside(out)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("at,n,k", [([0, 1, 1, 2, 2], 300, 7808), ([2, 20, 150, 151], 190, 4096), ([0, 0, 0], 130, 2048),
+                                    ([1, 40, 41, 60, 70], 1027, 2176)])
+def test_products_by_group_of_long_reductions(at, n, k, dtype):
+    """Few rows by group: the reduction is cut into parts, and rows of no group stay as they were."""
+    import torch
+    log(f"groups long {at} {n} {k} {dtype}")
+    rows, groups = max(at[-1], 1) + 3, len(at) - 1
+    rng = np.random.default_rng([n, k])
+    a, sa, a64 = _operand(rng, rows, k, 1)
+    b, sb, b64 = _operand(rng, n, k, 128, batch=groups)
+    out = _out(rows, n, dtype)
+    assert nsq.ns_scaled_matmul_workspace_bytes(rows, n, k, groups)
+    nsq.ns_scaled_matmul(a, sa, b, sb, out, offsets=_offsets(at))
+    torch.cuda.synchronize()
+    for e in range(groups):
+        if at[e + 1] > at[e]:
+            _check(out[at[e]:at[e + 1]], a64[at[e]:at[e + 1]], b64[e], f"group {e}")
+    assert torch.isnan(out[:at[0]].float()).all() and torch.isnan(out[at[-1]:].float()).all() and _beside(out)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_products_over_a_long_group(dtype):
+    """Groups of very different lengths, whose reductions are cut into parts."""
+    import torch
+    log(f"reduce long {dtype}")
+    at, rows = [0, 100, 100, 7000, 7001], 7100
+    rng = np.random.default_rng(51)
+    y, y64 = _values(rng, rows, 70, "bf16")
+    x, x64 = _values(rng, rows, 140, "bf16")
+    p, offsets = (rows // 128 + 4) * 128, _offsets(at)
+    yq, ys, xq, xs = _new8(70, p), _bytes(70, p // 128), _new8(140, p), _bytes(140, p // 128)
+    nsq.ns_quantize(y, None, None, yq, ys, offsets=offsets)
+    nsq.ns_quantize(x, None, None, xq, xs, offsets=offsets)
+    out = _out(70, 140, dtype, 4)
+    nsq.ns_scaled_matmul(yq, ys, xq, xs, out, offsets=offsets, reduce=True)
+    torch.cuda.synchronize()
+    for e in range(4):
         if at[e + 1] == at[e]:
             assert not out[e].any()
             continue
