@@ -685,6 +685,7 @@ ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_dtype dtype,
  *              groups) * 128. Without reduce `rows` is not used.
  * Offsets outside the rows or out of order give wrong results and no fault.
  * workspace from ns_scaled_matmul_workspace_bytes (may be NULL if it says 0).
+ * One launch, or two where a long reduction is cut into parts (fp32, added in order).
  * m, n 0 .. 2^30, groups up to 1024. Nothing may overlap out.
  * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
 ns_status ns_scaled_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t *bytes);

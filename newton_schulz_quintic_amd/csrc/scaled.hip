@@ -279,7 +279,8 @@ __device__ inline float max_rows(float v) {   // over the wave's four rows of 16
     return __builtin_bit_cast(float, max(b[0], b[1]));
 }
 
-// Rows only: 16 lanes take a block of 128 values, AT_ONCE blocks at a time.
+// Rows only: 16 lanes take a block of 128 values, AT_ONCE blocks at a time. 8192 x
+// 4096 bf16 18.3 us, 65536 x 7168 249 us (5.5 and 5.7 TB/s: memory).
 template <typename T, int AT_ONCE>
 __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
     const int64_t units = (int64_t)a.rows * a.nb;
@@ -318,7 +319,10 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
 // A tile of 128 x 128: a thread holds 8 x 8 values of it. SQUARE: one scale for
 // the tile, for q and for qt; else one for each row (q) and one for each column (qt).
 // The transpose goes through LDS, eight bytes (of a column) at a time: unit u of
-// column c at u ^ (c / 8 & 14), which spreads a wave's writes over the banks.
+// column c at u ^ (c / 8 & 14), which spreads a wave's writes over the banks. 14336 x
+// 4096 bf16 in squares, both ways 40 us (5.8 TB/s); 8192 x 14336, both ways by row and
+// column 95-110 us (4.3-4.9 TB/s), the transpose alone of 8192 x 4096 19 us (5.3). Loads
+// past the cache took 101 us for the second and 258 in place of 247 for 16384 x 16384.
 template <typename T, bool SQUARE>
 __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
     __shared__ __attribute__((aligned(16))) float part[4][kBlock];
@@ -578,7 +582,14 @@ __device__ inline void store4(char *out, int64_t at, f32x4 x, int left) {
         if (k < left) to[k] = (O)v[k];
 }
 
-// WIDE: fp32 output through bf16 products.
+// 128 x 128 a workgroup of four waves, two workgroups a CU, a block's loads under the
+// block before. 4096 x 4096 -> 2048 bf16 37 us (1840 TFLOP/s). WIDE: fp32 output
+// through bf16 products: 14336 x 8192 -> 4096 852 us (1130 TFLOP/s; 1205 on another
+// GPU; a bf16 library product of 8192^3 1421). Two conversions stand beside each matrix
+// instruction there and share its issue slots: instructions alone reach 1870 TFLOP/s,
+// with their conversions 1410. 256 x 256 tiles of eight waves (1185), 128 x 256 (1220)
+// and 256 x 128 (1096, 1205 for this) were no better. With one workgroup a CU a block
+// takes some 0.6 us (bf16), with two stages of loads under way as with four.
 template <int GROUPING, bool WIDE, class C>
 __device__ __forceinline__ void scaled_tile(const MatArgs &p, char *lds) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), wm = wave / C::WN, wn = wave % C::WN;
@@ -759,7 +770,8 @@ __global__ __launch_bounds__(C::THREADS) void scaled_tile_kernel(MatArgs p) {
 // 16 rows), its W waves a run of blocks of the reduction each, straight from memory
 // to registers (a wave's two loads of a block bring 128 bytes of each row); the
 // waves' sums meet in LDS. a comes from the caches NB times less often than with
-// one block of b.
+// one block of b. 16 x 4096 -> 14336 bf16 13 us (4.5 TB/s; what a CU can have under way
+// at once is the bound, 27 bytes a ns), 16 x 8192 -> 20000 32 us, one row 4096 -> 4096 8.
 template <bool WIDE, int MB, int NB, int W>
 __global__ __launch_bounds__(64 * W) void scaled_rows_kernel(MatArgs p) {
     // blocks of the reduction whose loads a wave has under way together (four: 16 x 6144 -> 6144 15.4 -> 19.0 us)
@@ -845,6 +857,14 @@ __global__ __launch_bounds__(64 * W) void scaled_rows_kernel(MatArgs p) {
 // as their place is free, and have two (A) and 1.5 (B) stages to land
 // (scaled_stage.inc). Stages past the last one are loaded and read as the last one
 // and not used, so that the loop has one form.
+// Measured: 8192 x 4096 -> 14336 385-410 us (2340-2500 TFLOP/s), 8192 x 14336 -> 4096
+// 347 (2770), 8192^3 428 (2570): 81-85 % of the library's unscaled 8-bit product on the
+// same GPU. A stage takes 1.39 us on all CUs (3.1 PFLOP/s; instructions alone, on
+// random values, 3.77 at the clock that their power leaves) and a tile 7 us beside its
+// stages, most of it the outputs of 256 tiles that end together. Other orders of
+// loads, reads and barriers within a stage were within 2 %, one barrier a stage 8 %
+// slower; a workgroup that goes from tile to tile and stores from its registers took
+// 3 % less at these sizes and 7 to 17 % more with rows at odd places or few tiles.
 #include "acc_pinned.h"
 #include "acc_scaled.h"
 
