@@ -1086,12 +1086,17 @@ size_t partial_bytes(int64_t m, int64_t n, int64_t nkb, int32_t groups, int32_t 
     return splits > 1 ? (size_t)splits * (reduce ? groups : 1) * m * n * sizeof(float) : 0;
 }
 
-// 256-tiles or 128-tiles, for bf16. Up to 512 of the smaller are resident at once, and on a CU two of them take less
-// time than one of the larger; beyond, a larger tile's fewer reads of its panels win: 2048 x 4096 -> 4096 37 us with
-// 128-tiles, 51 with 256-tiles; -> 4352 60, 53; -> 8192 70, 56; 8192 x 4096 -> 14336 490, 393. Groups of up to 128 rows
-// leave half of a 256-tile empty: 64 groups of 128 rows, 4096 -> 4096 241 us with 128-tiles, 279 with 256-tiles; of 187 365, 293.
+// 256-tiles or 128-tiles, for bf16: by the rounds that each takes, in us at a depth of 4096 (measured within 3 us of this
+// for 500 to 1300 small tiles). 512 of the small tiles are resident at once; a whole round of them takes 35 us, a last one
+// of few 22 and up to 13 more. A round of 256 large ones takes 54 however few they are. With small, with large tiles: 2048
+// x 4096 -> 4096 37, 51 us; -> 4352 60, 53; -> 8192 70, 56; -> 8300 93, 110; 64 x 4096 -> 70000 76, 105; 8192 x 4096 ->
+// 14336 490, 393. Groups of rows are taken as equal: 64 groups of 128 rows, 4096 -> 4096 241, 279 us; of 187 365, 293.
 bool quad_tiles(int64_t m, int64_t n, int32_t groups, int32_t reduce) {
-    return blocks_of(m) * blocks_of(n) * (reduce ? groups : 1) > 512 && (reduce || m > int64_t(kBlock) * groups);
+    const int64_t copies = std::max(groups, 1), rows = groups && !reduce ? (m + groups - 1) / groups : m;
+    const int64_t small = copies * blocks_of(rows) * blocks_of(n);
+    const int64_t large = copies * ((rows + kQuadTile - 1) / kQuadTile) * ((n + kQuadTile - 1) / kQuadTile);
+    const int64_t last = small % 512;
+    return (large + 255) / 256 * 54 < small / 512 * 35 + (last ? 22 + last * 13 / 512 : 0);
 }
 
 // e4m3 rows: 16-byte aligned, whole blocks.
