@@ -314,3 +314,26 @@ def test_refusals_of_the_binding():
                 lambda: nsq.ns_block_norm(x, x, x, x, post_weight=w, post_norm=False), lambda: nsq.ns_block_norm(x, x, x, x, eps=-1.0)):
         with pytest.raises(nsq.NSError):
             bad()
+
+
+def test_rows_further_apart_than_32_bits():
+    """Every tensor's rows 2^31 elements apart: the bits of a call on rows that lie together."""
+    import torch
+    log("far rows")
+    h = 1000
+    c = _case(3, h, "bf16", "bf16", 3, True)
+    names = ("x", "y", "gx", "gh", "x_out", "h_out", "dx", "dy")
+    big = torch.empty((2 << 31) + 8 * h, dtype=torch.bfloat16, device="cuda").as_strided((3, 8 * h), (1 << 31, 1))
+    big.fill_(float("nan"))
+    far = {name: big[:, i * h:(i + 1) * h] for i, name in enumerate(names)}
+    near = {name: torch.full((3, h), float("nan"), dtype=torch.bfloat16, device="cuda") for name in names}
+    sums = []
+    for t in (near, far):
+        for name in names[:4]:
+            t[name].copy_(c[name])
+        nsq.ns_block_norm(t["x"], t["y"], t["x_out"], t["h_out"], **_how(c))
+        sums.append([torch.empty(h, device="cuda"), torch.empty(h, device="cuda"), torch.empty_like(c["g"])])
+        nsq.ns_block_norm_backward(t["x"], t["y"], t["gx"], t["gh"], t["dx"], t["dy"], *sums[-1], **_how(c))
+    torch.cuda.synchronize()
+    assert all(torch.equal(near[name], far[name]) for name in names)
+    assert all(torch.equal(a, b) for a, b in zip(*sums))

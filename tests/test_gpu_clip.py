@@ -200,3 +200,17 @@ def test_refusals_of_the_binding():
             bad()
     with pytest.raises(nsq.NSError):
         nsq.ns_grad_clip([x], [x], norm=n, max_norm=-1.0)
+
+
+def test_a_tensor_of_more_than_2_to_the_31():
+    """Every value is reached: ones, whose squares are counted exactly, scaled in place by a power of two."""
+    import torch
+    log("huge tensor")
+    n = (1 << 31) + 5001
+    g = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    norm, sq = _norm([g])
+    assert sq.item() == n and abs(norm.item() - n ** 0.5) <= 1.01 * U * n ** 0.5
+    two = torch.full((1,), 2.0, device="cuda")
+    nsq.ns_grad_clip([g], [g], norm=two, max_norm=1.0, eps=0.0)
+    torch.cuda.synchronize()
+    assert (g == 0.5).all()

@@ -509,3 +509,81 @@ def test_refusals_of_the_binding():
                 lambda: nsq.ns_quantize(torch.zeros(4, 8, 200, device="cuda"), _new8(4, 8, 256), _bytes(4, 8, 2))):
         with pytest.raises(nsq.NSError):
             bad()
+
+
+def _far(rows, cols, ld, dtype):
+    """(rows, cols) of a buffer whose rows lie ld elements apart, NaN in and beside them."""
+    import torch
+    big = torch.empty((rows - 1) * ld + cols + 16, dtype=dtype, device="cuda")
+    t = big.as_strided((rows, cols + 16), (ld, 1)).fill_(float("nan"))
+    return t[:, 8:8 + cols], t
+
+
+def test_offsets_past_32_bits():
+    """Rows, matrices and outputs further apart than 2^31 give the bits of those that lie together."""
+    import torch
+    log("far rows")
+    rng = np.random.default_rng(31)
+    x, _ = _values(rng, 3, 300, "bf16")
+    far, beside = _far(3, 300, 1 << 31, torch.bfloat16)
+    far.copy_(x)
+    both = []
+    for t in (x, far):
+        q, s, qt, st = _new8(3, 384), _bytes(3, 3), _new8(300, 128), _bytes(300, 1)
+        nsq.ns_quantize(t, q, s, qt, st)
+        both.append([t.view(torch.uint8) for t in (q, s, qt, st)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*both))
+    del far, beside
+    for m, n, k, ld in ((3, 500, 384, 1 << 31), (200, 300, 256, 1 << 24), (3590, 3599, 256, 1 << 20)):
+        a, sa, _ = _operand(rng, m, k, 1)
+        b, sb, _ = _operand(rng, n, k, 128)
+        near = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+        far, beside = _far(m, n, ld, torch.bfloat16)
+        for out in (near, far):
+            nsq.ns_scaled_matmul(a, sa, b, sb, out)
+        torch.cuda.synchronize()
+        assert torch.equal(near, far), (m, n)
+        assert torch.isnan(beside[:, :8].float()).all() and torch.isnan(beside[:, 8 + n:].float()).all()
+        del far, beside
+    a, sa, _ = _operand(rng, 200, 256, 1)
+    b, sb, _ = _operand(rng, 40, 256, 128, batch=2)
+    apart = torch.empty((1 << 32) + 40 * 256, dtype=torch.uint8, device="cuda")
+    far = apart.as_strided((2, 40, 256), (1 << 32, 256, 1)).view(torch.float8_e4m3fn)
+    far.view(torch.uint8).copy_(b.view(torch.uint8))
+    outs = [torch.empty(200, 40, device="cuda") for _ in "ab"]
+    for o, w in zip(outs, (b, far)):
+        nsq.ns_scaled_matmul(a, sa, w, sb, o, offsets=_offsets([0, 70, 200]))
+    torch.cuda.synchronize()
+    assert torch.equal(*outs)
+    del far, apart
+    at, p = _offsets([0, 130, 200]), (200 // 128 + 2) * 128
+    qt, st = _new8(64, p), _bytes(64, p // 128)
+    nsq.ns_quantize(_values(rng, 200, 64, "f32")[0], None, None, qt, st, offsets=at)
+    near = torch.empty(2, 64, 64, device="cuda")
+    far = torch.empty((1 << 31) + 64 * 64, device="cuda").as_strided((2, 64, 64), (1 << 31, 64, 1))
+    for out in (near, far):
+        nsq.ns_scaled_matmul(qt, st, qt, st, out, offsets=at, reduce=True)
+    torch.cuda.synchronize()
+    assert torch.equal(near, far)
+
+
+def test_operands_of_more_than_2_gib():
+    """600000 rows of 4096: the last ones, quantized and multiplied."""
+    import torch
+    log("many rows")
+    m, k, n = 600000, 4096, 24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.randn(m, k, generator=g, device="cuda", dtype=torch.bfloat16)
+    q, s = torch.empty(m, k, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(m, k // 128, dtype=torch.uint8, device="cuda")
+    nsq.ns_quantize(x, q, s)
+    b, sb, b64 = _operand(np.random.default_rng(4), n, k, 1)
+    out = torch.empty(m, n, device="cuda")
+    nsq.ns_scaled_matmul(q, s, b, sb, out)
+    torch.cuda.synchronize()
+    for lo in (0, 524200, m - 80):
+        want = ops.quantize(_np(x[lo:lo + 80]), 1)
+        _same(q[lo:lo + 80], want[0])
+        _same(s[lo:lo + 80], want[1])
+        _check(out[lo:lo + 80], ops.value(*want), b64, f"rows {lo}")
