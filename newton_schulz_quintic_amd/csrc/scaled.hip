@@ -45,15 +45,17 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 // Row group e is offsets[e] .. offsets[e + 1], cut to [0, rows).
 __device__ inline int edge(const int32_t *offsets, int e, int rows) { return min(max(offsets[e], 0), rows); }
 
-// The groups' rows in blocks of `unit`, numbered through: the group and the place
-// in it of block `target` (group -1: there are no more than `total` blocks), or with
-// by_group the number of group `target`'s first block. A wave's lanes take a run of
-// groups each, so this is a short chain of loads and one scan.
+// The groups' rows in blocks of `unit`, numbered through: the group, its rows and the
+// place in it of block target_of(total) (group -1: there is no such block), or with
+// BY_GROUP the number of group `target`'s first block. A wave's lanes take a run of
+// groups each, so this is a short chain of loads and one scan. Edges out of order give
+// wrong blocks, but none outside the rows (a lane's sum is cut before the scan could
+// overflow).
 struct GroupBlock {
-    int group, index, total;
+    int group, index, total, begin, end;
 };
-template <bool BY_GROUP>
-__device__ inline GroupBlock find_block(const int32_t *offsets, int groups, int rows, int unit, int target) {
+template <bool BY_GROUP, class F>
+__device__ inline GroupBlock find_block(const int32_t *offsets, int groups, int rows, int unit, const F &target_of) {
     const int lane = threadIdx.x & 63, per = (groups + 63) / 64;
     const int from = min(lane * per, groups), to = min(from + per, groups);
     int sum = 0;
@@ -66,15 +68,18 @@ __device__ inline GroupBlock find_block(const int32_t *offsets, int groups, int 
     }
     GroupBlock r;
     r.total = uniform(__shfl(upto, 63));
+    const int target = target_of(r.total);
     const bool mine = BY_GROUP ? target >= from && target < to : target >= upto - sum && target < upto;
-    int group = -1, index = 0;
+    int group = -1, index = 0, begin = 0, end = 0;
     if (mine) {
         int before = upto - sum;
         for (int e = from; e < to; ++e) {
-            const int n = (max(edge(offsets, e + 1, rows) - edge(offsets, e, rows), 0) + unit - 1) / unit;
+            const int lo = edge(offsets, e, rows), hi = max(edge(offsets, e + 1, rows), lo), n = (hi - lo + unit - 1) / unit;
             if (BY_GROUP ? e == target : target < before + n) {
                 group = e;
                 index = BY_GROUP ? before : target - before;
+                begin = lo;
+                end = hi;
                 break;
             }
             before += n;
@@ -82,9 +87,10 @@ __device__ inline GroupBlock find_block(const int32_t *offsets, int groups, int 
     }
     const uint64_t who = __ballot(mine);
     const int at = who ? __ffsll((unsigned long long)who) - 1 : 0;
-    r.group = uniform(__shfl(group, at));
-    r.index = uniform(__shfl(index, at));
-    if (!who) r.group = -1;
+    r.group = who ? __builtin_amdgcn_readlane(group, at) : -1;
+    r.index = __builtin_amdgcn_readlane(index, at);
+    r.begin = __builtin_amdgcn_readlane(begin, at);
+    r.end = __builtin_amdgcn_readlane(end, at);
     return r;
 }
 
@@ -333,10 +339,10 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
     int r0 = blockIdx.y * kBlock, end = min(r0 + kBlock, a.rows), t0 = r0;
     bool turn = a.qt != nullptr;
     if (a.offsets) {
-        const GroupBlock g = find_block<false>(a.offsets, a.groups, a.rows, kBlock, blockIdx.y);
+        const GroupBlock g = find_block<false>(a.offsets, a.groups, a.rows, kBlock, [](int) { return (int)blockIdx.y; });
         if (g.group >= 0) {
-            r0 = edge(a.offsets, g.group, a.rows) + g.index * kBlock;
-            end = min(r0 + kBlock, edge(a.offsets, g.group + 1, a.rows));
+            r0 = g.begin + g.index * kBlock;
+            end = min(r0 + kBlock, g.end);
             turn = turn && t0 < a.nbt * kBlock;
         } else {   // rows behind the last group: they have no place in qt
             r0 = edge(a.offsets, a.groups, a.rows) + ((int)blockIdx.y - g.total) * kBlock;
@@ -501,20 +507,19 @@ __device__ inline Spot locate(const MatArgs &p) {
     Spot s = {0, 0, p.m, 0, 0, p.nkb, true};
     int tm, tn;
     if constexpr (GROUPING == kRows) {
-        const int blocks = find_block<false>(p.offsets, p.groups, p.rows, BM, 0).total;
-        const int total = min(blocks, (int)gridDim.x / p.tiles_n) * p.tiles_n;
-        s.any = (int)blockIdx.x < total;
-        if (!s.any) return s;
-        const int t = xcd_remap(blockIdx.x, total);
-        const GroupBlock g = find_block<false>(p.offsets, p.groups, p.rows, BM, t / p.tiles_n);
-        s.any = g.group >= 0;
+        int t = 0, all = 0;   // this workgroup's tile, the number of tiles
+        const GroupBlock g = find_block<false>(p.offsets, p.groups, p.rows, BM, [&](int total) {
+            all = min(total, (int)gridDim.x / p.tiles_n) * p.tiles_n;
+            t = xcd_remap(blockIdx.x, max(all, 1));
+            return (int)blockIdx.x < all ? t / p.tiles_n : -1;
+        });
+        s.any = (int)blockIdx.x < all && g.group >= 0;
         if (!s.any) return s;
         const int first = t / p.tiles_n - g.index;   // the group's first row of tiles
-        const int begin = edge(p.offsets, g.group, p.rows);
         s.group = g.group;
-        s.row_end = edge(p.offsets, g.group + 1, p.rows);
-        place(t - first * p.tiles_n, (s.row_end - begin + BM - 1) / BM, p.tiles_n, &tm, &tn);
-        s.row0 = begin + tm * BM;
+        s.row_end = g.end;
+        place(t - first * p.tiles_n, (g.end - g.begin + BM - 1) / BM, p.tiles_n, &tm, &tn);
+        s.row0 = g.begin + tm * BM;
     } else {
         const int per = p.tiles_m * p.tiles_n;
         const int t = xcd_remap(blockIdx.x, gridDim.x);
@@ -522,8 +527,9 @@ __device__ inline Spot locate(const MatArgs &p) {
         place(t - s.group * per, p.tiles_m, p.tiles_n, &tm, &tn);
         s.row0 = tm * BM;
         if constexpr (GROUPING == kReduce) {
-            s.kb0 = find_block<true>(p.offsets, p.groups, p.rows, kBlock, s.group).index;
-            const int rows = max(edge(p.offsets, s.group + 1, p.rows) - edge(p.offsets, s.group, p.rows), 0);
+            const GroupBlock g = find_block<true>(p.offsets, p.groups, p.rows, kBlock, [&](int) { return s.group; });
+            const int rows = g.end - g.begin;
+            s.kb0 = g.index;
             s.nk = max(0, min((rows + kBlock - 1) / kBlock, p.nkb - s.kb0));
         }
     }
