@@ -15,7 +15,8 @@
 // 64 bits, sums come out 1.4e-5 of their rms off where the values of a block are
 // normally distributed, 7e-5 where they spread over 2^12. Next to bf16's rounding
 // (1.7e-3) that is nothing; where fp32 is asked for it is not. There the values are
-// widened to bf16, scale included (exact: one conversion for two values), and go
+// widened to bf16, scale included (one conversion for two values, exact within bf16's
+// normal range: from blocks that hold only values under 5e-36 it can lose some), and go
 // through v_mfma_f32_16x16x32_bf16, whose sums are as good as fp32 adds (2e-8 to
 // 1e-7 here), at half the peak.
 
