@@ -369,7 +369,8 @@ __global__ __launch_bounds__(kJoinCols * kJoinRows) void block_norm_join_kernel(
 #pragma unroll
     for (int i = 0; i < kJoinRows; ++i) sum += part[i][col];
     float sum_gate = sum;
-    if (set == 1 && a.has_gate && !a.many_gates) sum *= value_at(a.gate.p, a.gate_f32, j);
+    // without rows a gate that is counted may have no address: its sums are zeros as they are
+    if (set == 1 && a.gate.p && !a.many_gates) sum *= value_at(a.gate.p, a.gate_f32, j);
     if (blockIdx.y == 0) a.dw_pre[j] = sum;
     if (blockIdx.y == 1 && a.dw_post) a.dw_post[j] = sum;
     if (blockIdx.y >= 2 || (blockIdx.y == 1 && a.dgate.p && !a.many_gates)) {
