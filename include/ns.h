@@ -655,7 +655,8 @@ ns_status ns_block_norm_backward(int64_t rows, int32_t hidden, ns_dtype residual
  *              ceil(rows / block_rows) x cols' / 128 bytes, contiguous.
  * qt, scales_t the transpose in the same form, blocks along the rows: batch x cols
  *              x rows' and batch x ceil(cols / block_rows) x rows' / 128 bytes.
- *              Either pair may be NULL.
+ *              Either pair may be NULL. Matrices of a batch may lie behind each
+ *              other or between each other's rows; they must not overlap.
  * offsets      NULL, or [groups + 1] on the GPU (as ns_moe_sort leaves them), which
  *              divides the rows into groups: in qt each group then starts at a
  *              whole block, rows' = (rows / 128 + groups) * 128 (rounded down
@@ -683,8 +684,9 @@ ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_dtype dtype,
  *              group are left as they were. With reduce = 1 they divide `rows`
  *              rows that both a and b hold transposed, as ns_quantize lays them
  *              out, and each group has a product of its own, out + e * out_batch
- *              elements (zeros for a group without rows); k = (rows / 128 +
- *              groups) * 128. Without reduce `rows` is not used.
+ *              elements (zeros for a group without rows), which must not
+ *              overlap; k = (rows / 128 + groups) * 128. Without reduce `rows`
+ *              is not used.
  * Offsets outside the rows or out of order give wrong results and no fault.
  * workspace from ns_scaled_matmul_workspace_bytes (may be NULL if it says 0).
  * One launch, or two where a long reduction is cut into parts (fp32, added in order).

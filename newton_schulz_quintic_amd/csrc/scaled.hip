@@ -1119,6 +1119,19 @@ ns_status check_bytes(const char *name, const void *p, int64_t rows, int64_t col
     return NS_OK;
 }
 
+// Outputs: whether any two of `count` matrices of rows x cols values, `ld` and `stride` apart, share a place. Matrices may lie
+// behind each other or between each other's rows. (cols <= ld; a matrix g further on has its row i where this one has row
+// i + q, and r values behind it.)
+bool overlap(int64_t count, int64_t stride, int64_t rows, int64_t ld, int64_t cols) {
+    const int64_t extent = (rows - 1) * ld + cols;
+    if (stride >= extent) return false;
+    for (int64_t g = 1; g < count && g * stride < extent; ++g) {
+        const int64_t q = g * stride / ld, r = g * stride % ld;
+        if (r < cols || (q + 1 < rows && ld - r < cols)) return true;
+    }
+    return false;
+}
+
 // Blocks of 16 rows of b to a workgroup of scaled_rows_kernel. A CU brings some 27 bytes a ns to its registers, of a
 // as of b, and a call ends with its busiest CU.
 int row_blocks(int64_t n, int mb) {
@@ -1209,6 +1222,8 @@ extern "C" ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_d
         if (ns_status s = check_bytes("q", q, rows, nb * kBlock, q_ld, batch, q_batch)) return s;
     if (qt)
         if (ns_status s = check_bytes("qt", qt, cols, nbt * kBlock, qt_ld, batch, qt_batch)) return s;
+    if (rows && ((q && overlap(batch, q_batch, rows, q_ld, nb * kBlock)) || (qt && overlap(batch, qt_batch, cols, qt_ld, nbt * kBlock))))
+        return fail(NS_ERR_INVALID_ARG, "matrices of q or of qt overlap");
     QuantArgs a{};
     a.x = reinterpret_cast<const char *>(x);
     a.x_ld = x_ld;
@@ -1285,6 +1300,7 @@ extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const voi
     if (!out || misaligned(out, es)) return fail(NS_ERR_INVALID_ARG, "out is NULL or not aligned to its type");
     if (out_ld < n || too_far(m, out_ld) || m * (double)out_ld > 1e18 || (reduce && groups > 1 && (out_batch < 0 || too_far(groups, out_batch * es))))
         return fail(NS_ERR_INVALID_ARG, "out: bad strides");
+    if (reduce && overlap(groups, out_batch, m, out_ld, n)) return fail(NS_ERR_INVALID_ARG, "the groups' products overlap in out");
     if (k) {
         if (ns_status s = check_bytes("a", a, m, k, a_ld, 1, 0)) return s;
         if (ns_status s = check_bytes("b", b, n, k, b_ld, offsets && !reduce ? groups : 1, b_batch)) return s;

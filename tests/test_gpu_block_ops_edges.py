@@ -2,12 +2,15 @@
 
 import ctypes
 
+import numpy as np
 import pytest
 
 import newton_schulz_quintic_amd as nsq
 from newton_schulz_quintic_amd import _lib
 from newton_schulz_quintic_amd._ops import ns_rows
+from oracle import block_ops as ops
 from tests.helpers import log
+from tests.test_gpu_scaled import _bytes, _new8, _offsets, _same, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +28,31 @@ def test_block_norm_backward_without_rows_and_gate(given):
     assert status == 0, nsq.ns_last_error()
     torch.cuda.synchronize()
     assert not dwp.any() and not dwn.any()
+
+
+def test_outputs_that_overlap_are_refused():
+    """A batch or groups whose matrices share memory; matrices between each other's rows do not."""
+    import torch
+    log("overlapping outputs")
+    x = torch.zeros(3, 150, 200, device="cuda")
+    q, s, qt, st = _new8(3, 150, 256), _bytes(3, 2, 2), _new8(3, 200, 256), _bytes(3, 2, 2)
+    off, k = _offsets([0, 2, 4]), 256
+    a, sa, b, sb = _new8(4, k), _bytes(4, 2), _new8(8, k), _bytes(8, 2)
+    for bad in (lambda: nsq.ns_quantize(x, q[:1].expand(3, 150, 256), s, block_rows=128),
+                lambda: nsq.ns_quantize(x, None, None, qt[:1].expand(3, 200, 256), st, block_rows=128),
+                lambda: nsq.ns_scaled_matmul(a, sa, b, sb, torch.empty(4, 8, device="cuda").expand(2, 4, 8), offsets=off, reduce=True)):
+        with pytest.raises(nsq.NSError, match="overlap"):
+            bad()
+
+
+def test_outputs_between_each_others_rows():
+    import torch
+    log("interleaved outputs")
+    x, x64 = _values(np.random.default_rng(3), 3 * 150, 200, "bf16")
+    q, s, qt, st = _new8(150, 3, 256).transpose(0, 1), _bytes(3, 2, 2), _new8(200, 3, 256).transpose(0, 1), _bytes(3, 2, 2)
+    nsq.ns_quantize(x.view(3, 150, 200), q, s, qt, st, block_rows=128)
+    torch.cuda.synchronize()
+    for i in range(3):
+        part = x64[150 * i:150 * i + 150]
+        for got, ref in zip((q[i], s[i], qt[i], st[i]), ops.quantize(part, 128) + ops.quantize(part.T, 128)):
+            _same(got, ref)
