@@ -660,8 +660,9 @@ ns_status ns_block_norm_backward(int64_t rows, int32_t hidden, ns_dtype residual
  * offsets      NULL, or [groups + 1] on the GPU (as ns_moe_sort leaves them), which
  *              divides the rows into groups: in qt each group then starts at a
  *              whole block, rows' = (rows / 128 + groups) * 128 (rounded down
- *              first), and rows behind the last group have no place; blocks
- *              behind the last group's are left as they were. Needs block_rows 1.
+ *              first), and rows in no group (in front of the first, behind the
+ *              last) have no place; blocks behind the last group's are left as they
+ *              were. q has every row, as without offsets. Needs block_rows 1.
  * rows 0 .. 2^30, cols 1 .. 2^22, batch 0 .. 65535, groups 1 .. 1024; with qt or
  * square blocks at most 65534 blocks of rows. One launch.
  * Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
@@ -680,8 +681,8 @@ ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_dtype dtype,
  * out          (m, n) of out_dtype (BF16 or F32), rows out_ld elements apart.
  * offsets      NULL, or [groups + 1] on the GPU. With reduce = 0 they divide a's
  *              rows: those of group e are multiplied by b + e * b_batch bytes with
- *              the scales of its own behind each other; rows behind the last
- *              group are left as they were. With reduce = 1 they divide `rows`
+ *              the scales of its own behind each other; rows in no group are
+ *              left as they were. With reduce = 1 they divide `rows`
  *              rows that both a and b hold transposed, as ns_quantize lays them
  *              out, and each group has a product of its own, out + e * out_batch
  *              elements (zeros for a group without rows), which must not

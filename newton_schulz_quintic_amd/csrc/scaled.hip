@@ -345,9 +345,10 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
             r0 = g.begin + g.index * kBlock;
             end = min(r0 + kBlock, g.end);
             turn = turn && t0 < a.nbt * kBlock;
-        } else {   // rows behind the last group: they have no place in qt
-            r0 = edge(a.offsets, a.groups, a.rows) + ((int)blockIdx.y - g.total) * kBlock;
-            end = min(r0 + kBlock, a.rows);
+        } else {   // rows in front of the first group, and those behind the last: they have no place in qt
+            const int first = edge(a.offsets, 0, a.rows), front = (first + kBlock - 1) / kBlock, i = (int)blockIdx.y - g.total;
+            r0 = i < front ? i * kBlock : edge(a.offsets, a.groups, a.rows) + (i - front) * kBlock;
+            end = min(r0 + kBlock, i < front ? first : a.rows);
             turn = false;
             if (r0 >= end || !a.q) return;
         }
@@ -1257,8 +1258,8 @@ extern "C" ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_d
         if (dtype == NS_BF16) few ? go(quant_rows_kernel<__bf16, 1>) : go(quant_rows_kernel<__bf16, 4>);
         else few ? go(quant_rows_kernel<float, 1>) : go(quant_rows_kernel<float, 4>);
     } else {
-        // with groups a row of tiles more, for the rows behind the last one
-        const int64_t down = a.offsets ? nbt + 1 : nbt;
+        // for q with groups two rows of tiles more: the rows in front of the first and behind the last are two runs more to round up
+        const int64_t down = a.offsets && q ? nbt + 2 : nbt;
         if (down > 65535) return fail(NS_ERR_OVERFLOW, "rows too many for qt or square blocks");
         const dim3 grid((unsigned)nb, (unsigned)down, (unsigned)batch);
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a); };

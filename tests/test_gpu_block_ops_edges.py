@@ -56,3 +56,24 @@ def test_outputs_between_each_others_rows():
         part = x64[150 * i:150 * i + 150]
         for got, ref in zip((q[i], s[i], qt[i], st[i]), ops.quantize(part, 128) + ops.quantize(part.T, 128)):
             _same(got, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [[3, 100, 228, 228, 290], [128, 130, 300], [129, 129, 300], [300, 300], [257, 258, 258, 259]])
+def test_quantize_rows_in_front_of_the_first_group(at, dtype):
+    """q and its scales hold every row, whether or not qt is asked for."""
+    import torch
+    log(f"quantize in front {at} {dtype}")
+    rows, groups = 300, len(at) - 1
+    p = (rows // 128 + groups) * 128
+    x, x64 = _values(np.random.default_rng(at[0]), rows, 200, dtype)
+    want = ops.quantize(x64, 1)
+    vt, sw, written = ops.quantize_groups(x64, at)
+    for turned in (True, False):
+        q, s, qt, st = _new8(rows, 256), _bytes(rows, 2), _new8(200, p), _bytes(200, p // 128)
+        nsq.ns_quantize(x, q, s, *((qt, st) if turned else ()), offsets=_offsets(at))
+        torch.cuda.synchronize()
+        _same(q, want[0])
+        _same(s, want[1])
+        _same(qt, np.where(written & turned, vt, np.nan))
+        np.testing.assert_array_equal(st.cpu().numpy(), np.where(written[::128] & turned, sw, 255))
