@@ -623,6 +623,7 @@ struct BlockCall {
             if (g->dim() != 2) raise(PyExc_ValueError, "gate must be (gate_rows, hidden)");
             g_dtype = code(*g, "gate");
             gate_rows = g->size(0);
+            if (n > 0 && gate_rows < 1) raise(PyExc_ValueError, "gate must have a row for each rows / gate_rows rows, not none");
             gate = rows(g, "gate", gate_rows, hidden, g->scalar_type());
         }
     }

@@ -77,3 +77,15 @@ def test_quantize_rows_in_front_of_the_first_group(at, dtype):
         _same(s, want[1])
         _same(qt, np.where(written & turned, vt, np.nan))
         np.testing.assert_array_equal(st.cpu().numpy(), np.where(written[::128] & turned, sw, 255))
+
+
+def test_a_gate_without_rows_is_refused():
+    import torch
+    log("empty gate")
+    x, w = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    none = torch.empty(0, 64, device="cuda")
+    for bad in (lambda: nsq.ns_block_norm(x, x, x.clone(), x.clone(), gate=none),
+                lambda: nsq.ns_block_norm_backward(x, x, x, x, x.clone(), x.clone(), dgate=none, gate=none),
+                lambda: nsq.ns_block_norm_backward(x, x, x, x, x.clone(), x.clone(), dpost_weight=w.clone(), gate=none)):
+        with pytest.raises(ValueError, match="gate"):
+            bad()
