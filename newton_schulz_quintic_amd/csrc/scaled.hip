@@ -1203,10 +1203,10 @@ extern "C" ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_d
     if (cols < 1 || cols > kMaxCols) return fail(NS_ERR_INVALID_ARG, "cols outside [1, 2^22]");
     if (block_rows != 1 && block_rows != kBlock) return fail(NS_ERR_INVALID_ARG, "block_rows must be 1 or 128");
     if (block_rows == 1 && batch > 1) return fail(NS_ERR_INVALID_ARG, "a batch needs block_rows = 128");
+    if (!batch || !rows) return NS_OK;   // no address is looked at: empty tensors have none
     if (!q != !scales || !qt != !scales_t || (!q && !qt))
         return fail(NS_ERR_INVALID_ARG, "q and scales, or qt and scales_t, or both pairs are required");
-    if (!batch || (!rows && !offsets)) return NS_OK;
-    if (rows && !x) return fail(NS_ERR_INVALID_ARG, "x is NULL");
+    if (!x) return fail(NS_ERR_INVALID_ARG, "x is NULL");
     if (misaligned(x, es)) return fail(NS_ERR_INVALID_ARG, "x not aligned to its type");
     if (x_ld < 0 || (batch > 1 && x_batch < 0)) return fail(NS_ERR_INVALID_ARG, "negative stride");
     if (too_far(rows, x_ld) || too_far(batch, x_batch) || rows * (double)x_ld + batch * (double)x_batch > 4.6e18 / es)
@@ -1223,7 +1223,7 @@ extern "C" ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_d
         if (ns_status s = check_bytes("q", q, rows, nb * kBlock, q_ld, batch, q_batch)) return s;
     if (qt)
         if (ns_status s = check_bytes("qt", qt, cols, nbt * kBlock, qt_ld, batch, qt_batch)) return s;
-    if (rows && ((q && overlap(batch, q_batch, rows, q_ld, nb * kBlock)) || (qt && overlap(batch, qt_batch, cols, qt_ld, nbt * kBlock))))
+    if ((q && overlap(batch, q_batch, rows, q_ld, nb * kBlock)) || (qt && overlap(batch, qt_batch, cols, qt_ld, nbt * kBlock)))
         return fail(NS_ERR_INVALID_ARG, "matrices of q or of qt overlap");
     QuantArgs a{};
     a.x = reinterpret_cast<const char *>(x);
@@ -1248,7 +1248,6 @@ extern "C" ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_d
     hipStream_t st = as_stream(stream);
     if (block_rows == 1 && !qt) {
         const int64_t units = rows * nb;
-        if (!units) return NS_OK;
         // One block a group of lanes, four in large calls: 2048 x 4096 bf16 6.6 and 7.0 us, 8192 x 4096 18.4 both, 65536
         // x 7168 259 and 248.
         const bool few = units < 16 * 4 * 4096;

@@ -3,7 +3,7 @@
 import pytest
 
 import newton_schulz_quintic_amd as nsq
-from tests.test_block_ops_host import INVALID, MAT, P, QUANT, _matmul, _quantize
+from tests.test_block_ops_host import INVALID, MAT, OK, P, QUANT, _matmul, _quantize
 
 BATCH = {**QUANT, "batch": 3, "tall": 128, "xb": 800}
 
@@ -37,3 +37,9 @@ def test_overlap_is_found_exactly():
                     assert _matmul({**OVER, "m": rows, "n": cols, "ldo": ld, "ob": stride, "a": None}) == INVALID
                     told = "overlap" if len(set(places)) < len(places) else "a is NULL"
                     assert told in nsq.ns_last_error(), (rows, cols, ld, stride)
+
+
+def test_quantize_groups_without_rows():
+    """Empty tensors have no address; there is nothing to write."""
+    assert _quantize({**QUANT, "rows": 0, "x": None, "q": None, "s": None, "qt": None, "st": None, "off": P, "groups": 3}) == OK
+    assert _quantize({**QUANT, "rows": 0, "x": None, "off": P, "groups": 3, "tld": 384}) == OK

@@ -89,3 +89,15 @@ def test_a_gate_without_rows_is_refused():
                 lambda: nsq.ns_block_norm_backward(x, x, x, x, x.clone(), x.clone(), dpost_weight=w.clone(), gate=none)):
         with pytest.raises(ValueError, match="gate"):
             bad()
+
+
+@pytest.mark.parametrize("turned", [False, True])
+def test_quantize_groups_without_rows(turned):
+    """No row in any group: nothing to write, with or without the transpose."""
+    import torch
+    log(f"quantize groups no rows {turned}")
+    x, q, s = torch.empty(0, 200, device="cuda"), _new8(0, 256), _bytes(0, 2)
+    qt, st = _new8(200, 3 * 128), _bytes(200, 3)
+    nsq.ns_quantize(x, q, s, *((qt, st) if turned else ()), offsets=_offsets([0, 0, 0, 0]))
+    torch.cuda.synchronize()
+    assert torch.isnan(qt.float()).all() and (st == 255).all()
