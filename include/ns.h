@@ -663,8 +663,9 @@ ns_status ns_block_norm_backward(int64_t rows, int32_t hidden, ns_dtype residual
  *              first), and rows in no group (in front of the first, behind the
  *              last) have no place; blocks behind the last group's are left as they
  *              were. q has every row, as without offsets. Needs block_rows 1.
- * rows 0 .. 2^30, cols 1 .. 2^22, batch 0 .. 65535, groups 1 .. 1024; with qt or
- * square blocks at most 65534 blocks of rows. One launch.
+ * rows 0 .. 2^30, cols 1 .. 2^22, batch 0 .. 65535, groups 1 .. 1024; with qt rows'
+ * is at most 2^22 (it is a stride), with square blocks rows at most 65535 * 128.
+ * One launch, of fewer than 2^32 threads (some 2^30 blocks of 128 values; OVERFLOW).
  * Errors: INVALID_ARG, DTYPE, OVERFLOW, HIP. */
 ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_dtype dtype, const void *x, int64_t x_ld,
                       int64_t x_batch, int32_t block_rows, const int32_t *offsets, int32_t groups, void *q,
@@ -691,7 +692,8 @@ ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_dtype dtype,
  * Offsets outside the rows or out of order give wrong results and no fault.
  * workspace from ns_scaled_matmul_workspace_bytes (may be NULL if it says 0).
  * One launch, or two where a long reduction is cut into parts (fp32, added in order).
- * m, n 0 .. 2^30, groups up to 1024. Nothing may overlap out.
+ * m, n 0 .. 2^30, groups up to 1024. A launch has fewer than 2^32 threads: some
+ * 2^24 tiles of 128 x 128 of out, or 2^30 columns (OVERFLOW). Nothing may overlap out.
  * Errors: INVALID_ARG, DTYPE, WORKSPACE, OVERFLOW, HIP. */
 ns_status ns_scaled_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t *bytes);
 ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, int64_t a_ld, const uint8_t *a_scales,

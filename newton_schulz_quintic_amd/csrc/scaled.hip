@@ -1108,6 +1108,12 @@ bool quad_tiles(int64_t m, int64_t n, int32_t groups, int32_t reduce) {
     return (large + 255) / 256 * 54 < small / 512 * 35 + (last ? 22 + last * 13 / 512 : 0);
 }
 
+// Whether one launch takes `groups` workgroups of `threads` along an axis: fewer than 2^32 threads.
+ns_status check_grid(int64_t groups, int64_t threads) {
+    if (groups > UINT32_MAX / threads) return fail(NS_ERR_OVERFLOW, "%lld workgroups are more than a launch takes", (long long)groups);
+    return NS_OK;
+}
+
 // e4m3 rows: 16-byte aligned, whole blocks.
 ns_status check_bytes(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t batch, int64_t batch_stride) {
     if (!p) return fail(NS_ERR_INVALID_ARG, "%s is NULL", name);
@@ -1147,7 +1153,9 @@ int row_blocks(int64_t n, int mb) {
 
 ns_status launch_rows(const MatArgs &p, hipStream_t st) {
     const int mb = p.m <= 16 ? 1 : 2, nb = row_blocks(p.n, mb);
-    const dim3 grid((p.n + 16 * nb - 1) / (16 * nb));
+    const int64_t workgroups = ((int64_t)p.n + 16 * nb - 1) / (16 * nb);
+    if (ns_status s = check_grid(workgroups, 512)) return s;
+    const dim3 grid((unsigned)workgroups);
     auto go = [&](auto kernel, int waves) { hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, p); };
     auto pick = [&](auto wide, auto mb) {
         constexpr bool WIDE = decltype(wide)::value;
@@ -1252,7 +1260,7 @@ extern "C" ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_d
         // x 7168 259 and 248.
         const bool few = units < 16 * 4 * 4096;
         const int64_t grid = (units + (few ? 16 : 64) - 1) / (few ? 16 : 64);
-        if (grid > INT32_MAX) return fail(NS_ERR_OVERFLOW, "rows x cols too large");
+        if (ns_status s = check_grid(grid, 256)) return s;
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, st, a); };
         if (dtype == NS_BF16) few ? go(quant_rows_kernel<__bf16, 1>) : go(quant_rows_kernel<__bf16, 4>);
         else few ? go(quant_rows_kernel<float, 1>) : go(quant_rows_kernel<float, 4>);
@@ -1336,7 +1344,7 @@ extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const voi
         int64_t quads = (int64_t)p.tiles_m * p.tiles_n;
         if (offsets && !reduce) quads = (m / kQuadTile + groups) * p.tiles_n;
         if (reduce) quads *= groups;
-        if (quads > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
+        if (ns_status s = check_grid(quads, kQuadThreads)) return s;
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)quads), dim3(kQuadThreads), 0, st, p); };
         if (!offsets) p.b_square ? go(scaled_quad_kernel<kDense, true>) : go(scaled_quad_kernel<kDense, false>);
         else if (!reduce) p.b_square ? go(scaled_quad_kernel<kRows, true>) : go(scaled_quad_kernel<kRows, false>);
@@ -1351,7 +1359,7 @@ extern "C" ns_status ns_scaled_matmul(int64_t m, int64_t n, int64_t k, const voi
     if (reduce) grid *= groups;
     p.splits = splits_of(m, n, p.nkb, groups, reduce);
     p.partial = reinterpret_cast<float *>(workspace);
-    if (grid > INT32_MAX) return fail(NS_ERR_OVERFLOW, "too many tiles");
+    if (ns_status s = check_grid(grid, 256)) return s;
     if (!offsets) return launch_tile<kDense>(p, grid, st);
     return reduce ? launch_tile<kReduce>(p, grid, st) : launch_tile<kRows>(p, grid, st);
 }

@@ -3,7 +3,7 @@
 import pytest
 
 import newton_schulz_quintic_amd as nsq
-from tests.test_block_ops_host import INVALID, MAT, OK, P, QUANT, _matmul, _quantize
+from tests.test_block_ops_host import INVALID, MAT, OK, OVERFLOW, P, QUANT, _matmul, _quantize
 
 BATCH = {**QUANT, "batch": 3, "tall": 128, "xb": 800}
 
@@ -43,3 +43,13 @@ def test_quantize_groups_without_rows():
     """Empty tensors have no address; there is nothing to write."""
     assert _quantize({**QUANT, "rows": 0, "x": None, "q": None, "s": None, "qt": None, "st": None, "off": P, "groups": 3}) == OK
     assert _quantize({**QUANT, "rows": 0, "x": None, "off": P, "groups": 3, "tld": 384}) == OK
+
+
+def test_more_workgroups_than_a_launch_takes():
+    """A launch has fewer than 2^32 threads along an axis."""
+    top = 1 << 30
+    assert _quantize({**QUANT, "rows": top, "cols": 1, "ld": 1, "qt": None, "st": None, "qld": 128}) == OVERFLOW
+    few = {**MAT, "k": 128, "lda": 128, "ldb": 128, "tall": 1, "ldo": top}
+    assert _matmul({**few, "m": 1, "n": top}) == OVERFLOW and _matmul({**few, "m": 32, "n": top}) == OVERFLOW
+    wide = {**few, "m": 2048, "n": 1 << 22, "off": P, "groups": 1024, "od": 1}
+    assert _matmul(wide) == OVERFLOW and _matmul({**wide, "od": 0}) == OVERFLOW
