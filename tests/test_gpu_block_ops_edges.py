@@ -10,7 +10,7 @@ from newton_schulz_quintic_amd import _lib
 from newton_schulz_quintic_amd._ops import ns_rows
 from oracle import block_ops as ops
 from tests.helpers import log
-from tests.test_gpu_scaled import _bytes, _new8, _offsets, _same, _values
+from tests.test_gpu_scaled import _beside, _bytes, _check, _new8, _offsets, _operand, _out, _same, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +101,22 @@ def test_quantize_groups_without_rows(turned):
     nsq.ns_quantize(x, q, s, *((qt, st) if turned else ()), offsets=_offsets([0, 0, 0, 0]))
     torch.cuda.synchronize()
     assert torch.isnan(qt.float()).all() and (st == 255).all()
+
+
+def test_groups_of_many_tiles_with_scales_for_each_row():
+    """Groups on the 256-tiles, the matrices' rows with scales of their own."""
+    import torch
+    log("groups many tiles, rows' scales")
+    rng = np.random.default_rng(19)
+    at = [0, 0, 1, 700, 700, 2300, 2556, 4000]
+    rows, n, k = 4100, 3001, 640
+    a, sa, a64 = _operand(rng, rows, k, 1)
+    b, sb, b64 = _operand(rng, n, k, 1, batch=7)
+    out = _out(rows, n, "bfloat16")
+    nsq.ns_scaled_matmul(a, sa, b, sb, out, offsets=_offsets(at))
+    torch.cuda.synchronize()
+    for e in range(7):
+        picked = np.unique(np.concatenate([rng.integers(at[e], at[e + 1], 12), [at[e], at[e + 1] - 1]])) if at[e + 1] > at[e] else []
+        if len(picked):
+            _check(out[torch.from_numpy(picked).cuda()], a64[picked], b64[e], f"group {e}")
+    assert torch.isnan(out[4000:].float()).all() and _beside(out)
