@@ -775,13 +775,16 @@ __global__ __launch_bounds__(C::THREADS) void scaled_tile_kernel(MatArgs p) {
 // --- few rows ---------------------------------------------------------------------
 // Up to 32 rows, as of tokens being decoded: bound by b's bytes, so every CU has to
 // be reading. A workgroup takes NB blocks of 16 rows of b and all of a (MB blocks of
-// 16 rows), its W waves a run of blocks of the reduction each, straight from memory
+// 16 rows), its eight waves a run of blocks of the reduction each, straight from memory
 // to registers (a wave's two loads of a block bring 128 bytes of each row); the
 // waves' sums meet in LDS. a comes from the caches NB times less often than with
 // one block of b. 16 x 4096 -> 14336 bf16 13 us (4.5 TB/s; what a CU can have under way
 // at once is the bound, 27 bytes a ns), 16 x 8192 -> 20000 32 us, one row 4096 -> 4096 8.
-template <bool WIDE, int MB, int NB, int W>
-__global__ __launch_bounds__(64 * W) void scaled_rows_kernel(MatArgs p) {
+constexpr int kRowsThreads = 512;
+template <bool WIDE, int MB, int NB>
+__global__ __launch_bounds__(kRowsThreads) void scaled_rows_kernel(MatArgs p) {
+    // 16 waves: 16 x 4096 -> 1024 6.7 -> 6.8 us, 16 x 14336 -> 4096 17.7 -> 19.7, 32 x 6144 -> 2048 12.4 -> 15.4
+    constexpr int W = kRowsThreads / 64;
     // blocks of the reduction whose loads a wave has under way together (four: 16 x 6144 -> 6144 15.4 -> 19.0 us)
     constexpr int AT_ONCE = MB + NB <= 4 ? 2 : 1;
     __shared__ f32x4 part[W][MB * NB][64];
@@ -1154,21 +1157,21 @@ int row_blocks(int64_t n, int mb) {
 ns_status launch_rows(const MatArgs &p, hipStream_t st) {
     const int mb = p.m <= 16 ? 1 : 2, nb = row_blocks(p.n, mb);
     const int64_t workgroups = ((int64_t)p.n + 16 * nb - 1) / (16 * nb);
-    if (ns_status s = check_grid(workgroups, 512)) return s;
+    if (ns_status s = check_grid(workgroups, kRowsThreads)) return s;
     const dim3 grid((unsigned)workgroups);
-    auto go = [&](auto kernel, int waves) { hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, p); };
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kRowsThreads), 0, st, p); };
     auto pick = [&](auto wide, auto mb) {
         constexpr bool WIDE = decltype(wide)::value;
         constexpr int MB = decltype(mb)::value;
         switch (nb) {
-            case 1: return grid.x >= 208 ? go(scaled_rows_kernel<WIDE, MB, 1, 8>, 8) : go(scaled_rows_kernel<WIDE, MB, 1, 16>, 16);
-            case 2: return go(scaled_rows_kernel<WIDE, MB, 2, 8>, 8);
-            case 3: return go(scaled_rows_kernel<WIDE, MB, 3, 8>, 8);
-            case 4: return go(scaled_rows_kernel<WIDE, MB, 4, 8>, 8);
-            case 5: return go(scaled_rows_kernel<WIDE, MB, 5, 8>, 8);
-            case 6: return go(scaled_rows_kernel<WIDE, MB, 6, 8>, 8);
-            case 7: return go(scaled_rows_kernel<WIDE, MB, 7, 8>, 8);
-            default: return go(scaled_rows_kernel<WIDE, MB, 8, 8>, 8);
+            case 1: return go(scaled_rows_kernel<WIDE, MB, 1>);
+            case 2: return go(scaled_rows_kernel<WIDE, MB, 2>);
+            case 3: return go(scaled_rows_kernel<WIDE, MB, 3>);
+            case 4: return go(scaled_rows_kernel<WIDE, MB, 4>);
+            case 5: return go(scaled_rows_kernel<WIDE, MB, 5>);
+            case 6: return go(scaled_rows_kernel<WIDE, MB, 6>);
+            case 7: return go(scaled_rows_kernel<WIDE, MB, 7>);
+            default: return go(scaled_rows_kernel<WIDE, MB, 8>);
         }
     };
     typedef std::integral_constant<int, 1> One;
