@@ -675,8 +675,12 @@ ns_status ns_quantize(int64_t batch, int64_t rows, int64_t cols, ns_dtype dtype,
 /* out = a b^T for such matrices a (m x k) and b (n x k), k a multiple of 128 up to
  * 2^22: out[i, j] = the sum over blocks of 2^(sa + sb - 254) times the block's sum
  * of products, added in fp32 and rounded once. Scale bytes are 1 .. 254 (others, which
- * ns_quantize does not write, are undefined). For F32 outputs a value times its scale is
- * taken as a bf16 number: below 2^-126 it may count as zero, past bf16's largest it is infinite.
+ * ns_quantize does not write, are undefined).
+ * BF16 outputs: within a block, bits of a product below some 2^-13 of the block's
+ * largest product are dropped, so a block's sum is off by up to some 2^-6 of that (1e-5
+ * to 1e-4 of a result's rms on random values), also where its products cancel.
+ * F32 outputs: every product counts in full. A value times its scale is taken as a bf16
+ * number: below 2^-126 it may count as zero, past bf16's largest it is infinite.
  * a_scales     [m, k / 128].
  * b_scales     [n, k / 128] (b_block_rows 1) or [ceil(n / 128), k / 128] (128).
  * out          (m, n) of out_dtype (BF16 or F32), rows out_ld elements apart.

@@ -22,6 +22,8 @@
 // of 4096 bf16 with a gate and both norms: forward 100 us (537 MB, 5.4 TB/s), backward
 // 171 us (805 MB, 4.7 TB/s; 5 us of it the second launch). The non-temporal hint
 // changed neither. 16 rows: 4.2 us, a launch and two chains of load, sum and barrier.
+// Backward, whose forms were settled at 4096, keeps less under way at other widths:
+// 16384 x 1024 52 us (3.9 TB/s), x 2141 222 (1.9), x 2560 146 (3.5), x 5120 253 (4.0).
 
 #include <algorithm>
 
@@ -404,7 +406,9 @@ struct BlockCall {
 
 // The form of a call by its width: the fewest waves whose lanes hold the row in 8 or 16 elements each. 4096 values on eight
 // waves of 8 in place of four of 16: 16384 rows bf16 forward 113 -> 109 us, backward, whose sums over rows fill the
-// registers, 186 -> 171 (with one partial row less). Above 8192 the backward form keeps some of them in scratch.
+// registers, 186 -> 171 (with one partial row less). The backward form keeps some of them in scratch above 8192 (48 to 636 bytes a lane)
+// and, all in fp32, above 4096 (92 bytes); forward does with an fp32 residual above 8192 (88, 108). 4096 x 16384 bf16 131 us
+// forward, 630 backward.
 void pick_form(BlockCall &c, int32_t hidden) {
     const int cap[6][3] = {{512, 1, 8}, {1024, 1, 16}, {2048, 4, 8}, {4096, 8, 8}, {8192, 8, 16}, {16384, 16, 16}};
     for (const auto &f : cap)

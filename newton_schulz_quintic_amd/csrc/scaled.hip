@@ -869,7 +869,7 @@ __global__ __launch_bounds__(kRowsThreads) void scaled_rows_kernel(MatArgs p) {
 // (scaled_stage.inc). Stages past the last one are loaded and read as the last one
 // and not used, so that the loop has one form.
 // Measured: 8192 x 4096 -> 14336 385-410 us (2340-2500 TFLOP/s), 8192 x 14336 -> 4096
-// 347 (2770), 8192^3 428 (2570): 81-85 % of the library's unscaled 8-bit product on the
+// 347 (2770), 8192^3 428 (2570): 80-84 % of the library's unscaled 8-bit product on the
 // same GPU. A stage takes 1.39 us on all CUs (3.1 PFLOP/s; instructions alone, on
 // random values, 3.77 at the clock that their power leaves) and a tile 7 us beside its
 // stages, most of it the outputs of 256 tiles that end together. Timed for what the
@@ -1103,6 +1103,7 @@ size_t partial_bytes(int64_t m, int64_t n, int64_t nkb, int32_t groups, int32_t 
 // of few 22 and up to 13 more. A round of 256 large ones takes 54 however few they are. With small, with large tiles: 2048
 // x 4096 -> 4096 37, 51 us; -> 4352 60, 53; -> 8192 70, 56; -> 8300 93, 110; 64 x 4096 -> 70000 76, 105; 8192 x 4096 ->
 // 14336 490, 393. Groups of rows are taken as equal: 64 groups of 128 rows, 4096 -> 4096 241, 279 us; of 187 365, 293.
+// Other depths are not weighed (32000 x 640 -> 7744 234 us, floor 100).
 bool quad_tiles(int64_t m, int64_t n, int32_t groups, int32_t reduce) {
     const int64_t copies = std::max(groups, 1), rows = groups && !reduce ? (m + groups - 1) / groups : m;
     const int64_t small = copies * blocks_of(rows) * blocks_of(n);
